@@ -22,6 +22,11 @@
  *     with reserved slots, the verify call advances the length in place).
  *   * Options of the chain call: top-p after top-k (§4 names it), the early
  *     end of a round at EOS or the length limit (§5).
+ *   * The cache between rounds: the target forward's attention of a round's
+ *     candidates over the committed pages (spec_verify_attention), the
+ *     attention weight each cached entry accumulates from the committed
+ *     candidates (spec_attention_weights) and the eviction of the lightest
+ *     entries (spec_evict_kv).
  *   * The draft side: one level of a topKSpec/topHead draft tree per
  *     spec_tree_level call ("投机推理" 树形投机怎么配置), and prompt-lookup
  *     drafts from the token history (spec_ngram_draft; §10.6.3 实际部署).
@@ -93,6 +98,13 @@ extern "C" {
                                 (top_k == 0; about 2 KiB per request position at V = 128,256) */
 #define SPEC_WS_TREE_LEVEL 5 /* n = H (parents a spec_tree_level call expands): one 144-byte
                                 summary per (row, 2048-logit slice) and per row */
+
+#define SPEC_WS_ATTENTION 6  /* n = S*Hq, V = D: arrival counters and the partial results of
+                                requests whose keys are split (spec_verify_attention);
+                                spec_attention_weights uses its header only */
+#define SPEC_WS_ATTENTION_SHARED 7 /* SPEC_WS_ATTENTION plus one f32 row per (request, candidate,
+                                head) for the part over a shared prefix */
+#define SPEC_WS_EVICT 8 /* n = budget, V = max_blocks * block_size: the moves of each request */
 
 /*
  * Chain verification, sampled (temperature > 0) or greedy (temperature == 0).
@@ -481,6 +493,176 @@ typedef struct SpecTreeLevelArgs {
 } SpecTreeLevelArgs;
 
 int spec_tree_level(const SpecTreeLevelArgs *args, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of a round's candidates over the paged cache: the part of the
+ * target's verify forward that reads what spec_commit_kv writes ("10.6 投机
+ * 解码" §10.6.3: the forward over [x, d_1..d_gamma], or over a tree's nodes with
+ * Table 10-17's mask).  One call per layer.
+ *
+ * Queries: candidate i (0 <= i < S) of request b, query head h (0 <= h < Hq) at
+ *   q + b*q_stride_b + i*q_stride_s + h*q_stride_h, D elements; head h reads
+ *   cached head h / (Hq/H).
+ * Keys: request b sees its committed_len[b] cached entries and the S
+ *   candidates themselves.  Entry c lies in block block_table[b][c/block_size]
+ *   of `cache` (spec_commit_kv's layout), the candidates' K/V in temp_kv (its
+ *   layout too), or with temp_kv NULL in the cache at entries
+ *   committed_len[b]..+S-1 (the reserved slots of the in-place commit).
+ *   Candidate j is a key of candidate i iff bit j of tree_mask[b][i] is set
+ *   (spec_verify_tree's mask with S = N+1; it and pos depend on the node
+ *   arrays only, so a call on one-logit rows gives them before the forward), or
+ *   without a mask iff j <= i.
+ * Positions: candidate i is at pos[b][i] (NULL: committed_len[b] + i), entry c
+ *   at key_pos[b][c] (row stride key_pos_stride; NULL: c; needed once entries
+ *   have been evicted).  They matter to the bias and the masks only.
+ * Score of query i, head h and a key, with dist = their positions' difference:
+ *   x = scale * (q . k);  softcap > 0: x = softcap * tanh(x / softcap);
+ *   slopes: x -= slopes[h] * dist;  the key is masked when window > 0 and
+ *   dist >= window, or its position is below first_pos[b] (the start of the
+ *   current document).  out = softmax(x) . v over the keys not masked;
+ *   lse = log(sum(exp(x))).  A query with no key left gets out = 0, lse = -inf.
+ *   What lies in a masked place, NaN included, does not matter.  A NaN or
+ *   infinite K or V that is not masked gives non-finite results in its rows.
+ * Shared prefix: with shared_len > 0 the first shared_len entries of every
+ *   request lie in the blocks of shared_table (block_table's entries for them
+ *   are not read where a block holds shared entries only) and are read once
+ *   for the batch.  key_pos must then be NULL.
+ * Outputs: out [B][S][Hq][D] in the inputs' type, lse f32 [B][S][Hq] (NULL =
+ *   not written), flags[b] (bits OR-ed in; NULL = not written).
+ * Data errors: a committed_len[b] that is negative, below shared_len or past
+ *   the table gives that request out = 0, lse = -inf; the entries of a block id
+ *   outside [0, num_blocks) are left out.  Both set SPEC_FLAG_BAD_INPUT in
+ *   flags[b] (a bad block of the shared table: in every request's) and in the
+ *   status word.
+ * Limits: bf16 or f32 (all of q, cache, temp_kv, out), D * element size a
+ *   multiple of 16 and D <= 256, H divides Hq, S <= 1024, B <= 32768, q, its
+ *   strides, cache, temp_kv and out on 16-byte boundaries.
+ * Arithmetic: f32 sums and softmax statistics; bf16 calls multiply on the
+ *   tensor cores with the softmax weights rounded to bf16.  The result does not
+ *   depend on timing: sums are taken in a fixed order.
+ * Workspace: SPEC_WS_ATTENTION bytes, or SPEC_WS_ATTENTION_SHARED with
+ *   shared_len > 0; zero before the first call, left zeroed where it must be.
+ */
+#define SPEC_ATTENTION_MAX_D 256
+#define SPEC_ATTENTION_MAX_S 1024
+typedef struct SpecAttentionArgs {
+    int32_t B, S, Hq, H, D, L, layer, dtype;
+    const void *q;               /* device */
+    int64_t q_stride_b, q_stride_s, q_stride_h; /* elements */
+    const void *cache;           /* device, [L][2][num_blocks][block_size][H][D] */
+    int64_t num_blocks;
+    int32_t block_size, max_blocks;
+    const int32_t *block_table;  /* device, int32 [B][max_blocks] */
+    const int32_t *committed_len; /* device, int32 [B] */
+    const void *temp_kv;         /* device, [B][L][2][S][H][D], or NULL: in place */
+    const uint32_t *tree_mask;   /* device, [B][S][ceil(S/32)] or NULL: causal */
+    const int32_t *pos;          /* device, int32 [B][S] or NULL */
+    const int32_t *key_pos;      /* device, int32 [B][key_pos_stride] or NULL */
+    int64_t key_pos_stride;
+    const int32_t *first_pos;    /* device, int32 [B] or NULL */
+    const float *slopes;         /* device, f32 [Hq] or NULL */
+    float scale;                 /* finite */
+    float softcap;               /* 0 = off */
+    int32_t window;              /* 0 = off */
+    int32_t shared_len;          /* 0 = off */
+    const int32_t *shared_table; /* device, int32 [ceil(shared_len/block_size)] */
+    void *out;                   /* device out */
+    float *lse;                  /* device out or NULL */
+    uint32_t *flags;             /* device in/out or NULL */
+} SpecAttentionArgs;
+
+int spec_verify_attention(const SpecAttentionArgs *args, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
+ * The attention weight that cached entries accumulate, for an eviction that
+ * goes by it.  Called after the round's commit, once per layer: for request b
+ * with n = n_slots[b] committed candidates, the j-th of them (candidate
+ * slots[b][j], or j with slots NULL) now being entry e_j = committed_len[b]-n+j,
+ *   weight[b][c] += sum over j with c <= e_j and the query heads h of
+ *                   exp(x(j, h, c) - lse[b][slots[b][j]][h])
+ * for shared_len <= c < committed_len[b], x being spec_verify_attention's score
+ * and lse what that call wrote in the same layer.  (The accepted path's
+ * ancestors are the committed candidates before it, so these are the weights
+ * of that call's softmax; rejected candidates leave none.)  Adding up over
+ * layers and rounds is the caller's choice of calls.  A candidate whose lse is
+ * -inf adds nothing.
+ * key_pos (in/out when given): entry e_j gets pos[b][slots[b][j]].
+ * weight's entries at or past committed_len must be zero before the commit
+ *   (spec_evict_kv leaves them so).
+ * Data errors: n_slots[b] outside [0, S] or above committed_len[b], a
+ *   committed_len[b] past the table, a slot outside [0, S): the request is
+ *   skipped; the entries of a bad block id are left out; SPEC_FLAG_BAD_INPUT in
+ *   flags[b] and the status word.  Limits as for spec_verify_attention.
+ * Workspace: SPEC_WS_COMMIT bytes suffice (the status word).
+ */
+typedef struct SpecWeightsArgs {
+    int32_t B, S, Hq, H, D, L, layer, dtype;
+    const void *q;               /* device, as in the attention call */
+    int64_t q_stride_b, q_stride_s, q_stride_h;
+    const float *lse;            /* device, f32 [B][S][Hq] */
+    const void *cache;
+    int64_t num_blocks;
+    int32_t block_size, max_blocks;
+    const int32_t *block_table;
+    const int32_t *committed_len; /* device, int32 [B]: after the commit */
+    const int32_t *slots;        /* device, int32 [B][slots_stride] or NULL (identity) */
+    int32_t slots_stride;        /* >= S when slots != NULL */
+    const int32_t *n_slots;      /* device, int32 [B] */
+    const int32_t *pos;          /* device, int32 [B][S] or NULL: e_j */
+    int32_t *key_pos;            /* device in/out, int32 [B][key_pos_stride] or NULL */
+    int64_t key_pos_stride;
+    const int32_t *first_pos;
+    const float *slopes;
+    float scale, softcap;
+    int32_t window, shared_len;
+    float *weight;               /* device in/out, f32 [B][weight_stride] */
+    int64_t weight_stride;       /* >= max_blocks * block_size */
+    uint32_t *flags;             /* device in/out [B] or NULL */
+} SpecWeightsArgs;
+
+int spec_attention_weights(const SpecWeightsArgs *args, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
+ * Eviction: every request with more than `budget` entries is cut back to
+ * `budget`, in every layer alike.  Entry c has position key_pos[b][c].  Kept are
+ * the entries at positions below `sink`, those within `recent` of the newest
+ * (position > newest - recent), and of the others the heaviest by weight[b][c]
+ * (ties to the lowest entry).  The kept entries at or past `budget` move into
+ * the evicted ones' places below it, both in ascending order, so as few
+ * entries as possible are copied; a cache entry's index is then no longer its
+ * position, which key_pos keeps.  weight and key_pos move along and are zero
+ * at and past the new length up to the old one; committed_len[b] becomes
+ * budget; blocks_in_use[b] (optional) = ceil(length / block_size), for every
+ * request whose length is in range.  Entries at or past the new length keep
+ * their bytes.
+ * A batch that shares a prefix passes sink >= shared_len, so that no shared
+ * entry moves.
+ * Errors: SPEC_ERR_INVALID_ARG for budget < 1, sink < 0, recent < 0 or sink +
+ *   recent > budget.  A request with a length outside [0, max_blocks *
+ *   block_size], a block id it holds outside [0, num_blocks), a NaN weight or
+ *   negative position, or (its positions repeat) more than `budget` protected
+ *   entries is left as it is and flagged SPEC_FLAG_BAD_INPUT.
+ * Workspace: SPEC_WS_EVICT bytes (no zeroing needed but for the status word).
+ */
+typedef struct SpecEvictArgs {
+    int32_t B, L, H, D, block_size, elem_bytes;
+    void *cache;                 /* device in/out, [L][2][num_blocks][block_size][H][D] */
+    int64_t num_blocks;
+    const int32_t *block_table;  /* device, int32 [B][max_blocks] */
+    int32_t max_blocks;
+    int32_t budget, sink, recent;
+    int32_t *committed_len;      /* device in/out [B] */
+    float *weight;               /* device in/out, f32 [B][weight_stride] */
+    int64_t weight_stride;       /* >= max_blocks * block_size */
+    int32_t *key_pos;            /* device in/out, int32 [B][key_pos_stride] */
+    int64_t key_pos_stride;      /* >= max_blocks * block_size */
+    int32_t *blocks_in_use;      /* device out [B] or NULL */
+    uint32_t *flags;             /* device in/out [B] or NULL (bits are OR-ed in) */
+} SpecEvictArgs;
+
+int spec_evict_kv(const SpecEvictArgs *args, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Diagnostic: the largest relative error of the GPU's hardware exponential
  * (ex2.approx.ftz.f32) against fp64 over every fp32 input in [-126, 1], on the

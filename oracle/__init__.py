@@ -9,3 +9,5 @@ from .spec_oracle import (BOUNDARY_MARGIN, DEFAULT_EPS, FLAG_BAD_INPUT, FLAG_BAD
                           FLAG_FALLBACK)
 from .ngram_oracle import NgramDraft, ngram_draft  # noqa: F401
 from .tree_build_oracle import Level, Tree, build_tree, expand_level  # noqa: F401
+from .attention_oracle import (Attention, Eviction, attend, candidate_mask, entries, entry_weights,  # noqa: F401
+                               evict, hidden, scores)

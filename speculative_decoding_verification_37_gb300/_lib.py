@@ -22,6 +22,7 @@ SPEC_DTYPE_BF16, SPEC_DTYPE_F32 = 0, 1
 SPEC_FLAG_BAD_INPUT, SPEC_FLAG_FALLBACK, SPEC_FLAG_BAD_ROW, SPEC_FLAG_TIMEOUT = 1, 2, 4, 8
 SPEC_WS_CHAIN, SPEC_WS_TREE, SPEC_WS_COMMIT, SPEC_WS_CHAIN_TOPK, SPEC_WS_CHAIN_FULL = 0, 1, 2, 3, 4
 SPEC_WS_TREE_LEVEL = 5
+SPEC_WS_ATTENTION, SPEC_WS_ATTENTION_SHARED, SPEC_WS_EVICT = 6, 7, 8
 SPEC_FLAG_EOS, SPEC_FLAG_LIMIT = 16, 32
 SPEC_TREE_MAX_HEADS = 64
 TOPK_FAST_MAX = 128   # top_k served by the candidate-pool path when the workspace holds it
@@ -29,7 +30,7 @@ TOPK_FAST_MAX = 128   # top_k served by the candidate-pool path when the workspa
 EXPORTED = ("spec_verify_chain", "spec_verify_tree", "spec_commit_kv", "spec_workspace_bytes",
             "spec_get_status", "spec_error_string", "spec_last_cuda_error",
             "spec_verify_chain_static", "spec_selftest_ex2", "spec_ngram_draft", "spec_tree_level",
-            "spec_set_idle_limit")
+            "spec_set_idle_limit", "spec_verify_attention", "spec_attention_weights", "spec_evict_kv")
 
 
 class SpecChainArgs(ctypes.Structure):
@@ -83,6 +84,43 @@ class SpecTreeLevelArgs(ctypes.Structure):
                 ("next_parents", c_void_p), ("flags", c_void_p)]
 
 
+class SpecAttentionArgs(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("S", c_int32), ("Hq", c_int32), ("H", c_int32), ("D", c_int32),
+                ("L", c_int32), ("layer", c_int32), ("dtype", c_int32), ("q", c_void_p),
+                ("q_stride_b", c_int64), ("q_stride_s", c_int64), ("q_stride_h", c_int64),
+                ("cache", c_void_p), ("num_blocks", c_int64), ("block_size", c_int32),
+                ("max_blocks", c_int32), ("block_table", c_void_p), ("committed_len", c_void_p),
+                ("temp_kv", c_void_p), ("tree_mask", c_void_p), ("pos", c_void_p),
+                ("key_pos", c_void_p), ("key_pos_stride", c_int64), ("first_pos", c_void_p),
+                ("slopes", c_void_p), ("scale", c_float), ("softcap", c_float), ("window", c_int32),
+                ("shared_len", c_int32), ("shared_table", c_void_p), ("out", c_void_p),
+                ("lse", c_void_p), ("flags", c_void_p)]
+
+
+class SpecWeightsArgs(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("S", c_int32), ("Hq", c_int32), ("H", c_int32), ("D", c_int32),
+                ("L", c_int32), ("layer", c_int32), ("dtype", c_int32), ("q", c_void_p),
+                ("q_stride_b", c_int64), ("q_stride_s", c_int64), ("q_stride_h", c_int64),
+                ("lse", c_void_p), ("cache", c_void_p), ("num_blocks", c_int64),
+                ("block_size", c_int32), ("max_blocks", c_int32), ("block_table", c_void_p),
+                ("committed_len", c_void_p), ("slots", c_void_p), ("slots_stride", c_int32),
+                ("n_slots", c_void_p), ("pos", c_void_p), ("key_pos", c_void_p),
+                ("key_pos_stride", c_int64), ("first_pos", c_void_p), ("slopes", c_void_p),
+                ("scale", c_float), ("softcap", c_float), ("window", c_int32),
+                ("shared_len", c_int32), ("weight", c_void_p), ("weight_stride", c_int64),
+                ("flags", c_void_p)]
+
+
+class SpecEvictArgs(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("L", c_int32), ("H", c_int32), ("D", c_int32),
+                ("block_size", c_int32), ("elem_bytes", c_int32), ("cache", c_void_p),
+                ("num_blocks", c_int64), ("block_table", c_void_p), ("max_blocks", c_int32),
+                ("budget", c_int32), ("sink", c_int32), ("recent", c_int32),
+                ("committed_len", c_void_p), ("weight", c_void_p), ("weight_stride", c_int64),
+                ("key_pos", c_void_p), ("key_pos_stride", c_int64), ("blocks_in_use", c_void_p),
+                ("flags", c_void_p)]
+
+
 class SpecError(RuntimeError):
     def __init__(self, fn: str, code: int):
         msg = f"{fn} returned {code} ({lib().spec_error_string(code).decode()})"
@@ -126,6 +164,10 @@ def lib():
         L.spec_ngram_draft.restype = c_int
         L.spec_tree_level.argtypes = [POINTER(SpecTreeLevelArgs), c_void_p, c_size_t, c_void_p]
         L.spec_tree_level.restype = c_int
+        for f, args in (("spec_verify_attention", SpecAttentionArgs), ("spec_attention_weights", SpecWeightsArgs),
+                        ("spec_evict_kv", SpecEvictArgs)):
+            getattr(L, f).argtypes = [POINTER(args), c_void_p, c_size_t, c_void_p]
+            getattr(L, f).restype = c_int
         _LIB = L
     return _LIB
 
@@ -338,3 +380,157 @@ def spec_verify_chain_static(*, target_logits: torch.Tensor, draft_tokens: torch
                       eos_token=0 if eos_token is None else int(eos_token), max_new=_ptr(max_new),
                       top_p=float(top_p))
     _check("spec_verify_chain_static", lib().spec_verify_chain_static(ctypes.byref(a), _stream(stream)))
+
+
+def _device_args(fn: str, device, **tensors) -> None:
+    """Checks (tensor, dtype, shape or None) triples: on `device`, of the
+    dtype, of the shape (-1 = any; a shape asks for contiguous rows)."""
+    for name, (t, dtype, shape) in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+        if t.device != device:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
+        if shape is not None:
+            if t.dim() != len(shape) or any(w not in (-1, n) for n, w in zip(t.shape, shape)):
+                raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+            if not t.is_contiguous():
+                raise ValueError(f"{fn}: {name} must be contiguous")
+
+
+def _rows(fn: str, device, name: str, t: Optional[torch.Tensor], dtype, B: int, width: int) -> int:
+    """Row stride of a [B, >= width] tensor whose rows are contiguous."""
+    if t is None:
+        return 0
+    _device_args(fn, device, **{name: (t, dtype, None)})
+    if t.dim() != 2 or t.shape[0] != B or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected [{B}, >= {width}] with contiguous rows")
+    return t.stride(0) if B > 1 else t.shape[1]
+
+
+def _cache_args(fn: str, device, cache: torch.Tensor, block_table: torch.Tensor, committed_len: torch.Tensor,
+                block_size: int):
+    if cache.dim() != 6 or cache.shape[1] != 2 or cache.shape[3] != block_size or not cache.is_contiguous():
+        raise ValueError(f"{fn}: cache must be contiguous [L, 2, num_blocks, {block_size}, H, D], "
+                         f"not {tuple(cache.shape)}")
+    if block_table.dim() != 2:
+        raise ValueError(f"{fn}: block_table must be [B, max_blocks]")
+    B = block_table.shape[0]
+    _device_args(fn, device, cache=(cache, cache.dtype, None), block_table=(block_table, torch.int32, (B, -1)),
+                 committed_len=(committed_len, torch.int32, (B,)))
+    return B
+
+
+def _scored_args(fn: str, q, cache, block_table, committed_len, block_size, layer, pos, key_pos, first_pos,
+                 slopes, flags):
+    """The arguments spec_verify_attention and spec_attention_weights share."""
+    dev = q.device
+    if not q.is_cuda:
+        raise ValueError(f"{fn}: q must be on a CUDA device")
+    B = _cache_args(fn, dev, cache, block_table, committed_len, block_size)
+    L, _, nb, bs, H, D = cache.shape
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or (D > 1 and q.stride(3) != 1):
+        raise ValueError(f"{fn}: q must be [{B}, S, Hq, {D}] with contiguous last dimension, not {tuple(q.shape)}")
+    if q.dtype != cache.dtype:
+        raise TypeError(f"{fn}: q is {q.dtype} and cache {cache.dtype}")
+    S, Hq = q.shape[1], q.shape[2]
+    cap = block_table.shape[1] * bs
+    _device_args(fn, dev, pos=(pos, torch.int32, (B, S)), first_pos=(first_pos, torch.int32, (B,)),
+                 slopes=(slopes, torch.float32, (Hq,)), flags=(flags, torch.int32, (B,)))
+    kps = _rows(fn, dev, "key_pos", key_pos, torch.int32, B, cap)
+    # strides of dimensions of one element do not matter; the library wants them aligned
+    sb, ss, sh = (q.stride(i) if q.shape[i] > 1 else 0 for i in range(3))
+    return dict(B=B, S=S, Hq=Hq, H=H, D=D, L=L, layer=int(layer), dtype=_dtype_code(q), q=_ptr(q), q_stride_b=sb,
+                q_stride_s=ss, q_stride_h=sh, cache=_ptr(cache), num_blocks=nb, block_size=bs,
+                max_blocks=block_table.shape[1], block_table=_ptr(block_table), committed_len=_ptr(committed_len),
+                pos=_ptr(pos), key_pos=_ptr(key_pos), key_pos_stride=kps, first_pos=_ptr(first_pos),
+                slopes=_ptr(slopes), flags=_ptr(flags))
+
+
+def _launch(fn: str, args, workspace: torch.Tensor, device, stream) -> None:
+    """Calls `fn` with `device` current, on the given stream or that device's current one."""
+    if workspace.device != device:
+        raise ValueError(f"{fn}: the workspace is on {workspace.device}, not {device}")
+    with torch.cuda.device(device):
+        _check(fn, getattr(lib(), fn)(ctypes.byref(args), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def spec_verify_attention(*, q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                          committed_len: torch.Tensor, block_size: int, out: torch.Tensor,
+                          workspace: torch.Tensor, scale: float, layer: int = 0,
+                          temp_kv: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+                          pos: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None,
+                          first_pos: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                          softcap: float = 0.0, window: int = 0, shared_table: Optional[torch.Tensor] = None,
+                          shared_len: int = 0, lse: Optional[torch.Tensor] = None,
+                          flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Marshals one spec_verify_attention call: q [B, S, Hq, D] (last dimension
+    contiguous), cache [L, 2, num_blocks, block_size, H, D], temp_kv
+    [B, L, 2, S, H, D], tree_mask int32 [B, S, ceil(S/32)], out [B, S, Hq, D],
+    lse f32 [B, S, Hq]."""
+    fn = "spec_verify_attention"
+    common = _scored_args(fn, q, cache, block_table, committed_len, block_size, layer, pos, key_pos, first_pos,
+                          slopes, flags)
+    B, S, Hq, H, D, L = (common[k] for k in ("B", "S", "Hq", "H", "D", "L"))
+    need = -(-int(shared_len) // block_size)
+    _device_args(fn, q.device, temp_kv=(temp_kv, q.dtype, (B, L, 2, S, H, D)),
+                 tree_mask=(tree_mask, torch.int32, (B, S, (S + 31) // 32)), out=(out, q.dtype, (B, S, Hq, D)),
+                 lse=(lse, torch.float32, (B, S, Hq)), shared_table=(shared_table, torch.int32, (-1,)))
+    if shared_len > 0 and (shared_table is None or shared_table.numel() < need):
+        raise ValueError(f"{fn}: shared_len {shared_len} needs a shared_table of {need} blocks")
+    a = SpecAttentionArgs(temp_kv=_ptr(temp_kv), tree_mask=_ptr(tree_mask), scale=float(scale),
+                          softcap=float(softcap), window=int(window), shared_len=int(shared_len),
+                          shared_table=_ptr(shared_table), out=_ptr(out), lse=_ptr(lse), **common)
+    _launch(fn, a, workspace, q.device, stream)
+
+
+def spec_attention_weights(*, q: torch.Tensor, lse: torch.Tensor, cache: torch.Tensor,
+                           block_table: torch.Tensor, committed_len: torch.Tensor, n_slots: torch.Tensor,
+                           weight: torch.Tensor, block_size: int, workspace: torch.Tensor, scale: float,
+                           layer: int = 0, slots: Optional[torch.Tensor] = None,
+                           pos: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None,
+                           first_pos: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                           softcap: float = 0.0, window: int = 0, shared_len: int = 0,
+                           flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Marshals one spec_attention_weights call: q, lse as in the attention
+    call, committed_len after the commit, slots int32 [B, >= S], weight f32
+    [B, >= max_blocks*block_size]."""
+    fn = "spec_attention_weights"
+    common = _scored_args(fn, q, cache, block_table, committed_len, block_size, layer, pos, key_pos, first_pos,
+                          slopes, flags)
+    B, S, Hq = common["B"], common["S"], common["Hq"]
+    _device_args(fn, q.device, lse=(lse, torch.float32, (B, S, Hq)), n_slots=(n_slots, torch.int32, (B,)))
+    cap = block_table.shape[1] * block_size
+    a = SpecWeightsArgs(lse=_ptr(lse), slots=_ptr(slots),
+                        slots_stride=_rows(fn, q.device, "slots", slots, torch.int32, B, S),
+                        n_slots=_ptr(n_slots), scale=float(scale), softcap=float(softcap), window=int(window),
+                        shared_len=int(shared_len), weight=_ptr(weight),
+                        weight_stride=_rows(fn, q.device, "weight", weight, torch.float32, B, cap), **common)
+    _launch(fn, a, workspace, q.device, stream)
+
+
+def spec_evict_kv(*, cache: torch.Tensor, block_table: torch.Tensor, committed_len: torch.Tensor,
+                  weight: torch.Tensor, key_pos: torch.Tensor, block_size: int, budget: int,
+                  workspace: torch.Tensor, sink: int = 0, recent: int = 0,
+                  blocks_in_use: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+                  stream=None) -> None:
+    """Marshals one spec_evict_kv call: cache [L, 2, num_blocks, block_size, H, D],
+    weight f32 and key_pos int32 [B, >= max_blocks*block_size], all in/out."""
+    fn = "spec_evict_kv"
+    if not cache.is_cuda:
+        raise ValueError(f"{fn}: cache must be on a CUDA device")
+    B = _cache_args(fn, cache.device, cache, block_table, committed_len, block_size)
+    L, _, nb, bs, H, D = cache.shape
+    cap = block_table.shape[1] * bs
+    _device_args(fn, cache.device, blocks_in_use=(blocks_in_use, torch.int32, (B,)),
+                 flags=(flags, torch.int32, (B,)))
+    a = SpecEvictArgs(B=B, L=L, H=H, D=D, block_size=bs, elem_bytes=cache.element_size(), cache=_ptr(cache),
+                      num_blocks=nb, block_table=_ptr(block_table), max_blocks=block_table.shape[1],
+                      budget=int(budget), sink=int(sink), recent=int(recent), committed_len=_ptr(committed_len),
+                      weight=_ptr(weight),
+                      weight_stride=_rows(fn, cache.device, "weight", weight, torch.float32, B, cap),
+                      key_pos=_ptr(key_pos),
+                      key_pos_stride=_rows(fn, cache.device, "key_pos", key_pos, torch.int32, B, cap),
+                      blocks_in_use=_ptr(blocks_in_use), flags=_ptr(flags))
+    _launch(fn, a, workspace, cache.device, stream)

@@ -168,6 +168,88 @@ def commit_kv(temp_kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
 
 
 @dataclass
+class AttentionOut:
+    out: torch.Tensor            # [B, S, Hq, D], q's type
+    lse: torch.Tensor            # f32 [B, S, Hq]
+
+
+def verify_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                     committed_len: torch.Tensor, *, block_size: int, layer: int = 0,
+                     temp_kv: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None,
+                     pos: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None,
+                     first_pos: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                     scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                     shared_table: Optional[torch.Tensor] = None, shared_len: int = 0,
+                     flags: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                     stream=None) -> AttentionOut:
+    """One layer's attention of a round's candidates (the last emitted token
+    and the drafts, or a tree's nodes) over the paged cache and the candidates
+    themselves.
+
+    q [B, S, Hq, D] (bf16 or f32, Hq a multiple of the cache's H; strides are
+    free but for the last dimension's), cache [L, 2, num_blocks, block_size,
+    H, D].  The candidates' K/V are temp_kv [B, L, 2, S, H, D], or without it
+    the cache's entries committed_len[b] .. + S - 1.  tree_mask and pos as
+    verify_tree returns them (without: a chain at committed_len[b] + i);
+    key_pos int32 [B, max_blocks*block_size]: the entries' positions once some
+    were evicted.  scale defaults to D**-0.5; softcap > 0 caps the scores by a
+    tanh; slopes f32 [Hq] subtract slope * distance; window > 0 and first_pos
+    (int32 [B]) mask by position.  With shared_len > 0 every request's first
+    shared_len entries lie in shared_table's blocks and are read once for the
+    whole batch.  A query that sees no key gets 0 and an lse of -inf."""
+    B, S, Hq, D = q.shape
+    out = AttentionOut(out=torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device),
+                       lse=torch.empty((B, S, Hq), dtype=torch.float32, device=q.device))
+    if ws is None:
+        ws = workspace(L.SPEC_WS_ATTENTION_SHARED if shared_len > 0 else L.SPEC_WS_ATTENTION, B, S * Hq, D, q.device)
+    L.spec_verify_attention(q=q, cache=cache, block_table=block_table, committed_len=committed_len,
+                            block_size=block_size, out=out.out, lse=out.lse, workspace=ws, layer=layer,
+                            scale=D ** -0.5 if scale is None else scale, temp_kv=temp_kv, tree_mask=tree_mask,
+                            pos=pos, key_pos=key_pos, first_pos=first_pos, slopes=slopes, softcap=softcap,
+                            window=window, shared_table=shared_table, shared_len=shared_len, flags=flags,
+                            stream=stream)
+    return out
+
+
+def attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                      committed_len: torch.Tensor, n_slots: torch.Tensor, weight: torch.Tensor, *,
+                      block_size: int, layer: int = 0, slots: Optional[torch.Tensor] = None,
+                      pos: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None,
+                      first_pos: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                      scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                      shared_len: int = 0, flags: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """After a commit, adds to weight (f32 [B, max_blocks*block_size], in
+    place) what each cached entry got of the committed candidates' attention
+    in one layer: n_slots and slots as passed to commit_kv, committed_len as it
+    left it, q and lse those of verify_attention, and the same scoring
+    arguments.  key_pos, if given, gets the new entries' positions."""
+    if ws is None:
+        ws = workspace(L.SPEC_WS_COMMIT, q.shape[0], 0, 0, q.device)
+    L.spec_attention_weights(q=q, lse=lse, cache=cache, block_table=block_table, committed_len=committed_len,
+                             n_slots=n_slots, weight=weight, block_size=block_size, workspace=ws, layer=layer,
+                             scale=q.shape[-1] ** -0.5 if scale is None else scale, slots=slots, pos=pos,
+                             key_pos=key_pos, first_pos=first_pos, slopes=slopes, softcap=softcap,
+                             window=window, shared_len=shared_len, flags=flags, stream=stream)
+
+
+def evict_kv(cache: torch.Tensor, block_table: torch.Tensor, committed_len: torch.Tensor, weight: torch.Tensor,
+             key_pos: torch.Tensor, *, block_size: int, budget: int, sink: int = 0, recent: int = 0,
+             blocks_in_use: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+             ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cuts every request with more than `budget` entries back to it, in place
+    and in every layer: the entries at positions below `sink`, the `recent`
+    newest positions and the heaviest others stay; those at or past the
+    budget move into the places of the evicted ones.  cache, committed_len,
+    weight and key_pos are updated on the device."""
+    if ws is None:
+        ws = workspace(L.SPEC_WS_EVICT, block_table.shape[0], budget, block_table.shape[1] * block_size, cache.device)
+    L.spec_evict_kv(cache=cache, block_table=block_table, committed_len=committed_len, weight=weight,
+                    key_pos=key_pos, block_size=block_size, budget=budget, workspace=ws, sink=sink, recent=recent,
+                    blocks_in_use=blocks_in_use, flags=flags, stream=stream)
+
+
+@dataclass
 class NgramOut:
     draft_tokens: torch.Tensor   # int32 [B, gamma], -1 past n_draft
     n_draft: torch.Tensor        # int32 [B]

@@ -235,12 +235,20 @@ extern "C" size_t spec_workspace_bytes(int kind, int32_t B, int32_t n, int32_t V
         return kWsHeader + ws_align((size_t)B * sizeof(unsigned));
     case SPEC_WS_TREE_LEVEL:
         return tree_level_layout(B, n, V, nullptr, nullptr);
+    case SPEC_WS_ATTENTION:
+    case SPEC_WS_ATTENTION_SHARED:
+        return attn_ws_layout(B, n, V, kind == SPEC_WS_ATTENTION_SHARED, nullptr, nullptr);
+    case SPEC_WS_EVICT:
+        return evict_ws_layout(B, n, V, nullptr, nullptr);
     default:
         return 0;
     }
 }
 
 namespace specv {
+
+int report_cuda_error(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : cuda_fail(e); }
+int device_sms() { return sm_count(); }
 
 // Every host-side check of a chain call's arguments except the workspace's:
 // SPEC_OK or the code the call returns, before anything is enqueued.

@@ -1,0 +1,160 @@
+"""The attention, entry-weight and eviction entry points on the CPU: struct
+layouts, workspace sizes and the refusals, all before anything is enqueued."""
+import ctypes
+import os
+import subprocess
+import tempfile
+
+import pytest
+import torch
+
+from conftest import ROOT
+from speculative_decoding_verification_37_gb300 import _lib as L
+from speculative_decoding_verification_37_gb300 import build as B
+
+HEADER = os.path.join(ROOT, "include", "spec_verify.h")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return L.lib()
+
+
+def test_struct_layouts_match_c():
+    structs = {"SpecAttentionArgs": L.SpecAttentionArgs, "SpecWeightsArgs": L.SpecWeightsArgs,
+               "SpecEvictArgs": L.SpecEvictArgs}
+    lines = []
+    for name, cls in structs.items():
+        lines.append('printf("%s %%zu\\n", sizeof(%s));' % (name, name))
+        lines += ['printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (name, f, name, f) for f, _ in cls._fields_]
+    src = "#include <stdio.h>\n#include <stddef.h>\n#include \"spec_verify.h\"\nint main(void) {\n%s\nreturn 0; }\n" % "\n".join(lines)
+    with tempfile.TemporaryDirectory() as d:
+        c, exe = os.path.join(d, "l.c"), os.path.join(d, "l")
+        open(c, "w").write(src)
+        subprocess.run(["gcc", "-I", os.path.dirname(HEADER), c, "-o", exe], check=True)
+        out = subprocess.run([exe], capture_output=True, text=True, check=True).stdout
+    for line in out.split("\n"):
+        if line:
+            key, val = line.split()
+            s, _, f = key.partition(".")
+            assert int(val) == (getattr(structs[s], f).offset if f else ctypes.sizeof(structs[s])), key
+
+
+def test_workspace_sizes(lib):
+    one = L.spec_workspace_bytes(L.SPEC_WS_ATTENTION, 4, 20, 128)
+    assert one == L.spec_workspace_bytes(L.SPEC_WS_ATTENTION, 400, 20, 128) > 256
+    shared = L.spec_workspace_bytes(L.SPEC_WS_ATTENTION_SHARED, 4, 20, 128)
+    assert shared >= one + 4 * 20 * (128 + 1) * 4
+    # a request's moves: at most what lies past the budget, or below it
+    ev = lambda budget, cap: L.spec_workspace_bytes(L.SPEC_WS_EVICT, 3, budget, cap)  # noqa: E731
+    assert ev(100, 100) <= 512 + 256 and ev(100, 130) >= 3 * 30 * 8 and ev(10, 1000) < 3 * 20 * 8 + 1024
+
+
+def attention(**over):
+    a = L.SpecAttentionArgs(B=2, S=3, Hq=4, H=2, D=64, L=2, layer=1, dtype=L.SPEC_DTYPE_BF16, q=4096,
+                            q_stride_b=768, q_stride_s=256, q_stride_h=64, cache=4096, num_blocks=9, block_size=16,
+                            max_blocks=4, block_table=4096, committed_len=4096, scale=0.125, out=4096, lse=4096)
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+def weights(**over):
+    a = L.SpecWeightsArgs(B=2, S=3, Hq=4, H=2, D=64, L=2, layer=1, dtype=L.SPEC_DTYPE_BF16, q=4096, q_stride_b=768,
+                          q_stride_s=256, q_stride_h=64, lse=4096, cache=4096, num_blocks=9, block_size=16,
+                          max_blocks=4, block_table=4096, committed_len=4096, n_slots=4096, scale=0.125,
+                          weight=4096, weight_stride=64)
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+def evict(**over):
+    a = L.SpecEvictArgs(B=2, L=2, H=2, D=64, block_size=16, elem_bytes=2, cache=4096, num_blocks=9, block_table=4096,
+                        max_blocks=4, budget=20, sink=2, recent=4, committed_len=4096, weight=4096, weight_stride=64,
+                        key_pos=4096, key_pos_stride=64)
+    for k, v in over.items():
+        setattr(a, k, v)
+    return a
+
+
+NAN, INF = float("nan"), float("inf")
+SCORED = [dict(B=-1), dict(B=32769), dict(S=0), dict(S=1025), dict(H=0), dict(Hq=0), dict(Hq=5), dict(D=0),
+          dict(L=0), dict(layer=-1), dict(layer=2), dict(dtype=2), dict(block_size=0), dict(max_blocks=0),
+          dict(num_blocks=0), dict(scale=NAN), dict(scale=INF), dict(softcap=-1.0), dict(softcap=NAN),
+          dict(softcap=INF), dict(softcap=1e-45), dict(window=-1), dict(shared_len=-1), dict(shared_len=65),
+          dict(key_pos=4096, key_pos_stride=63), dict(q=None), dict(cache=None), dict(block_table=None),
+          dict(committed_len=None), dict(q=4104), dict(cache=4100), dict(q_stride_b=4), dict(q_stride_s=7),
+          dict(q_stride_h=65)]
+
+
+def refused(lib, fn, a, nbytes=1 << 28):
+    # no kernel may start: on a host without a GPU it would return SPEC_ERR_CUDA
+    return getattr(lib, fn)(ctypes.byref(a), ctypes.c_void_p(4096), nbytes, None)
+
+
+@pytest.mark.parametrize("bad", SCORED + [
+    dict(out=None), dict(out=4104), dict(temp_kv=4104), dict(shared_len=8), dict(shared_len=8, shared_table=4096,
+                                                                                key_pos=4096, key_pos_stride=64)])
+def test_attention_refusals(lib, bad):
+    assert refused(lib, "spec_verify_attention", attention(**bad)) == L.SPEC_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", SCORED + [
+    dict(lse=None), dict(n_slots=None), dict(weight=None), dict(weight_stride=63), dict(slots=4096, slots_stride=2)])
+def test_weights_refusals(lib, bad):
+    assert refused(lib, "spec_attention_weights", weights(**bad)) == L.SPEC_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("bad", [
+    dict(B=-1), dict(B=32769), dict(L=0), dict(H=0), dict(D=0), dict(block_size=0), dict(num_blocks=0),
+    dict(max_blocks=0), dict(elem_bytes=3), dict(budget=0), dict(sink=-1), dict(recent=-1), dict(sink=10, recent=11),
+    dict(weight_stride=63), dict(key_pos_stride=63), dict(cache=None), dict(cache=4104), dict(block_table=None),
+    dict(committed_len=None), dict(weight=None), dict(key_pos=None)])
+def test_evict_refusals(lib, bad):
+    assert refused(lib, "spec_evict_kv", evict(**bad)) == L.SPEC_ERR_INVALID_ARG
+
+
+def test_unsupported_sizes_and_workspaces(lib):
+    for fn, make in (("spec_verify_attention", attention), ("spec_attention_weights", weights)):
+        for bad in (dict(D=260), dict(D=12), dict(max_blocks=1 << 30, weight_stride=1 << 40) if make is weights else
+                    dict(max_blocks=1 << 30)):
+            assert refused(lib, fn, make(**bad)) == L.SPEC_ERR_UNSUPPORTED, bad
+        assert getattr(lib, fn)(None, None, 0, None) == L.SPEC_ERR_INVALID_ARG
+        assert getattr(lib, fn)(ctypes.byref(make()), None, 1 << 28, None) == L.SPEC_ERR_INVALID_ARG
+        assert getattr(lib, fn)(ctypes.byref(make()), ctypes.c_void_p(4096), 64, None) == L.SPEC_ERR_INVALID_ARG
+        assert getattr(lib, fn)(ctypes.byref(make()), ctypes.c_void_p(4097), 1 << 28, None) == L.SPEC_ERR_INVALID_ARG
+        assert getattr(lib, fn)(ctypes.byref(make(B=0, q=None)), None, 0, None) == L.SPEC_OK
+    assert refused(lib, "spec_verify_attention", attention(shared_len=8, shared_table=4096),
+                   L.spec_workspace_bytes(L.SPEC_WS_ATTENTION, 2, 12, 64)) == L.SPEC_ERR_INVALID_ARG
+    assert refused(lib, "spec_evict_kv", evict(D=65, H=1)) == L.SPEC_ERR_UNSUPPORTED
+    assert refused(lib, "spec_evict_kv", evict(), 300) == L.SPEC_ERR_INVALID_ARG
+    assert lib.spec_evict_kv(ctypes.byref(evict(B=0)), None, 0, None) == L.SPEC_OK
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
+    from speculative_decoding_verification_37_gb300 import api
+    cache = torch.zeros((1, 2, 4, 16, 2, 64), dtype=torch.bfloat16)
+    table, lens = torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q = torch.zeros((1, 3, 4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        api.verify_attention(q, cache, table, lens, block_size=16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        api.attention_weights(q, torch.zeros((1, 3, 4)), cache, table, lens, lens, torch.zeros((1, 32)), block_size=16)
+    with pytest.raises(ValueError, match="CUDA device"):
+        api.evict_kv(cache, table, lens, torch.zeros((1, 32)), torch.zeros((1, 32), dtype=torch.int32), block_size=16,
+                     budget=4)
+    # the checks of shape and type themselves
+    with pytest.raises(ValueError, match="cache must be"):
+        L._cache_args("f", cache.device, cache, table, lens, 8)
+    with pytest.raises(TypeError, match="block_table must be"):
+        L._cache_args("f", cache.device, cache, table.long(), lens, 16)
+    with pytest.raises(ValueError, match="committed_len has shape"):
+        L._cache_args("f", cache.device, cache, table, torch.zeros(2, dtype=torch.int32), 16)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        L._rows("f", cache.device, "weight", torch.zeros((1, 31)), torch.float32, 1, 32)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        L._rows("f", cache.device, "weight", torch.zeros((32, 2)).T, torch.float32, 2, 32)
+    with pytest.raises(ValueError, match="must be contiguous"):
+        L._device_args("f", cache.device, pos=(torch.zeros((3, 2), dtype=torch.int32).T, torch.int32, (2, 3)))

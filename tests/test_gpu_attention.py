@@ -1,0 +1,679 @@
+"""GPU parity of the attention over the paged cache, the entry weights and the
+eviction with the float64 oracle, through the C ABI.
+
+Tolerances.  A score's error is at most E = 2^-24 ((D + 4) scale sum|q||k| + 8
+cap + 4 |x|): the products' float32 sum, the cap (1 - 2 / (1 + e): rounding of
+three operations and two hardware functions of 2 ulp, times the cap) and the
+bias.  A weight p moves by at most 2E relative (its own score and the
+softmax's sum), by 2^-8 more where it is rounded to bf16; n sums of float32 add
+n 2^-24.  So |out - ref| <= (2E + 2^-8 [bf16] + (n + 16) 2^-24) sum p|v| + half a
+step of the output's type (2^-8 or 2^-24) |ref|, and |lse - ref| <= E + (n + 16)
+2^-24 + 2^-22 |ref| (log2, its scaling, and the running reference)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from speculative_decoding_verification_37_gb300 import _lib as L
+from speculative_decoding_verification_37_gb300 import api
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+class Case:
+    """A batch with its tensors on the GPU and its oracle's arrays."""
+
+    def __init__(self, lens, S=5, H=2, G=2, D=64, bs=16, dtype="bf16", layers=1, layer=0, tree=False, inplace=False,
+                 gaps=False, window=0, docs=None, cap=0.0, slopes=False, shared=0, seed=0, spare=0, extra_blocks=0):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.S, self.H, self.G, self.D, self.bs = list(lens), S, H, G, D, bs
+        self.B, self.dtype, self.layer, self.layers = len(lens), DT[dtype], layer, layers
+        self.shared, self.inplace = shared, inplace
+        cap_len = max(lens) + (S if inplace else 0) + spare
+        self.max_blocks = max(1, -(-cap_len // bs))
+        need = [-(-(n + S + spare) // bs) for n in lens]
+        nb = sum(need) + extra_blocks + -(-shared // bs)
+        perm = rng.permutation(nb)
+        table = np.zeros((self.B, self.max_blocks), np.int32)
+        at = 0
+        for b, k in enumerate(need):
+            k = min(k, self.max_blocks)
+            table[b, :k] = perm[at:at + k]
+            at += k
+        self.stable = None
+        if shared:
+            self.stable = perm[at:at + -(-shared // bs)].astype(np.int32)
+        self.table = table
+        self.nb = nb
+        self.cache = torch.randn((layers, 2, nb, bs, H, D), generator=g).to(self.dtype)
+        self.temp = None if inplace else torch.randn((self.B, layers, 2, S, H, D), generator=g).to(self.dtype)
+        self.q = (1.5 * torch.randn((self.B, S, H * G, D), generator=g)).to(self.dtype)
+        width = self.max_blocks * bs
+        text = np.array(lens, np.int64)
+        self.key_pos = None
+        if gaps:
+            self.key_pos = np.cumsum(rng.integers(1, 4, (self.B, width)), 1).astype(np.int32)
+            text = np.array([self.key_pos[b, n - 1] + 1 if n else 0 for b, n in enumerate(lens)])
+        self.mask = None
+        depth = np.tile(np.arange(S), (self.B, 1))
+        if tree:
+            W = (S + 31) // 32
+            self.mask = np.zeros((self.B, S, W), np.uint32)
+            self.parent = np.full((self.B, S), -1)
+            depth[:] = 0
+            for b in range(self.B):
+                for i in range(S):
+                    if i:
+                        p = self.parent[b, i] = int(rng.integers(0, i))
+                        depth[b, i] = depth[b, p] + 1
+                        self.mask[b, i] = self.mask[b, p]
+                    self.mask[b, i, i // 32] |= np.uint32(1 << (i % 32))
+        self.pos = (text[:, None] + depth).astype(np.int32) if tree or gaps else None
+        self.first = None if docs is None else np.array([int(t * docs) for t in text], np.int32)
+        self.slopes = (2.0 ** -(1 + np.arange(H * G) % 6)).astype(np.float32) if slopes else None
+        self.score = dict(scale=1.0 / math.sqrt(D), softcap=cap)
+        self.window = window
+
+    # -- oracle ------------------------------------------------------------
+    def planes(self):
+        return self.cache[self.layer, 0].float().numpy(), self.cache[self.layer, 1].float().numpy()
+
+    def row_keys(self, b):
+        n, P = self.lens[b], self.shared
+        kc, vc = self.planes()
+        total = n + (self.S if self.inplace else 0)
+        k, v = (O.entries(x, self.table[b], self.bs, total) for x in (kc, vc))
+        if P:
+            k[:P], v[:P] = (O.entries(x, self.stable, self.bs, P) for x in (kc, vc))
+        if not self.inplace:
+            t = self.temp[b, self.layer].double().numpy()
+            k, v = np.concatenate([k, t[0]]), np.concatenate([v, t[1]])
+        qp = self.pos[b] if self.pos is not None else np.arange(n, n + self.S)
+        kp = np.concatenate([self.key_pos[b, :n] if self.key_pos is not None else np.arange(n), qp])
+        return k, v, qp, kp
+
+    def masked(self, b, qp, kp):
+        n = self.lens[b]
+        off = O.hidden(qp, kp, first_pos=None if self.first is None else self.first[b], window=self.window)
+        off[:, n:] |= O.candidate_mask(self.S, None if self.mask is None else self.mask[b])
+        return off
+
+    def oracle(self, b):
+        k, v, qp, kp = self.row_keys(b)
+        off = self.masked(b, qp, kp)
+        return O.attend(self.q[b].double().numpy(), k, v, qp, kp, off, slopes=self.slopes, **self.score), k, off
+
+    # -- GPU ---------------------------------------------------------------
+    def args(self):
+        d = lambda x: None if x is None else (x if torch.is_tensor(x) else torch.from_numpy(  # noqa: E731
+            np.ascontiguousarray(x).view(np.int32) if x.dtype == np.uint32 else np.ascontiguousarray(x))).cuda()
+        a = dict(block_size=self.bs, layer=self.layer, temp_kv=d(self.temp), tree_mask=d(self.mask), pos=d(self.pos),
+                 key_pos=d(self.key_pos), first_pos=d(self.first), slopes=d(self.slopes), window=self.window, **self.score)
+        if self.shared:
+            a.update(shared_table=d(self.stable), shared_len=self.shared)
+        return [self.q.cuda(), self.cache.cuda(), d(self.table), d(np.array(self.lens, np.int32))], a
+
+    def run(self, **over):
+        pos, a = self.args()
+        a.update(over)
+        r = api.verify_attention(*pos, **a)
+        torch.cuda.synchronize()
+        return r
+
+    def score_error(self, b, k):
+        """E of the module's note, the largest over the request's pairs."""
+        aq = np.abs(self.q[b].double().numpy())
+        dots = max(float((aq[:, h] @ np.abs(k[:, h // self.G]).T).max()) for h in range(self.H * self.G)) if len(k) else 0.0
+        reach = 0.0 if self.slopes is None else 4 * 40.0     # a farther key's weight is below 2^-57
+        return 2.0 ** -24 * ((self.D + 4) * self.score["scale"] * dots + 8 * self.score["softcap"] + reach)
+
+    def check(self, r, rows=None):
+        out, lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
+        half = 2.0 ** -8 if self.dtype == torch.bfloat16 else 2.0 ** -24
+        for b in range(self.B) if rows is None else rows:
+            ref, k, off = self.oracle(b)
+            e, n = self.score_error(b, k), len(k) + self.shared
+            tol = (2 * e + (2.0 ** -8 if half > 1e-4 else 0) + (n + 16) * 2.0 ** -24) * ref.mass + half * np.abs(ref.out)
+            bad = np.abs(out[b] - ref.out) > tol + 1e-30
+            assert not bad.any() and np.isfinite(out[b]).all(), (b, np.argwhere(bad)[:4], np.abs(out[b] - ref.out).max())
+            seen = np.isfinite(ref.lse)
+            assert np.array_equal(np.isneginf(lse[b]), ~seen), b
+            assert not out[b][~seen].any(), b
+            far = np.abs(lse[b][seen] - ref.lse[seen])
+            assert (far <= e + (n + 16) * 2.0 ** -24 + 2.0 ** -22 * np.abs(ref.lse[seen])).all(), (b, far.max())
+
+
+SHAPES = [
+    dict(lens=[1], S=1, H=1, G=1, D=64),
+    dict(lens=[0, 0], S=1, H=1, G=1, D=64),                            # nothing cached: the candidate alone
+    dict(lens=[0, 1, 31, 32, 33, 63, 64, 65, 127, 129, 300], S=5, H=2, G=2, D=64),
+    dict(lens=[100, 7], S=13, H=2, G=4, D=128, tree=True),
+    dict(lens=[257, 64], S=3, H=1, G=7, D=128, bs=1),
+    dict(lens=[90, 200, 13], S=2, H=3, G=1, D=72, bs=5),
+    dict(lens=[500], S=8, H=4, G=8, D=128, bs=48),                     # 64 rows a head
+    dict(lens=[70, 130], S=20, H=2, G=4, D=128, tree=True),            # 80 rows
+    dict(lens=[40, 77], S=70, H=1, G=2, D=64, tree=True, inplace=True),  # 140 rows, three mask words
+    dict(lens=[33, 90], S=4, H=2, G=3, D=256, bs=64),
+    dict(lens=[60, 10], S=3, H=2, G=2, D=8),
+    dict(lens=[129, 130], S=33, H=1, G=1, D=160, inplace=True),
+    dict(lens=[3000], S=2, H=2, G=2, D=128),                           # keys split over blocks
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_shapes(i, dtype):
+    c = Case(dtype=dtype, seed=i, **SHAPES[i])
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [
+    dict(cap=5.0), dict(slopes=True), dict(window=40), dict(window=1), dict(docs=0.5), dict(docs=1.0),
+    dict(gaps=True, window=50, slopes=True), dict(gaps=True, docs=0.7, cap=2.0),
+    dict(tree=True, window=2, docs=0.99), dict(cap=30.0, slopes=True, window=100, docs=0.3, tree=True, gaps=True),
+    dict(inplace=True, window=7), dict(inplace=True, tree=True, gaps=True, slopes=True),
+    dict(layers=3, layer=2, spare=40),
+])
+def test_scores_and_masks(kw, dtype):
+    c = Case([5, 64, 200, 131, 0 if not kw.get("gaps") else 1], S=6, H=2, G=3, D=64, dtype=dtype, seed=3, **kw)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [
+    dict(shared=64), dict(shared=50), dict(shared=1), dict(shared=600, D=128, G=4), dict(shared=130, inplace=True),
+    dict(shared=90, tree=True, cap=4.0, slopes=True), dict(shared=200, window=60), dict(shared=200, docs=0.9),
+    dict(shared=256, G=8, S=9, lens=[256] * 20),                       # nothing of one's own but the candidates
+    dict(shared=77, bs=7, D=72),
+])
+def test_shared_prefix(kw, dtype):
+    kw = dict(kw)
+    lens = kw.pop("lens", [kw["shared"] + n for n in (0, 1, 15, 100, 33)])
+    args = dict(S=4, H=2, G=2, D=64)
+    args.update(kw)
+    c = Case(lens, dtype=dtype, seed=5, **args)
+    c.check(c.run())
+
+
+def test_shared_prefix_equals_reading_it_per_request():
+    """The same entries, once through every request's own table: the same up
+    to the arithmetic's own tolerance (both are checked against the oracle)."""
+    c = Case([300, 290, 512], S=5, H=2, G=4, D=128, shared=256, seed=8)
+    c.check(c.run())
+    whole = c.shared // c.bs
+    c.table[:, :whole] = c.stable[:whole]
+    c.shared = 0
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_places_may_hold_anything(dtype):
+    """NaN and infinities past the length, before the document, outside the
+    window and in other branches do not show; visible ones stay in their rows."""
+    c = Case([70, 100], S=6, H=2, G=2, D=64, tree=True, docs=0.5, window=30, dtype=dtype, seed=9, spare=30)
+    clean = c.run()
+    c.check(clean)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        dirty = Case([70, 100], S=6, H=2, G=2, D=64, tree=True, docs=0.5, window=30, dtype=dtype, seed=9, spare=30)
+        dirty.parent = c.parent
+        for b, n in enumerate(c.lens):
+            lo = max(int(c.first[b]), n - 29)            # the first position that candidate 0 sees
+            for e in list(range(0, lo)) + list(range(n, c.max_blocks * c.bs)):
+                if e // c.bs < c.max_blocks and (e < n or e // c.bs < -(-(n + 36) // c.bs)):
+                    dirty.cache[0, :, c.table[b, e // c.bs], e % c.bs] = bad
+            dirty.temp[b, 0, :, 5] = bad                 # node 5: the last one, nobody's ancestor
+        r = dirty.run()
+        assert torch.equal(r.out[:, :5], clean.out[:, :5]) and torch.equal(r.lse[:, :5], clean.lse[:, :5])
+        assert not torch.isfinite(r.out[:, 5]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_value_in_a_tile_other_rows_see(dtype):
+    """A non-finite V that one branch sees must not reach the others."""
+    c = Case([40], S=3, H=1, G=2, D=64, tree=True, dtype=dtype, seed=1)
+    c.mask[0, :, 0] = [1, 0b11, 0b101]
+    c.pos[0] = [40, 41, 41]
+    clean = c.run()
+    c.temp[0, 0, 1, 1, 0, 5] = float("nan")
+    r = c.run()
+    assert torch.equal(r.out[0, [0, 2]], clean.out[0, [0, 2]])
+    assert torch.isnan(r.out[0, 1, :, 5]).all() and torch.equal(r.lse, clean.lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_see_nothing(dtype):
+    c = Case([50, 0, 20], S=3, H=2, G=2, D=64, tree=True, dtype=dtype, seed=2)
+    c.mask[:, 1] = 0                                     # candidate 1 sees no candidate
+    c.first = np.array([49, 0, 99], np.int32)            # request 2: the document starts past everything
+    r = c.run()
+    c.check(r)
+    assert torch.isneginf(r.lse[1, 1]).all() and torch.isneginf(r.lse[2]).all()
+
+
+def test_strides_and_views():
+    """q as a slice of a fused projection, in other dimension orders."""
+    c = Case([33, 100], S=5, H=2, G=2, D=64, seed=4)
+    want = c.run()
+    pos, a = c.args()
+    q = pos[0]
+    fused = torch.full((2, 5, 8, 64), float("nan"), dtype=q.dtype, device="cuda")
+    fused[:, :, 2:6] = q
+    heads_first = q.permute(2, 0, 1, 3).contiguous().permute(1, 2, 0, 3)
+    for view in (fused[:, :, 2:6], heads_first):
+        got = api.verify_attention(view, *pos[1:], **a)
+        assert torch.equal(got.out, want.out) and torch.equal(got.lse, want.lse)
+
+
+def test_bad_requests_are_flagged():
+    c = Case([60, 61, 62, 63], S=2, H=1, G=2, D=64, seed=6)
+    pos, a = c.args()
+    lens = torch.tensor([60, -1, 2000, 63], dtype=torch.int32, device="cuda")
+    table = pos[2].clone()
+    table[3, 1] = c.nb                                    # entries 16..31 of request 3
+    flags = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = api.workspace(L.SPEC_WS_ATTENTION, 4, 2 * 2, 64, "cuda")
+    assert L.spec_get_status(ws) == 0
+    r = api.verify_attention(pos[0], pos[1], table, lens, flags=flags, ws=ws, **a)
+    assert L.spec_get_status(ws) == L.SPEC_FLAG_BAD_INPUT and L.spec_get_status(ws) == 0
+    assert flags.tolist() == [0, 1, 1, 1]
+    assert not r.out[1:3].any() and torch.isneginf(r.lse[1:3]).all()
+    c.check(r, rows=[0])
+    # the bad block's entries are left out: as if they were masked
+    k, v, qp, kp = c.row_keys(3)
+    off = c.masked(3, qp, kp)
+    off[:, 16:32] = True
+    ref = O.attend(c.q[3].double().numpy(), k, v, qp, kp, off, **c.score)
+    assert np.abs(r.lse[3].cpu().numpy() - ref.lse).max() < 1e-5
+    # below a shared prefix
+    c = Case([60, 61], S=2, H=1, G=2, D=64, seed=6, shared=48)
+    pos, a = c.args()
+    flags = torch.zeros(2, dtype=torch.int32, device="cuda")
+    r = api.verify_attention(*pos[:3], torch.tensor([60, 47], dtype=torch.int32, device="cuda"), flags=flags, **a)
+    assert flags.tolist() == [0, 1] and not r.out[1].any()
+    c.check(r, rows=[0])
+    a["shared_table"][1] = -1
+    r = api.verify_attention(*pos, flags=flags.zero_(), **a)
+    assert flags.tolist() == [1, 1]
+
+
+def test_repeats_graphs_and_streams_agree():
+    """The same call again, on another stream, captured and replayed, and after
+    a call of another shape on the same workspace: the same bits."""
+    c = Case([3000, 17, 900], S=5, H=2, G=4, D=128, seed=7, shared=16)
+    pos, a = c.args()
+    want = api.verify_attention(*pos, **a)
+    other = Case([10, 20, 30], S=5, H=2, G=4, D=128, seed=8, shared=8)
+    other.check(other.run())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        r = api.verify_attention(*pos, **a)
+        r2 = api.verify_attention(*pos, stream=s, **a)
+    torch.cuda.synchronize()
+    for x in (r, r2):
+        assert torch.equal(x.out, want.out) and torch.equal(x.lse, want.lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cap = api.verify_attention(*pos, **a)
+    cap.out.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cap.out, want.out) and torch.equal(cap.lse, want.lse)
+    # lengths are read on the device: a replay follows them
+    pos[3][1] = 16
+    g.replay()
+    torch.cuda.synchronize()
+    c.lens[1] = 16
+    c.check(cap)
+
+
+def test_offsets_past_32_bits():
+    """Blocks at the end of a cache of more than 2^32 elements."""
+    H, D, bs, S = 8, 128, 16, 2
+    nb = (1 << 32) // (bs * H * D) + 64
+    cache = torch.empty((1, 2, nb, bs, H, D), dtype=torch.bfloat16, device="cuda")
+    ids = torch.tensor([[nb - 1, 3, nb - 7]], dtype=torch.int32, device="cuda")
+    g = torch.Generator("cuda").manual_seed(0)
+    small = torch.randn((1, 2, 3, bs, H, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    cache[:, :, ids[0].long()] = small
+    q = torch.randn((1, S, H, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    temp = torch.randn((1, 1, 2, S, H, D), generator=g, device="cuda", dtype=torch.bfloat16)
+    lens = torch.tensor([40], dtype=torch.int32, device="cuda")
+    a = api.verify_attention(q, cache, ids, lens, block_size=bs, temp_kv=temp)
+    b = api.verify_attention(q, small, torch.arange(3, dtype=torch.int32, device="cuda")[None], lens, block_size=bs,
+                             temp_kv=temp)
+    assert torch.equal(a.out, b.out) and torch.equal(a.lse, b.lse)
+
+
+def test_many_requests_ragged():
+    """More requests than threads of a block, most of them tiny."""
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 50, 700)
+    lens[123] = 2000
+    c = Case(lens.tolist(), S=1, H=2, G=2, D=64, seed=10)
+    c.check(c.run(), rows=[0, 1, 122, 123, 124, 350, 511, 512, 699])
+
+
+# ---------------------------------------------------------------------------
+# entry weights
+# ---------------------------------------------------------------------------
+def weights_case(kw, seed, dtype):
+    """A batch whose last entries are committed candidates."""
+    kw = dict(kw)
+    S = kw.pop("S", 5)
+    lens = kw.pop("lens", [5, 64, 200, 131])
+    c = Case(lens, S=S, inplace=True, dtype=dtype, seed=seed, **{**dict(H=2, G=2, D=64), **kw})
+    rng = np.random.default_rng(seed + 100)
+    n_slots = np.array([min(n, int(x)) for n, x in zip(lens, rng.integers(0, S + 1, len(lens)))], np.int32)
+    slots = np.full((c.B, S + 2), -5, np.int32)
+    pos = np.zeros((c.B, S), np.int32)
+    lse = rng.uniform(3, 6, (c.B, S, c.H * c.G)).astype(np.float32)
+    for b, n in enumerate(n_slots):
+        slots[b, :n] = np.sort(rng.permutation(S)[:n])
+        start = lens[b] - n if c.key_pos is None else (c.key_pos[b, lens[b] - n - 1] + 1 if lens[b] > n else 0)
+        pos[b, slots[b, :n]] = start + np.arange(n)
+    return c, n_slots, slots, pos, lse
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [
+    dict(), dict(G=7, D=128, S=13, lens=[300, 40, 13, 64, 65]), dict(cap=5.0, slopes=True), dict(window=30),
+    dict(docs=0.5), dict(gaps=True, window=60, slopes=True), dict(D=72, bs=5, H=3), dict(D=256, G=1),
+    dict(S=1, G=1, lens=[1, 2, 0, 70]), dict(D=8, H=1), dict(layers=2, layer=1), dict(S=40, G=4, lens=[100, 39]),
+    dict(D=160, bs=64),
+])
+@pytest.mark.parametrize("start", [0, 20])
+def test_entry_weights(kw, dtype, start):
+    c, n_slots, slots, pos, lse = weights_case(kw, 11, dtype)
+    lse[0, :, 0] = -np.inf                                # a candidate head that saw nothing adds nothing
+    width = c.max_blocks * c.bs
+    rng = np.random.default_rng(0)
+    w0 = np.zeros((c.B, width + 3), np.float32)
+    for b, n in enumerate(c.lens):
+        w0[b, :n - n_slots[b]] = rng.uniform(0, 2, n - n_slots[b])
+    (q, cache, table, lens), a = c.args()
+    for k in ("temp_kv", "tree_mask"):
+        a.pop(k)
+    kp0 = None if c.key_pos is None else a["key_pos"].clone()
+    weight = torch.from_numpy(w0).cuda()
+    a.update(pos=torch.from_numpy(pos).cuda(), slots=torch.from_numpy(slots).cuda())
+    api.attention_weights(q, torch.from_numpy(lse).cuda(), cache, table, lens, torch.from_numpy(n_slots).cuda(), weight,
+                          shared_len=start, **a)
+    torch.cuda.synchronize()
+    got = weight.double().cpu().numpy()
+    for b, n in enumerate(c.lens):
+        m = int(n_slots[b])
+        sl = slots[b, :m]
+        k = O.entries(c.planes()[0], table[b].tolist(), c.bs, n)
+        kp = (c.key_pos[b, :n] if c.key_pos is not None else np.arange(n)).copy()
+        kp[n - m:] = pos[b, sl]
+        gain = O.entry_weights(c.q[b, sl].double().numpy(), lse[b, sl].astype(np.float64), k, pos[b, sl], kp, m,
+                               first_pos=None if c.first is None else c.first[b], window=c.window, start=start,
+                               slopes=c.slopes, **c.score)
+        # a term moves by its score's error and by lse's rounding to log2 units (2^-24 * 2 |lse|), the
+        # exponential's 2 ulp; the float32 sum of m*Hq terms and the old weight
+        rel = 2 * c.score_error(b, k) + (m * c.H * c.G + 32) * 2.0 ** -24
+        tol = rel * gain + 2.0 ** -23 * (w0[b, :n] + gain)
+        assert (np.abs(got[b, :n] - w0[b, :n] - gain) <= tol + 1e-30).all(), (b, np.abs(got[b, :n] - w0[b, :n] - gain).max())
+        assert not got[b, n:].any() and np.array_equal(got[b, :min(start, n)], w0[b, :min(start, n)])
+        if kp0 is not None:
+            want = kp0[b].cpu().numpy().copy()
+            want[n - m:n] = pos[b, sl]
+            lo = max(start, n - m)                        # entries of a shared prefix are not touched
+            assert np.array_equal(a["key_pos"][b].cpu().numpy()[lo:n], want[lo:n])
+
+
+def test_entry_weights_without_slots_or_positions():
+    """The chain's defaults: candidate j is slot j at its own entry."""
+    c = Case([40, 9], S=4, H=1, G=2, D=64, inplace=True, seed=12)
+    (q, cache, table, lens), a = c.args()
+    n = torch.tensor([3, 4], dtype=torch.int32, device="cuda")
+    lse = torch.full((2, 4, 2), 4.0, device="cuda")
+    w = torch.zeros((2, c.max_blocks * c.bs), device="cuda")
+    api.attention_weights(q, lse, cache, table, lens, n, w, block_size=c.bs)
+    for b in range(2):
+        m = int(n[b])
+        k = O.entries(c.planes()[0], c.table[b], c.bs, c.lens[b])
+        qp = np.arange(c.lens[b] - m, c.lens[b])
+        gain = O.entry_weights(c.q[b, :m].double().numpy(), np.full((m, 2), 4.0), k, qp, np.arange(c.lens[b]), m, **c.score)
+        assert np.allclose(w[b, :c.lens[b]].cpu().numpy(), gain, rtol=1e-4, atol=0)
+
+
+def test_entry_weights_bad_requests():
+    c = Case([40, 41, 42, 43, 44], S=3, H=1, G=2, D=64, inplace=True, seed=13)
+    (q, cache, table, lens), a = c.args()
+    lse = torch.full((5, 3, 2), 4.0, device="cuda")
+    n = torch.tensor([2, 4, 2, 2, 2], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([[0, 1, 9], [0, 1, 2], [0, 3, 0], [0, 1, 0], [0, 2, 0]], dtype=torch.int32, device="cuda")
+    lens = lens.clone()
+    lens[3] = -4
+    table = table.clone()
+    table[4, 0] = -1
+    w = torch.zeros((5, c.max_blocks * c.bs), device="cuda")
+    flags = torch.zeros(5, dtype=torch.int32, device="cuda")
+    api.attention_weights(q, lse, cache, table, lens, n, w, block_size=c.bs, slots=slots, flags=flags)
+    torch.cuda.synchronize()
+    assert flags.tolist() == [0, 1, 1, 1, 1]
+    assert w[0].any() and not w[1:4].any()
+    assert not w[4, :c.bs].any() and w[4, c.bs:44].all()
+
+
+# ---------------------------------------------------------------------------
+# eviction
+# ---------------------------------------------------------------------------
+def evict_case(lens, budget, *, layers=2, H=2, D=8, bs=4, seed=0, dtype=torch.bfloat16, spare=5, ties=False, order=None):
+    rng = np.random.default_rng(seed)
+    B = len(lens)
+    mb = max(1, -(-(max(lens) + spare) // bs))
+    nb = B * mb + 3
+    table = rng.permutation(nb)[:B * mb].reshape(B, mb).astype(np.int32)
+    bits = torch.from_numpy(rng.integers(0, 256, (layers, 2, nb, bs, H, D * dtype.itemsize), dtype=np.uint8))
+    width = mb * bs + 2
+    w = np.zeros((B, width), np.float32)
+    pos = np.zeros((B, width), np.int32)
+    for b, n in enumerate(lens):
+        w[b, :n] = rng.integers(0, 5, n) if ties else rng.exponential(1, n)
+        p = np.sort(rng.permutation(3 * n + 1)[:n])
+        pos[b, :n] = rng.permutation(p) if order == "mixed" else p
+    return table, bits, w, pos, nb
+
+
+def run_evict(table, bits, w, pos, lens, dtype, bs, **kw):
+    cache = bits.cuda().view(dtype)
+    t = dict(table=torch.from_numpy(table).cuda(), len=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+             w=torch.from_numpy(w).cuda(), pos=torch.from_numpy(pos).cuda(),
+             blocks=torch.full((len(lens),), -7, dtype=torch.int32, device="cuda"),
+             flags=torch.zeros(len(lens), dtype=torch.int32, device="cuda"))
+    api.evict_kv(cache, t["table"], t["len"], t["w"], t["pos"], block_size=bs, blocks_in_use=t["blocks"],
+                 flags=t["flags"], **kw)
+    torch.cuda.synchronize()
+    return cache.view(torch.uint8).cpu().numpy(), {k: v.cpu().numpy() for k, v in t.items()}
+
+
+def check_evict(lens, budget, seed=0, sink=0, recent=0, bs=4, dtype=torch.bfloat16, **kw):
+    table, bits, w, pos, nb = evict_case(lens, budget, bs=bs, seed=seed, dtype=dtype, **kw)
+    cache, t = run_evict(table, bits, w, pos, lens, dtype, bs, budget=budget, sink=sink, recent=recent)
+    want, ww, wp = bits.numpy().copy(), w.copy(), pos.copy()
+    moved = 0
+    for b, n in enumerate(lens):
+        e = O.evict(w[b], pos[b], n, budget=budget, sink=sink, recent=recent)
+        assert t["flags"][b] == 0 and t["len"][b] == e.length and t["blocks"][b] == -(-e.length // bs)
+        for f, to in e.moves:
+            want[:, :, table[b, to // bs], to % bs] = bits.numpy()[:, :, table[b, f // bs], f % bs]
+            ww[b, to], wp[b, to] = w[b, f], pos[b, f]
+        ww[b, e.length:] = 0
+        wp[b, e.length:] = 0
+        moved += len(e.moves)
+    assert np.array_equal(cache, want) and np.array_equal(t["w"], ww) and np.array_equal(t["pos"], wp)
+    return moved
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lens=[30], budget=20), dict(lens=[0, 1, 19, 20, 21, 40, 64], budget=20, sink=2, recent=5),
+    dict(lens=[50, 33], budget=1), dict(lens=[50, 51], budget=50, sink=25, recent=25),
+    dict(lens=[90, 70, 41], budget=40, ties=True, order="mixed", sink=3, recent=9),
+    dict(lens=[3000, 1024, 1025, 2047], budget=1000, ties=True, sink=4, recent=100, order="mixed"),
+    dict(lens=[60, 31], budget=30, layers=1, H=1, D=8, bs=1), dict(lens=[60, 31], budget=30, bs=7, dtype=torch.float32),
+    dict(lens=[60, 31], budget=30, D=16, dtype=torch.float8_e4m3fn),
+    dict(lens=[45, 20], budget=16, layers=9, H=8, D=128, bs=16),
+    dict(lens=[40], budget=16, layers=2, H=64, D=256, bs=4),            # a unit of 32 KiB: two pieces
+    dict(lens=[5000], budget=4999), dict(lens=[70] * 40, budget=33, recent=33),
+])
+def test_evict(kw):
+    assert check_evict(**{**kw, "lens": list(kw["lens"])}) >= 0
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_evict_random(seed):
+    rng = np.random.default_rng(seed)
+    budget = int(rng.integers(1, 200))
+    lens = rng.integers(0, 2 * budget + 3, 9).tolist()
+    check_evict(lens, budget, seed=seed, sink=int(rng.integers(0, budget // 2 + 1)),
+                recent=int(rng.integers(0, budget // 2 + 1)), ties=bool(seed % 2), order="mixed" if seed > 2 else None)
+
+
+def test_evict_special_weights():
+    """-0 ties with 0, infinities order, negative weights are light."""
+    lens, bs = [10], 4
+    table, bits, w, pos, nb = evict_case(lens, 5, bs=bs, seed=1)
+    w[0, :10] = [-0.0, 0.0, np.inf, -np.inf, -1.0, 1e-40, 0.0, 3.0, -0.0, 2.0]
+    cache, t = run_evict(table, bits, w, pos, lens, torch.bfloat16, bs, budget=5)
+    # inf, 3, 2, 1e-40, then the first of the zeros
+    assert sorted(t["pos"][0, :5].tolist()) == sorted(pos[0, [2, 7, 9, 5, 0]].tolist())
+
+
+def test_evict_bad_requests_stay_as_they_are():
+    lens, bs = [30, 31, 32, 33, 34, 35], 4
+    table, bits, w, pos, nb = evict_case(lens, 20, bs=bs, seed=2)
+    w[1, 7] = np.nan
+    pos[2, 3] = -1
+    table[3, 5] = nb
+    pos[4, :34] = 6                                       # all of them the newest
+    given = [30, 31, 32, 33, 34, 1000]
+    cache, t = run_evict(table, bits, w, pos, given, torch.bfloat16, bs, budget=20, recent=3)
+    assert t["flags"].tolist() == [0, 1, 1, 1, 1, 1] and t["len"].tolist() == [20] + given[1:]
+    assert np.array_equal(t["w"][1:], w[1:], equal_nan=True) and np.array_equal(t["pos"][1:], pos[1:])
+    want = bits.numpy()
+    for b in range(1, 6):
+        for j in table[b]:
+            if j < nb:
+                assert np.array_equal(cache[:, :, j], want[:, :, j])
+    assert t["blocks"].tolist() == [5, 8, 8, 9, 9, -7]
+
+
+def test_evict_again_and_in_a_graph():
+    """Two evictions in a row with shrinking budgets, captured and replayed."""
+    lens, bs = [60, 75], 4
+    table, bits, w, pos, nb = evict_case(lens, 40, bs=bs, seed=3, order="mixed")
+    base = [torch.from_numpy(x).cuda() for x in (table, w, pos)]
+    n0 = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cache0 = bits.cuda().view(torch.bfloat16)
+
+    def once(cache, n, w, p):
+        api.evict_kv(cache, base[0], n, w, p, block_size=bs, budget=50, sink=1, recent=7)
+        api.evict_kv(cache, base[0], n, w, p, block_size=bs, budget=31, sink=1, recent=7)
+
+    plain = [cache0.clone(), n0.clone(), base[1].clone(), base[2].clone()]
+    once(*plain)
+    held = [cache0.clone(), n0.clone(), base[1].clone(), base[2].clone()]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        once(*held)
+    for _ in range(2):
+        for h, s in zip(held, (cache0, n0, base[1], base[2])):
+            h.copy_(s)
+        g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(plain, held):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    assert plain[1].tolist() == [31, 31]
+
+
+# ---------------------------------------------------------------------------
+# the operators together
+# ---------------------------------------------------------------------------
+def test_rounds_of_tree_decoding_with_eviction():
+    """Rounds as a user's loop makes them: tree masks and positions, the
+    attention of two layers, the walk, the commit, the weights, the eviction;
+    a shadow copy of every request's entries follows the oracle."""
+    rng = np.random.default_rng(0)
+    B, Ly, H, G, D, bs, N, budget, V = 3, 2, 2, 2, 64, 4, 5, 24, 50
+    S, mb = N + 1, 10
+    g = torch.Generator("cuda").manual_seed(1)
+    cache = torch.zeros((Ly, 2, B * mb, bs, H, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.from_numpy(rng.permutation(B * mb).reshape(B, mb).astype(np.int32)).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    lens, text = torch.zeros(B, **i32), torch.zeros(B, **i32)
+    weight, key_pos = torch.zeros((B, mb * bs), device="cuda"), torch.zeros((B, mb * bs), **i32)
+    shadow = [[] for _ in range(B)]          # (position, weight, K/V [Ly, 2, H, D]) of every entry, in cache order
+    kw = dict(block_size=bs, softcap=20.0, slopes=torch.full((H * G,), 0.05, device="cuda"))
+    okw = dict(scale=D ** -0.5, softcap=20.0, slopes=[0.05] * (H * G))
+    evicted = 0
+    for rnd in range(14):
+        par = np.array([[0, 0, 1, 1, 3]] * B, np.int32)
+        tok = rng.integers(0, V, (B, N)).astype(np.int32)
+        tree = [torch.from_numpy(x).cuda() for x in (tok, par)]
+        rows = torch.from_numpy(np.tile(np.arange(S, dtype=np.int32), (B, 1))).cuda()
+        # the mask and positions depend on the node arrays only: one-logit rows give them before the forward
+        shape = api.verify_tree(torch.zeros((B * S, 1), device="cuda"), torch.zeros_like(tree[0]), tree[1], rows, text, R=S)
+        q = [torch.randn((B, S, H * G, D), generator=g, device="cuda").bfloat16() for _ in range(Ly)]
+        temp = torch.randn((B, Ly, 2, S, H, D), generator=g, device="cuda").bfloat16()
+        att = [api.verify_attention(q[l], cache, table, lens, layer=l, temp_kv=temp, tree_mask=shape.tree_mask,
+                                    pos=shape.pos, key_pos=key_pos, **kw) for l in range(Ly)]
+        logits = rng.standard_normal((B * S, V)).astype(np.float32)
+        for b in range(B):                    # the walk follows node 1 most rounds, then node 4, then node 5
+            for node, child in ((0, 1), (1, 4), (4, 5))[:int(rng.integers(0, 4))]:
+                logits[b * S + node, tok[b, child - 1]] = 9.0
+        won = api.verify_tree(torch.from_numpy(logits).cuda(), tree[0], tree[1], rows, text, R=S)
+        api.commit_kv(temp, cache, table, won.n_commit, lens, block_size=bs, slots=won.commit_slots)
+        for l in range(Ly):
+            api.attention_weights(q[l], att[l].lse, cache, table, lens, won.n_commit, weight, layer=l,
+                                  slots=won.commit_slots, pos=shape.pos, key_pos=key_pos, **kw)
+        text += won.n_commit
+        torch.cuda.synchronize()
+        for b in range(B):
+            n, sl = int(won.n_commit[b]), won.commit_slots[b].tolist()
+            e = shadow[b]
+            qp = shape.pos[b].cpu().numpy()
+            for l in range(Ly):
+                t = temp[b, l].double().cpu().numpy()
+                k = np.concatenate([np.array([x[2][l, 0] for x in e]).reshape(-1, H, D), t[0]])
+                v = np.concatenate([np.array([x[2][l, 1] for x in e]).reshape(-1, H, D), t[1]])
+                kp = np.array([x[0] for x in e] + qp.tolist())
+                off = np.concatenate([np.zeros((S, len(e)), bool),
+                                      O.candidate_mask(S, shape.tree_mask[b].cpu().numpy().view(np.uint32))], 1)
+                ref = O.attend(q[l][b].double().cpu().numpy(), k, v, qp, kp, off, **okw)
+                assert np.abs(att[l].lse[b].cpu().numpy() - ref.lse).max() < 1e-4
+                assert (np.abs(att[l].out[b].double().cpu().numpy() - ref.out) <= 2.0 ** -7 * ref.mass + 1e-6).all()
+                kept = sl[:n]
+                gain = ref.p[:, kept].sum((0, 1))
+                e = [(x[0], x[1] + gain[i], x[2]) for i, x in enumerate(e)]
+                new = gain[len(e) + np.array(kept)]
+                fresh = new if l == 0 else fresh + new
+            shadow[b] = e + [(int(qp[s]), fresh[j], temp[b, :, :, s].double().cpu().numpy()) for j, s in enumerate(kept)]
+            w = weight[b, :len(shadow[b])].cpu().numpy()
+            assert np.allclose(w, [x[1] for x in shadow[b]], rtol=1e-3), (rnd, b)
+            assert key_pos[b, :len(w)].tolist() == [x[0] for x in shadow[b]]
+            shadow[b] = [(x[0], float(w[i]), x[2]) for i, x in enumerate(shadow[b])]
+        api.evict_kv(cache, table, lens, weight, key_pos, block_size=bs, budget=budget, sink=2, recent=8)
+        torch.cuda.synchronize()
+        for b in range(B):
+            e = O.evict([x[1] for x in shadow[b]], [x[0] for x in shadow[b]], len(shadow[b]), budget=budget, sink=2, recent=8)
+            for f, to in e.moves:
+                shadow[b][to] = shadow[b][f]
+            shadow[b] = shadow[b][:e.length]
+            evicted += len(e.moves)
+            assert int(lens[b]) == e.length
+            assert key_pos[b, :e.length].tolist() == [x[0] for x in shadow[b]] and not key_pos[b, e.length:].any()
+            got = cache[:, :, table[b].long()].flatten(2, 3)[:, :, :e.length].double().cpu().numpy()
+            want = np.array([x[2] for x in shadow[b]]).transpose(1, 2, 0, 3, 4)
+            assert np.array_equal(got, want), (rnd, b)
+    assert evicted > 0 and int(text.min()) > budget
