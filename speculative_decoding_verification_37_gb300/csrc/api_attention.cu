@@ -140,13 +140,16 @@ extern "C" int spec_verify_attention(const SpecAttentionArgs *a, void *workspace
     p.min_share = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int sms = device_sms();
+    auto launch = [&](const AttnParams &x) {
+        return a->dtype == SPEC_DTYPE_BF16 ? launch_attn_mma(x, sms, s) : launch_attn_simt(x, a->dtype, sms, s);
+    };
     if (a->shared_len > 0) {
         AttnParams q = p;
         q.mode = 1;
-        const cudaError_t err = launch_attn_simt(q, a->dtype, sms, s);
+        const cudaError_t err = launch(q);
         if (err != cudaSuccess) return report_cuda_error(err);
     }
-    return report_cuda_error(launch_attn_simt(p, a->dtype, sms, s));
+    return report_cuda_error(launch(p));
 }
 
 extern "C" int spec_attention_weights(const SpecWeightsArgs *a, void *workspace, size_t ws_bytes, void *stream) {

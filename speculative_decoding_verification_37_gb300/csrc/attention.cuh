@@ -113,7 +113,7 @@ struct AttnPlan {
     int chunk;                  // requests per thread
 };
 
-// Fills `pl` (shared memory); every thread of a block of NT threads calls it.
+// Fills `pl` (shared memory); the first NT threads of the block call it.
 // `per`: items of a request.
 template <int NT> __device__ __forceinline__ void attn_plan(const AttnParams &p, AttnPlan &pl, int per, int kt) {
     const int tid = threadIdx.x;
@@ -122,7 +122,7 @@ template <int NT> __device__ __forceinline__ void attn_plan(const AttnParams &p,
     int64_t sum = 0;
     for (int b = tid * chunk; b < min(nreq, (tid + 1) * chunk); ++b) sum += attn_tiles(attn_keys(p, b), kt);
     pl.pre[tid + 1] = sum * per;
-    __syncthreads();
+    sync_nt<NT>();
     if (tid < 32) {  // inclusive scan by one warp, NT/32 values a lane
         constexpr int V = NT / 32;
         int64_t v[V], s = 0;
@@ -148,7 +148,7 @@ template <int NT> __device__ __forceinline__ void attn_plan(const AttnParams &p,
             pl.pre[0] = 0;
         }
     }
-    __syncthreads();
+    sync_nt<NT>();
 }
 
 struct AttnItem {
@@ -340,7 +340,7 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
             if (w.out[r] >= 0)
                 attn_write<T>(p, it.keys.ok, w.out[r], d, sm[r], sl[r], *reinterpret_cast<const float4 *>(so + r * ld + d));
         }
-        __syncthreads();
+        sync_nt<NT>();
         return;
     }
     // partial results: slot 0 of a block holds the item that began before it,
@@ -357,9 +357,9 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
         __stcg(mine + RT * p.D + RT + r, sl[r]);
     }
     __threadfence();
-    __syncthreads();
+    sync_nt<NT>();
     if (tid == 0) *last_flag = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-    __syncthreads();
+    sync_nt<NT>();
     if (!*last_flag) return;
     __threadfence();
     for (int i = tid; i < RT * d4; i += NT) {
@@ -379,7 +379,7 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
         attn_write<T>(p, it.keys.ok, w.out[r], d, m, l, o);
     }
     if (tid == 0) p.counters[c0] = 0u;
-    __syncthreads();
+    sync_nt<NT>();
 }
 
 }  // namespace specv

@@ -251,6 +251,7 @@ struct AttnParams {
     float *pre_o, *pre_lse;       // shared part: normalised rows and log2 sums
 };
 cudaError_t launch_attn_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_attn_mma(const AttnParams &p, int sms, cudaStream_t s);  // bf16
 
 struct WeightsParams {
     AttnParams a;                 // q, cache, tables, score (P: entries left out)

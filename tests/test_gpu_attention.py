@@ -361,6 +361,17 @@ def test_many_requests_ragged():
     c.check(c.run(), rows=[0, 1, 122, 123, 124, 350, 511, 512, 699])
 
 
+@pytest.mark.parametrize("D,G,S,H", [(64, 2, 3, 4), (128, 1, 2, 8), (128, 4, 5, 8), (128, 4, 13, 8), (256, 1, 9, 4),
+                                     (256, 2, 10, 4), (256, 4, 11, 2), (72, 8, 5, 8)])
+def test_many_tiles_per_block(D, G, S, H):
+    """Long items, several to a block: the ring of stages goes round often."""
+    c = Case([2500, 1900, 2000, 2501, 2300, 2048, 2049, 2200] * 3, S=S, H=H, G=G, D=D, seed=D + G)
+    r = c.run()
+    c.check(r, rows=[0, 11, 23])
+    again = c.run()
+    assert torch.equal(r.out, again.out) and torch.equal(r.lse, again.lse)
+
+
 # ---------------------------------------------------------------------------
 # entry weights
 # ---------------------------------------------------------------------------
