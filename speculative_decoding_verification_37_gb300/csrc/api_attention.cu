@@ -62,6 +62,8 @@ template <typename A> int scored_call(const A *a, AttnParams &p) {
     p.slopes = a->slopes;
     p.score = ScoreArgs{a->scale, a->softcap, cap_arg, a->slopes != nullptr};
     p.window = a->window;
+    p.layers = a->L;
+    p.layer = a->layer;
     p.P = a->shared_len;
     p.flags = a->flags;
     return SPEC_OK;
@@ -76,7 +78,7 @@ size_t attn_ws_layout(int32_t B, int32_t n, int32_t D, bool shared, void *base, 
     const size_t o_cnt = off;
     off += ws_align(kAttnCounters * sizeof(unsigned));
     const size_t o_part = off;
-    off += ws_align((size_t)kAttnSmsMax * 2 * kAttnSlotRows * ((size_t)D + 2) * sizeof(float));
+    off += ws_align((size_t)kAttnSmsMax * 2 * kAttnSlotRows * (shared ? 2 : 1) * ((size_t)D + 2) * sizeof(float));
     const size_t o_pre = off;
     if (shared) off += ws_align((size_t)B * n * D * sizeof(float));
     const size_t o_lse = off;
@@ -132,6 +134,7 @@ extern "C" int spec_verify_attention(const SpecAttentionArgs *a, void *workspace
         p.tk = static_cast<const char *>(a->temp_kv) + one * 2 * a->layer;
         p.tv = static_cast<const char *>(p.tk) + one;
         p.tsb = (int64_t)a->L * 2 * a->S * a->H * a->D;
+        p.temp_base = a->temp_kv;
     }
     p.mask = a->tree_mask;
     p.stable = a->shared_table;
@@ -140,8 +143,10 @@ extern "C" int spec_verify_attention(const SpecAttentionArgs *a, void *workspace
     p.min_share = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int sms = device_sms();
-    auto launch = [&](const AttnParams &x) {
-        return a->dtype == SPEC_DTYPE_BF16 ? launch_attn_mma(x, sms, s) : launch_attn_simt(x, a->dtype, sms, s);
+    auto launch = [&](AttnParams &x) {
+        if (a->dtype != SPEC_DTYPE_BF16) return launch_attn_simt(x, a->dtype, sms, s);
+        x.box = attn_tc_box(x);
+        return x.box ? launch_attn_tc(x, sms, s) : launch_attn_mma(x, sms, s);
     };
     if (a->shared_len > 0) {
         AttnParams q = p;

@@ -102,7 +102,26 @@ __device__ __forceinline__ KeyRange attn_keys(const AttnParams &p, int b) {
     return r;
 }
 
-__device__ __forceinline__ int attn_tiles(const KeyRange &r, int kt) { return max(1, (r.hi - r.lo + kt - 1) / kt); }
+// Where keys are copied in boxes of p.box rows of one page (p.box > 0), a tile
+// line starts at a box boundary and the candidates begin a new box: `lo` is the
+// first key of the line, `entries` the keys before the candidates.
+struct KeyLine {
+    int lo, entries;
+};
+__device__ __forceinline__ KeyLine attn_line(const AttnParams &p, const KeyRange &r) {
+    KeyLine k;
+    const int box = p.box;
+    k.lo = r.lo / box * box;
+    const int end = p.tk && p.mode == 0 ? r.len : r.hi;
+    k.entries = (end - k.lo + box - 1) / box * box;
+    return k;
+}
+
+__device__ __forceinline__ int attn_tiles(const AttnParams &p, const KeyRange &r, int kt) {
+    int n = r.hi - r.lo;
+    if (p.box > 0 && r.ok) n = attn_line(p, r).entries + (p.tk && p.mode == 0 ? p.S : 0);
+    return max(1, (n + kt - 1) / kt);
+}
 
 // ---------------------------------------------------------------------------
 // the line of tiles
@@ -120,7 +139,7 @@ template <int NT> __device__ __forceinline__ void attn_plan(const AttnParams &p,
     const int nreq = p.mode == 1 ? 1 : p.B;
     const int chunk = (nreq + NT - 1) / NT;
     int64_t sum = 0;
-    for (int b = tid * chunk; b < min(nreq, (tid + 1) * chunk); ++b) sum += attn_tiles(attn_keys(p, b), kt);
+    for (int b = tid * chunk; b < min(nreq, (tid + 1) * chunk); ++b) sum += attn_tiles(p, attn_keys(p, b), kt);
     pl.pre[tid + 1] = sum * per;
     sync_nt<NT>();
     if (tid < 32) {  // inclusive scan by one warp, NT/32 values a lane
@@ -171,11 +190,11 @@ __device__ __forceinline__ AttnItem attn_find(const AttnParams &p, const AttnPla
     const int nreq = p.mode == 1 ? 1 : p.B;
     int b = lo * pl.chunk;
     KeyRange r = attn_keys(p, b);
-    int nt = attn_tiles(r, kt);
+    int nt = attn_tiles(p, r, kt);
     while (at + (int64_t)nt * per <= u && b + 1 < nreq) {
         at += (int64_t)nt * per;
         r = attn_keys(p, ++b);
-        nt = attn_tiles(r, kt);
+        nt = attn_tiles(p, r, kt);
     }
     const int k = (int)((u - at) / nt);
     it.b = b;
@@ -197,7 +216,7 @@ __device__ __forceinline__ AttnItem attn_next(const AttnParams &p, const AttnIte
             n.h = 0;
             ++n.b;
             n.keys = attn_keys(p, n.b);
-            n.ntiles = attn_tiles(n.keys, kt);
+            n.ntiles = attn_tiles(p, n.keys, kt);
         }
     }
     return n;
@@ -379,6 +398,69 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
         attn_write<T>(p, it.keys.ok, w.out[r], d, m, l, o);
     }
     if (tid == 0) p.counters[c0] = 0u;
+    sync_nt<NT>();
+}
+
+// The same for a kernel whose thread holds a whole row: (m2, l) and, by
+// `chunk(d, o)`, 32 columns from d on (every lane of a warp calls it together).
+// `r`: the thread's row in the item's tile of RT rows.
+template <typename T, int RT, int NT, typename F>
+__device__ __forceinline__ void attn_finish_row(const AttnParams &p, const AttnPlan &pl, const AttnItem &it,
+                                                int64_t out_row, int r, float m, float l, F &&chunk, int *last_flag) {
+    const int64_t share = pl.share;
+    const int c0 = (int)(it.u0 / share), c1 = (int)((it.u0 + it.ntiles - 1) / share);
+    const bool split = c0 != c1;
+    const int64_t slot_floats = (int64_t)RT * (p.D + 2);
+    const int me = blockIdx.x;
+    float *mine = p.part + ((int64_t)me * 2 + (me == c0 ? 1 : 0)) * slot_floats;
+    for (int d0 = 0; d0 < p.D; d0 += 32) {
+        float o[32];
+        chunk(d0, o);
+        if (out_row < 0) continue;
+#pragma unroll
+        for (int d = 0; d < 32; d += 4) {
+            if (d0 + d >= p.D) break;
+            const float4 v = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
+            if (split) __stcg(reinterpret_cast<float4 *>(mine + (int64_t)r * p.D + d0 + d), v);
+            else attn_write<T>(p, it.keys.ok, out_row, d0 + d, m, l, v);
+        }
+    }
+    if (!split) return;
+    __stcg(mine + RT * p.D + r, m);
+    __stcg(mine + RT * p.D + RT + r, l);
+    __threadfence();
+    sync_nt<NT>();
+    if (threadIdx.x == 0) *last_flag = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
+    sync_nt<NT>();
+    if (!*last_flag) return;
+    __threadfence();
+    if (out_row >= 0) {
+        float mm = -INFINITY;
+        for (int c = c0; c <= c1; ++c)
+            mm = fmaxf(mm, __ldcg(p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats + RT * p.D + r));
+        for (int d0 = 0; d0 < p.D; d0 += 32) {
+            float4 o[8];
+            float ll = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int c = c0; c <= c1; ++c) {
+                const float *s = p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats;
+                const float k = rel_weight(__ldcg(s + RT * p.D + r), mm);
+                if (k == 0.0f) continue;  // this block saw no key of the row
+                ll += __ldcg(s + RT * p.D + RT + r) * k;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (d0 + 4 * j >= p.D) break;
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(s + (int64_t)r * p.D + d0 + 4 * j));
+                    o[j] = make_float4(fmaf(x.x, k, o[j].x), fmaf(x.y, k, o[j].y), fmaf(x.z, k, o[j].z), fmaf(x.w, k, o[j].w));
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (d0 + 4 * j < p.D) attn_write<T>(p, it.keys.ok, out_row, d0 + 4 * j, mm, ll, o[j]);
+        }
+    }
+    if (threadIdx.x == 0) p.counters[c0] = 0u;
     sync_nt<NT>();
 }
 

@@ -1,0 +1,715 @@
+// Attention over the paged cache for bf16 on the fifth-generation tensor cores
+// (tcgen05, accumulators in TMEM; attention.cuh: score, split, join).
+//
+// One persistent block per SM.  A tile is 128 keys; an item's queries fill the
+// 128 rows of the MMA:
+//   C = 1: up to 128 rows (QT = 2: two such tiles that share the keys, 256 rows,
+//     for the pass over a shared prefix, which is bound by arithmetic);
+//   C = 2 or 4: 64 or 32 rows, repeated C times down the MMA's rows.  Copy g
+//     takes only its own 128/C keys of a tile (the other columns of its P stay
+//     zero), so all four softmax warps have 128/C scores per thread and need
+//     not talk to each other; the copies are joined at the item's end like
+//     split keys.  The tensor work this wastes is there anyway: at few rows the
+//     kernel is bound by HBM.
+// Roles: a TMA warp copies K and V tiles, a box of a page's rows (and 64
+// columns, the swizzle's width) per copy, into a ring of 32 KB buffers; one
+// thread issues S = Q K^T and O += P V; four (eight) softmax warps take a row
+// per thread from TMEM, keep the running maximum and sum in registers and put
+// P, rounded to bf16, back into TMEM.  O is rescaled only when a row's maximum
+// grows by more than 2^8 (the weights then stay below 2^8 of the final scale,
+// well within f32 and bf16).
+//
+// A masked key's V may hold anything: where a tile masks a key, the softmax
+// threads look at V's rows, one each, zero what is not finite and make NaN the
+// rows that see such a key.
+#include <cuda.h>
+
+#include "attention.cuh"
+#include "tma.cuh"
+
+namespace specv {
+namespace {
+
+constexpr int KT = 128;
+constexpr uint32_t kHalf = KT * 128;  // bytes: 128 keys x 64 columns
+constexpr int kInfo = 8;              // tiles whose notes are kept
+
+// ---- tcgen05 -------------------------------------------------------------
+__device__ __forceinline__ void tc_alloc(uint32_t *dst) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(dst)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_dealloc(uint32_t t) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(t) : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(unsigned long long *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+// D (TMEM) (+)= A (shared) B (shared)^T
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// D (TMEM) (+)= A (TMEM) B (shared)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+#define R8(x, i) "=f"(x[i]), "=f"(x[i + 1]), "=f"(x[i + 2]), "=f"(x[i + 3]), "=f"(x[i + 4]), "=f"(x[i + 5]), "=f"(x[i + 6]), "=f"(x[i + 7])
+#define W8(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3]), "r"(x[i + 4]), "r"(x[i + 5]), "r"(x[i + 6]), "r"(x[i + 7])
+// 32 columns of this thread's lane
+__device__ __forceinline__ void tc_ld32(float *x, uint32_t t) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
+        : "r"(t));
+}
+__device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t *x) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        W8(x, 0), W8(x, 8)
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t t, const uint32_t *x) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+        W8(x, 0), W8(x, 8), W8(x, 16), W8(x, 24)
+        : "memory");
+}
+#undef R8
+#undef W8
+
+// Shared-memory operand, 128-byte swizzle (8 rows of 128 bytes an atom): lbo /
+// sbo are the byte steps described at the uses.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+// bf16 x bf16 -> f32, M = 128; bn: B's rows (N) are contiguous
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool bn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (bn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+}
+
+__device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap *m, int x, int y, int z, unsigned long long *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w,
+                                     unsigned long long *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+            dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(unsigned long long *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t x) { return __vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
+
+template <int NH, int C, int QT> struct TcCfg {
+    static constexpr int kRows = 128 * QT / C;       // queries of an item
+    static constexpr int kNT = 128 * QT;             // softmax threads
+    static constexpr int kThreads = kNT + (QT == 2 ? 128 : 64);
+    static constexpr uint32_t kTile = NH * kHalf;    // bytes of a K or V tile
+    // the ring takes what the queries and the join leave of 227 KB
+    static constexpr int kRing = NH == 1 ? 8 : QT == 2 || C == 2 ? 4 : 5;
+};
+
+template <int NH, int C, int QT> struct TcSmem {
+    using K = TcCfg<NH, C, QT>;
+    alignas(1024) unsigned char kv[K::kRing][K::kTile];
+    alignas(1024) unsigned char q[QT][K::kTile];
+    alignas(16) float o[C == 1 ? 1 : K::kRows][NH * 64 + 4];
+    float m[C][K::kRows], l[C][K::kRows], tm[K::kRows], tl[K::kRows];
+    AttnRows<K::kRows> rows[2];
+    int kc[2][KT], kp[2][KT];       // a masked tile's keys: index (-1: none), position
+    unsigned bad[kInfo];            // boxes of a tile with a bad block
+    unsigned dirty[4];
+    int low_max[2];                 // the largest first visible position of an item's rows
+    AttnPlan plan;
+    alignas(8) unsigned long long full[K::kRing], empty[K::kRing], s_full[2], p_full[2], pv_done[2], q_full;
+    uint32_t tmem;
+    int flag;
+};
+
+template <int NH, int C, int QT>
+__global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
+    attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap cache_map,
+                   const __grid_constant__ CUtensorMap temp_map) {
+    using K = TcCfg<NH, C, QT>;
+    using T = __nv_bfloat16;
+    constexpr int RT = K::kRows, NT = K::kNT, NS = K::kRing, NC = KT / C;
+    extern __shared__ unsigned char raw_[];
+    TcSmem<NH, C, QT> &sh = *reinterpret_cast<TcSmem<NH, C, QT> *>(
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = p.S * p.G;
+    const int64_t nrows = p.mode == 1 ? (int64_t)p.B * per : per;
+    const int rtiles = (int)((nrows + RT - 1) / RT), items = p.H * rtiles;
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.pv_done[i], 1);
+        }
+        mbar_init(&sh.q_full, NT);
+        fence_barrier_init();
+    }
+    if (warp < NT / 32) attn_plan<NT>(p, sh.plan, items, KT);
+    __syncthreads();
+    int64_t u = (int64_t)blockIdx.x * sh.plan.share;
+    const int64_t uend = min(sh.plan.total, u + sh.plan.share);
+    if (u >= uend) return;
+    if (warp == 0) tc_alloc(&sh.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    // TMEM columns: S of two tiles (QT = 2: of the two query tiles), O, P.  With
+    // copies P has its own columns, zero outside a copy's keys; QT = 2 puts P
+    // over S.
+    constexpr uint32_t kS = 0, kO = 256, kP = 384;
+    bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
+    AttnItem it = attn_find<NT>(p, sh.plan, u, items, rtiles, KT);
+
+    if (QT == 2) {  // 12 warps of 168 registers: 4 * 56 + 8 * 224
+        if (warp >= NT / 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    }
+
+    if (warp == NT / 32) {
+        // ---------------- TMA ----------------
+        const int nbox = KT / p.box;
+        const int zero_row = (int)(2 * p.nb * p.bs);  // past the map: zeros are written
+        const int v_row = (int)(p.nb * p.bs);
+        int n = 0, tiles = 0;
+        while (true) {
+            if (!it.keys.ok && u == it.u0 && it.h == 0 && it.rt == 0 && lane == 0) attn_flag(p, it.b);
+            const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
+            const int *table = p.mode == 1 ? p.stable : p.table + (int64_t)it.b * p.max_blocks;
+            const bool temp = p.tk && p.mode == 0;
+            const KeyLine line = it.keys.ok ? attn_line(p, it.keys) : KeyLine{0, 0};
+            const int end = temp ? it.keys.len : it.keys.hi;
+            int row_k = 0, row_v = 0;      // this lane's box: row of the cache, or -1 - candidate
+            auto look_up = [&](int t) {
+                int r = zero_row;
+                bool bad = false;
+                if (lane < nbox && it.keys.ok) {
+                    const int k = t * KT + lane * p.box, c = line.lo + k;
+                    if (k < line.entries) {
+                        if (c < end) {
+                            const int j = (int)fast_div((unsigned)c, p.bs_div), blk = __ldg(table + j);
+                            bad = blk < 0 || (int64_t)blk >= p.nb;
+                            if (!bad) r = blk * p.bs + (c - j * p.bs);
+                        }
+                    } else if (temp && k - line.entries < p.S) {
+                        r = -1 - (k - line.entries);
+                    }
+                }
+                if (bad) attn_flag(p, it.b);
+                const unsigned b = __ballot_sync(kFull, bad);
+                if (lane == 0) sh.bad[tiles % kInfo] = b;
+                ++tiles;
+                return r;
+            };
+            auto copy = [&](int r, int is_v) {
+                const int s = n % NS;
+                if (n >= NS && ok) ok = mbar_wait_bounded(&sh.empty[s], (unsigned)((n / NS - 1) & 1));
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], K::kTile);
+                __syncwarp();
+                if (lane < nbox) {
+                    const uint32_t dst = smem_u32(sh.kv[s]) + (uint32_t)lane * p.box * 128;
+#pragma unroll
+                    for (int h = 0; h < NH; ++h) {
+                        if (r < 0) tma4(dst + h * kHalf, &temp_map, h * 64, it.h, -1 - r, 2 * (it.b * p.layers + p.layer) + is_v, &sh.full[s]);
+                        else tma3(dst + h * kHalf, &cache_map, h * 64, it.h, is_v && r != zero_row ? r + v_row : r, &sh.full[s]);
+                    }
+                }
+                ++n;
+            };
+            // the order of use: K0 K1 V0 K2 V1 ... (QT = 2: K0 V0 K1 V1 ...)
+            row_v = row_k = look_up(t0);
+            copy(row_k, 0);
+            for (int t = t0; t < t1; ++t) {
+                if (QT == 2) copy(row_v, 1);
+                if (t + 1 < t1) {
+                    row_k = look_up(t + 1);
+                    copy(row_k, 0);
+                }
+                if (QT == 1) copy(row_v, 1);
+                row_v = row_k;
+            }
+            u = it.u0 + it.ntiles;
+            if (u >= uend) break;
+            it = attn_next(p, it, items, rtiles, KT);
+        }
+        // no copy may land after the block has gone
+        for (int i = max(0, n - NS); i < n; ++i) ok = mbar_drain(&sh.full[i % NS], (unsigned)((i / NS) & 1)) && ok;
+    } else if (warp == NT / 32 + 1) {
+        // ---------------- MMA ----------------
+        if (lane == 0) {
+            // K and Q: rows of 128 bytes (64 columns), 8 rows = 1,024 bytes to the
+            // next (sbo); 16 columns of the product are 32 bytes, the next 64
+            // columns kHalf.  V: N (its columns) contiguous, 64 columns to the next
+            // kHalf (lbo), 8 keys 1,024 bytes (sbo).
+            constexpr uint32_t id_s = tc_idesc(KT, false), id_o = tc_idesc(NH * 64, true);
+            const int ksteps = (p.D + 15) / 16;
+            int n = 0, j = 0, item = 0;
+            auto wait_full = [&](int i) {
+                if (ok) ok = mbar_wait_bounded(&sh.full[i % NS], (unsigned)((i / NS) & 1));
+                tc_fence_after();
+            };
+            auto scores = [&](uint32_t d, int qt, int slot) {
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint32_t off = (uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32;
+                    tc_mma_ss(d, tc_desc(smem_u32(sh.q[qt]) + off, 16, 1024), tc_desc(smem_u32(sh.kv[slot]) + off, 16, 1024),
+                              id_s, k > 0);
+                }
+            };
+            auto values = [&](uint32_t d, uint32_t pt, int slot, bool first) {
+#pragma unroll
+                for (int k = 0; k < KT / 16; ++k)
+                    tc_mma_ts(d, pt + k * 8, tc_desc(smem_u32(sh.kv[slot]) + k * 2048, kHalf, 1024), id_o, !(first && k == 0));
+            };
+            while (true) {
+                const int nt = (int)(min(uend, it.u0 + it.ntiles) - u);
+                if (ok) ok = mbar_wait_bounded(&sh.q_full, (unsigned)(item & 1));
+                if (QT == 1) {
+                    wait_full(n);
+                    scores(tmem + kS + (j & 1) * 128, 0, n % NS);
+                    tc_commit(&sh.empty[n % NS]);
+                    tc_commit(&sh.s_full[j & 1]);
+                    ++n;
+                    for (int t = 0; t < nt; ++t, ++j) {
+                        if (t + 1 < nt) {
+                            wait_full(n);
+                            scores(tmem + kS + ((j + 1) & 1) * 128, 0, n % NS);
+                            tc_commit(&sh.empty[n % NS]);
+                            tc_commit(&sh.s_full[(j + 1) & 1]);
+                            ++n;
+                        }
+                        wait_full(n);
+                        if (ok) ok = mbar_wait_bounded(&sh.p_full[j & 1], (unsigned)((j >> 1) & 1));
+                        tc_fence_after();
+                        values(tmem + kO, tmem + kP + (j & 1) * 64, n % NS, t == 0);
+                        tc_commit(&sh.empty[n % NS]);
+                        tc_commit(&sh.pv_done[0]);
+                        ++n;
+                    }
+                } else {
+                    wait_full(n);
+                    for (int q = 0; q < 2; ++q) {
+                        scores(tmem + kS + q * 128, q, n % NS);
+                        tc_commit(&sh.s_full[q]);
+                    }
+                    tc_commit(&sh.empty[n % NS]);
+                    ++n;
+                    for (int t = 0; t < nt; ++t, ++j) {
+                        const int nv = n, nk = n + 1;
+                        const bool more = t + 1 < nt;
+                        wait_full(nv);
+                        if (more) wait_full(nk);
+                        for (int q = 0; q < 2; ++q) {
+                            if (ok) ok = mbar_wait_bounded(&sh.p_full[q], (unsigned)(j & 1));
+                            tc_fence_after();
+                            values(tmem + kO + q * 128, tmem + kS + q * 128, nv % NS, t == 0);
+                            tc_commit(&sh.pv_done[q]);
+                            if (q == 1) tc_commit(&sh.empty[nv % NS]);
+                            if (more) {
+                                scores(tmem + kS + q * 128, q, nk % NS);
+                                tc_commit(&sh.s_full[q]);
+                                if (q == 1) tc_commit(&sh.empty[nk % NS]);
+                            }
+                        }
+                        n += more ? 2 : 1;
+                    }
+                }
+                ++item;
+                u = it.u0 + it.ntiles;
+                if (u >= uend) break;
+                it = attn_next(p, it, items, rtiles, KT);
+            }
+        }
+        __syncwarp();
+    } else if (warp < NT / 32) {
+        // ---------------- softmax ----------------
+        const int wq = warp & 3, qt = warp >> 2;                  // TMEM lanes 32 wq .. + 31 of query tile qt
+        const int mrow = wq * 32 + lane;                          // row of the MMA
+        const int copy = C == 1 ? 0 : wq / (4 / C);
+        const int row = C == 1 ? qt * 128 + mrow : mrow % RT;     // query of the item
+        const int cb = copy * NC;                                 // first key of the copy in a tile
+        const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
+        const bool by_pos = p.window > 0 || p.first != nullptr;
+        const float scale2 = fabsf(p.score.scale) * kLog2e;
+        if (C > 1) {  // P's other columns stay zero
+            uint32_t z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tc_st32(tl + kP + i * 32, z);
+            tc_wait_st();
+        }
+        int buf = 0, j = 0, nring = 0;
+        // the item's rows and queries; the MMA of the item before has read its own
+        auto load_item = [&](const AttnItem &x, int bufn) {
+            AttnRows<RT> &w = sh.rows[bufn];
+            if (tid == 0) sh.low_max[bufn] = (int)0x80000000;
+            attn_rows<RT, NT>(p, x, w);
+            sync_nt<NT>();
+            if (by_pos)
+                for (int i = tid; i < RT; i += NT)
+                    if (w.out[i] >= 0)
+                        atomicMax(&sh.low_max[bufn], max(w.first[i], p.window > 0 ? w.qp[i] - p.window + 1 : (int)0x80000000));
+            // a negative scale: the queries are negated instead
+            const uint32_t neg = p.score.scale < 0.0f ? 0x80008000u : 0u;
+            for (int i = tid; i < QT * 128 * NH * 8; i += NT) {
+                const int r = i / (NH * 8), c = i - r * (NH * 8), d = c * 8;  // row, 16-byte chunk
+                const int64_t src = w.q[C == 1 ? r : r % RT];
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (src >= 0 && d < p.D) v = ld_nc16(static_cast<const T *>(p.q) + src + d);
+                v.x ^= neg, v.y ^= neg, v.z ^= neg, v.w ^= neg;
+                const int mr = r & 127;
+                *reinterpret_cast<uint4 *>(sh.q[r >> 7] + (c >> 3) * kHalf + mr * 128 + (((c & 7) ^ (mr & 7)) << 4)) = v;
+            }
+            fence_async_shared();
+            mbar_arrive(&sh.q_full);
+            sync_nt<NT>();  // low_max
+        };
+        load_item(it, buf);
+        while (true) {
+            const AttnRows<RT> &w = sh.rows[buf];
+            const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), nt = t1 - t0;
+            const int64_t out_row = w.out[row];
+            const int qp = w.qp[row], cand = w.cand[row];
+            const int low = max(w.first[row], p.window > 0 ? qp - p.window + 1 : (int)0x80000000);
+            const float slope = w.slope[row];
+            const bool temp = p.tk && p.mode == 0;
+            const KeyLine line = it.keys.ok ? attn_line(p, it.keys) : KeyLine{0, 0};
+            const int end = temp ? it.keys.len : it.keys.hi;
+            float m = -INFINITY, l = 0.0f;  // reference (log2 units), sum
+            bool poison = false;
+            int kp_next = 0;
+            auto key_pos_of = [&](int t) {  // position of key `mrow` of tile t, when key_pos is given
+                const int k = t * KT + mrow, c = line.lo + k;
+                return k < line.entries && c < it.keys.len ? p.key_pos[(int64_t)it.b * p.kps + c] : 0;
+            };
+            if (p.key_pos) kp_next = key_pos_of(t0);
+            for (int t = t0; t < t1; ++t, ++j) {
+                const int sb = QT == 1 ? j & 1 : qt;
+                const unsigned sp = QT == 1 ? (j >> 1) & 1 : j & 1;
+                const int kp_mine = kp_next;
+                if (p.key_pos && t + 1 < t1) kp_next = key_pos_of(t + 1);
+                if (ok) ok = mbar_wait_bounded(&sh.s_full[sb], sp);
+                tc_fence_after();
+                float x[NC];
+#pragma unroll
+                for (int i = 0; i < NC / 32; ++i) tc_ld32(x + i * 32, tl + kS + sb * 128 + cb + i * 32);
+                const int k0 = t * KT, c0 = line.lo + k0;
+                // whether the tile may mask a key: the line's ends, a bad block, the
+                // window's and the document's first tile
+                const bool special = !it.keys.ok || c0 < it.keys.lo || c0 + KT > it.keys.len || k0 + KT > line.entries ||
+                                     sh.bad[j % kInfo] != 0u || (by_pos && (p.key_pos || c0 < sh.low_max[buf]));
+                const bool listed = special || (p.key_pos && p.score.bias);
+                if (listed) {
+                    if (qt == 0) {
+                        const int k = k0 + mrow, c = c0 + mrow;
+                        int idx = -1, kp = 0;
+                        if (it.keys.ok && k < line.entries) {
+                            if (c >= it.keys.lo && c < end && !((sh.bad[j % kInfo] >> (mrow / p.box)) & 1u)) {
+                                idx = c;
+                                kp = c < it.keys.len ? (p.key_pos ? kp_mine : c) : key_position(p, it, c);
+                            }
+                        } else if (it.keys.ok && temp && k - line.entries < p.S) {
+                            idx = it.keys.len + k - line.entries;
+                            kp = key_position(p, it, idx);
+                        }
+                        sh.kc[j & 1][mrow] = idx;
+                        sh.kp[j & 1][mrow] = kp;
+                    }
+                    sync_nt<NT>();
+                }
+                tc_wait_ld();
+                float cf = scale2;
+                bool hid = false;
+                if (listed) {
+                    cf = kLog2e;
+                    ScoreArgs sc = p.score;
+                    sc.scale = fabsf(sc.scale);
+                    const int *kc = sh.kc[j & 1] + cb, *kp = sh.kp[j & 1] + cb;
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        const int c = kc[i], pos = kp[i];
+                        x[i] = attn_score<false>(x[i], sc, slope, pos_dist(qp, pos));
+                        bool v = c >= 0 && pos >= low;
+                        if (p.mode == 0 && c >= it.keys.len && v) {
+                            const int jj = c - it.keys.len;
+                            v = p.mask ? (p.mask[((int64_t)it.b * p.S + cand) * p.W + (jj >> 5)] >> (jj & 31)) & 1u : jj <= cand;
+                        }
+                        if (!v) {
+                            x[i] = -INFINITY;
+                            hid = true;
+                        }
+                    }
+                } else if (p.score.cap > 0.0f || p.score.bias) {
+                    cf = kLog2e;
+                    const float scale = fabsf(p.score.scale), d0 = (float)(qp - (c0 + cb));
+#pragma unroll
+                    for (int i = 0; i < NC; ++i) {
+                        x[i] *= scale;
+                        if (p.score.cap > 0.0f) x[i] = cap_score(x[i], p.score.cap, p.score.cap_arg);
+                        if (p.score.bias) x[i] = fmaf(-slope, d0 - (float)i, x[i]);
+                    }
+                }
+                float mt = x[0];
+#pragma unroll
+                for (int i = 1; i < NC; ++i) mt = fmaxf(mt, x[i]);
+                mt *= cf;
+                // a new reference when the maximum has grown past 2^8 of the old one
+                const bool grew = mt > m + 8.0f || (m == -INFINITY && mt > -INFINITY);
+                float corr = 1.0f;
+                if (grew) {
+                    corr = rel_weight(m, mt);
+                    m = mt;
+                    l *= corr;
+                }
+                const bool rescale = __any_sync(kFull, grew) && t > t0;
+                if (rescale) {
+                    if (ok) ok = mbar_wait_bounded(&sh.pv_done[qt], (unsigned)((j - 1) & 1));
+                    tc_fence_after();
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const uint32_t pt = tl + (QT == 1 ? kP + sb * 64 : kS + sb * 128) + cb / 2;
+                float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NC; i += 32) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float a = ex2f(fmaf(x[i + e], cf, -ref)), b = ex2f(fmaf(x[i + e + 1], cf, -ref));
+                        s0 += a;
+                        s1 += b;
+                        pk[e / 2] = pack_bf16(a, b);
+                        if (special) {
+                            x[i + e] = a;
+                            x[i + e + 1] = b;
+                        }
+                    }
+                    tc_st16(pt + i / 2, pk);
+                }
+                l += s0 + s1;
+                if (rescale) {
+                    for (int d = 0; d < NH * 64; d += 32) {
+                        float o[32];
+                        tc_ld32(o, tl + kO + qt * 128 + d);
+                        tc_wait_ld();
+                        uint32_t y[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(o[i] * corr);
+                        tc_st32(tl + kO + qt * 128 + d, y);
+                    }
+                }
+                if (special && sync_nt_or<NT>(hid)) {
+                    // V of this tile: ring place by the order of the copies
+                    const int tt = t - t0;
+                    const int nv = nring + (QT == 2 ? 2 * tt + 1 : tt + 1 < nt ? 2 * tt + 2 : 2 * tt + 1);
+                    if (ok) ok = mbar_wait_bounded(&sh.full[nv % NS], (unsigned)((nv / NS) & 1));
+                    if (qt == 0) {
+                        unsigned char *vr = sh.kv[nv % NS] + mrow * 128;
+                        uint32_t found = 0;
+#pragma unroll 4
+                        for (int i = 0; i < NH * 8; ++i) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * kHalf + (i & 7) * 16);
+                            found |= nonfinite2(y.x) | nonfinite2(y.y) | nonfinite2(y.z) | nonfinite2(y.w);
+                        }
+                        if (found) {
+                            for (int i = 0; i < NH * 8; ++i)
+                                *reinterpret_cast<uint4 *>(vr + (i >> 3) * kHalf + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        const unsigned b = __ballot_sync(kFull, found != 0u);
+                        if (lane == 0) sh.dirty[wq] = b;
+                        fence_async_shared();
+                    }
+                    sync_nt<NT>();
+#pragma unroll
+                    for (int i = 0; i < NC; ++i)
+                        poison = poison || (((sh.dirty[(cb + i) / 32] >> ((cb + i) & 31)) & 1u) && x[i] != 0.0f);
+                    sync_nt<NT>();  // dirty may be written again
+                }
+                // every product's end is seen before the next is let go: the barrier's
+                // phase bit tells only neighbours apart (QT = 2: S came after it)
+                if (QT == 1 && t > t0 && !rescale && ok)
+                    ok = mbar_wait_bounded(&sh.pv_done[qt], (unsigned)((j - 1) & 1));
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(&sh.p_full[sb]);
+            }
+            nring += 2 * nt;
+            const AttnItem done = it;
+            u = it.u0 + it.ntiles;
+            const bool more = u < uend;
+            if (more) {
+                it = attn_next(p, it, items, rtiles, KT);
+                load_item(it, buf ^ 1);
+            }
+            if (ok) ok = mbar_wait_bounded(&sh.pv_done[qt], (unsigned)((j - 1) & 1));
+            tc_fence_after();
+            auto chunk = [&](int d, float *o) {
+                tc_ld32(o, tl + kO + qt * 128 + d);
+                tc_wait_ld();
+                if (poison)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = __int_as_float(0x7fffffff);
+            };
+            if (C == 1) {
+                attn_finish_row<T, RT, NT>(p, sh.plan, done, out_row, row, m, l, chunk, &sh.flag);
+            } else {
+                sh.m[copy][row] = m;
+                sh.l[copy][row] = l;
+                sync_nt<NT>();
+                float mm = -INFINITY, ll = 0.0f;
+#pragma unroll
+                for (int g = 0; g < C; ++g) mm = fmaxf(mm, sh.m[g][row]);
+#pragma unroll
+                for (int g = 0; g < C; ++g) ll += sh.l[g][row] * rel_weight(sh.m[g][row], mm);
+                if (copy == 0) {
+                    sh.tm[row] = mm;
+                    sh.tl[row] = ll;
+                }
+                const float f = rel_weight(m, mm);
+                for (int g = 0; g < C; ++g) {
+                    if (copy == g) {
+                        for (int d = 0; d < NH * 64; d += 32) {
+                            float o[32];
+                            chunk(d, o);
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                float4 *at = reinterpret_cast<float4 *>(&sh.o[row][d + i]);
+                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (f != 0.0f) v = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+                                if (g > 0) {
+                                    const float4 b = *at;
+                                    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+                                }
+                                *at = v;
+                            }
+                        }
+                    }
+                    sync_nt<NT>();
+                }
+                attn_finish<T, RT, NT>(p, sh.plan, done, w, &sh.o[0][0], NH * 64 + 4, sh.tm, sh.tl, &sh.flag);
+            }
+            tc_fence_before();
+            if (!more) break;
+            buf ^= 1;
+        }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, SPEC_FLAG_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tc_dealloc(tmem);
+}
+
+// ---- host ------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+            const cuuint32_t *box) {
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box,
+                       ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NH, int C, int QT>
+cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {
+    using K = TcCfg<NH, C, QT>;
+    constexpr int smem = (int)sizeof(TcSmem<NH, C, QT>) + 1024;
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static_assert(K::kRows <= kAttnSlotRows * QT, "partial results");
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NH, C, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kAttnSmsMax ? sms : kAttnSmsMax;
+    attn_tc_kernel<NH, C, QT><<<grid, K::kThreads, smem, s>>>(p, cm, tm);
+    return cudaGetLastError();
+}
+
+template <int NH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {
+    const int64_t rows = p.mode == 1 ? (int64_t)p.B * p.S * p.G : (int64_t)p.S * p.G;
+    if (rows <= 32) return launch<NH, 4, 1>(p, cm, tm, sms, s);
+    if (rows <= 64) return launch<NH, 2, 1>(p, cm, tm, sms, s);
+    if (rows <= 128 || p.mode == 0) return launch<NH, 1, 1>(p, cm, tm, sms, s);
+    return launch<NH, 1, 2>(p, cm, tm, sms, s);
+}
+
+}  // namespace
+
+// Rows of a page a box takes: the pages must be whole boxes and a tile's 128
+// keys too, 8 rows at least (a swizzle atom).
+int attn_tc_box(const AttnParams &p) {
+    if (p.D < 64 || p.D > 128 || 2 * p.nb * p.bs > 0x7fffff00LL || (int64_t)p.B * p.layers > 0x3fffffffLL) return 0;
+    int box = 128;
+    while (box >= 8 && p.bs % box != 0) box >>= 1;
+    return box >= 8 && encode_fn() ? box : 0;
+}
+
+cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t s) {
+    CUtensorMap cm, tm;
+    const cuuint64_t row = (cuuint64_t)p.H * p.D * 2;
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)p.box, 1};
+    {
+        const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)(2 * p.nb * p.bs)};
+        const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, row};
+        if (!encode(&cm, p.kc, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    tm = cm;
+    if (p.tk && p.mode == 0) {
+        const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.S, (cuuint64_t)p.B * p.layers * 2};
+        const cuuint64_t strides[3] = {(cuuint64_t)p.D * 2, row, row * p.S};
+        if (!encode(&tm, p.temp_base, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    }
+    return p.D <= 64 ? launch_nh<1>(p, cm, tm, sms, s) : launch_nh<2>(p, cm, tm, sms, s);
+}
+
+}  // namespace specv

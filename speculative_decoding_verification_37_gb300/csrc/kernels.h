@@ -217,7 +217,7 @@ struct ScoreArgs {
 
 constexpr int kAttnThreadsMax = 256;
 constexpr int kAttnSmsMax = 160;     // grids are sized for at most this many SMs
-constexpr int kAttnSlotRows = 128;   // rows of partial results per SM and slot
+constexpr int kAttnSlotRows = 128;   // rows of partial results per SM and slot; twice that with a shared prefix
 constexpr int kAttnCounters = kAttnSmsMax * 8;
 
 struct AttnParams {
@@ -229,6 +229,8 @@ struct AttnParams {
     const void *kc, *vc;          // the layer's planes [nb][bs][H][D]
     const void *tk, *tv;          // the layer's candidates of request 0, or null (in place)
     int64_t tsb;                  // elements between two requests' candidates
+    const void *temp_base;        // [B][layers][2][S][H][D]
+    int layers, layer;
     const int *table, *len;
     const uint32_t *mask;
     const int *pos, *key_pos;
@@ -244,6 +246,7 @@ struct AttnParams {
     const int *slots, *n_slots;   // mode 2: the committed candidates
     int slots_stride;
     int min_share;                // tiles a block takes at least
+    int box;                      // rows of a page copied at once (0: row by row)
     void *out;
     float *lse;
     unsigned *flags, *status, *counters;
@@ -252,6 +255,9 @@ struct AttnParams {
 };
 cudaError_t launch_attn_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_attn_mma(const AttnParams &p, int sms, cudaStream_t s);  // bf16
+// bf16, keys in boxes: p.box from attn_tc_box (0: this kernel does not take the call)
+int attn_tc_box(const AttnParams &p);
+cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t s);
 
 struct WeightsParams {
     AttnParams a;                 // q, cache, tables, score (P: entries left out)
