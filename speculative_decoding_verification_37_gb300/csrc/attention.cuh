@@ -386,14 +386,26 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
         if (w.out[r] < 0) continue;
         float m = -INFINITY, l = 0.0f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; ++c) {
-            const float *s = p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats;
-            const float mc = __ldcg(s + RT * p.D + r), lc = __ldcg(s + RT * p.D + RT + r);
-            const float4 oc = __ldcg(reinterpret_cast<const float4 *>(s + r * p.D + d));
-            const float mn = fmaxf(m, mc), a = rel_weight(m, mn), k = rel_weight(mc, mn);
-            l = l * a + lc * k;
-            o = make_float4(o.x * a + oc.x * k, o.y * a + oc.y * k, o.z * a + oc.z * k, o.w * a + oc.w * k);
-            m = mn;
+        constexpr int U = 8;  // blocks' results in flight
+        for (int cb = c0; cb <= c1; cb += U) {
+            float mc[U], lc[U];
+            float4 oc[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int c = min(cb + i, c1);
+                const float *s = p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats;
+                mc[i] = __ldcg(s + RT * p.D + r);
+                lc[i] = __ldcg(s + RT * p.D + RT + r);
+                oc[i] = __ldcg(reinterpret_cast<const float4 *>(s + r * p.D + d));
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (cb + i > c1) break;
+                const float mn = fmaxf(m, mc[i]), a = rel_weight(m, mn), k = rel_weight(mc[i], mn);
+                l = l * a + lc[i] * k;
+                o = make_float4(o.x * a + oc[i].x * k, o.y * a + oc[i].y * k, o.z * a + oc[i].z * k, o.w * a + oc[i].w * k);
+                m = mn;
+            }
         }
         attn_write<T>(p, it.keys.ok, w.out[r], d, m, l, o);
     }

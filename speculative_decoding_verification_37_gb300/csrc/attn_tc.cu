@@ -2,22 +2,23 @@
 // (tcgen05, accumulators in TMEM; attention.cuh: score, split, join).
 //
 // One persistent block per SM.  A tile is 128 keys; an item's queries fill the
-// 128 rows of the MMA:
-//   C = 1: up to 128 rows (QT = 2: two such tiles that share the keys, 256 rows,
-//     for the pass over a shared prefix, which is bound by arithmetic);
-//   C = 2 or 4: 64 or 32 rows, repeated C times down the MMA's rows.  Copy g
-//     takes only its own 128/C keys of a tile (the other columns of its P stay
-//     zero), so all four softmax warps have 128/C scores per thread and need
-//     not talk to each other; the copies are joined at the item's end like
-//     split keys.  The tensor work this wastes is there anyway: at few rows the
-//     kernel is bound by HBM.
-// Roles: a TMA warp copies K and V tiles, a box of a page's rows (and 64
-// columns, the swizzle's width) per copy, into a ring of 32 KB buffers; one
-// thread issues S = Q K^T and O += P V; four (eight) softmax warps take a row
-// per thread from TMEM, keep the running maximum and sum in registers and put
-// P, rounded to bf16, back into TMEM.  O is rescaled only when a row's maximum
-// grows by more than 2^8 (the weights then stay below 2^8 of the final scale,
-// well within f32 and bf16).
+// 128 rows of the MMA.  Two groups of four softmax warps (a row per thread) keep
+// a tile each in work:
+//   * few rows (64 or 32 an item; bound by HBM): the groups take turns at the
+//     tiles, with an accumulator each, and the queries are repeated C = 2 or 4
+//     times down the MMA's rows.  Copy g takes only its own 128/C keys of a tile
+//     (its P is zero elsewhere), so a thread has 128/C scores and no thread needs
+//     another's.  The groups' and copies' results are joined at the item's end
+//     like those of split keys.  The tensor work this wastes is there anyway;
+//   * many rows (the pass over a shared prefix; bound by arithmetic): a query
+//     tile of 128 rows for each group, both on the same keys;
+//   * up to 128 rows: one group, two score tiles.
+// Roles: a TMA warp copies K and V tiles, a box of a page's rows per copy, into
+// a ring of buffers; one thread issues S = Q K^T and O += P V; the softmax warps
+// read S from TMEM 32 columns at a time, first for the maximum, then for the
+// weights, and put P, rounded to bf16, over S.  O is rescaled only when a row's
+// maximum grows by more than 2^8 (the weights then stay below 2^8 of the final
+// scale, well within f32 and bf16).
 //
 // A masked key's V may hold anything: where a tile masks a key, the softmax
 // threads look at V's rows, one each, zero what is not finite and make NaN the
@@ -76,6 +77,14 @@ __device__ __forceinline__ void tc_ld32(float *x, uint32_t t) {
         : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
         : "r"(t));
 }
+__device__ __forceinline__ void tc_ld16(float *x, uint32_t t) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : R8(x, 0), R8(x, 8)
+                 : "r"(t));
+}
+__device__ __forceinline__ void tc_ld8(float *x, uint32_t t) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : R8(x, 0) : "r"(t));
+}
 __device__ __forceinline__ void tc_st16(uint32_t t, const uint32_t *x) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
@@ -118,6 +127,14 @@ __device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap *m, int x, 
         "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, int v,
+                                     unsigned long long *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+            dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(unsigned long long *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -129,25 +146,30 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 __device__ __forceinline__ uint32_t nonfinite2(uint32_t x) { return __vcmpeq2(x & 0x7f807f80u, 0x7f807f80u); }
 
-template <int NH, int C, int QT> struct TcCfg {
-    static constexpr int kRows = 128 * QT / C;       // queries of an item
-    static constexpr int kNT = 128 * QT;             // softmax threads
-    static constexpr int kThreads = kNT + (QT == 2 ? 128 : 64);
+// How the two softmax groups share the work: W = 0 one group, 1 tiles in turn, 2
+// a query tile each.
+template <int NH, int C, int W> struct TcCfg {
+    static constexpr int kQT = W == 2 ? 2 : 1;       // query tiles
+    static constexpr int kRows = 128 * kQT / C;      // queries of an item
+    static constexpr int kNT = W == 0 ? 128 : 256;   // softmax threads
+    static constexpr int kThreads = kNT + 64;
+    static constexpr int kCopies = W == 1 ? 2 * C : C;
     static constexpr uint32_t kTile = NH * kHalf;    // bytes of a K or V tile
     // the ring takes what the queries and the join leave of 227 KB
-    static constexpr int kRing = NH == 1 ? 8 : QT == 2 || C == 2 ? 4 : 5;
+    static constexpr int kRing = NH == 1 ? 8 : W == 2 || C == 2 ? 4 : 5;
 };
 
-template <int NH, int C, int QT> struct TcSmem {
-    using K = TcCfg<NH, C, QT>;
+template <int NH, int C, int W> struct TcSmem {
+    using K = TcCfg<NH, C, W>;
     alignas(1024) unsigned char kv[K::kRing][K::kTile];
-    alignas(1024) unsigned char q[QT][K::kTile];
-    alignas(16) float o[C == 1 ? 1 : K::kRows][NH * 64 + 4];
-    float m[C][K::kRows], l[C][K::kRows], tm[K::kRows], tl[K::kRows];
+    alignas(1024) unsigned char q[K::kQT][K::kTile];
+    alignas(16) float o[W == 1 ? K::kRows : 1][NH * 64 + 4];
+    float m[K::kCopies][K::kRows], l[K::kCopies][K::kRows], tm[K::kRows], tl[K::kRows];
     AttnRows<K::kRows> rows[2];
-    int kc[2][KT], kp[2][KT];       // a masked tile's keys: index (-1: none), position
+    alignas(16) int kc[2][KT];      // a listed tile's keys: index (-1: masked for all),
+    alignas(16) int kp[2][KT];      // position
     unsigned bad[kInfo];            // boxes of a tile with a bad block
-    unsigned dirty[4];
+    unsigned dirty[2][4];
     int low_max[2];                 // the largest first visible position of an item's rows
     AttnPlan plan;
     alignas(8) unsigned long long full[K::kRing], empty[K::kRing], s_full[2], p_full[2], pv_done[2], q_full;
@@ -155,15 +177,28 @@ template <int NH, int C, int QT> struct TcSmem {
     int flag;
 };
 
-template <int NH, int C, int QT>
-__global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
+// barriers of n threads under an id of their own
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)pred), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+template <int NH, int C, int W>
+__global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap cache_map,
                    const __grid_constant__ CUtensorMap temp_map) {
-    using K = TcCfg<NH, C, QT>;
+    using K = TcCfg<NH, C, W>;
     using T = __nv_bfloat16;
-    constexpr int RT = K::kRows, NT = K::kNT, NS = K::kRing, NC = KT / C;
+    constexpr int RT = K::kRows, NT = K::kNT, NS = K::kRing, NC = KT / C, NCH = NC / 32;
     extern __shared__ unsigned char raw_[];
-    TcSmem<NH, C, QT> &sh = *reinterpret_cast<TcSmem<NH, C, QT> *>(
+    TcSmem<NH, C, W> &sh = *reinterpret_cast<TcSmem<NH, C, W> *>(
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = p.S * p.G;
@@ -192,17 +227,11 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    // TMEM columns: S of two tiles (QT = 2: of the two query tiles), O, P.  With
-    // copies P has its own columns, zero outside a copy's keys; QT = 2 puts P
-    // over S.
-    constexpr uint32_t kS = 0, kO = 256, kP = 384;
+    // TMEM columns: two score tiles (P lies over the first half of each), then
+    // one or two accumulators
+    constexpr uint32_t kS = 0, kO = 256;
     bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
     AttnItem it = attn_find<NT>(p, sh.plan, u, items, rtiles, KT);
-
-    if (QT == 2) {  // 12 warps of 168 registers: 4 * 56 + 8 * 224
-        if (warp >= NT / 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-    }
 
     if (warp == NT / 32) {
         // ---------------- TMA ----------------
@@ -245,25 +274,34 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], K::kTile);
                 __syncwarp();
                 if (lane < nbox) {
-                    const uint32_t dst = smem_u32(sh.kv[s]) + (uint32_t)lane * p.box * 128;
+                    // row groups of 8: 1,024 bytes for each half of the columns
+                    const uint32_t dst = smem_u32(sh.kv[s]) + (uint32_t)lane * p.box * (NH * 128);
+                    const int z = is_v && r >= 0 && r != zero_row ? r + v_row : r;
+                    const int plane = 2 * (it.b * p.layers + p.layer) + is_v;
+                    if (r < 0) {  // candidates: 8 rows and 64 columns at a time
+                        for (int g = 0; g < p.box; g += 8)
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        if (r < 0) tma4(dst + h * kHalf, &temp_map, h * 64, it.h, -1 - r, 2 * (it.b * p.layers + p.layer) + is_v, &sh.full[s]);
-                        else tma3(dst + h * kHalf, &cache_map, h * 64, it.h, is_v && r != zero_row ? r + v_row : r, &sh.full[s]);
+                            for (int h = 0; h < NH; ++h)
+                                tma4(dst + (uint32_t)(g >> 3) * (NH * 1024) + h * 1024, &temp_map, h * 64, it.h, -1 - r + g,
+                                     plane, &sh.full[s]);
+                    } else if (NH == 2) {
+                        tma5(dst, &cache_map, 0, 0, 0, z >> 3, it.h, &sh.full[s]);
+                    } else {
+                        tma3(dst, &cache_map, 0, it.h, z, &sh.full[s]);
                     }
                 }
                 ++n;
             };
-            // the order of use: K0 K1 V0 K2 V1 ... (QT = 2: K0 V0 K1 V1 ...)
+            // the order of use: K0 K1 V0 K2 V1 ... (W = 2: K0 V0 K1 V1 ...)
             row_v = row_k = look_up(t0);
             copy(row_k, 0);
             for (int t = t0; t < t1; ++t) {
-                if (QT == 2) copy(row_v, 1);
+                if (W == 2) copy(row_v, 1);
                 if (t + 1 < t1) {
                     row_k = look_up(t + 1);
                     copy(row_k, 0);
                 }
-                if (QT == 1) copy(row_v, 1);
+                if (W != 2) copy(row_v, 1);
                 row_v = row_k;
             }
             u = it.u0 + it.ntiles;
@@ -275,10 +313,11 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
     } else if (warp == NT / 32 + 1) {
         // ---------------- MMA ----------------
         if (lane == 0) {
-            // K and Q: rows of 128 bytes (64 columns), 8 rows = 1,024 bytes to the
-            // next (sbo); 16 columns of the product are 32 bytes, the next 64
-            // columns kHalf.  V: N (its columns) contiguous, 64 columns to the next
-            // kHalf (lbo), 8 keys 1,024 bytes (sbo).
+            // Operands in atoms of 8 rows x 128 bytes (64 columns).  Q: the next 8
+            // rows 1,024 bytes on, the next 64 columns kHalf.  K and V: the halves
+            // of the columns follow each other, so 8 keys are NH * 1,024 bytes and
+            // the next 64 columns 1,024.  16 columns of K and Q are 32 bytes; V's
+            // columns are its N, contiguous (lbo: the next 64, sbo: the next 8 keys).
             constexpr uint32_t id_s = tc_idesc(KT, false), id_o = tc_idesc(NH * 64, true);
             const int ksteps = (p.D + 15) / 16;
             int n = 0, j = 0, item = 0;
@@ -286,47 +325,49 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
                 if (ok) ok = mbar_wait_bounded(&sh.full[i % NS], (unsigned)((i / NS) & 1));
                 tc_fence_after();
             };
-            auto scores = [&](uint32_t d, int qt, int slot) {
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t off = (uint32_t)(k >> 2) * kHalf + (uint32_t)(k & 3) * 32;
-                    tc_mma_ss(d, tc_desc(smem_u32(sh.q[qt]) + off, 16, 1024), tc_desc(smem_u32(sh.kv[slot]) + off, 16, 1024),
-                              id_s, k > 0);
-                }
+            auto scores = [&](int d, int qt, int slot) {
+                for (int k = 0; k < ksteps; ++k)
+                    tc_mma_ss(tmem + kS + d * 128,
+                              tc_desc(smem_u32(sh.q[qt]) + (uint32_t)(k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
+                              tc_desc(smem_u32(sh.kv[slot]) + (uint32_t)(k >> 2) * 1024 + (k & 3) * 32, 16, NH * 1024), id_s,
+                              k > 0);
             };
-            auto values = [&](uint32_t d, uint32_t pt, int slot, bool first) {
+            auto values = [&](int o, int pt, int slot, bool first) {
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
-                    tc_mma_ts(d, pt + k * 8, tc_desc(smem_u32(sh.kv[slot]) + k * 2048, kHalf, 1024), id_o, !(first && k == 0));
+                    tc_mma_ts(tmem + kO + o * 128, tmem + kS + pt * 128 + k * 8,
+                              tc_desc(smem_u32(sh.kv[slot]) + k * (NH * 2048), 1024, NH * 1024), id_o, !(first && k == 0));
+            };
+            auto wait_p = [&](int i, unsigned phase) {
+                if (ok) ok = mbar_wait_bounded(&sh.p_full[i], phase);
+                tc_fence_after();
             };
             while (true) {
                 const int nt = (int)(min(uend, it.u0 + it.ntiles) - u);
                 if (ok) ok = mbar_wait_bounded(&sh.q_full, (unsigned)(item & 1));
-                if (QT == 1) {
-                    wait_full(n);
-                    scores(tmem + kS + (j & 1) * 128, 0, n % NS);
-                    tc_commit(&sh.empty[n % NS]);
-                    tc_commit(&sh.s_full[j & 1]);
-                    ++n;
-                    for (int t = 0; t < nt; ++t, ++j) {
-                        if (t + 1 < nt) {
-                            wait_full(n);
-                            scores(tmem + kS + ((j + 1) & 1) * 128, 0, n % NS);
-                            tc_commit(&sh.empty[n % NS]);
-                            tc_commit(&sh.s_full[(j + 1) & 1]);
-                            ++n;
-                        }
+                if (W != 2) {
+                    auto next_scores = [&](int d) {
                         wait_full(n);
-                        if (ok) ok = mbar_wait_bounded(&sh.p_full[j & 1], (unsigned)((j >> 1) & 1));
-                        tc_fence_after();
-                        values(tmem + kO, tmem + kP + (j & 1) * 64, n % NS, t == 0);
+                        scores(d, 0, n % NS);
                         tc_commit(&sh.empty[n % NS]);
-                        tc_commit(&sh.pv_done[0]);
+                        tc_commit(&sh.s_full[d]);
                         ++n;
+                    };
+                    next_scores(j & 1);
+                    if (nt > 1) next_scores((j + 1) & 1);
+                    for (int t = 0; t < nt; ++t, ++j) {
+                        wait_full(n);
+                        wait_p(j & 1, (unsigned)((j >> 1) & 1));
+                        values(W == 0 ? 0 : j & 1, j & 1, n % NS, W == 0 ? t == 0 : t < 2);
+                        tc_commit(&sh.empty[n % NS]);
+                        tc_commit(&sh.pv_done[W == 0 ? 0 : j & 1]);
+                        ++n;
+                        if (t + 2 < nt) next_scores(j & 1);
                     }
                 } else {
                     wait_full(n);
                     for (int q = 0; q < 2; ++q) {
-                        scores(tmem + kS + q * 128, q, n % NS);
+                        scores(q, q, n % NS);
                         tc_commit(&sh.s_full[q]);
                     }
                     tc_commit(&sh.empty[n % NS]);
@@ -337,13 +378,12 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
                         wait_full(nv);
                         if (more) wait_full(nk);
                         for (int q = 0; q < 2; ++q) {
-                            if (ok) ok = mbar_wait_bounded(&sh.p_full[q], (unsigned)(j & 1));
-                            tc_fence_after();
-                            values(tmem + kO + q * 128, tmem + kS + q * 128, nv % NS, t == 0);
+                            wait_p(q, (unsigned)(j & 1));
+                            values(q, q, nv % NS, t == 0);
                             tc_commit(&sh.pv_done[q]);
                             if (q == 1) tc_commit(&sh.empty[nv % NS]);
                             if (more) {
-                                scores(tmem + kS + q * 128, q, nk % NS);
+                                scores(q, q, nk % NS);
                                 tc_commit(&sh.s_full[q]);
                                 if (q == 1) tc_commit(&sh.empty[nk % NS]);
                             }
@@ -358,26 +398,21 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp < NT / 32) {
+    } else {
         // ---------------- softmax ----------------
-        const int wq = warp & 3, qt = warp >> 2;                  // TMEM lanes 32 wq .. + 31 of query tile qt
+        const int wq = warp & 3, grp = warp >> 2;                 // TMEM lanes 32 wq .. + 31
         const int mrow = wq * 32 + lane;                          // row of the MMA
         const int copy = C == 1 ? 0 : wq / (4 / C);
-        const int row = C == 1 ? qt * 128 + mrow : mrow % RT;     // query of the item
+        const int row = W == 2 ? grp * 128 + mrow : mrow % RT;    // query of the item
         const int cb = copy * NC;                                 // first key of the copy in a tile
+        const int acc = W == 0 ? 0 : grp;                         // accumulator
+        const int bar = W == 1 ? 2 + grp : 1, nbar = W == 1 ? 128 : NT;  // the threads that share a tile
         const uint32_t tl = tmem + ((uint32_t)(wq * 32) << 16);
+        const uint32_t to = tl + kO + acc * 128;
         const bool by_pos = p.window > 0 || p.first != nullptr;
-        const float scale2 = fabsf(p.score.scale) * kLog2e;
-        if (C > 1) {  // P's other columns stay zero
-            uint32_t z[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tc_st32(tl + kP + i * 32, z);
-            tc_wait_st();
-        }
+        const float scale = fabsf(p.score.scale);
         int buf = 0, j = 0, nring = 0;
-        // the item's rows and queries; the MMA of the item before has read its own
+        // the item's rows and queries; the MMA has read the ones before
         auto load_item = [&](const AttnItem &x, int bufn) {
             AttnRows<RT> &w = sh.rows[bufn];
             if (tid == 0) sh.low_max[bufn] = (int)0x80000000;
@@ -389,9 +424,9 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
                         atomicMax(&sh.low_max[bufn], max(w.first[i], p.window > 0 ? w.qp[i] - p.window + 1 : (int)0x80000000));
             // a negative scale: the queries are negated instead
             const uint32_t neg = p.score.scale < 0.0f ? 0x80008000u : 0u;
-            for (int i = tid; i < QT * 128 * NH * 8; i += NT) {
+            for (int i = tid; i < K::kQT * 128 * NH * 8; i += NT) {
                 const int r = i / (NH * 8), c = i - r * (NH * 8), d = c * 8;  // row, 16-byte chunk
-                const int64_t src = w.q[C == 1 ? r : r % RT];
+                const int64_t src = w.q[W == 2 ? r : r % RT];
                 uint4 v = make_uint4(0, 0, 0, 0);
                 if (src >= 0 && d < p.D) v = ld_nc16(static_cast<const T *>(p.q) + src + d);
                 v.x ^= neg, v.y ^= neg, v.z ^= neg, v.w ^= neg;
@@ -415,34 +450,35 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
             const int end = temp ? it.keys.len : it.keys.hi;
             float m = -INFINITY, l = 0.0f;  // reference (log2 units), sum
             bool poison = false;
-            int kp_next = 0;
-            auto key_pos_of = [&](int t) {  // position of key `mrow` of tile t, when key_pos is given
+            // position of key `mrow` of tile t, when key_pos is given: read a tile ahead
+            auto key_pos_of = [&](int t) {
                 const int k = t * KT + mrow, c = line.lo + k;
-                return k < line.entries && c < it.keys.len ? p.key_pos[(int64_t)it.b * p.kps + c] : 0;
+                return k < line.entries && c < it.keys.len ? __ldg(p.key_pos + (int64_t)it.b * p.kps + c) : 0;
             };
-            if (p.key_pos) kp_next = key_pos_of(t0);
-            for (int t = t0; t < t1; ++t, ++j) {
-                const int sb = QT == 1 ? j & 1 : qt;
-                const unsigned sp = QT == 1 ? (j >> 1) & 1 : j & 1;
+            const int step = W == 1 ? 2 : 1, first = W == 1 && (j & 1) != grp ? t0 + 1 : t0;
+            int kp_next = p.key_pos && first < t1 ? key_pos_of(first) : 0;
+            const int j0 = j;
+            for (int t = first; t < t1; t += step) {
+                const int jj = j0 + (t - t0);                      // tiles of the block so far
+                const int sb = W == 0 ? jj & 1 : grp;
+                const unsigned sp = W == 2 ? jj & 1 : (jj >> 1) & 1;
                 const int kp_mine = kp_next;
-                if (p.key_pos && t + 1 < t1) kp_next = key_pos_of(t + 1);
+                if (p.key_pos && t + step < t1) kp_next = key_pos_of(t + step);
                 if (ok) ok = mbar_wait_bounded(&sh.s_full[sb], sp);
                 tc_fence_after();
-                float x[NC];
-#pragma unroll
-                for (int i = 0; i < NC / 32; ++i) tc_ld32(x + i * 32, tl + kS + sb * 128 + cb + i * 32);
-                const int k0 = t * KT, c0 = line.lo + k0;
-                // whether the tile may mask a key: the line's ends, a bad block, the
-                // window's and the document's first tile
+                const uint32_t ts = tl + kS + sb * 128 + cb;       // this thread's scores
+                const int k0 = t * KT, c0 = line.lo + k0, kb = W == 2 ? jj & 1 : W == 1 ? grp : jj & 1;
+                // whether the tile may mask a key: the line's ends, candidates, a bad
+                // block, the window's and the document's first tile
                 const bool special = !it.keys.ok || c0 < it.keys.lo || c0 + KT > it.keys.len || k0 + KT > line.entries ||
-                                     sh.bad[j % kInfo] != 0u || (by_pos && (p.key_pos || c0 < sh.low_max[buf]));
+                                     sh.bad[jj % kInfo] != 0u || (by_pos && (p.key_pos || c0 < sh.low_max[buf]));
                 const bool listed = special || (p.key_pos && p.score.bias);
                 if (listed) {
-                    if (qt == 0) {
+                    if (W != 2 || grp == 0) {
                         const int k = k0 + mrow, c = c0 + mrow;
                         int idx = -1, kp = 0;
                         if (it.keys.ok && k < line.entries) {
-                            if (c >= it.keys.lo && c < end && !((sh.bad[j % kInfo] >> (mrow / p.box)) & 1u)) {
+                            if (c >= it.keys.lo && c < end && !((sh.bad[jj % kInfo] >> (mrow / p.box)) & 1u)) {
                                 idx = c;
                                 kp = c < it.keys.len ? (p.key_pos ? kp_mine : c) : key_position(p, it, c);
                             }
@@ -450,47 +486,107 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
                             idx = it.keys.len + k - line.entries;
                             kp = key_position(p, it, idx);
                         }
-                        sh.kc[j & 1][mrow] = idx;
-                        sh.kp[j & 1][mrow] = kp;
+                        sh.kc[kb][mrow] = idx;
+                        sh.kp[kb][mrow] = kp;
                     }
-                    sync_nt<NT>();
+                    bar_sync(bar, nbar);
                 }
-                tc_wait_ld();
-                float cf = scale2;
+                // the 32 scores of chunk i, from TMEM: scaled to natural units where
+                // they are capped, biased or masked (and put back if they are many)
+                float x[32];
+                float cf = scale * kLog2e;
                 bool hid = false;
-                if (listed) {
-                    cf = kLog2e;
-                    ScoreArgs sc = p.score;
-                    sc.scale = fabsf(sc.scale);
-                    const int *kc = sh.kc[j & 1] + cb, *kp = sh.kp[j & 1] + cb;
+                float mt = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        const int c = kc[i], pos = kp[i];
-                        x[i] = attn_score<false>(x[i], sc, slope, pos_dist(qp, pos));
-                        bool v = c >= 0 && pos >= low;
-                        if (p.mode == 0 && c >= it.keys.len && v) {
-                            const int jj = c - it.keys.len;
-                            v = p.mask ? (p.mask[((int64_t)it.b * p.S + cand) * p.W + (jj >> 5)] >> (jj & 31)) & 1u : jj <= cand;
+                for (int i = 0; i < NCH; ++i) {
+                    tc_ld32(x, ts + i * 32);
+                    tc_wait_ld();
+                    const bool plain = !listed && p.score.cap == 0.0f && !p.score.bias;
+                    if (!plain) {
+                        cf = kLog2e;
+                        if (p.score.cap > 0.0f) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = cap_score(x[e] * scale, p.score.cap, p.score.cap_arg);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] *= scale;
                         }
-                        if (!v) {
-                            x[i] = -INFINITY;
-                            hid = true;
+                        const int *kc = sh.kc[kb] + cb + i * 32, *kp = sh.kp[kb] + cb + i * 32;
+                        if (p.score.bias) {
+                            if (listed) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = fmaf(-slope, (float)pos_dist(qp, kp[e]), x[e]);
+                            } else {
+                                const float d0 = (float)(qp - (c0 + cb + i * 32));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = fmaf(-slope, d0 - (float)e, x[e]);
+                            }
+                        }
+                        if (special) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const int c = kc[e];
+                                bool v = c >= 0 && kp[e] >= low;
+                                if (p.mode == 0 && c >= it.keys.len && v) {
+                                    const int q = c - it.keys.len;
+                                    v = p.mask ? (p.mask[((int64_t)it.b * p.S + cand) * p.W + (q >> 5)] >> (q & 31)) & 1u : q <= cand;
+                                }
+                                if (!v) {
+                                    x[e] = -INFINITY;
+                                    hid = true;
+                                }
+                            }
+                        }
+                        if (NCH > 1) {
+                            uint32_t y[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(x[e]);
+                            tc_st32(ts + i * 32, y);
                         }
                     }
-                } else if (p.score.cap > 0.0f || p.score.bias) {
-                    cf = kLog2e;
-                    const float scale = fabsf(p.score.scale), d0 = (float)(qp - (c0 + cb));
+                    float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]), c = fmaxf(x[4], x[5]), d = fmaxf(x[6], x[7]);
 #pragma unroll
-                    for (int i = 0; i < NC; ++i) {
-                        x[i] *= scale;
-                        if (p.score.cap > 0.0f) x[i] = cap_score(x[i], p.score.cap, p.score.cap_arg);
-                        if (p.score.bias) x[i] = fmaf(-slope, d0 - (float)i, x[i]);
+                    for (int e = 8; e < 32; e += 8) {
+                        a = fmaxf(a, fmaxf(x[e], x[e + 1]));
+                        b = fmaxf(b, fmaxf(x[e + 2], x[e + 3]));
+                        c = fmaxf(c, fmaxf(x[e + 4], x[e + 5]));
+                        d = fmaxf(d, fmaxf(x[e + 6], x[e + 7]));
                     }
+                    mt = fmaxf(mt, fmaxf(fmaxf(a, b), fmaxf(c, d)));
                 }
-                float mt = x[0];
-#pragma unroll
-                for (int i = 1; i < NC; ++i) mt = fmaxf(mt, x[i]);
+                if (NCH > 1) tc_wait_st();
                 mt *= cf;
+                // a masked key's V: zeros for what is not finite
+                unsigned dirty[NCH];
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) dirty[i] = 0u;
+                if (special && bar_or(bar, nbar, hid)) {
+                    // V of this tile: its place in the ring by the order of the copies
+                    const int tt = t - t0;
+                    const int nv = nring + (W == 2 ? 2 * tt + 1 : tt + 1 < nt ? 2 * tt + 2 : 2 * tt + 1);
+                    const int db = W == 1 ? grp : 0;
+                    if (ok) ok = mbar_wait_bounded(&sh.full[nv % NS], (unsigned)((nv / NS) & 1));
+                    if (W != 2 || grp == 0) {
+                        unsigned char *vr = sh.kv[nv % NS] + (mrow >> 3) * (NH * 1024) + (mrow & 7) * 128;
+                        uint32_t found = 0;
+#pragma unroll 4
+                        for (int i = 0; i < NH * 8; ++i) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * 1024 + (i & 7) * 16);
+                            found |= nonfinite2(y.x) | nonfinite2(y.y) | nonfinite2(y.z) | nonfinite2(y.w);
+                        }
+                        if (found) {
+                            for (int i = 0; i < NH * 8; ++i)
+                                *reinterpret_cast<uint4 *>(vr + (i >> 3) * 1024 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        const unsigned b = __ballot_sync(kFull, found != 0u);
+                        if (lane == 0) sh.dirty[db][wq] = b;
+                        fence_async_shared();
+                    }
+                    bar_sync(bar, nbar);
+#pragma unroll
+                    for (int i = 0; i < NCH; ++i) dirty[i] = sh.dirty[db][cb / 32 + i];
+                    bar_sync(bar, nbar);  // dirty may be written again
+                }
                 // a new reference when the maximum has grown past 2^8 of the old one
                 const bool grew = mt > m + 8.0f || (m == -INFINITY && mt > -INFINITY);
                 float corr = 1.0f;
@@ -499,127 +595,127 @@ __global__ void __launch_bounds__(TcCfg<NH, C, QT>::kThreads, 1)
                     m = mt;
                     l *= corr;
                 }
-                const bool rescale = __any_sync(kFull, grew) && t > t0;
-                if (rescale) {
-                    if (ok) ok = mbar_wait_bounded(&sh.pv_done[qt], (unsigned)((j - 1) & 1));
-                    tc_fence_after();
-                }
-                const float ref = m == -INFINITY ? 0.0f : m;
-                const uint32_t pt = tl + (QT == 1 ? kP + sb * 64 : kS + sb * 128) + cb / 2;
-                float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NC; i += 32) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float a = ex2f(fmaf(x[i + e], cf, -ref)), b = ex2f(fmaf(x[i + e + 1], cf, -ref));
-                        s0 += a;
-                        s1 += b;
-                        pk[e / 2] = pack_bf16(a, b);
-                        if (special) {
-                            x[i + e] = a;
-                            x[i + e + 1] = b;
-                        }
+                // (W > 0: the scores came after the product before, so O is still)
+                if (__any_sync(kFull, grew) && t > first) {
+                    if (W == 0) {
+                        if (ok) ok = mbar_wait_bounded(&sh.pv_done[0], (unsigned)((jj - 1) & 1));
+                        tc_fence_after();
                     }
-                    tc_st16(pt + i / 2, pk);
-                }
-                l += s0 + s1;
-                if (rescale) {
+#pragma unroll 1
                     for (int d = 0; d < NH * 64; d += 32) {
                         float o[32];
-                        tc_ld32(o, tl + kO + qt * 128 + d);
-                        tc_wait_ld();
                         uint32_t y[32];
+                        tc_ld32(o, to + d);
+                        tc_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) y[i] = __float_as_uint(o[i] * corr);
-                        tc_st32(tl + kO + qt * 128 + d, y);
+                        tc_st32(to + d, y);
                     }
+                } else if (W == 0 && t > first) {
+                    // every product's end is seen before the next is let go: the
+                    // barrier's phase bit tells only neighbours apart
+                    if (ok) ok = mbar_wait_bounded(&sh.pv_done[0], (unsigned)((jj - 1) & 1));
                 }
-                if (special && sync_nt_or<NT>(hid)) {
-                    // V of this tile: ring place by the order of the copies
-                    const int tt = t - t0;
-                    const int nv = nring + (QT == 2 ? 2 * tt + 1 : tt + 1 < nt ? 2 * tt + 2 : 2 * tt + 1);
-                    if (ok) ok = mbar_wait_bounded(&sh.full[nv % NS], (unsigned)((nv / NS) & 1));
-                    if (qt == 0) {
-                        unsigned char *vr = sh.kv[nv % NS] + mrow * 128;
-                        uint32_t found = 0;
-#pragma unroll 4
-                        for (int i = 0; i < NH * 8; ++i) {
-                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * kHalf + (i & 7) * 16);
-                            found |= nonfinite2(y.x) | nonfinite2(y.y) | nonfinite2(y.z) | nonfinite2(y.w);
-                        }
-                        if (found) {
-                            for (int i = 0; i < NH * 8; ++i)
-                                *reinterpret_cast<uint4 *>(vr + (i >> 3) * kHalf + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        const unsigned b = __ballot_sync(kFull, found != 0u);
-                        if (lane == 0) sh.dirty[wq] = b;
-                        fence_async_shared();
-                    }
-                    sync_nt<NT>();
+                const float ref = m == -INFINITY ? 0.0f : m;
+                const uint32_t pt = tl + kS + sb * 128 + cb / 2;
+                float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < NC; ++i)
-                        poison = poison || (((sh.dirty[(cb + i) / 32] >> ((cb + i) & 31)) & 1u) && x[i] != 0.0f);
-                    sync_nt<NT>();  // dirty may be written again
+                for (int i = 0; i < NCH; ++i) {
+                    if (NCH > 1) {
+                        tc_ld32(x, ts + i * 32);
+                        tc_wait_ld();
+                    }
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float a = ex2f(fmaf(x[e], cf, -ref)), b = ex2f(fmaf(x[e + 1], cf, -ref));
+                        const float c = ex2f(fmaf(x[e + 2], cf, -ref)), d = ex2f(fmaf(x[e + 3], cf, -ref));
+                        s0 += a;
+                        s1 += b;
+                        s2 += c;
+                        s3 += d;
+                        pk[e / 2] = pack_bf16(a, b);
+                        pk[e / 2 + 1] = pack_bf16(c, d);
+                    }
+                    if (dirty[i] != 0u)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            poison = poison || (((dirty[i] >> e) & 1u) && ((pk[e / 2] >> ((e & 1) * 16)) & 0xffffu) != 0u);
+                    tc_st16(pt + i * 16, pk);
                 }
-                // every product's end is seen before the next is let go: the barrier's
-                // phase bit tells only neighbours apart (QT = 2: S came after it)
-                if (QT == 1 && t > t0 && !rescale && ok)
-                    ok = mbar_wait_bounded(&sh.pv_done[qt], (unsigned)((j - 1) & 1));
+                l += (s0 + s1) + (s2 + s3);
+                if (C > 1) {  // nothing of the other copies' keys
+                    uint32_t z[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) z[i] = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (i < cb / 32 || i >= cb / 32 + NCH) tc_st16(tl + kS + sb * 128 + i * 16, z);
+                }
                 tc_wait_st();
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[sb]);
             }
+            j = j0 + nt;
             nring += 2 * nt;
             const AttnItem done = it;
+            const bool any = first < t1;                             // this group had a tile
+            const int last = any ? j0 + ((t1 - 1 - first) / step) * step + (first - t0) : 0;
             u = it.u0 + it.ntiles;
             const bool more = u < uend;
             if (more) {
+                // all tiles' scores have been read (the other group's too)
                 it = attn_next(p, it, items, rtiles, KT);
                 load_item(it, buf ^ 1);
             }
-            if (ok) ok = mbar_wait_bounded(&sh.pv_done[qt], (unsigned)((j - 1) & 1));
+            if (any && ok)
+                ok = mbar_wait_bounded(&sh.pv_done[acc], (unsigned)((W == 1 ? last >> 1 : last) & 1));
             tc_fence_after();
-            auto chunk = [&](int d, float *o) {
-                tc_ld32(o, tl + kO + qt * 128 + d);
-                tc_wait_ld();
-                if (poison)
+            if (W != 1) {
+                auto chunk = [&](int d, float *o) {
+                    tc_ld32(o, to + d);
+                    tc_wait_ld();
+                    if (poison)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = __int_as_float(0x7fffffff);
-            };
-            if (C == 1) {
+                        for (int i = 0; i < 32; ++i) o[i] = __int_as_float(0x7fffffff);
+                };
                 attn_finish_row<T, RT, NT>(p, sh.plan, done, out_row, row, m, l, chunk, &sh.flag);
             } else {
-                sh.m[copy][row] = m;
-                sh.l[copy][row] = l;
+                // join the copies of both groups: 8 blocks of columns, each copy at
+                // another one in each of 8 rounds (the first to come stores)
+                const int g = grp * C + copy;
+                sh.m[g][row] = m;
+                sh.l[g][row] = l;
                 sync_nt<NT>();
                 float mm = -INFINITY, ll = 0.0f;
 #pragma unroll
-                for (int g = 0; g < C; ++g) mm = fmaxf(mm, sh.m[g][row]);
+                for (int i = 0; i < K::kCopies; ++i) mm = fmaxf(mm, sh.m[i][row]);
 #pragma unroll
-                for (int g = 0; g < C; ++g) ll += sh.l[g][row] * rel_weight(sh.m[g][row], mm);
-                if (copy == 0) {
+                for (int i = 0; i < K::kCopies; ++i) ll += sh.l[i][row] * rel_weight(sh.m[i][row], mm);
+                if (g == 0) {
                     sh.tm[row] = mm;
                     sh.tl[row] = ll;
                 }
                 const float f = rel_weight(m, mm);
-                for (int g = 0; g < C; ++g) {
-                    if (copy == g) {
-                        for (int d = 0; d < NH * 64; d += 32) {
-                            float o[32];
-                            chunk(d, o);
+                constexpr int BW = NH * 8, STEP = 8 / K::kCopies;    // columns of a block; blocks between two copies
+#pragma unroll 1
+                for (int s = 0; s < 8; ++s) {
+                    const int blk = (g * STEP + s) & 7;
+                    float o[BW];
+                    if (BW == 16) tc_ld16(o, to + blk * BW);
+                    else tc_ld8(o, to + blk * BW);
+                    tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                float4 *at = reinterpret_cast<float4 *>(&sh.o[row][d + i]);
-                                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (f != 0.0f) v = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
-                                if (g > 0) {
-                                    const float4 b = *at;
-                                    v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
-                                }
-                                *at = v;
-                            }
+                    for (int i = 0; i < BW; i += 4) {
+                        float4 *at = reinterpret_cast<float4 *>(&sh.o[row][blk * BW + i]);
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (f != 0.0f) v = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
+                        if (poison) v.x = v.y = v.z = v.w = __int_as_float(0x7fffffff);
+                        if (s >= STEP) {
+                            const float4 b = *at;
+                            v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
                         }
+                        *at = v;
                     }
                     sync_nt<NT>();
                 }
@@ -656,22 +752,22 @@ EncodeFn encode_fn() {
 
 bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
             const cuuint32_t *box) {
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
     return encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box,
                        ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NH, int C, int QT>
+template <int NH, int C, int W>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {
-    using K = TcCfg<NH, C, QT>;
-    constexpr int smem = (int)sizeof(TcSmem<NH, C, QT>) + 1024;
-    static_assert(smem <= 227 * 1024, "shared memory");
-    static_assert(K::kRows <= kAttnSlotRows * QT, "partial results");
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NH, C, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    using K = TcCfg<NH, C, W>;
+    constexpr int smem = (int)sizeof(TcSmem<NH, C, W>) + 1024;
+    static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
+    static_assert(K::kRows <= kAttnSlotRows * K::kQT, "partial results");
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NH, C, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = sms < kAttnSmsMax ? sms : kAttnSmsMax;
-    attn_tc_kernel<NH, C, QT><<<grid, K::kThreads, smem, s>>>(p, cm, tm);
+    attn_tc_kernel<NH, C, W><<<grid, K::kThreads, smem, s>>>(p, cm, tm);
     return cudaGetLastError();
 }
 
@@ -679,16 +775,17 @@ template <int NH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &
     const int64_t rows = p.mode == 1 ? (int64_t)p.B * p.S * p.G : (int64_t)p.S * p.G;
     if (rows <= 32) return launch<NH, 4, 1>(p, cm, tm, sms, s);
     if (rows <= 64) return launch<NH, 2, 1>(p, cm, tm, sms, s);
-    if (rows <= 128 || p.mode == 0) return launch<NH, 1, 1>(p, cm, tm, sms, s);
+    if (rows <= 128 || p.mode == 0) return launch<NH, 1, 0>(p, cm, tm, sms, s);
     return launch<NH, 1, 2>(p, cm, tm, sms, s);
 }
 
 }  // namespace
 
 // Rows of a page a box takes: the pages must be whole boxes and a tile's 128
-// keys too, 8 rows at least (a swizzle atom).
+// keys too, 8 rows at least (a swizzle atom).  Head sizes that fill the
+// swizzle's 64 columns (others would read past their rows).
 int attn_tc_box(const AttnParams &p) {
-    if (p.D < 64 || p.D > 128 || 2 * p.nb * p.bs > 0x7fffff00LL || (int64_t)p.B * p.layers > 0x3fffffffLL) return 0;
+    if ((p.D != 64 && p.D != 128) || 2 * p.nb * p.bs > 0x7fffff00LL || (int64_t)p.B * p.layers > 0x3fffffffLL) return 0;
     int box = 128;
     while (box >= 8 && p.bs % box != 0) box >>= 1;
     return box >= 8 && encode_fn() ? box : 0;
@@ -696,20 +793,26 @@ int attn_tc_box(const AttnParams &p) {
 
 cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t s) {
     CUtensorMap cm, tm;
-    const cuuint64_t row = (cuuint64_t)p.H * p.D * 2;
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)p.box, 1};
-    {
-        const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)(2 * p.nb * p.bs)};
-        const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, row};
-        if (!encode(&cm, p.kc, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    const cuuint64_t row = (cuuint64_t)p.H * p.D * 2, rows = (cuuint64_t)(2 * p.nb * p.bs);
+    bool ok;
+    if (p.D == 128) {  // [row group][half of the columns][8 rows][64 columns]: a page's rows in one copy
+        const cuuint64_t dims[5] = {64, 8, 2, rows / 8, (cuuint64_t)p.H}, strides[4] = {row, 128, 8 * row, 256};
+        const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)p.box / 8, 1};
+        ok = encode(&cm, p.kc, 5, dims, strides, box);
+    } else {
+        const cuuint64_t dims[3] = {64, (cuuint64_t)p.H, rows}, strides[2] = {128, row};
+        const cuuint32_t box[3] = {64, 1, (cuuint32_t)p.box};
+        ok = encode(&cm, p.kc, 3, dims, strides, box);
     }
     tm = cm;
-    if (p.tk && p.mode == 0) {
+    if (ok && p.tk && p.mode == 0) {
         const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)p.H, (cuuint64_t)p.S, (cuuint64_t)p.B * p.layers * 2};
         const cuuint64_t strides[3] = {(cuuint64_t)p.D * 2, row, row * p.S};
-        if (!encode(&tm, p.temp_base, 4, dims, strides, box)) return cudaErrorInvalidValue;
+        const cuuint32_t box[4] = {64, 1, 8, 1};
+        ok = encode(&tm, p.temp_base, 4, dims, strides, box);
     }
-    return p.D <= 64 ? launch_nh<1>(p, cm, tm, sms, s) : launch_nh<2>(p, cm, tm, sms, s);
+    if (!ok) return cudaErrorInvalidValue;
+    return p.D == 64 ? launch_nh<1>(p, cm, tm, sms, s) : launch_nh<2>(p, cm, tm, sms, s);
 }
 
 }  // namespace specv
