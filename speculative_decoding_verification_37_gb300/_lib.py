@@ -382,78 +382,72 @@ def spec_verify_chain_static(*, target_logits: torch.Tensor, draft_tokens: torch
     _check("spec_verify_chain_static", lib().spec_verify_chain_static(ctypes.byref(a), _stream(stream)))
 
 
-def _device_args(fn: str, device, **tensors) -> None:
-    """Checks (tensor, dtype, shape or None) triples: on `device`, of the
-    dtype, of the shape (-1 = any; a shape asks for contiguous rows)."""
-    for name, (t, dtype, shape) in tensors.items():
-        if t is None:
-            continue
-        if t.dtype != dtype:
-            raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-        if t.device != device:
-            raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
-        if shape is not None:
-            if t.dim() != len(shape) or any(w not in (-1, n) for n, w in zip(t.shape, shape)):
-                raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-            if not t.is_contiguous():
-                raise ValueError(f"{fn}: {name} must be contiguous")
-
-
-def _rows(fn: str, device, name: str, t: Optional[torch.Tensor], dtype, B: int, width: int) -> int:
-    """Row stride of a [B, >= width] tensor whose rows are contiguous."""
+def _checked(fn: str, name: str, t: Optional[torch.Tensor], dtype, shape, device) -> Optional[int]:
+    """The address of a contiguous tensor of this dtype and shape (-1 = any
+    size) on `device`; None for None."""
     if t is None:
-        return 0
-    _device_args(fn, device, **{name: (t, dtype, None)})
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
+    if t.shape != shape and (t.dim() != len(shape) or any(w not in (-1, n) for n, w in zip(t.shape, shape))):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(fn: str, name: str, t: Optional[torch.Tensor], dtype, B: int, width: int, device):
+    """Address and row stride of a [B, >= width] tensor whose rows are contiguous."""
+    if t is None:
+        return None, 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
     if t.dim() != 2 or t.shape[0] != B or t.shape[1] < width or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, expected [{B}, >= {width}] with contiguous rows")
-    return t.stride(0) if B > 1 else t.shape[1]
+    return t.data_ptr(), t.stride(0) if B > 1 else t.shape[1]
 
 
-def _cache_args(fn: str, device, cache: torch.Tensor, block_table: torch.Tensor, committed_len: torch.Tensor,
-                block_size: int):
-    if cache.dim() != 6 or cache.shape[1] != 2 or cache.shape[3] != block_size or not cache.is_contiguous():
-        raise ValueError(f"{fn}: cache must be contiguous [L, 2, num_blocks, {block_size}, H, D], "
-                         f"not {tuple(cache.shape)}")
-    if block_table.dim() != 2:
-        raise ValueError(f"{fn}: block_table must be [B, max_blocks]")
-    B = block_table.shape[0]
-    _device_args(fn, device, cache=(cache, cache.dtype, None), block_table=(block_table, torch.int32, (B, -1)),
-                 committed_len=(committed_len, torch.int32, (B,)))
-    return B
+def _cache_shape(fn: str, cache: torch.Tensor, block_size: int):
+    shape = cache.shape
+    if len(shape) != 6 or shape[1] != 2 or shape[3] != block_size or not cache.is_contiguous():
+        raise ValueError(f"{fn}: cache must be contiguous [L, 2, num_blocks, {block_size}, H, D], not {tuple(shape)}")
+    if not cache.is_cuda:
+        raise ValueError(f"{fn}: cache must be on a CUDA device")
+    return shape
 
 
-def _scored_args(fn: str, q, cache, block_table, committed_len, block_size, layer, pos, key_pos, first_pos,
-                 slopes, flags):
-    """The arguments spec_verify_attention and spec_attention_weights share."""
-    dev = q.device
-    if not q.is_cuda:
-        raise ValueError(f"{fn}: q must be on a CUDA device")
-    B = _cache_args(fn, dev, cache, block_table, committed_len, block_size)
-    L, _, nb, bs, H, D = cache.shape
+def _query_strides(fn: str, q: torch.Tensor, cache: torch.Tensor, B: int):
+    """q's strides over requests, candidates and heads."""
+    D = cache.shape[5]
+    if q.dtype is not cache.dtype:
+        raise TypeError(f"{fn}: q is {q.dtype} and cache {cache.dtype}")
+    if q.device != cache.device:
+        raise ValueError(f"{fn}: q is on {q.device}, cache on {cache.device}")
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or (D > 1 and q.stride(3) != 1):
         raise ValueError(f"{fn}: q must be [{B}, S, Hq, {D}] with contiguous last dimension, not {tuple(q.shape)}")
-    if q.dtype != cache.dtype:
-        raise TypeError(f"{fn}: q is {q.dtype} and cache {cache.dtype}")
-    S, Hq = q.shape[1], q.shape[2]
-    cap = block_table.shape[1] * bs
-    _device_args(fn, dev, pos=(pos, torch.int32, (B, S)), first_pos=(first_pos, torch.int32, (B,)),
-                 slopes=(slopes, torch.float32, (Hq,)), flags=(flags, torch.int32, (B,)))
-    kps = _rows(fn, dev, "key_pos", key_pos, torch.int32, B, cap)
     # strides of dimensions of one element do not matter; the library wants them aligned
-    sb, ss, sh = (q.stride(i) if q.shape[i] > 1 else 0 for i in range(3))
-    return dict(B=B, S=S, Hq=Hq, H=H, D=D, L=L, layer=int(layer), dtype=_dtype_code(q), q=_ptr(q), q_stride_b=sb,
-                q_stride_s=ss, q_stride_h=sh, cache=_ptr(cache), num_blocks=nb, block_size=bs,
-                max_blocks=block_table.shape[1], block_table=_ptr(block_table), committed_len=_ptr(committed_len),
-                pos=_ptr(pos), key_pos=_ptr(key_pos), key_pos_stride=kps, first_pos=_ptr(first_pos),
-                slopes=_ptr(slopes), flags=_ptr(flags))
+    return [st if n > 1 else 0 for st, n in zip(q.stride(), q.shape)][:3]
 
 
 def _launch(fn: str, args, workspace: torch.Tensor, device, stream) -> None:
     """Calls `fn` with `device` current, on the given stream or that device's current one."""
     if workspace.device != device:
         raise ValueError(f"{fn}: the workspace is on {workspace.device}, not {device}")
-    with torch.cuda.device(device):
-        _check(fn, getattr(lib(), fn)(ctypes.byref(args), _ptr(workspace), workspace.numel(), _stream(stream)))
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    call = getattr(lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        code = call(args, workspace.data_ptr(), workspace.numel(), raw)
+    else:
+        with torch.cuda.device(device):
+            code = call(args, workspace.data_ptr(), workspace.numel(), raw)
+    if code != SPEC_OK:
+        raise SpecError(fn, code)
 
 
 def spec_verify_attention(*, q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
@@ -470,19 +464,25 @@ def spec_verify_attention(*, q: torch.Tensor, cache: torch.Tensor, block_table: 
     [B, L, 2, S, H, D], tree_mask int32 [B, S, ceil(S/32)], out [B, S, Hq, D],
     lse f32 [B, S, Hq]."""
     fn = "spec_verify_attention"
-    common = _scored_args(fn, q, cache, block_table, committed_len, block_size, layer, pos, key_pos, first_pos,
-                          slopes, flags)
-    B, S, Hq, H, D, L = (common[k] for k in ("B", "S", "Hq", "H", "D", "L"))
-    need = -(-int(shared_len) // block_size)
-    _device_args(fn, q.device, temp_kv=(temp_kv, q.dtype, (B, L, 2, S, H, D)),
-                 tree_mask=(tree_mask, torch.int32, (B, S, (S + 31) // 32)), out=(out, q.dtype, (B, S, Hq, D)),
-                 lse=(lse, torch.float32, (B, S, Hq)), shared_table=(shared_table, torch.int32, (-1,)))
-    if shared_len > 0 and (shared_table is None or shared_table.numel() < need):
-        raise ValueError(f"{fn}: shared_len {shared_len} needs a shared_table of {need} blocks")
-    a = SpecAttentionArgs(temp_kv=_ptr(temp_kv), tree_mask=_ptr(tree_mask), scale=float(scale),
-                          softcap=float(softcap), window=int(window), shared_len=int(shared_len),
-                          shared_table=_ptr(shared_table), out=_ptr(out), lse=_ptr(lse), **common)
-    _launch(fn, a, workspace, q.device, stream)
+    Ly, _, nb, bs, H, D = _cache_shape(fn, cache, block_size)
+    dev, i32, dtype = cache.device, torch.int32, cache.dtype
+    B, mb = block_table.shape
+    sb, ss, sh = _query_strides(fn, q, cache, B)
+    S, Hq = q.shape[1], q.shape[2]
+    kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
+    if shared_len > 0 and (shared_table is None or shared_table.numel() * bs < shared_len):
+        raise ValueError(f"{fn}: shared_len {shared_len} needs a shared_table of {-(-shared_len // bs)} blocks")
+    a = SpecAttentionArgs(
+        B, S, Hq, H, D, Ly, layer, _dtype_code(q), q.data_ptr(), sb, ss, sh, cache.data_ptr(), nb, bs, mb,
+        _checked(fn, "block_table", block_table, i32, (B, mb), dev),
+        _checked(fn, "committed_len", committed_len, i32, (B,), dev),
+        _checked(fn, "temp_kv", temp_kv, dtype, (B, Ly, 2, S, H, D), dev),
+        _checked(fn, "tree_mask", tree_mask, i32, (B, S, (S + 31) // 32), dev),
+        _checked(fn, "pos", pos, i32, (B, S), dev), kp, kps, _checked(fn, "first_pos", first_pos, i32, (B,), dev),
+        _checked(fn, "slopes", slopes, torch.float32, (Hq,), dev), scale, softcap, window, shared_len,
+        _checked(fn, "shared_table", shared_table, i32, (-1,), dev), _checked(fn, "out", out, dtype, (B, S, Hq, D), dev),
+        _checked(fn, "lse", lse, torch.float32, (B, S, Hq), dev), _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)
 
 
 def spec_attention_weights(*, q: torch.Tensor, lse: torch.Tensor, cache: torch.Tensor,
@@ -497,17 +497,23 @@ def spec_attention_weights(*, q: torch.Tensor, lse: torch.Tensor, cache: torch.T
     call, committed_len after the commit, slots int32 [B, >= S], weight f32
     [B, >= max_blocks*block_size]."""
     fn = "spec_attention_weights"
-    common = _scored_args(fn, q, cache, block_table, committed_len, block_size, layer, pos, key_pos, first_pos,
-                          slopes, flags)
-    B, S, Hq = common["B"], common["S"], common["Hq"]
-    _device_args(fn, q.device, lse=(lse, torch.float32, (B, S, Hq)), n_slots=(n_slots, torch.int32, (B,)))
-    cap = block_table.shape[1] * block_size
-    a = SpecWeightsArgs(lse=_ptr(lse), slots=_ptr(slots),
-                        slots_stride=_rows(fn, q.device, "slots", slots, torch.int32, B, S),
-                        n_slots=_ptr(n_slots), scale=float(scale), softcap=float(softcap), window=int(window),
-                        shared_len=int(shared_len), weight=_ptr(weight),
-                        weight_stride=_rows(fn, q.device, "weight", weight, torch.float32, B, cap), **common)
-    _launch(fn, a, workspace, q.device, stream)
+    Ly, _, nb, bs, H, D = _cache_shape(fn, cache, block_size)
+    dev, i32 = cache.device, torch.int32
+    B, mb = block_table.shape
+    sb, ss, sh = _query_strides(fn, q, cache, B)
+    S, Hq = q.shape[1], q.shape[2]
+    kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
+    sl, sls = _rows(fn, "slots", slots, i32, B, S, dev)
+    w, ws = _rows(fn, "weight", weight, torch.float32, B, mb * bs, dev)
+    a = SpecWeightsArgs(
+        B, S, Hq, H, D, Ly, layer, _dtype_code(q), q.data_ptr(), sb, ss, sh,
+        _checked(fn, "lse", lse, torch.float32, (B, S, Hq), dev), cache.data_ptr(), nb, bs, mb,
+        _checked(fn, "block_table", block_table, i32, (B, mb), dev),
+        _checked(fn, "committed_len", committed_len, i32, (B,), dev), sl, sls,
+        _checked(fn, "n_slots", n_slots, i32, (B,), dev), _checked(fn, "pos", pos, i32, (B, S), dev), kp, kps,
+        _checked(fn, "first_pos", first_pos, i32, (B,), dev), _checked(fn, "slopes", slopes, torch.float32, (Hq,), dev),
+        scale, softcap, window, shared_len, w, ws, _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)
 
 
 def spec_evict_kv(*, cache: torch.Tensor, block_table: torch.Tensor, committed_len: torch.Tensor,
@@ -518,19 +524,14 @@ def spec_evict_kv(*, cache: torch.Tensor, block_table: torch.Tensor, committed_l
     """Marshals one spec_evict_kv call: cache [L, 2, num_blocks, block_size, H, D],
     weight f32 and key_pos int32 [B, >= max_blocks*block_size], all in/out."""
     fn = "spec_evict_kv"
-    if not cache.is_cuda:
-        raise ValueError(f"{fn}: cache must be on a CUDA device")
-    B = _cache_args(fn, cache.device, cache, block_table, committed_len, block_size)
-    L, _, nb, bs, H, D = cache.shape
-    cap = block_table.shape[1] * bs
-    _device_args(fn, cache.device, blocks_in_use=(blocks_in_use, torch.int32, (B,)),
-                 flags=(flags, torch.int32, (B,)))
-    a = SpecEvictArgs(B=B, L=L, H=H, D=D, block_size=bs, elem_bytes=cache.element_size(), cache=_ptr(cache),
-                      num_blocks=nb, block_table=_ptr(block_table), max_blocks=block_table.shape[1],
-                      budget=int(budget), sink=int(sink), recent=int(recent), committed_len=_ptr(committed_len),
-                      weight=_ptr(weight),
-                      weight_stride=_rows(fn, cache.device, "weight", weight, torch.float32, B, cap),
-                      key_pos=_ptr(key_pos),
-                      key_pos_stride=_rows(fn, cache.device, "key_pos", key_pos, torch.int32, B, cap),
-                      blocks_in_use=_ptr(blocks_in_use), flags=_ptr(flags))
-    _launch(fn, a, workspace, cache.device, stream)
+    Ly, _, nb, bs, H, D = _cache_shape(fn, cache, block_size)
+    dev, i32 = cache.device, torch.int32
+    B, mb = block_table.shape
+    w, ws = _rows(fn, "weight", weight, torch.float32, B, mb * bs, dev)
+    kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
+    a = SpecEvictArgs(
+        B, Ly, H, D, bs, cache.element_size(), cache.data_ptr(), nb,
+        _checked(fn, "block_table", block_table, i32, (B, mb), dev), mb, budget, sink, recent,
+        _checked(fn, "committed_len", committed_len, i32, (B,), dev), w, ws, kp, kps,
+        _checked(fn, "blocks_in_use", blocks_in_use, i32, (B,), dev), _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)

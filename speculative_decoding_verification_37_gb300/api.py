@@ -17,7 +17,7 @@ def workspace(kind: int, B: int, n: int, V: int, device) -> torch.Tensor:
     some kinds depends on V).  Every call leaves it zeroed, so it is reused
     without clearing; calls that share it must be ordered on one stream.
     The cache lives as long as the process; clear_workspaces() frees it."""
-    dev = torch.device(device)
+    dev = device if isinstance(device, torch.device) else torch.device(device)
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
     key = (dev.type, dev.index, kind, B, n, V)

@@ -254,12 +254,12 @@ template <int RT> struct AttnRows {
     int cand[RT];      // candidate index
 };
 
-// Row r of the item (mode 1: over all requests).
+// Row r of the item (mode 1: over all requests), by NT threads.
 template <int RT, int NT>
-__device__ __forceinline__ void attn_rows(const AttnParams &p, const AttnItem &it, AttnRows<RT> &w) {
+__device__ __forceinline__ void attn_rows(const AttnParams &p, const AttnItem &it, AttnRows<RT> &w, int tid) {
     const int per = p.S * p.G;
     const int64_t nrows = p.mode == 1 ? (int64_t)p.B * per : per;
-    for (int i = threadIdx.x; i < RT; i += NT) {
+    for (int i = tid; i < RT; i += NT) {
         const int64_t r = (int64_t)it.rt * RT + i;
         if (r >= nrows) {
             w.out[i] = w.q[i] = -1;
@@ -381,33 +381,44 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
     sync_nt<NT>();
     if (!*last_flag) return;
     __threadfence();
-    for (int i = tid; i < RT * d4; i += NT) {
-        const int r = i / d4, d = (i - r * d4) * 4;
+    // a warp per row: each lane a few blocks' (m, l), then the rows, many in flight
+    const int lane = tid & 31, n = c1 - c0 + 1;
+    auto part = [&](int c) { return p.part + ((int64_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * slot_floats; };
+    for (int r = tid >> 5; r < RT; r += NT / 32) {
         if (w.out[r] < 0) continue;
-        float m = -INFINITY, l = 0.0f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int U = 8;  // blocks' results in flight
-        for (int cb = c0; cb <= c1; cb += U) {
-            float mc[U], lc[U];
-            float4 oc[U];
+        constexpr int U = 8;
+        float m = -INFINITY;
+        for (int c = lane; c < n; c += 32) m = fmaxf(m, __ldcg(part(c) + RT * p.D + r));
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                const int c = min(cb + i, c1);
-                const float *s = p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats;
-                mc[i] = __ldcg(s + RT * p.D + r);
-                lc[i] = __ldcg(s + RT * p.D + RT + r);
-                oc[i] = __ldcg(reinterpret_cast<const float4 *>(s + r * p.D + d));
-            }
+        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+        for (int d = lane * 4; d < p.D + (128 - p.D % 128) % 128; d += 128) {  // all lanes stay
+            float l = 0.0f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int cb = 0; cb < n; cb += 32) {
+                float k = 0.0f, lk = 0.0f;
+                if (cb + lane < n) {
+                    k = rel_weight(__ldcg(part(cb + lane) + RT * p.D + r), m);
+                    lk = __ldcg(part(cb + lane) + RT * p.D + RT + r) * k;
+                    if (k == 0.0f) lk = 0.0f;  // that block saw no key of the row
+                }
+                const int e = min(32, n - cb);
+                for (int c = 0; c < e; c += U) {
+                    float4 x[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                if (cb + i > c1) break;
-                const float mn = fmaxf(m, mc[i]), a = rel_weight(m, mn), k = rel_weight(mc[i], mn);
-                l = l * a + lc[i] * k;
-                o = make_float4(o.x * a + oc[i].x * k, o.y * a + oc[i].y * k, o.z * a + oc[i].z * k, o.w * a + oc[i].w * k);
-                m = mn;
+                    for (int q = 0; q < U; ++q)
+                        x[q] = c + q < e && d < p.D ? __ldcg(reinterpret_cast<const float4 *>(part(cb + c + q) + (int64_t)r * p.D + d))
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < U; ++q) {
+                        const float kq = __shfl_sync(kFull, k, (c + q) & 31);
+                        l += __shfl_sync(kFull, c + q < e ? lk : 0.0f, (c + q) & 31);
+                        if (c + q < e && kq != 0.0f)
+                            o = make_float4(fmaf(x[q].x, kq, o.x), fmaf(x[q].y, kq, o.y), fmaf(x[q].z, kq, o.z), fmaf(x[q].w, kq, o.w));
+                    }
+                }
             }
+            if (d < p.D) attn_write<T>(p, it.keys.ok, w.out[r], d, m, l, o);
         }
-        attn_write<T>(p, it.keys.ok, w.out[r], d, m, l, o);
     }
     if (tid == 0) p.counters[c0] = 0u;
     sync_nt<NT>();

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * (WR * WK * NG + 4), 1) attn_mma_kernel(At
     int64_t u = u0;
     AttnItem it = attn_find<NT>(p, sh.plan, u0, p.H * rtiles, rtiles, KT);
     while (true) {
-        attn_rows<RT, NT>(p, it, sh.rows);
+        attn_rows<RT, NT>(p, it, sh.rows, tid);
         sync_nt<NT>();
         for (int i = tid; i < RT * (DP / 8); i += NT) {
             const int r = i / (DP / 8), d = (i - r * (DP / 8)) * 8;

@@ -45,7 +45,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_ke
     if (u >= uend) return;
     AttnItem it = attn_find<NT>(p, sh.plan, u, p.H * rtiles, rtiles, KT);
     while (true) {
-        attn_rows<RT, NT>(p, it, sh.rows);
+        attn_rows<RT, NT>(p, it, sh.rows, tid);
         __syncthreads();
         for (int i = tid; i < RT * DP; i += NT) {
             const int r = i / DP, d = i - r * DP;

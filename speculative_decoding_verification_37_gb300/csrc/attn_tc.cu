@@ -152,27 +152,28 @@ template <int NH, int C, int W> struct TcCfg {
     static constexpr int kQT = W == 2 ? 2 : 1;       // query tiles
     static constexpr int kRows = 128 * kQT / C;      // queries of an item
     static constexpr int kNT = W == 0 ? 128 : 256;   // softmax threads
-    static constexpr int kThreads = kNT + 64;
+    static constexpr int kThreads = kNT + (W == 2 ? 64 : 96);
+    static constexpr int kQB = W == 2 ? 1 : 2;       // buffers for the queries
     static constexpr int kCopies = W == 1 ? 2 * C : C;
     static constexpr uint32_t kTile = NH * kHalf;    // bytes of a K or V tile
     // the ring takes what the queries and the join leave of 227 KB
-    static constexpr int kRing = NH == 1 ? 8 : W == 2 || C == 2 ? 4 : 5;
+    static constexpr int kRing = NH == 1 ? 8 : C == 2 ? 3 : 4;
 };
 
 template <int NH, int C, int W> struct TcSmem {
     using K = TcCfg<NH, C, W>;
     alignas(1024) unsigned char kv[K::kRing][K::kTile];
-    alignas(1024) unsigned char q[K::kQT][K::kTile];
+    alignas(1024) unsigned char q[K::kQB][K::kQT][K::kTile];
     alignas(16) float o[W == 1 ? K::kRows : 1][NH * 64 + 4];
     float m[K::kCopies][K::kRows], l[K::kCopies][K::kRows], tm[K::kRows], tl[K::kRows];
     AttnRows<K::kRows> rows[2];
-    alignas(16) int kc[2][KT];      // a listed tile's keys: index (-1: masked for all),
-    alignas(16) int kp[2][KT];      // position
+    alignas(16) int kp[2][KT];      // a listed tile's keys: position,
+    unsigned valid[2][4];           // whether there is such a key
     unsigned bad[kInfo];            // boxes of a tile with a bad block
     unsigned dirty[2][4];
     int low_max[2];                 // the largest first visible position of an item's rows
     AttnPlan plan;
-    alignas(8) unsigned long long full[K::kRing], empty[K::kRing], s_full[2], p_full[2], pv_done[2], q_full;
+    alignas(8) unsigned long long full[K::kRing], empty[K::kRing], s_full[2], p_full[2], pv_done[2], q_full[2], q_free[2];
     uint32_t tmem;
     int flag;
 };
@@ -214,7 +215,10 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             mbar_init(&sh.p_full[i], 128);
             mbar_init(&sh.pv_done[i], 1);
         }
-        mbar_init(&sh.q_full, NT);
+        for (int i = 0; i < K::kQB; ++i) {
+            mbar_init(&sh.q_full[i], W == 2 ? NT : 32);
+            mbar_init(&sh.q_free[i], NT);
+        }
         fence_barrier_init();
     }
     if (warp < NT / 32) attn_plan<NT>(p, sh.plan, items, KT);
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             auto scores = [&](int d, int qt, int slot) {
                 for (int k = 0; k < ksteps; ++k)
                     tc_mma_ss(tmem + kS + d * 128,
-                              tc_desc(smem_u32(sh.q[qt]) + (uint32_t)(k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
+                              tc_desc(smem_u32(sh.q[item % K::kQB][qt]) + (uint32_t)(k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
                               tc_desc(smem_u32(sh.kv[slot]) + (uint32_t)(k >> 2) * 1024 + (k & 3) * 32, 16, NH * 1024), id_s,
                               k > 0);
             };
@@ -344,7 +348,8 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             };
             while (true) {
                 const int nt = (int)(min(uend, it.u0 + it.ntiles) - u);
-                if (ok) ok = mbar_wait_bounded(&sh.q_full, (unsigned)(item & 1));
+                if (ok) ok = mbar_wait_bounded(&sh.q_full[item % K::kQB], (unsigned)((item / K::kQB) & 1));
+                tc_fence_after();
                 if (W != 2) {
                     auto next_scores = [&](int d) {
                         wait_full(n);
@@ -398,6 +403,53 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             }
         }
         __syncwarp();
+    } else if (W != 2 && warp == NT / 32 + 2) {
+        // ---------------- queries ----------------
+        // The next item's rows and queries, while this one's keys go by.  (W = 2
+        // has no room for a second buffer: its softmax threads load them.)
+        const bool by_pos = p.window > 0 || p.first != nullptr;
+        const uint32_t neg = p.score.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale: the queries are negated
+        for (int item = 0;; ++item) {
+            const int qb = item % K::kQB;
+            // the buffer's last item, and its rows, are done with
+            if (item >= K::kQB && ok) ok = mbar_wait_bounded(&sh.q_free[qb], (unsigned)((item / K::kQB - 1) & 1));
+            AttnRows<RT> &w = sh.rows[item & 1];
+            attn_rows<RT, 32>(p, it, w, lane);
+            __syncwarp();
+            int low = (int)0x80000000;
+            if (by_pos)
+                for (int i = lane; i < RT; i += 32)
+                    if (w.out[i] >= 0) low = max(low, max(w.first[i], p.window > 0 ? w.qp[i] - p.window + 1 : (int)0x80000000));
+            low = __reduce_max_sync(kFull, low);
+            if (lane == 0) sh.low_max[item & 1] = low;
+            constexpr int CH = NH * 8, U = 8;  // 16-byte chunks of a row; loads in flight
+            for (int i0 = lane; i0 < RT * CH; i0 += 32 * U) {
+                uint4 v[U];
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    const int i = i0 + q * 32, r = i / CH, d = (i - r * CH) * 8;
+                    v[q] = make_uint4(0, 0, 0, 0);
+                    if (i < RT * CH && w.q[r] >= 0 && d < p.D) v[q] = ld_nc16(static_cast<const T *>(p.q) + w.q[r] + d);
+                }
+#pragma unroll
+                for (int q = 0; q < U; ++q) {
+                    const int i = i0 + q * 32, r = i / CH, c = i - r * CH;
+                    if (i >= RT * CH) continue;
+                    v[q].x ^= neg, v[q].y ^= neg, v[q].z ^= neg, v[q].w ^= neg;
+#pragma unroll
+                    for (int k = 0; k < C; ++k) {
+                        const int mr = (r + k * RT) & 127;
+                        *reinterpret_cast<uint4 *>(sh.q[qb][r >> 7] + (c >> 3) * kHalf + mr * 128 + (((c & 7) ^ (mr & 7)) << 4)) = v[q];
+                    }
+                }
+            }
+            fence_async_shared();
+            mbar_arrive(&sh.q_full[qb]);
+            u = it.u0 + it.ntiles;
+            if (u >= uend) break;
+            it = attn_next(p, it, items, rtiles, KT);
+        }
+        __syncwarp();
     } else {
         // ---------------- softmax ----------------
         const int wq = warp & 3, grp = warp >> 2;                 // TMEM lanes 32 wq .. + 31
@@ -411,34 +463,32 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
         const uint32_t to = tl + kO + acc * 128;
         const bool by_pos = p.window > 0 || p.first != nullptr;
         const float scale = fabsf(p.score.scale);
-        int buf = 0, j = 0, nring = 0;
-        // the item's rows and queries; the MMA has read the ones before
-        auto load_item = [&](const AttnItem &x, int bufn) {
+        int item = 0, j = 0, nring = 0;
+        auto load_item = [&](const AttnItem &x, int bufn) {  // W = 2
             AttnRows<RT> &w = sh.rows[bufn];
             if (tid == 0) sh.low_max[bufn] = (int)0x80000000;
-            attn_rows<RT, NT>(p, x, w);
+            attn_rows<RT, NT>(p, x, w, tid);
             sync_nt<NT>();
-            if (by_pos)
-                for (int i = tid; i < RT; i += NT)
-                    if (w.out[i] >= 0)
-                        atomicMax(&sh.low_max[bufn], max(w.first[i], p.window > 0 ? w.qp[i] - p.window + 1 : (int)0x80000000));
-            // a negative scale: the queries are negated instead
+            if (by_pos && w.out[tid] >= 0)
+                atomicMax(&sh.low_max[bufn], max(w.first[tid], p.window > 0 ? w.qp[tid] - p.window + 1 : (int)0x80000000));
             const uint32_t neg = p.score.scale < 0.0f ? 0x80008000u : 0u;
-            for (int i = tid; i < K::kQT * 128 * NH * 8; i += NT) {
-                const int r = i / (NH * 8), c = i - r * (NH * 8), d = c * 8;  // row, 16-byte chunk
-                const int64_t src = w.q[W == 2 ? r : r % RT];
+            constexpr int CH = NH * 8;
+#pragma unroll
+            for (int q = 0; q < CH; ++q) {
+                const int i = tid + q * NT, r = i / CH, c = i - r * CH, d = c * 8;
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (src >= 0 && d < p.D) v = ld_nc16(static_cast<const T *>(p.q) + src + d);
+                if (w.q[r] >= 0 && d < p.D) v = ld_nc16(static_cast<const T *>(p.q) + w.q[r] + d);
                 v.x ^= neg, v.y ^= neg, v.z ^= neg, v.w ^= neg;
                 const int mr = r & 127;
-                *reinterpret_cast<uint4 *>(sh.q[r >> 7] + (c >> 3) * kHalf + mr * 128 + (((c & 7) ^ (mr & 7)) << 4)) = v;
+                *reinterpret_cast<uint4 *>(sh.q[0][r >> 7] + (c >> 3) * kHalf + mr * 128 + (((c & 7) ^ (mr & 7)) << 4)) = v;
             }
             fence_async_shared();
-            mbar_arrive(&sh.q_full);
-            sync_nt<NT>();  // low_max
+            mbar_arrive(&sh.q_full[0]);
         };
-        load_item(it, buf);
+        if constexpr (W == 2) load_item(it, 0);
         while (true) {
+            const int buf = item & 1, qb = item % K::kQB;
+            if (ok) ok = mbar_wait_bounded(&sh.q_full[qb], (unsigned)((item / K::kQB) & 1));
             const AttnRows<RT> &w = sh.rows[buf];
             const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), nt = t1 - t0;
             const int64_t out_row = w.out[row];
@@ -473,20 +523,24 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 const bool special = !it.keys.ok || c0 < it.keys.lo || c0 + KT > it.keys.len || k0 + KT > line.entries ||
                                      sh.bad[jj % kInfo] != 0u || (by_pos && (p.key_pos || c0 < sh.low_max[buf]));
                 const bool listed = special || (p.key_pos && p.score.bias);
+                // the tile's first candidate, as an index into the tile
+                const int q0 = (temp ? line.entries - k0 : it.keys.len - c0);
                 if (listed) {
                     if (W != 2 || grp == 0) {
                         const int k = k0 + mrow, c = c0 + mrow;
-                        int idx = -1, kp = 0;
+                        bool in = false;
+                        int kp = 0;
                         if (it.keys.ok && k < line.entries) {
                             if (c >= it.keys.lo && c < end && !((sh.bad[jj % kInfo] >> (mrow / p.box)) & 1u)) {
-                                idx = c;
+                                in = true;
                                 kp = c < it.keys.len ? (p.key_pos ? kp_mine : c) : key_position(p, it, c);
                             }
                         } else if (it.keys.ok && temp && k - line.entries < p.S) {
-                            idx = it.keys.len + k - line.entries;
-                            kp = key_position(p, it, idx);
+                            in = true;
+                            kp = key_position(p, it, it.keys.len + k - line.entries);
                         }
-                        sh.kc[kb][mrow] = idx;
+                        const unsigned b = __ballot_sync(kFull, in);
+                        if (lane == 0) sh.valid[kb][wq] = b;
                         sh.kp[kb][mrow] = kp;
                     }
                     bar_sync(bar, nbar);
@@ -511,7 +565,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
 #pragma unroll
                             for (int e = 0; e < 32; ++e) x[e] *= scale;
                         }
-                        const int *kc = sh.kc[kb] + cb + i * 32, *kp = sh.kp[kb] + cb + i * 32;
+                        const int *kp = sh.kp[kb] + cb + i * 32;
                         if (p.score.bias) {
                             if (listed) {
 #pragma unroll
@@ -523,19 +577,32 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                             }
                         }
                         if (special) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int c = kc[e];
-                                bool v = c >= 0 && kp[e] >= low;
-                                if (p.mode == 0 && c >= it.keys.len && v) {
-                                    const int q = c - it.keys.len;
-                                    v = p.mask ? (p.mask[((int64_t)it.b * p.S + cand) * p.W + (q >> 5)] >> (q & 31)) & 1u : q <= cand;
+                            // bit e: key e of the chunk is seen by this row
+                            unsigned seen = sh.valid[kb][cb / 32 + i];
+                            const int q = cb + i * 32 - q0;   // the chunk's first key as a candidate
+                            if (p.mode == 0 && q > -32) {
+                                unsigned mine = 0u;           // candidates q .. q + 31
+                                if (p.mask) {
+                                    const uint32_t *mw = p.mask + ((int64_t)it.b * p.S + cand) * p.W;
+                                    const int w0 = q >> 5;    // (floor)
+                                    const uint32_t a = w0 >= 0 && w0 < p.W ? mw[w0] : 0u, b = w0 + 1 < p.W ? mw[w0 + 1] : 0u;
+                                    mine = __funnelshift_r(a, b, q & 31);
+                                } else if (cand >= q) {
+                                    mine = cand - q >= 31 ? kFull : (2u << (cand - q)) - 1u;
                                 }
-                                if (!v) {
-                                    x[e] = -INFINITY;
-                                    hid = true;
-                                }
+                                // keys before the first candidate are entries
+                                if (q < 0) mine |= (1u << -q) - 1u;
+                                seen &= mine;
                             }
+                            if (by_pos) {
+                                unsigned near = 0u;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) near |= (unsigned)(kp[e] >= low) << e;
+                                seen &= near;
+                            }
+                            hid = hid || seen != kFull;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : -INFINITY;
                         }
                         if (NCH > 1) {
                             uint32_t y[32];
@@ -664,9 +731,8 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             u = it.u0 + it.ntiles;
             const bool more = u < uend;
             if (more) {
-                // all tiles' scores have been read (the other group's too)
                 it = attn_next(p, it, items, rtiles, KT);
-                load_item(it, buf ^ 1);
+                if constexpr (W == 2) load_item(it, buf ^ 1);  // (its barrier: all scores have been read)
             }
             if (any && ok)
                 ok = mbar_wait_bounded(&sh.pv_done[acc], (unsigned)((W == 1 ? last >> 1 : last) & 1));
@@ -722,8 +788,9 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 attn_finish<T, RT, NT>(p, sh.plan, done, w, &sh.o[0][0], NH * 64 + 4, sh.tm, sh.tl, &sh.flag);
             }
             tc_fence_before();
+            if (W != 2) mbar_arrive(&sh.q_free[qb]);
             if (!more) break;
-            buf ^= 1;
+            ++item;
         }
     }
     if (!ok && lane == 0) atomicOr(p.status, SPEC_FLAG_TIMEOUT);

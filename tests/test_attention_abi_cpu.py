@@ -146,15 +146,29 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
         api.evict_kv(cache, table, lens, torch.zeros((1, 32)), torch.zeros((1, 32), dtype=torch.int32), block_size=16,
                      budget=4)
     # the checks of shape and type themselves
-    with pytest.raises(ValueError, match="cache must be"):
-        L._cache_args("f", cache.device, cache, table, lens, 8)
+    cpu, i32 = cache.device, torch.int32
+    with pytest.raises(ValueError, match="cache must be contiguous"):
+        L._cache_shape("f", cache, 8)
+    with pytest.raises(ValueError, match="CUDA device"):
+        L._cache_shape("f", cache, 16)
     with pytest.raises(TypeError, match="block_table must be"):
-        L._cache_args("f", cache.device, cache, table.long(), lens, 16)
+        L._checked("f", "block_table", table.long(), i32, (1, 2), cpu)
     with pytest.raises(ValueError, match="committed_len has shape"):
-        L._cache_args("f", cache.device, cache, table, torch.zeros(2, dtype=torch.int32), 16)
-    with pytest.raises(ValueError, match="contiguous rows"):
-        L._rows("f", cache.device, "weight", torch.zeros((1, 31)), torch.float32, 1, 32)
-    with pytest.raises(ValueError, match="contiguous rows"):
-        L._rows("f", cache.device, "weight", torch.zeros((32, 2)).T, torch.float32, 2, 32)
+        L._checked("f", "committed_len", torch.zeros(2, dtype=i32), i32, (1,), cpu)
     with pytest.raises(ValueError, match="must be contiguous"):
-        L._device_args("f", cache.device, pos=(torch.zeros((3, 2), dtype=torch.int32).T, torch.int32, (2, 3)))
+        L._checked("f", "pos", torch.zeros((3, 2), dtype=i32).T, i32, (2, 3), cpu)
+    with pytest.raises(ValueError, match="is on cpu"):
+        L._checked("f", "pos", torch.zeros((2, 3), dtype=i32), i32, (2, 3), torch.device("meta"))
+    assert L._checked("f", "pos", None, i32, (2, 3), cpu) is None
+    assert L._checked("f", "t", table, i32, (-1, 2), cpu) == table.data_ptr()
+    with pytest.raises(ValueError, match="contiguous rows"):
+        L._rows("f", "weight", torch.zeros((1, 31)), torch.float32, 1, 32, cpu)
+    with pytest.raises(ValueError, match="contiguous rows"):
+        L._rows("f", "weight", torch.zeros((32, 2)).T, torch.float32, 2, 32, cpu)
+    wide = torch.zeros((2, 40))
+    assert L._rows("f", "weight", wide[:, 3:36], torch.float32, 2, 32, cpu) == (wide.data_ptr() + 12, 40)
+    with pytest.raises(TypeError, match="q is"):
+        L._query_strides("f", q.float(), cache, 1)
+    with pytest.raises(ValueError, match="contiguous last dimension"):
+        L._query_strides("f", q.transpose(2, 3), cache, 1)
+    assert L._query_strides("f", q, cache, 1) == [0, 256, 64]
