@@ -177,7 +177,7 @@ extern "C" int spec_attention_weights(const SpecWeightsArgs *a, void *workspace,
     w.key_pos_out = a->key_pos;
     w.weight = a->weight;
     w.wstride = a->weight_stride;
-    return report_cuda_error(launch_weights_simt(w, a->dtype, device_sms(), static_cast<cudaStream_t>(stream)));
+    return report_cuda_error(launch_weights(w, a->dtype, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int spec_evict_kv(const SpecEvictArgs *a, void *workspace, size_t ws_bytes, void *stream) {

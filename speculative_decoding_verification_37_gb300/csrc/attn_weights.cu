@@ -13,6 +13,13 @@ namespace {
 
 constexpr int KT = 64, NT = 128, RQ = 16;  // entries per tile, queries staged at a time
 
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
 template <typename T, int DP> struct WSmem {
     float k[KT][DP + 4];
     float q[RQ][DP];
@@ -140,6 +147,204 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
     }
 }
 
+// bf16 version, on the warp tensor instructions; bound by HBM.
+//
+// A warp owns 16 entries of a tile for all cached heads: the entries' K rows are
+// the rows (M = 16) of its products, the queries the columns (N = 8).  The order
+// in which the products run over the head's columns is free as long as both
+// operands share it, so a lane's operand registers are four neighbouring pairs,
+// one 16-byte load of its row (and of the query's): K goes from memory straight
+// to registers, a head ahead of the arithmetic.  The queries of a request (all
+// heads) lie in shared memory.  A lane ends up with two entries and two queries
+// of each product, so an entry's sum is local but for three neighbours.
+constexpr int WM = 8, WKT = 16 * WM, WNT = 32 * WM;  // warps, entries of a tile, threads
+constexpr int kQueryBytes = 80 * 1024;               // shared memory for queries
+
+template <int DP> struct WRow {
+    static constexpr int kPitch = DP * 2 + 16;
+};
+
+template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weights_mma_kernel(WeightsParams wp, int per_pass) {
+    using T = __nv_bfloat16;
+    constexpr int PITCH = WRow<DP>::kPitch, NB = DP / 32;
+    extern __shared__ __align__(16) unsigned char raw[];
+    const AttnParams &p = wp.a;
+    // [queries: head, row][pitch], then per query lse (log2 units), slope,
+    // position, own entry
+    const int rows_max = (per_pass * p.G + 7) / 8 * 8, nq = p.H * rows_max;
+    unsigned char *sq = raw;
+    float *s_lse = reinterpret_cast<float *>(raw + (size_t)nq * PITCH), *s_slope = s_lse + nq;
+    int *s_qp = reinterpret_cast<int *>(s_slope + nq), *s_own = s_qp + nq;
+    __shared__ AttnPlan plan;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+    attn_plan<WNT>(p, plan, 1, WKT);
+    int64_t u = (int64_t)blockIdx.x * plan.share;
+    const int64_t uend = min(plan.total, u + plan.share);
+    if (u >= uend) return;
+    AttnItem it = attn_find<WNT>(p, plan, u, 1, 1, WKT);
+    while (true) {
+        const int b = it.b, n = it.keys.ok ? p.n_slots[b] : 0;
+        const int *slots = p.slots ? p.slots + (int64_t)b * p.slots_stride : nullptr;
+        bool bad = !it.keys.ok;
+        for (int j = tid; slots && j < n; j += WNT) bad = bad || slots[j] < 0 || slots[j] >= p.S;
+        const bool skip = __syncthreads_or(bad);
+        if (skip && u == it.u0 && tid == 0) attn_flag(p, b);
+        const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
+        const int first = p.first ? p.first[b] : (int)0x80000000;
+        const int cand0 = it.keys.len - n;  // the candidates' first entry
+        const int *table = p.table + (int64_t)b * p.max_blocks;
+        for (int j0 = 0; j0 < n && !skip && it.keys.lo < it.keys.hi; j0 += per_pass) {
+            const int nj = min(per_pass, n - j0), rows = nj * p.G, rp = (rows + 7) / 8 * 8;
+            __syncthreads();
+            for (int i = tid; i < p.H * rp; i += WNT) {
+                const int h = i / rp, r = i - h * rp, j = j0 + r / p.G, hq = h * p.G + r % p.G;
+                int own = -1, qp = 0;
+                float lse = 0.0f, slope = 0.0f;
+                if (r < rows) {
+                    const int s = slots ? slots[j] : j;
+                    lse = wp.lse_in[((int64_t)b * p.S + s) * p.Hq + hq];
+                    own = lse == -INFINITY ? -1 : cand0 + j;
+                    qp = p.pos ? p.pos[(int64_t)b * p.S + s] : cand0 + j;
+                    slope = p.slopes ? p.slopes[hq] : 0.0f;
+                }
+                s_lse[i] = lse * kLog2e;
+                s_own[i] = own;
+                s_qp[i] = qp;
+                s_slope[i] = slope;
+            }
+            for (int i = tid; i < p.H * rp * (DP / 8); i += WNT) {
+                const int row = i / (DP / 8), d = (i - row * (DP / 8)) * 8, h = row / rp, r = row - h * rp;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (r < rows && d < p.D) {
+                    const int j = j0 + r / p.G, s = slots ? slots[j] : j;
+                    x = ld_nc16(static_cast<const T *>(p.q) + b * p.qsb + s * p.qss + (h * p.G + r % p.G) * p.qsh + d);
+                }
+                *reinterpret_cast<uint4 *>(sq + (size_t)row * PITCH + d * 2) = x;
+            }
+            __syncthreads();
+            // this lane's entries: rows g and g + 8 of the warp's 16
+            int64_t off[2], off_next[2];
+            auto look_up = [&](int t, int64_t (&o)[2]) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = it.keys.lo + t * WKT + warp * 16 + e * 8 + g;
+                    o[e] = -1;
+                    if (c < it.keys.hi) {
+                        o[e] = entry_offset(p, table, c, 0);
+                        if (o[e] < 0) attn_flag(p, b);
+                    }
+                }
+            };
+            uint4 k[2][NB][2];  // [buffer][32 columns][entry]
+            auto load = [&](uint4 (&x)[NB][2], const int64_t (&o)[2], int h) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = i * 32 + q4 * 8;
+                        x[i][e] = make_uint4(0, 0, 0, 0);
+                        if (o[e] >= 0 && d < p.D) x[i][e] = ld_nc16(static_cast<const T *>(p.kc) + o[e] + (int64_t)h * p.D + d);
+                    }
+            };
+            look_up(t0, off_next);
+            load(k[0], off_next, 0);
+            for (int t = t0; t < t1; ++t) {
+                off[0] = off_next[0];
+                off[1] = off_next[1];
+                if (t + 1 < t1) look_up(t + 1, off_next);
+                const int c0 = it.keys.lo + t * WKT + warp * 16;
+                int kp[2];
+                bool in[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = c0 + e * 8 + g;
+                    in[e] = off[e] >= 0;
+                    kp[e] = c;
+                    if (in[e] && p.key_pos && c < cand0) kp[e] = p.key_pos[(int64_t)b * p.kps + c];
+                    if (in[e] && c >= cand0 && p.pos) kp[e] = p.pos[(int64_t)b * p.S + (slots ? slots[c - cand0] : c - cand0)];
+                    if (kp[e] < first) in[e] = false;
+                }
+                // candidates' own entries and the window mask by query
+                const bool special = c0 + 16 > cand0 || p.window > 0;
+                float acc[2] = {0.0f, 0.0f};
+                auto head = [&](const uint4 (&x)[NB][2], int h) {
+                    const unsigned char *qr = sq + (size_t)(h * rp + g) * PITCH + q4 * 16;
+                    for (int r0 = 0; r0 < rp; r0 += 8) {
+                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(qr + (size_t)r0 * PITCH + i * 64);
+                            mma(y, x[i][0].x, x[i][1].x, x[i][0].y, x[i][1].y, v.x, v.y);
+                            mma(y, x[i][0].z, x[i][1].z, x[i][0].w, x[i][1].w, v.z, v.w);
+                        }
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+                            const int q = h * rp + r0 + q4 * 2 + a, own = s_own[q];
+                            const float ls = s_lse[q], slope = p.score.bias ? s_slope[q] : 0.0f;
+                            const int qp = p.score.bias || special ? s_qp[q] : 0;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int dist = pos_dist(qp, kp[e]);
+                                const float w = ex2f(fmaf(attn_score<false>(y[e * 2 + a], p.score, slope, dist), kLog2e, -ls));
+                                bool v = in[e] && own >= 0;
+                                if (special) v = v && c0 + e * 8 + g <= own && (p.window == 0 || dist < p.window);
+                                acc[e] += v ? w : 0.0f;
+                            }
+                        }
+                    }
+                };
+                for (int h = 0; h < p.H; h += 2) {
+                    // two heads a turn, so that the buffers' indices are constants
+                    if (h + 1 < p.H) load(k[1], off, h + 1);
+                    else if (t + 1 < t1) load(k[1], off_next, 0);
+                    head(k[0], h);
+                    if (h + 1 < p.H) {
+                        if (h + 2 < p.H) load(k[0], off, h + 2);
+                        else if (t + 1 < t1) load(k[0], off_next, 0);
+                        head(k[1], h + 1);
+                    }
+                }
+                if (p.H & 1) {  // the next tile's first head is in the other buffer
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) k[0][i][e] = k[1][i][e];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float a = acc[e];
+                    a += __shfl_xor_sync(kFull, a, 1);
+                    a += __shfl_xor_sync(kFull, a, 2);
+                    const int c = c0 + e * 8 + g;
+                    if (off[e] >= 0 && q4 == 0) wp.weight[b * wp.wstride + c] += a;
+                    if (c < it.keys.hi && c >= cand0 && q4 == 1 && wp.key_pos_out && j0 == 0) {
+                        const int j = c - cand0;
+                        wp.key_pos_out[(int64_t)b * p.kps + c] = p.pos ? p.pos[(int64_t)b * p.S + (slots ? slots[j] : j)] : c;
+                    }
+                }
+            }
+        }
+        u = it.u0 + it.ntiles;
+        if (u >= uend) break;
+        it = attn_next(p, it, 1, 1, WKT);
+    }
+}
+
+template <int DP> cudaError_t launch_mma(const WeightsParams &p, int sms, cudaStream_t s) {
+    // candidates a pass holds the queries of (K is read once per pass)
+    const int row = WRow<DP>::kPitch + 16, heads = p.a.H * p.a.G;
+    int per = kQueryBytes / (heads * row);
+    while (per > 1 && (int64_t)p.a.H * ((per * p.a.G + 7) / 8 * 8) * row > kQueryBytes) --per;
+    if (per < 1) per = 1;
+    if (per > p.a.S) per = p.a.S;
+    const int64_t smem = (int64_t)p.a.H * ((per * p.a.G + 7) / 8 * 8) * row;
+    if (smem > 200 * 1024) return cudaErrorInvalidConfiguration;  // (launch_weights does not come here then)
+    cudaError_t e = cudaFuncSetAttribute(weights_mma_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    weights_mma_kernel<DP><<<sms * (DP == 256 || smem > 100 * 1024 ? 1 : 2), WNT, (size_t)smem, s>>>(p, per);
+    return cudaGetLastError();
+}
+
 template <typename T, int DP> cudaError_t launch(const WeightsParams &p, int sms, cudaStream_t s) {
     const int smem = (int)sizeof(WSmem<T, DP>);
     cudaError_t e = cudaFuncSetAttribute(weights_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -156,8 +361,12 @@ template <typename T> cudaError_t launch_t(const WeightsParams &p, int sms, cuda
 
 }  // namespace
 
-cudaError_t launch_weights_simt(const WeightsParams &p, int dtype, int sms, cudaStream_t s) {
-    return dtype == SPEC_DTYPE_BF16 ? launch_t<__nv_bfloat16>(p, sms, s) : launch_t<float>(p, sms, s);
+cudaError_t launch_weights(const WeightsParams &p, int dtype, int sms, cudaStream_t s) {
+    if (dtype != SPEC_DTYPE_BF16) return launch_t<float>(p, sms, s);
+    // one candidate's queries must fit: H * (G rounded up to 8) rows
+    const int dp = p.a.D <= 64 ? 64 : p.a.D <= 128 ? 128 : 256;
+    if ((int64_t)p.a.H * ((p.a.G + 7) / 8 * 8) * (dp * 2 + 32) > 200 * 1024) return launch_t<__nv_bfloat16>(p, sms, s);
+    return dp == 64 ? launch_mma<64>(p, sms, s) : dp == 128 ? launch_mma<128>(p, sms, s) : launch_mma<256>(p, sms, s);
 }
 
 }  // namespace specv

@@ -266,7 +266,7 @@ struct WeightsParams {
     float *weight;
     int64_t wstride;
 };
-cudaError_t launch_weights_simt(const WeightsParams &p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_weights(const WeightsParams &p, int dtype, int sms, cudaStream_t s);
 
 struct EvictParams {
     int B, L, bs, max_blocks, unit_bytes, budget, sink, recent, max_moves;
