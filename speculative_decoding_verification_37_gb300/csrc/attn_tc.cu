@@ -77,6 +77,21 @@ __device__ __forceinline__ void tc_ld32(float *x, uint32_t t) {
         : R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
         : "r"(t));
 }
+template <int N> __device__ __forceinline__ void tc_ldx(float *x, uint32_t t) {
+#pragma unroll
+    for (int i = 0; i < N; i += 32) tc_ld32(x + i, t + i);
+}
+template <int N> __device__ __forceinline__ float max_of(const float *x) {
+    float a = x[0], b = x[1], c = x[2], d = x[3];
+#pragma unroll
+    for (int i = 4; i < N; i += 4) {
+        a = fmaxf(a, x[i]);
+        b = fmaxf(b, x[i + 1]);
+        c = fmaxf(c, x[i + 2]);
+        d = fmaxf(d, x[i + 3]);
+    }
+    return fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
 __device__ __forceinline__ void tc_ld16(float *x, uint32_t t) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : R8(x, 0), R8(x, 8)
@@ -197,7 +212,8 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                    const __grid_constant__ CUtensorMap temp_map) {
     using K = TcCfg<NH, C, W>;
     using T = __nv_bfloat16;
-    constexpr int RT = K::kRows, NT = K::kNT, NS = K::kRing, NC = KT / C, NCH = NC / 32;
+    constexpr int RT = K::kRows, NT = K::kNT, NS = K::kRing, NC = KT / C;
+    constexpr int CH = NC < 64 ? NC : 64;  // scores a thread holds at once
     extern __shared__ unsigned char raw_[];
     TcSmem<NH, C, W> &sh = *reinterpret_cast<TcSmem<NH, C, W> *>(
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));
@@ -545,41 +561,47 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                     }
                     bar_sync(bar, nbar);
                 }
-                // the 32 scores of chunk i, from TMEM: scaled to natural units where
-                // they are capped, biased or masked (and put back if they are many)
-                float x[32];
-                float cf = scale * kLog2e;
+                const bool plain = !listed && p.score.cap == 0.0f && !p.score.bias;
+                float x[CH];
+                float cf = scale * kLog2e, mt = -INFINITY;
                 bool hid = false;
-                float mt = -INFINITY;
+                if (plain) {
 #pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    tc_ld32(x, ts + i * 32);
-                    tc_wait_ld();
-                    const bool plain = !listed && p.score.cap == 0.0f && !p.score.bias;
-                    if (!plain) {
-                        cf = kLog2e;
+                    for (int i = 0; i < NC; i += CH) {
+                        tc_ldx<CH>(x, ts + i);
+                        tc_wait_ld();
+                        mt = fmaxf(mt, max_of<CH>(x));
+                    }
+                } else {
+                    // scores in natural units, 32 at a time, and back into TMEM
+                    cf = kLog2e;
+#pragma unroll 1
+                    for (int i = 0; i < NC; i += 32) {
+                        float y[32];
+                        tc_ldx<32>(y, ts + i);
+                        tc_wait_ld();
                         if (p.score.cap > 0.0f) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = cap_score(x[e] * scale, p.score.cap, p.score.cap_arg);
+                            for (int e = 0; e < 32; ++e) y[e] = cap_score(y[e] * scale, p.score.cap, p.score.cap_arg);
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] *= scale;
+                            for (int e = 0; e < 32; ++e) y[e] *= scale;
                         }
-                        const int *kp = sh.kp[kb] + cb + i * 32;
+                        const int *kp = sh.kp[kb] + cb + i;
                         if (p.score.bias) {
                             if (listed) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = fmaf(-slope, (float)pos_dist(qp, kp[e]), x[e]);
+                                for (int e = 0; e < 32; ++e) y[e] = fmaf(-slope, (float)pos_dist(qp, kp[e]), y[e]);
                             } else {
-                                const float d0 = (float)(qp - (c0 + cb + i * 32));
+                                const float d0 = (float)(qp - (c0 + cb + i));
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = fmaf(-slope, d0 - (float)e, x[e]);
+                                for (int e = 0; e < 32; ++e) y[e] = fmaf(-slope, d0 - (float)e, y[e]);
                             }
                         }
                         if (special) {
                             // bit e: key e of the chunk is seen by this row
-                            unsigned seen = sh.valid[kb][cb / 32 + i];
-                            const int q = cb + i * 32 - q0;   // the chunk's first key as a candidate
+                            unsigned seen = sh.valid[kb][(cb + i) / 32];
+                            const int q = cb + i - q0;        // the chunk's first key as a candidate
                             if (p.mode == 0 && q > -32) {
                                 unsigned mine = 0u;           // candidates q .. q + 31
                                 if (p.mask) {
@@ -602,31 +624,19 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                             }
                             hid = hid || seen != kFull;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = (seen >> e) & 1u ? x[e] : -INFINITY;
+                            for (int e = 0; e < 32; ++e) y[e] = (seen >> e) & 1u ? y[e] : -INFINITY;
                         }
-                        if (NCH > 1) {
-                            uint32_t y[32];
+                        mt = fmaxf(mt, max_of<32>(y));
+                        uint32_t z[32];
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(x[e]);
-                            tc_st32(ts + i * 32, y);
-                        }
+                        for (int e = 0; e < 32; ++e) z[e] = __float_as_uint(y[e]);
+                        tc_st32(ts + i, z);
                     }
-                    float a = fmaxf(x[0], x[1]), b = fmaxf(x[2], x[3]), c = fmaxf(x[4], x[5]), d = fmaxf(x[6], x[7]);
-#pragma unroll
-                    for (int e = 8; e < 32; e += 8) {
-                        a = fmaxf(a, fmaxf(x[e], x[e + 1]));
-                        b = fmaxf(b, fmaxf(x[e + 2], x[e + 3]));
-                        c = fmaxf(c, fmaxf(x[e + 4], x[e + 5]));
-                        d = fmaxf(d, fmaxf(x[e + 6], x[e + 7]));
-                    }
-                    mt = fmaxf(mt, fmaxf(fmaxf(a, b), fmaxf(c, d)));
+                    tc_wait_st();
                 }
-                if (NCH > 1) tc_wait_st();
                 mt *= cf;
                 // a masked key's V: zeros for what is not finite
-                unsigned dirty[NCH];
-#pragma unroll
-                for (int i = 0; i < NCH; ++i) dirty[i] = 0u;
+                bool dirty = false;
                 if (special && bar_or(bar, nbar, hid)) {
                     // V of this tile: its place in the ring by the order of the copies
                     const int tt = t - t0;
@@ -650,9 +660,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                         fence_async_shared();
                     }
                     bar_sync(bar, nbar);
-#pragma unroll
-                    for (int i = 0; i < NCH; ++i) dirty[i] = sh.dirty[db][cb / 32 + i];
-                    bar_sync(bar, nbar);  // dirty may be written again
+                    dirty = (sh.dirty[db][0] | sh.dirty[db][1] | sh.dirty[db][2] | sh.dirty[db][3]) != 0u;
                 }
                 // a new reference when the maximum has grown past 2^8 of the old one
                 const bool grew = mt > m + 8.0f || (m == -INFINITY && mt > -INFINITY);
@@ -685,39 +693,45 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const uint32_t pt = tl + kS + sb * 128 + cb / 2;
-                float s0 = 0.0f, s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                const float2 cf2 = make_float2(cf, cf), nref = make_float2(-ref, -ref);
+                float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
-                for (int i = 0; i < NCH; ++i) {
-                    if (NCH > 1) {
-                        tc_ld32(x, ts + i * 32);
+                for (int i = 0; i < NC; i += CH) {
+                    if (NC > CH || !plain) {
+                        tc_ldx<CH>(x, ts + i);
                         tc_wait_ld();
                     }
-                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float a = ex2f(fmaf(x[e], cf, -ref)), b = ex2f(fmaf(x[e + 1], cf, -ref));
-                        const float c = ex2f(fmaf(x[e + 2], cf, -ref)), d = ex2f(fmaf(x[e + 3], cf, -ref));
-                        s0 += a;
-                        s1 += b;
-                        s2 += c;
-                        s3 += d;
-                        pk[e / 2] = pack_bf16(a, b);
-                        pk[e / 2 + 1] = pack_bf16(c, d);
+                    for (int e = 0; e < CH; e += 32) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 32; k += 4) {
+                            float2 a = __ffma2_rn(make_float2(x[e + k], x[e + k + 1]), cf2, nref);
+                            float2 b = __ffma2_rn(make_float2(x[e + k + 2], x[e + k + 3]), cf2, nref);
+                            a = make_float2(ex2f(a.x), ex2f(a.y));
+                            b = make_float2(ex2f(b.x), ex2f(b.y));
+                            sum0 = __fadd2_rn(sum0, a);
+                            sum1 = __fadd2_rn(sum1, b);
+                            pk[k / 2] = pack_bf16(a.x, a.y);
+                            pk[k / 2 + 1] = pack_bf16(b.x, b.y);
+                        }
+                        if (dirty) {
+                            const unsigned d = sh.dirty[W == 1 ? grp : 0][(cb + i + e) / 32];
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                poison = poison || (((d >> k) & 1u) && ((pk[k / 2] >> ((k & 1) * 16)) & 0xffffu) != 0u);
+                        }
+                        tc_st16(pt + (i + e) / 2, pk);
                     }
-                    if (dirty[i] != 0u)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            poison = poison || (((dirty[i] >> e) & 1u) && ((pk[e / 2] >> ((e & 1) * 16)) & 0xffffu) != 0u);
-                    tc_st16(pt + i * 16, pk);
                 }
-                l += (s0 + s1) + (s2 + s3);
+                l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
                 if (C > 1) {  // nothing of the other copies' keys
                     uint32_t z[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) z[i] = 0u;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        if (i < cb / 32 || i >= cb / 32 + NCH) tc_st16(tl + kS + sb * 128 + i * 16, z);
+                        if (i < cb / 32 || i >= (cb + NC) / 32) tc_st16(tl + kS + sb * 128 + i * 16, z);
                 }
                 tc_wait_st();
                 tc_fence_before();
