@@ -75,8 +75,10 @@ namespace specv {
 
 size_t attn_ws_layout(int32_t B, int32_t n, int32_t D, bool shared, void *base, AttnParams *p) {
     size_t off = kWsHeader;
+    const size_t o_split = off;
+    off += ws_align(kAttnBlocksMax * sizeof(SplitItem));
     const size_t o_cnt = off;
-    off += ws_align(kAttnCounters * sizeof(unsigned));
+    off += ws_align(kAttnBlocksMax * sizeof(unsigned));
     const size_t o_part = off;
     off += ws_align((size_t)kAttnSmsMax * 2 * kAttnSlotRows * (shared ? 2 : 1) * ((size_t)D + 2) * sizeof(float));
     const size_t o_pre = off;
@@ -86,6 +88,7 @@ size_t attn_ws_layout(int32_t B, int32_t n, int32_t D, bool shared, void *base, 
     if (p) {
         char *c = static_cast<char *>(base);
         p->status = reinterpret_cast<unsigned *>(c);
+        p->split = reinterpret_cast<SplitItem *>(c + o_split);
         p->counters = reinterpret_cast<unsigned *>(c + o_cnt);
         p->part = reinterpret_cast<float *>(c + o_part);
         p->pre_o = reinterpret_cast<float *>(c + o_pre);

@@ -6,9 +6,10 @@
 // the cached head.  The pass over a shared prefix is one request whose rows
 // are every request's.  All items' tiles form one line; block i takes tiles
 // [i*share, (i+1)*share), so lengths from one token to the longest give every
-// block the same work.  An item that lies in several blocks is joined by the
-// block that arrives last, from all blocks' partial results in block order:
-// the result does not depend on which block that is.
+// block the same work.  An item that lies in several blocks leaves its partial
+// results in the workspace, and they are joined in block order: by the block
+// that arrives last, or by a second kernel (attn_join.cu), which costs a call
+// that splits nothing 3 to 4 us but joins large items with all SMs.
 #pragma once
 
 #include "common.cuh"
@@ -89,6 +90,7 @@ __device__ __forceinline__ KeyRange attn_keys(const AttnParams &p, int b) {
             int qmin = p.mode == 2 ? r.len - n : r.len;
             if (p.pos) {
                 qmin = 0x7fffffff;
+#pragma unroll 1
                 for (int i = 0; i < n; ++i) {
                     const int s = p.mode == 2 && p.slots ? p.slots[(int64_t)b * p.slots_stride + i] : i;
                     if (s >= 0 && s < p.S) qmin = min(qmin, p.pos[(int64_t)b * p.S + s]);
@@ -110,10 +112,10 @@ struct KeyLine {
 };
 __device__ __forceinline__ KeyLine attn_line(const AttnParams &p, const KeyRange &r) {
     KeyLine k;
-    const int box = p.box;
-    k.lo = r.lo / box * box;
+    const int mask = ~(p.box - 1);  // (a power of two)
+    k.lo = r.lo & mask;
     const int end = p.tk && p.mode == 0 ? r.len : r.hi;
-    k.entries = (end - k.lo + box - 1) / box * box;
+    k.entries = (end - k.lo + p.box - 1) & mask;
     return k;
 }
 
@@ -315,12 +317,26 @@ template <> __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 
 // 2^(a - m) for a <= m; 0 for a = -inf, m = -inf included
 __device__ __forceinline__ float rel_weight(float a, float m) { return a == -INFINITY ? 0.0f : ex2f(a - m); }
 
+// What attn_write needs of the shared part, loaded ahead.
+struct SharedPart {
+    float lse;
+    float4 o;
+};
+__device__ __forceinline__ SharedPart attn_shared_part(const AttnParams &p, bool ok, int64_t row, int d) {
+    SharedPart s{-INFINITY, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (p.mode == 0 && p.P > 0 && ok && row >= 0) {
+        s.lse = p.pre_lse[row];
+        s.o = *reinterpret_cast<const float4 *>(p.pre_o + row * p.D + d);
+    }
+    return s;
+}
+
 // Writes four columns of row `row` from the joined (m2, l, o): to the shared
 // results in mode 1, else to the output, the shared part joined first (not for
 // a request whose length is bad: it gets zeros).
 template <typename T>
 __device__ __forceinline__ void attn_write(const AttnParams &p, bool ok, int64_t row, int d, float m2, float l,
-                                           float4 o) {
+                                           float4 o, const SharedPart &sp) {
     float lse2 = l > 0.0f || l != l ? m2 + lg2f(l) : -INFINITY;  // a NaN sum stays NaN
     if (p.mode == 1) {
         const float inv = lse2 == -INFINITY ? 0.0f : 1.0f / l;
@@ -329,12 +345,10 @@ __device__ __forceinline__ void attn_write(const AttnParams &p, bool ok, int64_t
         return;
     }
     if (p.P > 0 && ok) {
-        const float ls = p.pre_lse[row];
-        const float4 os = *reinterpret_cast<const float4 *>(p.pre_o + row * p.D + d);
-        const float m = fmaxf(m2, ls);
-        const float a = rel_weight(m2, m), c = ls != ls ? ls : rel_weight(ls, m);
+        const float m = fmaxf(m2, sp.lse);
+        const float a = rel_weight(m2, m), c = sp.lse != sp.lse ? sp.lse : rel_weight(sp.lse, m);
         l = l * a + c;
-        o = make_float4(o.x * a + os.x * c, o.y * a + os.y * c, o.z * a + os.z * c, o.w * a + os.w * c);
+        o = make_float4(o.x * a + sp.o.x * c, o.y * a + sp.o.y * c, o.z * a + sp.o.z * c, o.w * a + sp.o.w * c);
         lse2 = l > 0.0f || l != l ? m + lg2f(l) : -INFINITY;
     }
     const float inv = lse2 == -INFINITY ? 0.0f : 1.0f / l;
@@ -343,148 +357,166 @@ __device__ __forceinline__ void attn_write(const AttnParams &p, bool ok, int64_t
     if (d == 0 && p.lse) p.lse[row] = lse2 * kLn2;
 }
 
+// Whether the item lies in several blocks, and which.
+struct ItemBlocks {
+    int c0, c1;
+};
+__device__ __forceinline__ ItemBlocks attn_blocks(const AttnPlan &pl, const AttnItem &it) {
+    // mostly this block alone: no division then
+    const int64_t mine = (int64_t)blockIdx.x * pl.share;
+    if (it.u0 >= mine && it.u0 + it.ntiles <= mine + pl.share) return ItemBlocks{(int)blockIdx.x, (int)blockIdx.x};
+    return ItemBlocks{(int)(it.u0 / pl.share), (int)((it.u0 + it.ntiles - 1) / pl.share)};
+}
+// Block c's partial result: slot 0 of a block holds the item that began before
+// it, slot 1 the one that goes on after it.  RT rows of D sums, references,
+// weights.
+template <int RT> __device__ __forceinline__ float *attn_part(const AttnParams &p, int c, int c0) {
+    return p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * ((int64_t)RT * (p.D + 2));
+}
+
+// Query r (of the item's RT rows) joined by a warp from the partial results of n
+// blocks, from block c0 on:
+//   m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
+// A lane takes four columns; U blocks' rows are in flight.
+template <typename T, int U>
+__device__ __forceinline__ void attn_join_row(const AttnParams &p, bool ok, int rt_rows, int c0, int n, int r, int64_t row) {
+    const int lane = threadIdx.x & 31;
+    const int64_t slot = (int64_t)rt_rows * (p.D + 2), o_m = (int64_t)rt_rows * p.D, o_l = o_m + rt_rows;
+    const float *base = p.part + (int64_t)c0 * 2 * slot;
+    auto part = [&](int c) { return base + (int64_t)c * 2 * slot + (c == 0 ? slot : 0); };
+    float m = -INFINITY;
+    for (int c = lane; c < n; c += 32) m = fmaxf(m, __ldcg(part(c) + o_m + r));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+    for (int d0 = 0; d0 < p.D; d0 += 128) {
+        const int d = d0 + lane * 4;
+        const bool in = d < p.D;
+        const SharedPart sp = attn_shared_part(p, ok && in, row, in ? d : 0);
+        float l = 0.0f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cb = 0; cb < n; cb += 32) {
+            float w = 0.0f, lw = 0.0f;
+            if (cb + lane < n) {
+                w = rel_weight(__ldcg(part(cb + lane) + o_m + r), m);
+                lw = __ldcg(part(cb + lane) + o_l + r) * w;
+                if (w == 0.0f) lw = 0.0f;  // that block saw no key of the row
+            }
+            const int e = min(32, n - cb);
+            for (int c = 0; c < e; c += U) {
+                float4 x[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i)
+                    x[i] = c + i < e && in ? __ldcg(reinterpret_cast<const float4 *>(part(cb + c + i) + (int64_t)r * p.D + d))
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const float wc = __shfl_sync(kFull, w, (c + i) & 31), lc = __shfl_sync(kFull, lw, (c + i) & 31);
+                    if (c + i >= e || wc == 0.0f) continue;
+                    l += lc;
+                    o = make_float4(fmaf(x[i].x, wc, o.x), fmaf(x[i].y, wc, o.y), fmaf(x[i].z, wc, o.z), fmaf(x[i].w, wc, o.w));
+                }
+            }
+        }
+        if (in) attn_write<T>(p, ok, row, d, m, l, o, sp);
+    }
+}
+
+// After this block's partial result has been stored (NT threads): the block
+// that arrives last joins the item.  The counter is left zero.
+template <typename T, int RT, int NT>
+__device__ __forceinline__ void attn_join_here(const AttnParams &p, const AttnItem &it, const AttnRows<RT> &w, ItemBlocks ib,
+                                               int *last) {
+    const int tid = threadIdx.x, n = ib.c1 - ib.c0 + 1;
+    __threadfence();
+    sync_nt<NT>();
+    if (tid == 0) *last = atomicAdd(p.counters + ib.c0, 1u) == (unsigned)(n - 1);
+    sync_nt<NT>();
+    if (!*last) return;
+    __threadfence();
+    for (int r = tid >> 5; r < RT; r += NT / 32)
+        if (w.out[r] >= 0) attn_join_row<T, 8>(p, it.keys.ok, RT, ib.c0, n, r, w.out[r]);
+    if (tid == 0) p.counters[ib.c0] = 0u;
+    sync_nt<NT>();
+}
+
+// For the second kernel: marks the item that begins in this block and goes on in
+// others (thread 0; attn_begin has marked the block as having none).
+__device__ __forceinline__ void attn_begin(const AttnParams &p) {
+    if (threadIdx.x == 0) p.split[blockIdx.x].blocks = 0;
+}
+__device__ __forceinline__ void attn_mark(const AttnParams &p, const AttnItem &it, ItemBlocks ib) {
+    if (threadIdx.x == 0 && (int)blockIdx.x == ib.c0)
+        p.split[ib.c0] = SplitItem{ib.c1 - ib.c0 + 1, it.b, it.h, it.rt, it.keys.ok ? 1 : 0};
+}
+
 // The block's result for item `it`, in shared memory: sums so[RT][ld] with
-// reference m2 = sm[r] (log2 units) and weight sl[r].  [t0, t1) are the tiles
-// this block did.  Ends with the shared memory free for reuse.
+// reference m2 = sm[r] (log2 units) and weight sl[r].  Ends with the shared
+// memory free for reuse.  A split item is joined by the block that arrives last.
 template <typename T, int RT, int NT>
 __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan &pl, const AttnItem &it,
                                             const AttnRows<RT> &w, const float *so, int ld, const float *sm,
-                                            const float *sl, int *last_flag) {
-    const int tid = threadIdx.x, d4 = p.D / 4;
-    const int64_t share = pl.share;
-    const int c0 = (int)(it.u0 / share), c1 = (int)((it.u0 + it.ntiles - 1) / share);
-    if (c0 == c1) {
-        for (int i = tid; i < RT * d4; i += NT) {
-            const int r = i / d4, d = (i - r * d4) * 4;
-            if (w.out[r] >= 0)
-                attn_write<T>(p, it.keys.ok, w.out[r], d, sm[r], sl[r], *reinterpret_cast<const float4 *>(so + r * ld + d));
-        }
-        sync_nt<NT>();
-        return;
-    }
-    // partial results: slot 0 of a block holds the item that began before it,
-    // slot 1 the one that goes on after it
-    const int64_t slot_floats = (int64_t)RT * (p.D + 2);
-    const int me = blockIdx.x;
-    float *mine = p.part + ((int64_t)me * 2 + (me == c0 ? 1 : 0)) * slot_floats;
-    for (int i = tid; i < RT * d4; i += NT) {
-        const int r = i / d4, d = (i - r * d4) * 4;
-        if (w.out[r] >= 0) __stcg(reinterpret_cast<float4 *>(mine + r * p.D + d), *reinterpret_cast<const float4 *>(so + r * ld + d));
-    }
-    for (int r = tid; r < RT; r += NT) {
-        __stcg(mine + RT * p.D + r, sm[r]);
-        __stcg(mine + RT * p.D + RT + r, sl[r]);
-    }
-    __threadfence();
-    sync_nt<NT>();
-    if (tid == 0) *last_flag = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-    sync_nt<NT>();
-    if (!*last_flag) return;
-    __threadfence();
-    // a warp per row: each lane a few blocks' (m, l), then the rows, many in flight
-    const int lane = tid & 31, n = c1 - c0 + 1;
-    auto part = [&](int c) { return p.part + ((int64_t)(c0 + c) * 2 + (c == 0 ? 1 : 0)) * slot_floats; };
+                                            const float *sl, int *last) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const ItemBlocks ib = attn_blocks(pl, it);
+    const bool split = ib.c0 != ib.c1;
+    float *mine = attn_part<RT>(p, blockIdx.x, ib.c0);
+    // a warp per row
+#pragma unroll 1
     for (int r = tid >> 5; r < RT; r += NT / 32) {
-        if (w.out[r] < 0) continue;
-        constexpr int U = 8;
-        float m = -INFINITY;
-        for (int c = lane; c < n; c += 32) m = fmaxf(m, __ldcg(part(c) + RT * p.D + r));
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-        for (int d = lane * 4; d < p.D + (128 - p.D % 128) % 128; d += 128) {  // all lanes stay
-            float l = 0.0f;
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int cb = 0; cb < n; cb += 32) {
-                float k = 0.0f, lk = 0.0f;
-                if (cb + lane < n) {
-                    k = rel_weight(__ldcg(part(cb + lane) + RT * p.D + r), m);
-                    lk = __ldcg(part(cb + lane) + RT * p.D + RT + r) * k;
-                    if (k == 0.0f) lk = 0.0f;  // that block saw no key of the row
-                }
-                const int e = min(32, n - cb);
-                for (int c = 0; c < e; c += U) {
-                    float4 x[U];
-#pragma unroll
-                    for (int q = 0; q < U; ++q)
-                        x[q] = c + q < e && d < p.D ? __ldcg(reinterpret_cast<const float4 *>(part(cb + c + q) + (int64_t)r * p.D + d))
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int q = 0; q < U; ++q) {
-                        const float kq = __shfl_sync(kFull, k, (c + q) & 31);
-                        l += __shfl_sync(kFull, c + q < e ? lk : 0.0f, (c + q) & 31);
-                        if (c + q < e && kq != 0.0f)
-                            o = make_float4(fmaf(x[q].x, kq, o.x), fmaf(x[q].y, kq, o.y), fmaf(x[q].z, kq, o.z), fmaf(x[q].w, kq, o.w));
-                    }
-                }
-            }
-            if (d < p.D) attn_write<T>(p, it.keys.ok, w.out[r], d, m, l, o);
+        const int64_t row = w.out[r];
+        if (row < 0) continue;
+#pragma unroll 1
+        for (int d = lane * 4; d < p.D; d += 128) {
+            const float4 v = *reinterpret_cast<const float4 *>(so + r * ld + d);
+            if (split) __stcg(reinterpret_cast<float4 *>(mine + (int64_t)r * p.D + d), v);
+            else attn_write<T>(p, it.keys.ok, row, d, sm[r], sl[r], v, attn_shared_part(p, it.keys.ok, row, d));
         }
     }
-    if (tid == 0) p.counters[c0] = 0u;
-    sync_nt<NT>();
+    if (split) {
+        for (int r = tid; r < RT; r += NT) {
+            __stcg(mine + (int64_t)RT * p.D + r, sm[r]);
+            __stcg(mine + (int64_t)RT * p.D + RT + r, sl[r]);
+        }
+        attn_join_here<T, RT, NT>(p, it, w, ib, last);
+    } else {
+        sync_nt<NT>();
+    }
 }
 
 // The same for a kernel whose thread holds a whole row: (m2, l) and, by
 // `chunk(d, o)`, 32 columns from d on (every lane of a warp calls it together).
-// `r`: the thread's row in the item's tile of RT rows.
+// `r`: the thread's row in the item's tile of RT rows.  A split item is left to the
+// second kernel.
 template <typename T, int RT, int NT, typename F>
 __device__ __forceinline__ void attn_finish_row(const AttnParams &p, const AttnPlan &pl, const AttnItem &it,
-                                                int64_t out_row, int r, float m, float l, F &&chunk, int *last_flag) {
-    const int64_t share = pl.share;
-    const int c0 = (int)(it.u0 / share), c1 = (int)((it.u0 + it.ntiles - 1) / share);
-    const bool split = c0 != c1;
-    const int64_t slot_floats = (int64_t)RT * (p.D + 2);
-    const int me = blockIdx.x;
-    float *mine = p.part + ((int64_t)me * 2 + (me == c0 ? 1 : 0)) * slot_floats;
+                                                const AttnRows<RT> &w, int r, float m, float l, F &&chunk) {
+    const ItemBlocks ib = attn_blocks(pl, it);
+    const bool split = ib.c0 != ib.c1;
+    const int64_t out_row = w.out[r];
+    float *mine = attn_part<RT>(p, blockIdx.x, ib.c0);
+#pragma unroll 1
     for (int d0 = 0; d0 < p.D; d0 += 32) {
         float o[32];
         chunk(d0, o);
         if (out_row < 0) continue;
+        SharedPart sp[4];
 #pragma unroll
-        for (int d = 0; d < 32; d += 4) {
-            if (d0 + d >= p.D) break;
-            const float4 v = make_float4(o[d], o[d + 1], o[d + 2], o[d + 3]);
-            if (split) __stcg(reinterpret_cast<float4 *>(mine + (int64_t)r * p.D + d0 + d), v);
-            else attn_write<T>(p, it.keys.ok, out_row, d0 + d, m, l, v);
+        for (int j = 0; j < 8; ++j) {
+            const int d = d0 + 4 * j;
+            if (d >= p.D) break;
+            if (j % 4 == 0 && !split) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) sp[q] = attn_shared_part(p, it.keys.ok && d + 4 * q < p.D, out_row, d + 4 * q);
+            }
+            const float4 v = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            if (split) __stcg(reinterpret_cast<float4 *>(mine + (int64_t)r * p.D + d), v);
+            else attn_write<T>(p, it.keys.ok, out_row, d, m, l, v, sp[j % 4]);
         }
     }
     if (!split) return;
-    __stcg(mine + RT * p.D + r, m);
-    __stcg(mine + RT * p.D + RT + r, l);
-    __threadfence();
-    sync_nt<NT>();
-    if (threadIdx.x == 0) *last_flag = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-    sync_nt<NT>();
-    if (!*last_flag) return;
-    __threadfence();
-    if (out_row >= 0) {
-        float mm = -INFINITY;
-        for (int c = c0; c <= c1; ++c)
-            mm = fmaxf(mm, __ldcg(p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats + RT * p.D + r));
-        for (int d0 = 0; d0 < p.D; d0 += 32) {
-            float4 o[8];
-            float ll = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int c = c0; c <= c1; ++c) {
-                const float *s = p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot_floats;
-                const float k = rel_weight(__ldcg(s + RT * p.D + r), mm);
-                if (k == 0.0f) continue;  // this block saw no key of the row
-                ll += __ldcg(s + RT * p.D + RT + r) * k;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (d0 + 4 * j >= p.D) break;
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(s + (int64_t)r * p.D + d0 + 4 * j));
-                    o[j] = make_float4(fmaf(x.x, k, o[j].x), fmaf(x.y, k, o[j].y), fmaf(x.z, k, o[j].z), fmaf(x.w, k, o[j].w));
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (d0 + 4 * j < p.D) attn_write<T>(p, it.keys.ok, out_row, d0 + 4 * j, mm, ll, o[j]);
-        }
-    }
-    if (threadIdx.x == 0) p.counters[c0] = 0u;
-    sync_nt<NT>();
+    __stcg(mine + (int64_t)RT * p.D + r, m);
+    __stcg(mine + (int64_t)RT * p.D + RT + r, l);
+    attn_mark(p, it, ib);
 }
 
 }  // namespace specv

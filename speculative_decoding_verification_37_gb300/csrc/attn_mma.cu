@@ -92,7 +92,7 @@ template <int DP, int MT, int WR, int WK, int NK, int NG, int ST> struct MmaSmem
     AttnRows<C::kRows> rows;
     AttnPlan plan;
     alignas(8) unsigned long long full[ST], empty[ST];
-    int flag;
+    int last;
 };
 
 template <int DP, int MT, int WR, int WK, int NK, int NG, int ST>
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(32 * (WR * WK * NG + 4), 1) attn_mma_kernel(At
             }
             sync_nt<NT>();
         }
-        attn_finish<T, RT, NT>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP + 4, sh.tm, sh.tl, &sh.flag);
+        attn_finish<T, RT, NT>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP + 4, sh.tm, sh.tl, &sh.last);
         u = it.u0 + it.ntiles;
         if (u >= uend) break;
         it = attn_next(p, it, p.H * rtiles, rtiles, KT);

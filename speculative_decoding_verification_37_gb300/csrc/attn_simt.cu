@@ -28,7 +28,7 @@ template <typename T, int DP> struct SimtSmem {
     int64_t koff[KT];      // element offset of the key's row; -1: none
     AttnRows<RT> rows;
     AttnPlan plan;
-    int flag;
+    int last;
 };
 
 template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_kernel(AttnParams p) {
@@ -158,7 +158,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_ke
             sh.l[row] = l;
         }
         __syncthreads();
-        attn_finish<T, RT, NT>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP, sh.m, sh.l, &sh.flag);
+        attn_finish<T, RT, NT>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP, sh.m, sh.l, &sh.last);
         u = it.u0 + it.ntiles;
         if (u >= uend) break;
         it = attn_next(p, it, p.H * rtiles, rtiles, KT);

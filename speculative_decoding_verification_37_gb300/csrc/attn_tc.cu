@@ -190,7 +190,7 @@ template <int NH, int C, int W> struct TcSmem {
     AttnPlan plan;
     alignas(8) unsigned long long full[K::kRing], empty[K::kRing], s_full[2], p_full[2], pv_done[2], q_full[2], q_free[2];
     uint32_t tmem;
-    int flag;
+    int last;
 };
 
 // barriers of n threads under an id of their own
@@ -237,8 +237,10 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
         }
         fence_barrier_init();
     }
+    if (W != 1) attn_begin(p);
     if (warp < NT / 32) attn_plan<NT>(p, sh.plan, items, KT);
     __syncthreads();
+    if (W != 1) pdl_launch_dependents();
     int64_t u = (int64_t)blockIdx.x * sh.plan.share;
     const int64_t uend = min(sh.plan.total, u + sh.plan.share);
     if (u >= uend) return;
@@ -313,16 +315,14 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 ++n;
             };
             // the order of use: K0 K1 V0 K2 V1 ... (W = 2: K0 V0 K1 V1 ...)
-            row_v = row_k = look_up(t0);
-            copy(row_k, 0);
-            for (int t = t0; t < t1; ++t) {
-                if (W == 2) copy(row_v, 1);
-                if (t + 1 < t1) {
-                    row_k = look_up(t + 1);
-                    copy(row_k, 0);
-                }
-                if (W != 2) copy(row_v, 1);
+            constexpr int LAG = W == 2 ? 0 : 1;
+#pragma unroll 1
+            for (int t = t0; t < t1 + LAG; ++t) {
                 row_v = row_k;
+                if (t < t1) row_k = look_up(t);
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v)
+                    if (v ? t >= t0 + LAG : t < t1) copy(v && LAG ? row_v : row_k, v);
             }
             u = it.u0 + it.ntiles;
             if (u >= uend) break;
@@ -346,6 +346,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 tc_fence_after();
             };
             auto scores = [&](int d, int qt, int slot) {
+#pragma unroll 4
                 for (int k = 0; k < ksteps; ++k)
                     tc_mma_ss(tmem + kS + d * 128,
                               tc_desc(smem_u32(sh.q[item % K::kQB][qt]) + (uint32_t)(k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
@@ -367,37 +368,44 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 if (ok) ok = mbar_wait_bounded(&sh.q_full[item % K::kQB], (unsigned)((item / K::kQB) & 1));
                 tc_fence_after();
                 if (W != 2) {
-                    auto next_scores = [&](int d) {
-                        wait_full(n);
-                        scores(d, 0, n % NS);
-                        tc_commit(&sh.empty[n % NS]);
-                        tc_commit(&sh.s_full[d]);
-                        ++n;
-                    };
-                    next_scores(j & 1);
-                    if (nt > 1) next_scores((j + 1) & 1);
-                    for (int t = 0; t < nt; ++t, ++j) {
-                        wait_full(n);
-                        wait_p(j & 1, (unsigned)((j >> 1) & 1));
-                        values(W == 0 ? 0 : j & 1, j & 1, n % NS, W == 0 ? t == 0 : t < 2);
-                        tc_commit(&sh.empty[n % NS]);
-                        tc_commit(&sh.pv_done[W == 0 ? 0 : j & 1]);
-                        ++n;
-                        if (t + 2 < nt) next_scores(j & 1);
+                    // S0 S1, P0 V0, S2, P1 V1, S3 ...
+                    const int j0 = j;
+#pragma unroll 1
+                    for (int i = 0; i < nt + 2; ++i) {
+                        if (i >= 2) {
+                            wait_full(n);
+                            wait_p(j & 1, (unsigned)((j >> 1) & 1));
+                            values(W == 0 ? 0 : j & 1, j & 1, n % NS, W == 0 ? i == 2 : i < 4);
+                            tc_commit(&sh.empty[n % NS]);
+                            tc_commit(&sh.pv_done[W == 0 ? 0 : j & 1]);
+                            ++n;
+                            ++j;
+                        }
+                        if (i < nt) {
+                            const int d = (j0 + i) & 1;
+                            wait_full(n);
+                            scores(d, 0, n % NS);
+                            tc_commit(&sh.empty[n % NS]);
+                            tc_commit(&sh.s_full[d]);
+                            ++n;
+                        }
                     }
                 } else {
                     wait_full(n);
+#pragma unroll 1
                     for (int q = 0; q < 2; ++q) {
                         scores(q, q, n % NS);
                         tc_commit(&sh.s_full[q]);
                     }
                     tc_commit(&sh.empty[n % NS]);
                     ++n;
+#pragma unroll 1
                     for (int t = 0; t < nt; ++t, ++j) {
                         const int nv = n, nk = n + 1;
                         const bool more = t + 1 < nt;
                         wait_full(nv);
                         if (more) wait_full(nk);
+#pragma unroll 1
                         for (int q = 0; q < 2; ++q) {
                             wait_p(q, (unsigned)(j & 1));
                             values(q, q, nv % NS, t == 0);
@@ -439,6 +447,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             low = __reduce_max_sync(kFull, low);
             if (lane == 0) sh.low_max[item & 1] = low;
             constexpr int CH = NH * 8, U = 8;  // 16-byte chunks of a row; loads in flight
+#pragma unroll 1
             for (int i0 = lane; i0 < RT * CH; i0 += 32 * U) {
                 uint4 v[U];
 #pragma unroll
@@ -507,7 +516,6 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             if (ok) ok = mbar_wait_bounded(&sh.q_full[qb], (unsigned)((item / K::kQB) & 1));
             const AttnRows<RT> &w = sh.rows[buf];
             const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), nt = t1 - t0;
-            const int64_t out_row = w.out[row];
             const int qp = w.qp[row], cand = w.cand[row];
             const int low = max(w.first[row], p.window > 0 ? qp - p.window + 1 : (int)0x80000000);
             const float slope = w.slope[row];
@@ -648,7 +656,8 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                         uint32_t found = 0;
 #pragma unroll 4
                         for (int i = 0; i < NH * 8; ++i) {
-                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * 1024 + (i & 7) * 16);
+                            // (rows lie 128 bytes apart: neighbours start at another chunk)
+                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * 1024 + ((i + lane) & 7) * 16);
                             found |= nonfinite2(y.x) | nonfinite2(y.y) | nonfinite2(y.z) | nonfinite2(y.w);
                         }
                         if (found) {
@@ -715,12 +724,6 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                             pk[k / 2] = pack_bf16(a.x, a.y);
                             pk[k / 2 + 1] = pack_bf16(b.x, b.y);
                         }
-                        if (dirty) {
-                            const unsigned d = sh.dirty[W == 1 ? grp : 0][(cb + i + e) / 32];
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                poison = poison || (((d >> k) & 1u) && ((pk[k / 2] >> ((k & 1) * 16)) & 0xffffu) != 0u);
-                        }
                         tc_st16(pt + (i + e) / 2, pk);
                     }
                 }
@@ -734,6 +737,18 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                         if (i < cb / 32 || i >= (cb + NC) / 32) tc_st16(tl + kS + sb * 128 + i * 16, z);
                 }
                 tc_wait_st();
+                if (dirty) {  // a key with a non-finite V: the rows that give it weight
+#pragma unroll 1
+                    for (int i = 0; i < NC; i += 32) {
+                        const unsigned d = sh.dirty[W == 1 ? grp : 0][(cb + i) / 32];
+                        float y[16];
+                        tc_ld16(y, pt + i / 2);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            poison = poison || (((d >> k) & 1u) && ((__float_as_uint(y[k / 2]) >> ((k & 1) * 16)) & 0xffffu) != 0u);
+                    }
+                }
                 tc_fence_before();
                 mbar_arrive(&sh.p_full[sb]);
             }
@@ -759,7 +774,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = __int_as_float(0x7fffffff);
                 };
-                attn_finish_row<T, RT, NT>(p, sh.plan, done, out_row, row, m, l, chunk, &sh.flag);
+                attn_finish_row<T, RT, NT>(p, sh.plan, done, w, row, m, l, chunk);
             } else {
                 // join the copies of both groups: 8 blocks of columns, each copy at
                 // another one in each of 8 rounds (the first to come stores)
@@ -799,7 +814,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                     }
                     sync_nt<NT>();
                 }
-                attn_finish<T, RT, NT>(p, sh.plan, done, w, &sh.o[0][0], NH * 64 + 4, sh.tm, sh.tl, &sh.flag);
+                attn_finish<T, RT, NT>(p, sh.plan, done, w, &sh.o[0][0], NH * 64 + 4, sh.tm, sh.tl, &sh.last);
             }
             tc_fence_before();
             if (W != 2) mbar_arrive(&sh.q_free[qb]);
@@ -849,7 +864,8 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap
     if (e != cudaSuccess) return e;
     const int grid = sms < kAttnSmsMax ? sms : kAttnSmsMax;
     attn_tc_kernel<NH, C, W><<<grid, K::kThreads, smem, s>>>(p, cm, tm);
-    return cudaGetLastError();
+    e = cudaGetLastError();
+    return e == cudaSuccess && W != 1 ? launch_attn_join(p, K::kRows, grid, s) : e;
 }
 
 template <int NH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {

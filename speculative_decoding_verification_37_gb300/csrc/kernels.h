@@ -218,7 +218,12 @@ struct ScoreArgs {
 constexpr int kAttnThreadsMax = 256;
 constexpr int kAttnSmsMax = 160;     // grids are sized for at most this many SMs
 constexpr int kAttnSlotRows = 128;   // rows of partial results per SM and slot; twice that with a shared prefix
-constexpr int kAttnCounters = kAttnSmsMax * 8;
+constexpr int kAttnBlocksMax = kAttnSmsMax * 8;
+
+struct SplitItem {                // an item that goes on past the block it begins in
+    int blocks;                   // how many it lies in; 0: there is none
+    int b, h, rt, ok;
+};
 
 struct AttnParams {
     int B, S, Hq, H, G, D, bs, max_blocks, W;
@@ -249,10 +254,14 @@ struct AttnParams {
     int box;                      // rows of a page copied at once (0: row by row)
     void *out;
     float *lse;
-    unsigned *flags, *status, *counters;
+    unsigned *flags, *status;
+    unsigned *counters;           // [block] arrivals at the split item that begins in it; zero between calls
+    SplitItem *split;             // [block]
     float *part;                  // partial results [block][2][rows][D + 2]
     float *pre_o, *pre_lse;       // shared part: normalised rows and log2 sums
 };
+// joins what launch_attn_tc left split (it calls it; bf16); rt_rows: queries of an item
+cudaError_t launch_attn_join(const AttnParams &p, int rt_rows, int blocks, cudaStream_t s);
 cudaError_t launch_attn_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_attn_mma(const AttnParams &p, int sms, cudaStream_t s);  // bf16
 // bf16, keys in boxes: p.box from attn_tc_box (0: this kernel does not take the call)
