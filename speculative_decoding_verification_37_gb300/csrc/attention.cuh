@@ -14,6 +14,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "tma.cuh"
 
 namespace specv {
 
@@ -29,6 +30,14 @@ __device__ __forceinline__ float lg2f(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// mbar_wait_bounded in a few instructions: the kernels wait in many places.
+__device__ __forceinline__ bool attn_wait(unsigned long long *bar, unsigned phase) {
+#pragma unroll 1
+    for (int i = 0; i < (int)kSpinLimit; ++i)
+        if (mbar_try_wait(bar, phase)) return true;
+    return false;
 }
 
 // softcap * tanh(x / softcap) as softcap * (1 - 2 / (1 + exp(2x/softcap))).

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(32 * (WR * WK * NG + 4), 1) attn_mma_kernel(At
                     }
                     v[j] = __ballot_sync(kFull, (at[j] & 2ull) == 0);
                 }
-                if (n_issued >= ST && ok) ok = mbar_wait_bounded(&sh.empty[s], (unsigned)((n_issued / ST - 1) & 1));
+                if (n_issued >= ST && ok) ok = attn_wait(&sh.empty[s], (unsigned)((n_issued / ST - 1) & 1));
 #pragma unroll
                 for (int j = 0; j < KL; ++j) {
                     if (p.key_pos) sh.kp[s][j * 32 + lane] = kp[j];
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(32 * (WR * WK * NG + 4), 1) attn_mma_kernel(At
         for (int t = (int)(u - it.u0); t < t1; ++t, ++n_done) {
             if (n_done % NG != grp) continue;
             const int s = n_done % ST, c0 = it.keys.lo + t * KT + wk * 16 * NK;
-            if (ok) ok = mbar_wait_bounded(&sh.full[s], (unsigned)((n_done / ST) & 1));
+            if (ok) ok = attn_wait(&sh.full[s], (unsigned)((n_done / ST) & 1));
             const uint32_t kb = smem_u32(sh.kv[s][0]) + ka, vb = smem_u32(sh.kv[s][1]) + va;
             float x[MT][2 * NK][4];
 #pragma unroll

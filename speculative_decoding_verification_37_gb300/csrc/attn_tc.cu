@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             };
             auto copy = [&](int r, int is_v) {
                 const int s = n % NS;
-                if (n >= NS && ok) ok = mbar_wait_bounded(&sh.empty[s], (unsigned)((n / NS - 1) & 1));
+                if (n >= NS && ok) ok = attn_wait(&sh.empty[s], (unsigned)((n / NS - 1) & 1));
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], K::kTile);
                 __syncwarp();
                 if (lane < nbox) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             const int ksteps = (p.D + 15) / 16;
             int n = 0, j = 0, item = 0;
             auto wait_full = [&](int i) {
-                if (ok) ok = mbar_wait_bounded(&sh.full[i % NS], (unsigned)((i / NS) & 1));
+                if (ok) ok = attn_wait(&sh.full[i % NS], (unsigned)((i / NS) & 1));
                 tc_fence_after();
             };
             auto scores = [&](int d, int qt, int slot) {
@@ -360,12 +360,12 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                               tc_desc(smem_u32(sh.kv[slot]) + k * (NH * 2048), 1024, NH * 1024), id_o, !(first && k == 0));
             };
             auto wait_p = [&](int i, unsigned phase) {
-                if (ok) ok = mbar_wait_bounded(&sh.p_full[i], phase);
+                if (ok) ok = attn_wait(&sh.p_full[i], phase);
                 tc_fence_after();
             };
             while (true) {
                 const int nt = (int)(min(uend, it.u0 + it.ntiles) - u);
-                if (ok) ok = mbar_wait_bounded(&sh.q_full[item % K::kQB], (unsigned)((item / K::kQB) & 1));
+                if (ok) ok = attn_wait(&sh.q_full[item % K::kQB], (unsigned)((item / K::kQB) & 1));
                 tc_fence_after();
                 if (W != 2) {
                     // S0 S1, P0 V0, S2, P1 V1, S3 ...
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
         for (int item = 0;; ++item) {
             const int qb = item % K::kQB;
             // the buffer's last item, and its rows, are done with
-            if (item >= K::kQB && ok) ok = mbar_wait_bounded(&sh.q_free[qb], (unsigned)((item / K::kQB - 1) & 1));
+            if (item >= K::kQB && ok) ok = attn_wait(&sh.q_free[qb], (unsigned)((item / K::kQB - 1) & 1));
             AttnRows<RT> &w = sh.rows[item & 1];
             attn_rows<RT, 32>(p, it, w, lane);
             __syncwarp();
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
         if constexpr (W == 2) load_item(it, 0);
         while (true) {
             const int buf = item & 1, qb = item % K::kQB;
-            if (ok) ok = mbar_wait_bounded(&sh.q_full[qb], (unsigned)((item / K::kQB) & 1));
+            if (ok) ok = attn_wait(&sh.q_full[qb], (unsigned)((item / K::kQB) & 1));
             const AttnRows<RT> &w = sh.rows[buf];
             const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), nt = t1 - t0;
             const int qp = w.qp[row], cand = w.cand[row];
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 const unsigned sp = W == 2 ? jj & 1 : (jj >> 1) & 1;
                 const int kp_mine = kp_next;
                 if (p.key_pos && t + step < t1) kp_next = key_pos_of(t + step);
-                if (ok) ok = mbar_wait_bounded(&sh.s_full[sb], sp);
+                if (ok) ok = attn_wait(&sh.s_full[sb], sp);
                 tc_fence_after();
                 const uint32_t ts = tl + kS + sb * 128 + cb;       // this thread's scores
                 const int k0 = t * KT, c0 = line.lo + k0, kb = W == 2 ? jj & 1 : W == 1 ? grp : jj & 1;
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                     const int tt = t - t0;
                     const int nv = nring + (W == 2 ? 2 * tt + 1 : tt + 1 < nt ? 2 * tt + 2 : 2 * tt + 1);
                     const int db = W == 1 ? grp : 0;
-                    if (ok) ok = mbar_wait_bounded(&sh.full[nv % NS], (unsigned)((nv / NS) & 1));
+                    if (ok) ok = attn_wait(&sh.full[nv % NS], (unsigned)((nv / NS) & 1));
                     if (W != 2 || grp == 0) {
                         unsigned char *vr = sh.kv[nv % NS] + (mrow >> 3) * (NH * 1024) + (mrow & 7) * 128;
                         uint32_t found = 0;
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 // (W > 0: the scores came after the product before, so O is still)
                 if (__any_sync(kFull, grew) && t > first) {
                     if (W == 0) {
-                        if (ok) ok = mbar_wait_bounded(&sh.pv_done[0], (unsigned)((jj - 1) & 1));
+                        if (ok) ok = attn_wait(&sh.pv_done[0], (unsigned)((jj - 1) & 1));
                         tc_fence_after();
                     }
 #pragma unroll 1
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 } else if (W == 0 && t > first) {
                     // every product's end is seen before the next is let go: the
                     // barrier's phase bit tells only neighbours apart
-                    if (ok) ok = mbar_wait_bounded(&sh.pv_done[0], (unsigned)((jj - 1) & 1));
+                    if (ok) ok = attn_wait(&sh.pv_done[0], (unsigned)((jj - 1) & 1));
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
                 const uint32_t pt = tl + kS + sb * 128 + cb / 2;
@@ -764,7 +764,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 if constexpr (W == 2) load_item(it, buf ^ 1);  // (its barrier: all scores have been read)
             }
             if (any && ok)
-                ok = mbar_wait_bounded(&sh.pv_done[acc], (unsigned)((W == 1 ? last >> 1 : last) & 1));
+                ok = attn_wait(&sh.pv_done[acc], (unsigned)((W == 1 ? last >> 1 : last) & 1));
             tc_fence_after();
             if (W != 1) {
                 auto chunk = [&](int d, float *o) {
