@@ -393,37 +393,47 @@ __device__ __forceinline__ void attn_join_row(const AttnParams &p, bool ok, int 
     const int64_t slot = (int64_t)rt_rows * (p.D + 2), o_m = (int64_t)rt_rows * p.D, o_l = o_m + rt_rows;
     const float *base = p.part + (int64_t)c0 * 2 * slot;
     auto part = [&](int c) { return base + (int64_t)c * 2 * slot + (c == 0 ? slot : 0); };
-    float m = -INFINITY;
-    for (int c = lane; c < n; c += 32) m = fmaxf(m, __ldcg(part(c) + o_m + r));
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+    // the first blocks' rows, references and weights in one round
+    float mc = -INFINITY, lc = 0.0f;
+    if (lane < n) {
+        mc = __ldcg(part(lane) + o_m + r);
+        lc = __ldcg(part(lane) + o_l + r);
+    }
+#pragma unroll 1
     for (int d0 = 0; d0 < p.D; d0 += 128) {
         const int d = d0 + lane * 4;
         const bool in = d < p.D;
         const SharedPart sp = attn_shared_part(p, ok && in, row, in ? d : 0);
-        float l = 0.0f;
+        float4 x[U];
+        auto load = [&](int c0) {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                x[i] = c0 + i < n && in ? __ldcg(reinterpret_cast<const float4 *>(part(c0 + i) + (int64_t)r * p.D + d))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        load(0);
+        float m = mc;
+        for (int c = lane + 32; c < n; c += 32) m = fmaxf(m, __ldcg(part(c) + o_m + r));
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, k));
+        float l = 0.0f, w = 0.0f, lw = 0.0f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int cb = 0; cb < n; cb += 32) {
-            float w = 0.0f, lw = 0.0f;
-            if (cb + lane < n) {
-                w = rel_weight(__ldcg(part(cb + lane) + o_m + r), m);
-                lw = __ldcg(part(cb + lane) + o_l + r) * w;
-                if (w == 0.0f) lw = 0.0f;  // that block saw no key of the row
+#pragma unroll 1
+        for (int c = 0; c < n; c += U) {
+            if ((c & 31) == 0) {  // the weights of the next 32 blocks (0: it saw no key of the row)
+                const bool mine = c + lane < n;
+                const float a = c == 0 ? mc : mine ? __ldcg(part(c + lane) + o_m + r) : -INFINITY;
+                const float b = c == 0 ? lc : mine ? __ldcg(part(c + lane) + o_l + r) : 0.0f;
+                w = mine ? rel_weight(a, m) : 0.0f;
+                lw = w == 0.0f ? 0.0f : b * w;
             }
-            const int e = min(32, n - cb);
-            for (int c = 0; c < e; c += U) {
-                float4 x[U];
+            if (c > 0) load(c);
 #pragma unroll
-                for (int i = 0; i < U; ++i)
-                    x[i] = c + i < e && in ? __ldcg(reinterpret_cast<const float4 *>(part(cb + c + i) + (int64_t)r * p.D + d))
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const float wc = __shfl_sync(kFull, w, (c + i) & 31), lc = __shfl_sync(kFull, lw, (c + i) & 31);
-                    if (c + i >= e || wc == 0.0f) continue;
-                    l += lc;
+            for (int i = 0; i < U; ++i) {
+                const float wc = __shfl_sync(kFull, w, (c + i) & 31);
+                l += __shfl_sync(kFull, lw, (c + i) & 31);
+                if (wc != 0.0f)
                     o = make_float4(fmaf(x[i].x, wc, o.x), fmaf(x[i].y, wc, o.y), fmaf(x[i].z, wc, o.z), fmaf(x[i].w, wc, o.w));
-                }
             }
         }
         if (in) attn_write<T>(p, ok, row, d, m, l, o, sp);
@@ -469,18 +479,27 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
     const ItemBlocks ib = attn_blocks(pl, it);
     const bool split = ib.c0 != ib.c1;
     float *mine = attn_part<RT>(p, blockIdx.x, ib.c0);
-    // a warp per row
+    // a warp per row, the shared part of four rows in flight
+    constexpr int NW = NT / 32, U = 4;
 #pragma unroll 1
-    for (int r = tid >> 5; r < RT; r += NT / 32) {
-        const int64_t row = w.out[r];
-        if (row < 0) continue;
+    for (int r0 = tid >> 5; r0 < RT; r0 += NW * U)
 #pragma unroll 1
         for (int d = lane * 4; d < p.D; d += 128) {
-            const float4 v = *reinterpret_cast<const float4 *>(so + r * ld + d);
-            if (split) __stcg(reinterpret_cast<float4 *>(mine + (int64_t)r * p.D + d), v);
-            else attn_write<T>(p, it.keys.ok, row, d, sm[r], sl[r], v, attn_shared_part(p, it.keys.ok, row, d));
+            SharedPart sp[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const int r = r0 + q * NW;
+                sp[q] = attn_shared_part(p, it.keys.ok && !split, r < RT ? w.out[r] : -1, d);
+            }
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+                const int r = r0 + q * NW;
+                if (r >= RT || w.out[r] < 0) continue;
+                const float4 v = *reinterpret_cast<const float4 *>(so + r * ld + d);
+                if (split) __stcg(reinterpret_cast<float4 *>(mine + (int64_t)r * p.D + d), v);
+                else attn_write<T>(p, it.keys.ok, w.out[r], d, sm[r], sl[r], v, sp[q]);
+            }
         }
-    }
     if (split) {
         for (int r = tid; r < RT; r += NT) {
             __stcg(mine + (int64_t)RT * p.D + r, sm[r]);

@@ -339,25 +339,27 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             // the next 64 columns 1,024.  16 columns of K and Q are 32 bytes; V's
             // columns are its N, contiguous (lbo: the next 64, sbo: the next 8 keys).
             constexpr uint32_t id_s = tc_idesc(KT, false), id_o = tc_idesc(NH * 64, true);
-            const int ksteps = (p.D + 15) / 16;
+            // (one thread issues everything: an operand's descriptor is one addition.
+            // Put together anew, they held the tensor cores to half their rate.)
+            const uint64_t dq = tc_desc(smem_u32(sh.q[0][0]), 16, 1024), dk = tc_desc(smem_u32(sh.kv[0]), 16, NH * 1024),
+                           dv = tc_desc(smem_u32(sh.kv[0]), 1024, NH * 1024);
             int n = 0, j = 0, item = 0;
             auto wait_full = [&](int i) {
                 if (ok) ok = attn_wait(&sh.full[i % NS], (unsigned)((i / NS) & 1));
                 tc_fence_after();
             };
             auto scores = [&](int d, int qt, int slot) {
-#pragma unroll 4
-                for (int k = 0; k < ksteps; ++k)
-                    tc_mma_ss(tmem + kS + d * 128,
-                              tc_desc(smem_u32(sh.q[item % K::kQB][qt]) + (uint32_t)(k >> 2) * kHalf + (k & 3) * 32, 16, 1024),
-                              tc_desc(smem_u32(sh.kv[slot]) + (uint32_t)(k >> 2) * 1024 + (k & 3) * 32, 16, NH * 1024), id_s,
-                              k > 0);
+                const uint64_t a = dq + (uint32_t)((item % K::kQB) * K::kQT + qt) * (K::kTile / 16), b = dk + (uint32_t)slot * (K::kTile / 16);
+#pragma unroll
+                for (int k = 0; k < NH * 4; ++k)
+                    tc_mma_ss(tmem + kS + d * 128, a + ((k >> 2) * kHalf + (k & 3) * 32) / 16, b + ((k >> 2) * 1024 + (k & 3) * 32) / 16,
+                              id_s, k > 0);
             };
             auto values = [&](int o, int pt, int slot, bool first) {
+                const uint64_t b = dv + (uint32_t)slot * (K::kTile / 16);
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
-                    tc_mma_ts(tmem + kO + o * 128, tmem + kS + pt * 128 + k * 8,
-                              tc_desc(smem_u32(sh.kv[slot]) + k * (NH * 2048), 1024, NH * 1024), id_o, !(first && k == 0));
+                    tc_mma_ts(tmem + kO + o * 128, tmem + kS + pt * 128 + k * 8, b + k * (NH * 2048 / 16), id_o, !(first && k == 0));
             };
             auto wait_p = [&](int i, unsigned phase) {
                 if (ok) ok = attn_wait(&sh.p_full[i], phase);
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                         }
                         const unsigned b = __ballot_sync(kFull, found != 0u);
                         if (lane == 0) sh.dirty[db][wq] = b;
-                        fence_async_shared();
+                        if (b) fence_async_shared();
                     }
                     bar_sync(bar, nbar);
                     dirty = (sh.dirty[db][0] | sh.dirty[db][1] | sh.dirty[db][2] | sh.dirty[db][3]) != 0u;
@@ -794,25 +796,32 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 const float f = rel_weight(m, mm);
                 constexpr int BW = NH * 8, STEP = 8 / K::kCopies;    // columns of a block; blocks between two copies
 #pragma unroll 1
-                for (int s = 0; s < 8; ++s) {
-                    const int blk = (g * STEP + s) & 7;
-                    float o[BW];
-                    if (BW == 16) tc_ld16(o, to + blk * BW);
-                    else tc_ld8(o, to + blk * BW);
+                for (int h = 0; h < 8; h += 4) {
+                    float o[4][BW];                                  // the blocks of four rounds
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint32_t at = to + ((g * STEP + h + s) & 7) * BW;
+                        if (BW == 16) tc_ld16(o[s], at);
+                        else tc_ld8(o[s], at);
+                    }
                     tc_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < BW; i += 4) {
-                        float4 *at = reinterpret_cast<float4 *>(&sh.o[row][blk * BW + i]);
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (f != 0.0f) v = make_float4(o[i] * f, o[i + 1] * f, o[i + 2] * f, o[i + 3] * f);
-                        if (poison) v.x = v.y = v.z = v.w = __int_as_float(0x7fffffff);
-                        if (s >= STEP) {
-                            const float4 b = *at;
-                            v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+                    for (int s = 0; s < 4; ++s) {
+                        const int blk = (g * STEP + h + s) & 7;
+#pragma unroll
+                        for (int i = 0; i < BW; i += 4) {
+                            float4 *at = reinterpret_cast<float4 *>(&sh.o[row][blk * BW + i]);
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (f != 0.0f) v = make_float4(o[s][i] * f, o[s][i + 1] * f, o[s][i + 2] * f, o[s][i + 3] * f);
+                            if (poison) v.x = v.y = v.z = v.w = __int_as_float(0x7fffffff);
+                            if (h + s >= STEP) {
+                                const float4 b = *at;
+                                v = make_float4(v.x + b.x, v.y + b.y, v.z + b.z, v.w + b.w);
+                            }
+                            *at = v;
                         }
-                        *at = v;
+                        sync_nt<NT>();
                     }
-                    sync_nt<NT>();
                 }
                 attn_finish<T, RT, NT>(p, sh.plan, done, w, &sh.o[0][0], NH * 64 + 4, sh.tm, sh.tl, &sh.last);
             }
