@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
     using K = TcCfg<NH, C, W>;
     using T = __nv_bfloat16;
     constexpr int RT = K::kRows, NT = K::kNT, NS = K::kRing, NC = KT / C;
-    constexpr int CH = NC < 64 ? NC : 64;  // scores a thread holds at once
+    constexpr int CH = W == 2 || NC < 64 ? 32 : 64;  // scores a thread holds at once (64 spill where W = 2)
     extern __shared__ unsigned char raw_[];
     TcSmem<NH, C, W> &sh = *reinterpret_cast<TcSmem<NH, C, W> *>(
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));

@@ -169,12 +169,12 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
     constexpr int PITCH = WRow<DP>::kPitch, NB = DP / 32;
     extern __shared__ __align__(16) unsigned char raw[];
     const AttnParams &p = wp.a;
-    // [queries: head, row][pitch], then per query lse (log2 units), slope,
-    // position, own entry
+    // [queries: head, row][pitch], then per query -lse (log2 units; -inf for none
+    // that counts), slope, position, own entry
     const int rows_max = (per_pass * p.G + 7) / 8 * 8, nq = p.H * rows_max;
     unsigned char *sq = raw;
-    float *s_lse = reinterpret_cast<float *>(raw + (size_t)nq * PITCH), *s_slope = s_lse + nq;
-    int *s_qp = reinterpret_cast<int *>(s_slope + nq), *s_own = s_qp + nq;
+    float4 *s_info = reinterpret_cast<float4 *>(raw + (size_t)nq * PITCH);
+    float *s_nlse = reinterpret_cast<float *>(s_info + nq);  // the first of them again, closer together
     __shared__ AttnPlan plan;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
     attn_plan<WNT>(p, plan, 1, WKT);
@@ -199,27 +199,41 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
             for (int i = tid; i < p.H * rp; i += WNT) {
                 const int h = i / rp, r = i - h * rp, j = j0 + r / p.G, hq = h * p.G + r % p.G;
                 int own = -1, qp = 0;
-                float lse = 0.0f, slope = 0.0f;
+                float nlse = -INFINITY, slope = 0.0f;
                 if (r < rows) {
                     const int s = slots ? slots[j] : j;
-                    lse = wp.lse_in[((int64_t)b * p.S + s) * p.Hq + hq];
-                    own = lse == -INFINITY ? -1 : cand0 + j;
+                    const float lse = wp.lse_in[((int64_t)b * p.S + s) * p.Hq + hq];
+                    if (lse != -INFINITY) {
+                        nlse = -lse * kLog2e;
+                        own = cand0 + j;
+                    }
                     qp = p.pos ? p.pos[(int64_t)b * p.S + s] : cand0 + j;
                     slope = p.slopes ? p.slopes[hq] : 0.0f;
                 }
-                s_lse[i] = lse * kLog2e;
-                s_own[i] = own;
-                s_qp[i] = qp;
-                s_slope[i] = slope;
+                s_info[i] = make_float4(nlse, slope, __int_as_float(qp), __int_as_float(own));
+                s_nlse[i] = nlse;
             }
-            for (int i = tid; i < p.H * rp * (DP / 8); i += WNT) {
-                const int row = i / (DP / 8), d = (i - row * (DP / 8)) * 8, h = row / rp, r = row - h * rp;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < rows && d < p.D) {
-                    const int j = j0 + r / p.G, s = slots ? slots[j] : j;
-                    x = ld_nc16(static_cast<const T *>(p.q) + b * p.qsb + s * p.qss + (h * p.G + r % p.G) * p.qsh + d);
-                }
-                *reinterpret_cast<uint4 *>(sq + (size_t)row * PITCH + d * 2) = x;
+            {   // a warp per head: 16-byte chunks of its rows
+                constexpr int CPR = DP / 8, U = 4;
+                for (int h = warp; h < p.H; h += WM)
+                    for (int i0 = lane; i0 < rp * CPR; i0 += 32 * U) {
+                        uint4 x[U];
+#pragma unroll
+                        for (int q = 0; q < U; ++q) {
+                            const int i = i0 + q * 32, r = i / CPR, d = (i - r * CPR) * 8;
+                            x[q] = make_uint4(0, 0, 0, 0);
+                            if (r < rows && d < p.D) {
+                                const int jr = r / p.G, j = j0 + jr, s = slots ? slots[j] : j;
+                                x[q] = ld_nc16(static_cast<const T *>(p.q) + b * p.qsb + s * p.qss +
+                                               (h * p.G + r - jr * p.G) * p.qsh + d);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < U; ++q) {
+                            const int i = i0 + q * 32, r = i / CPR, d = (i - r * CPR) * 8;
+                            if (r < rp) *reinterpret_cast<uint4 *>(sq + (size_t)(h * rp + r) * PITCH + d * 2) = x[q];
+                        }
+                    }
             }
             __syncthreads();
             // this lane's entries: rows g and g + 8 of the warp's 16
@@ -267,28 +281,37 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
                 // candidates' own entries and the window mask by query
                 const bool special = c0 + 16 > cand0 || p.window > 0;
                 float acc[2] = {0.0f, 0.0f};
+                const bool plain = !special && p.score.cap == 0.0f && !p.score.bias;
+                const float cf = p.score.scale * kLog2e;
                 auto head = [&](const uint4 (&x)[NB][2], int h) {
                     const unsigned char *qr = sq + (size_t)(h * rp + g) * PITCH + q4 * 16;
+                    const int q0 = h * rp + q4 * 2;
+#pragma unroll 2
                     for (int r0 = 0; r0 < rp; r0 += 8) {
-                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+                        float y[4] = {0.f, 0.f, 0.f, 0.f}, z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int i = 0; i < NB; ++i) {
-                            const uint4 v = *reinterpret_cast<const uint4 *>(qr + (size_t)r0 * PITCH + i * 64);
+                            const uint4 v = *reinterpret_cast<const uint4 *>(qr + r0 * PITCH + i * 64);
                             mma(y, x[i][0].x, x[i][1].x, x[i][0].y, x[i][1].y, v.x, v.y);
-                            mma(y, x[i][0].z, x[i][1].z, x[i][0].w, x[i][1].w, v.z, v.w);
+                            mma(z, x[i][0].z, x[i][1].z, x[i][0].w, x[i][1].w, v.z, v.w);
                         }
+                        if (plain) {
+                            const float2 nl = *reinterpret_cast<const float2 *>(s_nlse + q0 + r0);
+                            acc[0] += ex2f(fmaf(y[0] + z[0], cf, nl.x)) + ex2f(fmaf(y[1] + z[1], cf, nl.y));
+                            acc[1] += ex2f(fmaf(y[2] + z[2], cf, nl.x)) + ex2f(fmaf(y[3] + z[3], cf, nl.y));
+                        } else {
 #pragma unroll
-                        for (int a = 0; a < 2; ++a) {
-                            const int q = h * rp + r0 + q4 * 2 + a, own = s_own[q];
-                            const float ls = s_lse[q], slope = p.score.bias ? s_slope[q] : 0.0f;
-                            const int qp = p.score.bias || special ? s_qp[q] : 0;
+                            for (int a = 0; a < 2; ++a) {
+                                const float4 qi = s_info[q0 + r0 + a];
+                                const int own = __float_as_int(qi.w), qp = __float_as_int(qi.z);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int dist = pos_dist(qp, kp[e]);
-                                const float w = ex2f(fmaf(attn_score<false>(y[e * 2 + a], p.score, slope, dist), kLog2e, -ls));
-                                bool v = in[e] && own >= 0;
-                                if (special) v = v && c0 + e * 8 + g <= own && (p.window == 0 || dist < p.window);
-                                acc[e] += v ? w : 0.0f;
+                                for (int e = 0; e < 2; ++e) {
+                                    const int dist = pos_dist(qp, kp[e]);
+                                    const float w = ex2f(fmaf(attn_score<false>(y[e * 2 + a] + z[e * 2 + a], p.score, qi.y, dist), kLog2e, qi.x));
+                                    bool v = own >= 0;
+                                    if (special) v = c0 + e * 8 + g <= own && (p.window == 0 || dist < p.window);
+                                    acc[e] += v ? w : 0.0f;
+                                }
                             }
                         }
                     }
@@ -312,11 +335,11 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float a = acc[e];
+                    float a = in[e] ? acc[e] : 0.0f;
                     a += __shfl_xor_sync(kFull, a, 1);
                     a += __shfl_xor_sync(kFull, a, 2);
                     const int c = c0 + e * 8 + g;
-                    if (off[e] >= 0 && q4 == 0) wp.weight[b * wp.wstride + c] += a;
+                    if (in[e] && q4 == 0) wp.weight[b * wp.wstride + c] += a;
                     if (c < it.keys.hi && c >= cand0 && q4 == 1 && wp.key_pos_out && j0 == 0) {
                         const int j = c - cand0;
                         wp.key_pos_out[(int64_t)b * p.kps + c] = p.pos ? p.pos[(int64_t)b * p.S + (slots ? slots[j] : j)] : c;
@@ -332,7 +355,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
 
 template <int DP> cudaError_t launch_mma(const WeightsParams &p, int sms, cudaStream_t s) {
     // candidates a pass holds the queries of (K is read once per pass)
-    const int row = WRow<DP>::kPitch + 16, heads = p.a.H * p.a.G;
+    const int row = WRow<DP>::kPitch + 20, heads = p.a.H * p.a.G;
     int per = kQueryBytes / (heads * row);
     while (per > 1 && (int64_t)p.a.H * ((per * p.a.G + 7) / 8 * 8) * row > kQueryBytes) --per;
     if (per < 1) per = 1;
@@ -365,7 +388,7 @@ cudaError_t launch_weights(const WeightsParams &p, int dtype, int sms, cudaStrea
     if (dtype != SPEC_DTYPE_BF16) return launch_t<float>(p, sms, s);
     // one candidate's queries must fit: H * (G rounded up to 8) rows
     const int dp = p.a.D <= 64 ? 64 : p.a.D <= 128 ? 128 : 256;
-    if ((int64_t)p.a.H * ((p.a.G + 7) / 8 * 8) * (dp * 2 + 32) > 200 * 1024) return launch_t<__nv_bfloat16>(p, sms, s);
+    if ((int64_t)p.a.H * ((p.a.G + 7) / 8 * 8) * (dp * 2 + 36) > 200 * 1024) return launch_t<__nv_bfloat16>(p, sms, s);
     return dp == 64 ? launch_mma<64>(p, sms, s) : dp == 128 ? launch_mma<128>(p, sms, s) : launch_mma<256>(p, sms, s);
 }
 
