@@ -1,7 +1,7 @@
 """GPU parity of the attention over the paged cache, the entry weights and the
 eviction with the float64 oracle, through the C ABI.
 
-Tolerances.  A score's error is at most E = 2^-24 ((D + 4) scale sum|q||k| + 8
+Tolerances.  A score's error is at most E = 2^-24 ((D + 4) |scale| sum|q||k| + 8
 cap + 4 |x|): the products' float32 sum, the cap (1 - 2 / (1 + e): rounding of
 three operations and two hardware functions of 2 ulp, times the cap) and the
 bias.  A weight p moves by at most 2E relative (its own score and the
@@ -130,7 +130,7 @@ class Case:
         aq = np.abs(self.q[b].double().numpy())
         dots = max(float((aq[:, h] @ np.abs(k[:, h // self.G]).T).max()) for h in range(self.H * self.G)) if len(k) else 0.0
         reach = 0.0 if self.slopes is None else 4 * 40.0     # a farther key's weight is below 2^-57
-        return 2.0 ** -24 * ((self.D + 4) * self.score["scale"] * dots + 8 * self.score["softcap"] + reach)
+        return 2.0 ** -24 * ((self.D + 4) * abs(self.score["scale"]) * dots + 8 * self.score["softcap"] + reach)
 
     def check(self, r, rows=None):
         out, lse = r.out.double().cpu().numpy(), r.lse.double().cpu().numpy()
@@ -162,6 +162,11 @@ SHAPES = [
     dict(lens=[60, 10], S=3, H=2, G=2, D=8),
     dict(lens=[129, 130], S=33, H=1, G=1, D=160, inplace=True),
     dict(lens=[3000], S=2, H=2, G=2, D=128),                           # keys split over blocks
+    dict(lens=[300, 40], S=12, H=2, G=8, D=128, tree=True),            # 96 rows
+    dict(lens=[500, 9], S=40, H=1, G=4, D=64, tree=True),              # 160 rows: two row tiles
+    dict(lens=[20], S=300, H=1, G=1, D=64, tree=True),                 # a wide tree, ten mask words
+    dict(lens=[131, 5], S=300, H=1, G=1, D=64, inplace=True, bs=8),
+    dict(lens=[200, 60], S=7, H=2, G=2, D=64, bs=128), dict(lens=[90], S=4, H=1, G=2, D=128, bs=24),
 ]
 
 
@@ -191,6 +196,11 @@ def test_scores_and_masks(kw, dtype):
     dict(shared=90, tree=True, cap=4.0, slopes=True), dict(shared=200, window=60), dict(shared=200, docs=0.9),
     dict(shared=256, G=8, S=9, lens=[256] * 20),                       # nothing of one's own but the candidates
     dict(shared=77, bs=7, D=72),
+    # more than 128 queries a head: two query tiles
+    dict(shared=300, G=8, S=6, lens=[300, 333, 310, 301, 450, 512], window=200),
+    dict(shared=300, G=8, S=6, lens=[300, 333, 310, 301, 450, 512], docs=0.8, cap=5.0, slopes=True, D=128),
+    dict(shared=700, G=4, S=9, lens=[700 + 7 * i for i in range(17)], tree=True, cap=30.0, D=128),
+    dict(shared=129, G=16, S=10, lens=[129, 140], slopes=True, inplace=True),
 ])
 def test_shared_prefix(kw, dtype):
     kw = dict(kw)
@@ -212,15 +222,20 @@ def test_shared_prefix_equals_reading_it_per_request():
     c.check(c.run())
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_masked_places_may_hold_anything(dtype):
+# every kernel: 32, 64 and 128 rows on tcgen05, the warp instructions, the CUDA cores
+KERNELS = [("bf16", 2, 16), ("bf16", 8, 16), ("bf16", 16, 16), ("bf16", 2, 5), ("bf16", 8, 5), ("f32", 2, 16)]
+
+
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+def test_masked_places_may_hold_anything(dtype, G, bs):
     """NaN and infinities past the length, before the document, outside the
     window and in other branches do not show; visible ones stay in their rows."""
-    c = Case([70, 100], S=6, H=2, G=2, D=64, tree=True, docs=0.5, window=30, dtype=dtype, seed=9, spare=30)
+    kw = dict(S=6, H=2, G=G, D=64, bs=bs, tree=True, docs=0.5, window=30, dtype=dtype, seed=9, spare=30)
+    c = Case([70, 100], **kw)
     clean = c.run()
     c.check(clean)
     for bad in (float("nan"), float("inf"), -float("inf")):
-        dirty = Case([70, 100], S=6, H=2, G=2, D=64, tree=True, docs=0.5, window=30, dtype=dtype, seed=9, spare=30)
+        dirty = Case([70, 100], **kw)
         dirty.parent = c.parent
         for b, n in enumerate(c.lens):
             lo = max(int(c.first[b]), n - 29)            # the first position that candidate 0 sees
@@ -233,10 +248,10 @@ def test_masked_places_may_hold_anything(dtype):
         assert not torch.isfinite(r.out[:, 5]).all()
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_masked_value_in_a_tile_other_rows_see(dtype):
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+def test_masked_value_in_a_tile_other_rows_see(dtype, G, bs):
     """A non-finite V that one branch sees must not reach the others."""
-    c = Case([40], S=3, H=1, G=2, D=64, tree=True, dtype=dtype, seed=1)
+    c = Case([40], S=3, H=1, G=G, D=64, bs=bs, tree=True, dtype=dtype, seed=1)
     c.mask[0, :, 0] = [1, 0b11, 0b101]
     c.pos[0] = [40, 41, 41]
     clean = c.run()
@@ -246,14 +261,60 @@ def test_masked_value_in_a_tile_other_rows_see(dtype):
     assert torch.isnan(r.out[0, 1, :, 5]).all() and torch.equal(r.lse, clean.lse)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_rows_that_see_nothing(dtype):
-    c = Case([50, 0, 20], S=3, H=2, G=2, D=64, tree=True, dtype=dtype, seed=2)
+def test_masked_value_of_the_shared_prefix():
+    """The same where two query tiles share the keys: an entry that only some
+    requests' documents reach."""
+    c = Case([140, 150, 160], S=8, H=1, G=8, D=64, shared=130, docs=0.0, seed=14)
+    c.first = np.array([0, 60, 100], np.int32)
+    clean = c.run()
+    c.check(clean)
+    e = 80                                                # request 2 does not see it
+    c.cache[0, 1, c.stable[e // c.bs], e % c.bs] = float("inf")
+    r = c.run()
+    assert torch.equal(r.out[2], clean.out[2]) and torch.equal(r.lse, clean.lse)
+    assert not torch.isfinite(r.out[:2]).any(-1).all()
+
+
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+def test_rows_that_see_nothing(dtype, G, bs):
+    c = Case([50, 0, 20], S=3, H=2, G=G, D=64, bs=bs, tree=True, dtype=dtype, seed=2)
     c.mask[:, 1] = 0                                     # candidate 1 sees no candidate
     c.first = np.array([49, 0, 99], np.int32)            # request 2: the document starts past everything
     r = c.run()
     c.check(r)
     assert torch.isneginf(r.lse[1, 1]).all() and torch.isneginf(r.lse[2]).all()
+
+
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+def test_scales(dtype, G, bs):
+    """Negative and zero scales."""
+    for scale in (-0.2, 0.0):
+        c = Case([70, 30], S=4, H=2, G=G, D=64, bs=bs, dtype=dtype, seed=15)
+        c.score["scale"] = scale
+        c.check(c.run())
+
+
+def test_growing_maxima():
+    """Scores that rise along the keys, so that every tile brings a new maximum."""
+    for G, D in ((2, 64), (8, 128), (16, 64)):
+        c = Case([1500], S=6, H=1, G=G, D=D, seed=16)
+        ramp = torch.linspace(0, 12, 1500)
+        u = torch.nn.functional.normalize(torch.randn(D, generator=torch.Generator().manual_seed(0)), dim=0)
+        for e in range(1500):
+            c.cache[0, 0, c.table[0, e // 16], e % 16, 0] += (ramp[e] * u).to(c.dtype)
+        c.q += (6 * u).to(c.dtype)
+        c.check(c.run())
+
+
+def test_empty_batch():
+    c = Case([5], S=3, H=1, G=2, D=64)
+    (q, cache, table, lens), a = c.args()
+    r = api.verify_attention(q[:0], cache, table[:0], lens[:0], block_size=c.bs)
+    assert r.out.shape == (0, 3, 2, 64) and r.lse.shape == (0, 3, 2)
+    w, kp = torch.zeros((0, 16), device="cuda"), torch.zeros((0, 16), dtype=torch.int32, device="cuda")
+    api.attention_weights(q[:0], r.lse, cache, table[:0], lens[:0], lens[:0], w, block_size=c.bs)
+    api.evict_kv(cache, table[:0], lens[:0], w, kp, block_size=c.bs, budget=4)
+    torch.cuda.synchronize()
 
 
 def test_strides_and_views():
@@ -361,7 +422,7 @@ def test_many_requests_ragged():
     c.check(c.run(), rows=[0, 1, 122, 123, 124, 350, 511, 512, 699])
 
 
-@pytest.mark.parametrize("D,G,S,H", [(64, 2, 3, 4), (128, 1, 2, 8), (128, 4, 5, 8), (128, 4, 13, 8), (256, 1, 9, 4),
+@pytest.mark.parametrize("D,G,S,H", [(64, 2, 3, 4), (128, 1, 2, 8), (128, 4, 5, 8), (128, 4, 13, 8), (256, 1, 9, 4), (128, 8, 12, 8), (64, 4, 40, 8),
                                      (256, 2, 10, 4), (256, 4, 11, 2), (72, 8, 5, 8)])
 def test_many_tiles_per_block(D, G, S, H):
     """Long items, several to a block: the ring of stages goes round often."""
