@@ -2,6 +2,7 @@
 torch and calls the library.  No arithmetic of the method happens here."""
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Dict, Optional, Tuple
 
@@ -167,6 +168,14 @@ def commit_kv(temp_kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
                      slots=slots, blocks_in_use=blocks_in_use, flags=flags, stream=stream)
 
 
+def _allocating_on(stream):
+    """Context in which outputs and a first workspace are allocated (and the
+    workspace zeroed) on the stream the call runs on."""
+    if stream is None:
+        return nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
 @dataclass
 class AttentionOut:
     out: torch.Tensor            # [B, S, Hq, D], q's type
@@ -198,10 +207,11 @@ def verify_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     shared_len entries lie in shared_table's blocks and are read once for the
     whole batch.  A query that sees no key gets 0 and an lse of -inf."""
     B, S, Hq, D = q.shape
-    out = AttentionOut(out=torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device),
-                       lse=torch.empty((B, S, Hq), dtype=torch.float32, device=q.device))
-    if ws is None:
-        ws = workspace(L.SPEC_WS_ATTENTION_SHARED if shared_len > 0 else L.SPEC_WS_ATTENTION, B, S * Hq, D, q.device)
+    with _allocating_on(stream):
+        out = AttentionOut(out=torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device),
+                           lse=torch.empty((B, S, Hq), dtype=torch.float32, device=q.device))
+        if ws is None:
+            ws = workspace(L.SPEC_WS_ATTENTION_SHARED if shared_len > 0 else L.SPEC_WS_ATTENTION, B, S * Hq, D, q.device)
     L.spec_verify_attention(q=q, cache=cache, block_table=block_table, committed_len=committed_len,
                             block_size=block_size, out=out.out, lse=out.lse, workspace=ws, layer=layer,
                             scale=D ** -0.5 if scale is None else scale, temp_kv=temp_kv, tree_mask=tree_mask,
@@ -225,7 +235,8 @@ def attention_weights(q: torch.Tensor, lse: torch.Tensor, cache: torch.Tensor, b
     left it, q and lse those of verify_attention, and the same scoring
     arguments.  key_pos, if given, gets the new entries' positions."""
     if ws is None:
-        ws = workspace(L.SPEC_WS_COMMIT, q.shape[0], 0, 0, q.device)
+        with _allocating_on(stream):
+            ws = workspace(L.SPEC_WS_COMMIT, q.shape[0], 0, 0, q.device)
     L.spec_attention_weights(q=q, lse=lse, cache=cache, block_table=block_table, committed_len=committed_len,
                              n_slots=n_slots, weight=weight, block_size=block_size, workspace=ws, layer=layer,
                              scale=q.shape[-1] ** -0.5 if scale is None else scale, slots=slots, pos=pos,
@@ -243,7 +254,8 @@ def evict_kv(cache: torch.Tensor, block_table: torch.Tensor, committed_len: torc
     budget move into the places of the evicted ones.  cache, committed_len,
     weight and key_pos are updated on the device."""
     if ws is None:
-        ws = workspace(L.SPEC_WS_EVICT, block_table.shape[0], budget, block_table.shape[1] * block_size, cache.device)
+        with _allocating_on(stream):
+            ws = workspace(L.SPEC_WS_EVICT, block_table.shape[0], budget, block_table.shape[1] * block_size, cache.device)
     L.spec_evict_kv(cache=cache, block_table=block_table, committed_len=committed_len, weight=weight,
                     key_pos=key_pos, block_size=block_size, budget=budget, workspace=ws, sink=sink, recent=recent,
                     blocks_in_use=blocks_in_use, flags=flags, stream=stream)

@@ -395,6 +395,24 @@ def test_repeats_graphs_and_streams_agree():
     c.check(cap)
 
 
+def test_another_stream_with_a_new_workspace():
+    """The workspace's first use on a side stream: zeroed there, before the call."""
+    c = Case([700, 40], S=3, H=2, G=2, D=64, seed=21)
+    pos, a = c.args()
+    want = api.verify_attention(*pos, **a)
+    torch.cuda.synchronize()
+    for how in (lambda s: s, lambda s: s.cuda_stream):
+        api.clear_workspaces()
+        s = torch.cuda.Stream()
+        busy = torch.empty(1 << 28, device="cuda")
+        for _ in range(20):
+            busy.fill_(1.0)                               # the current stream is late
+        r = api.verify_attention(*pos, stream=how(s), **a)
+        s.synchronize()
+        assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
+        torch.cuda.synchronize()
+
+
 def test_offsets_past_32_bits():
     """Blocks at the end of a cache of more than 2^32 elements."""
     H, D, bs, S = 8, 128, 16, 2
