@@ -147,7 +147,7 @@ extern "C" int spec_verify_attention(const SpecAttentionArgs *a, void *workspace
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int sms = device_sms();
     auto launch = [&](AttnParams &x) {
-        if (a->dtype != SPEC_DTYPE_BF16) return launch_attn_simt(x, a->dtype, sms, s);
+        if (a->dtype != SPEC_DTYPE_BF16) return launch_attn_simt(x, sms, s);
         x.box = attn_tc_box(x);
         return x.box ? launch_attn_tc(x, sms, s) : launch_attn_mma(x, sms, s);
     };

@@ -1,23 +1,23 @@
-// Attention over the paged cache on the CUDA cores: any element type, head
-// size and row count.  float32 calls use it (the tensor cores would round
-// their operands).
+// Attention over the paged cache on the CUDA cores, for float32 (the tensor cores
+// would round its operands).
 //
 // Per (query, key): x = score(q . k), running maximum m and l = sum 2^(x - m),
 // o = sum 2^(x - m) v, one pass over the keys (attention.cuh: the split over
-// the grid and the join).  A block holds 16 queries and stages 32 keys at a
-// time in shared memory as float32; 8 threads share a query: each scores four
-// of the 32 keys and owns D/8 output columns.
+// the grid and the join).  A block holds 16 R queries and stages 32 keys at a
+// time in shared memory as float32; 8 threads share R queries: each scores four
+// of the 32 keys and owns D/8 output columns for each of them.
 //
 // Bound by shared-memory reads and FMA issue (per key 2*D FMA for each query),
-// not by HBM.
+// not by HBM: R = 4 reads 8 times 16 bytes for 64 FMA where R = 1 reads 5 for
+// 16.  Few queries take R = 1, whose blocks are smaller and more.
 #include "attention.cuh"
 
 namespace specv {
 namespace {
 
-constexpr int RT = 16, KT = 32, NT = 128;
+constexpr int KT = 32, NT = 128;
 
-template <typename T, int DP> struct SimtSmem {
+template <typename T, int DP, int RT> struct SimtSmem {
     float q[RT][DP];
     float k[KT][DP + 4];   // + 4: the eight keys a warp reads lie in different banks
     float v[KT][DP];
@@ -31,11 +31,12 @@ template <typename T, int DP> struct SimtSmem {
     int last;
 };
 
-template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_kernel(AttnParams p) {
+template <typename T, int DP, int R> __global__ void __launch_bounds__(NT) attn_simt_kernel(AttnParams p) {
+    constexpr int RT = 16 * R;
     extern __shared__ __align__(16) unsigned char raw[];
-    SimtSmem<T, DP> &sh = *reinterpret_cast<SimtSmem<T, DP> *>(raw);
+    SimtSmem<T, DP, RT> &sh = *reinterpret_cast<SimtSmem<T, DP, RT> *>(raw);
     constexpr int VEC = Elem<T>::VEC;
-    const int tid = threadIdx.x, row = tid >> 3, sub = tid & 7;
+    const int tid = threadIdx.x, row0 = tid >> 3, sub = tid & 7;  // rows row0, row0 + 16, ...
     const int per = p.S * p.G;
     const int64_t nrows = p.mode == 1 ? (int64_t)p.B * per : per;
     const int rtiles = (int)((nrows + RT - 1) / RT);
@@ -52,9 +53,14 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_ke
             sh.q[r][d] = sh.rows.q[r] >= 0 && d < p.D ? to_f32(static_cast<const T *>(p.q)[sh.rows.q[r] + d]) : 0.0f;
         }
         if (!it.keys.ok && u == it.u0 && it.h == 0 && it.rt == 0 && tid == 0) attn_flag(p, it.b);
-        float m = -INFINITY, l = 0.0f, o[DP / 8];
+        float m[R], l[R], o[R][DP / 8];
 #pragma unroll
-        for (int j = 0; j < DP / 8; ++j) o[j] = 0.0f;
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < DP / 8; ++j) o[r][j] = 0.0f;
+        }
         const int t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
         const int *table = p.mode == 1 ? p.stable : p.table + (int64_t)it.b * p.max_blocks;
         for (int t = (int)(u - it.u0); t < t1; ++t) {
@@ -93,69 +99,88 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_ke
                 }
             }
             __syncthreads();
-            float dot[4] = {0.f, 0.f, 0.f, 0.f};
+            float dot[R][4];
+#pragma unroll
+            for (int r = 0; r < R; ++r) dot[r][0] = dot[r][1] = dot[r][2] = dot[r][3] = 0.0f;
 #pragma unroll 4
             for (int d = 0; d < DP; d += 4) {
-                const float4 a = *reinterpret_cast<const float4 *>(&sh.q[row][d]);
+                float4 a[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) a[r] = *reinterpret_cast<const float4 *>(&sh.q[row0 + 16 * r][d]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float4 b = *reinterpret_cast<const float4 *>(&sh.k[sub + 8 * j][d]);
-                    dot[j] = fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, fmaf(a.w, b.w, dot[j]))));
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        dot[r][j] = fmaf(a[r].x, b.x, fmaf(a[r].y, b.y, fmaf(a[r].z, b.z, fmaf(a[r].w, b.w, dot[r][j]))));
                 }
             }
-            float mt = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = sub + 8 * j;
-                float x = -INFINITY;
-                if (sh.koff[k] >= 0) {
-                    const int dist = pos_dist(sh.rows.qp[row], sh.kp[k]);
-                    if (attn_visible<RT>(p, it, sh.rows, row, c0 + k, sh.kp[k], dist))
-                        x = attn_score<sizeof(T) == 4>(dot[j], p.score, sh.rows.slope[row], dist);
+            for (int r = 0; r < R; ++r) {
+                const int row = row0 + 16 * r;
+                float mt = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = sub + 8 * j;
+                    float x = -INFINITY;
+                    if (sh.koff[k] >= 0) {
+                        const int dist = pos_dist(sh.rows.qp[row], sh.kp[k]);
+                        if (attn_visible<RT>(p, it, sh.rows, row, c0 + k, sh.kp[k], dist))
+                            x = attn_score<sizeof(T) == 4>(dot[r][j], p.score, sh.rows.slope[row], dist);
+                    }
+                    dot[r][j] = x;
+                    mt = fmaxf(mt, x);
                 }
-                dot[j] = x;
-                mt = fmaxf(mt, x);
+#pragma unroll
+                for (int q = 4; q > 0; q >>= 1) mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, q));
+                // the reference m2 = max * log2(e), rounded; weights 2^(x*log2(e) - m2)
+                const float m2 = fmaxf(m[r], mt * kLog2e), ref = m2 == -INFINITY ? 0.0f : m2;
+                const float corr = rel_weight(m[r], ref);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float e = dot[r][j] == -INFINITY ? 0.0f : exp2f(fmaf(dot[r][j], kLog2e, -ref));
+                    sh.s[row][sub + 8 * j] = e;
+                    sum += e;
+                }
+#pragma unroll
+                for (int q = 4; q > 0; q >>= 1) sum += __shfl_xor_sync(kFull, sum, q);
+                l[r] = l[r] * corr + sum;
+                m[r] = m2;
+#pragma unroll
+                for (int j = 0; j < DP / 8; ++j) o[r][j] *= corr;
             }
-#pragma unroll
-            for (int q = 4; q > 0; q >>= 1) mt = fmaxf(mt, __shfl_xor_sync(kFull, mt, q));
-            // the reference m2 = max * log2(e), rounded; weights 2^(x*log2(e) - m2)
-            const float m2 = fmaxf(m, mt * kLog2e), ref = m2 == -INFINITY ? 0.0f : m2;
-            const float corr = rel_weight(m, ref);
-            float sum = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float e = dot[j] == -INFINITY ? 0.0f : exp2f(fmaf(dot[j], kLog2e, -ref));
-                sh.s[row][sub + 8 * j] = e;
-                sum += e;
-            }
-#pragma unroll
-            for (int q = 4; q > 0; q >>= 1) sum += __shfl_xor_sync(kFull, sum, q);
-            l = l * corr + sum;
-            m = m2;
             __syncwarp();
-#pragma unroll
-            for (int j = 0; j < DP / 8; ++j) o[j] *= corr;
 #pragma unroll 4
             for (int k = 0; k < KT; ++k) {
-                const float w = sh.s[row][k];
-                if (w != 0.0f) {  // a masked key's V may hold anything
+                float w[R];
 #pragma unroll
-                    for (int j = 0; j < DP / 32; ++j) {
-                        const float4 b = *reinterpret_cast<const float4 *>(&sh.v[k][(j * 8 + sub) * 4]);
-                        o[4 * j] = fmaf(w, b.x, o[4 * j]);
-                        o[4 * j + 1] = fmaf(w, b.y, o[4 * j + 1]);
-                        o[4 * j + 2] = fmaf(w, b.z, o[4 * j + 2]);
-                        o[4 * j + 3] = fmaf(w, b.w, o[4 * j + 3]);
-                    }
+                for (int r = 0; r < R; ++r) w[r] = sh.s[row0 + 16 * r][k];
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    const float4 b = *reinterpret_cast<const float4 *>(&sh.v[k][(j * 8 + sub) * 4]);
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (w[r] != 0.0f) {  // a masked key's V may hold anything
+                            o[r][4 * j] = fmaf(w[r], b.x, o[r][4 * j]);
+                            o[r][4 * j + 1] = fmaf(w[r], b.y, o[r][4 * j + 1]);
+                            o[r][4 * j + 2] = fmaf(w[r], b.z, o[r][4 * j + 2]);
+                            o[r][4 * j + 3] = fmaf(w[r], b.w, o[r][4 * j + 3]);
+                        }
                 }
             }
         }
 #pragma unroll
-        for (int j = 0; j < DP / 32; ++j)
-            *reinterpret_cast<float4 *>(&sh.o[row][(j * 8 + sub) * 4]) = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        if (sub == 0) {
-            sh.m[row] = m;
-            sh.l[row] = l;
+        for (int r = 0; r < R; ++r) {
+            const int row = row0 + 16 * r;
+#pragma unroll
+            for (int j = 0; j < DP / 32; ++j)
+                *reinterpret_cast<float4 *>(&sh.o[row][(j * 8 + sub) * 4]) =
+                    make_float4(o[r][4 * j], o[r][4 * j + 1], o[r][4 * j + 2], o[r][4 * j + 3]);
+            if (sub == 0) {
+                sh.m[row] = m[r];
+                sh.l[row] = l[r];
+            }
         }
         __syncthreads();
         attn_finish<T, RT, NT>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP, sh.m, sh.l, &sh.last);
@@ -165,25 +190,33 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) attn_simt_ke
     }
 }
 
-template <typename T, int DP> cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
-    const int smem = (int)sizeof(SimtSmem<T, DP>);
-    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <typename T, int DP, int R> cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
+    const int smem = (int)sizeof(SimtSmem<T, DP, 16 * R>);
+    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, DP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int grid = (sms < kAttnSmsMax ? sms : kAttnSmsMax) * (DP == 256 ? 2 : 4);
-    attn_simt_kernel<T, DP><<<grid, NT, smem, s>>>(p);
+    // (at most 8 / R blocks an SM: the workspace's partial results)
+    const int grid = (sms < kAttnSmsMax ? sms : kAttnSmsMax) * (DP == 256 || R == 4 ? 2 : 4);
+    attn_simt_kernel<T, DP, R><<<grid, NT, smem, s>>>(p);
     return cudaGetLastError();
 }
 
+template <typename T, int DP> cudaError_t launch_r(const AttnParams &p, int sms, cudaStream_t s) {
+    const int64_t rows = p.mode == 1 ? (int64_t)p.B * p.S * p.G : (int64_t)p.S * p.G;
+    if (rows <= 16) return launch<T, DP, 1>(p, sms, s);
+    if (rows <= 32 || DP == 256) return launch<T, DP, 2>(p, sms, s);
+    return launch<T, DP, DP == 256 ? 2 : 4>(p, sms, s);
+}
+
 template <typename T> cudaError_t launch_t(const AttnParams &p, int sms, cudaStream_t s) {
-    if (p.D <= 64) return launch<T, 64>(p, sms, s);
-    if (p.D <= 128) return launch<T, 128>(p, sms, s);
-    return launch<T, 256>(p, sms, s);
+    if (p.D <= 64) return launch_r<T, 64>(p, sms, s);
+    if (p.D <= 128) return launch_r<T, 128>(p, sms, s);
+    return launch_r<T, 256>(p, sms, s);
 }
 
 }  // namespace
 
-cudaError_t launch_attn_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s) {
-    return dtype == SPEC_DTYPE_BF16 ? launch_t<__nv_bfloat16>(p, sms, s) : launch_t<float>(p, sms, s);
+cudaError_t launch_attn_simt(const AttnParams &p, int sms, cudaStream_t s) {
+    return launch_t<float>(p, sms, s);
 }
 
 }  // namespace specv

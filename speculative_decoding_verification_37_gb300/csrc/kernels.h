@@ -262,7 +262,7 @@ struct AttnParams {
 };
 // joins what launch_attn_tc left split (it calls it; bf16); rt_rows: queries of an item
 cudaError_t launch_attn_join(const AttnParams &p, int rt_rows, int blocks, cudaStream_t s);
-cudaError_t launch_attn_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s);
+cudaError_t launch_attn_simt(const AttnParams &p, int sms, cudaStream_t s);  // f32
 cudaError_t launch_attn_mma(const AttnParams &p, int sms, cudaStream_t s);  // bf16
 // bf16, keys in boxes: p.box from attn_tc_box (0: this kernel does not take the call)
 int attn_tc_box(const AttnParams &p);
