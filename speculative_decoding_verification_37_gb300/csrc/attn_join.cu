@@ -11,6 +11,8 @@ namespace {
 constexpr int kWarps = 8;
 
 template <typename T> __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(AttnParams p, int rt_rows) {
+    // what comes next may start once every block here has
+    pdl_launch_dependents();
     pdl_wait_primary();
     const SplitItem it = p.split[blockIdx.x];
     if (it.blocks < 2) return;

@@ -237,7 +237,10 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
         }
         fence_barrier_init();
     }
-    if (W != 1) attn_begin(p);
+    if (W != 1) {  // (the marks of the shared pass have been read)
+        pdl_wait_primary();
+        attn_begin(p);
+    }
     if (warp < NT / 32) attn_plan<NT>(p, sh.plan, items, KT);
     __syncthreads();
     if (W != 1) pdl_launch_dependents();
@@ -768,6 +771,9 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
             if (any && ok)
                 ok = attn_wait(&sh.pv_done[acc], (unsigned)((W == 1 ? last >> 1 : last) & 1));
             tc_fence_after();
+            // the shared part's results are there, and its partial results done with
+            // (no wait but after a shared pass, whose end this kernel's start overlaps)
+            if (item == 0) pdl_wait_primary();
             if (W != 1) {
                 auto chunk = [&](int d, float *o) {
                     tc_ld32(o, to + d);
@@ -872,8 +878,17 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap
     cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NH, C, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = sms < kAttnSmsMax ? sms : kAttnSmsMax;
-    attn_tc_kernel<NH, C, W><<<grid, K::kThreads, smem, s>>>(p, cm, tm);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(K::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = p.mode == 0 && p.P > 0 ? 1 : 0;  // after the shared pass's join
+    e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<NH, C, W>, p, cm, tm);
     return e == cudaSuccess && W != 1 ? launch_attn_join(p, K::kRows, grid, s) : e;
 }
 
