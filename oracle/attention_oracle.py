@@ -117,7 +117,8 @@ def evict(weight, pos, length, *, budget, sink=0, recent=0) -> Optional[Eviction
     safe = [c for c in range(length) if p[c] < sink or p[c] > newest - recent]
     if len(safe) > budget:
         return None
-    others = sorted((c for c in range(length) if c not in set(safe)), key=lambda c: (-w[c], c))
+    protected = set(safe)
+    others = sorted((c for c in range(length) if c not in protected), key=lambda c: (-w[c], c))
     kept = sorted(safe + others[:budget - len(safe)])
-    holes = [c for c in range(budget) if c not in set(kept)]
+    holes = sorted(set(range(budget)) - set(kept))
     return Eviction(kept, list(zip([c for c in kept if c >= budget], holes)), budget)

@@ -4,14 +4,16 @@
 // evict_select_kernel, one block per request: the entries kept are the
 // protected ones (sinks, newest) and the heaviest others; the threshold is the
 // exact need-th largest order key, found by four 8-bit histogram passes, ties
-// by index.  It writes the list of moves (kept entries at or past the budget,
+// by index.  The keys stay in shared memory where they fit (48 K entries; read
+// from L2 in every pass, 2,304 entries took 14 us).  It writes the list of moves (kept entries at or past the budget,
 // evicted ones below it, both ascending), moves the weights and positions and
 // sets the lengths.
 //
 // evict_move_kernel: the moves' sources lie at or past the budget and their
 // destinations below it, so no move can overwrite another's source and all run
 // at once, in every layer.  Like the commit, one warp moves up to 16 KiB of a
-// token's 2*L units with the bulk-copy engine, through shared memory.
+// token's 2*L units with the bulk-copy engine, through shared memory.  It is a
+// programmatic dependent of the selection.
 #include "common.cuh"
 #include "kernels.h"
 #include "tma.cuh"
@@ -21,6 +23,8 @@ namespace {
 
 constexpr int NT = 1024;
 constexpr uint32_t kStage = 16384;
+constexpr int kKeysMax = 48 * 1024;      // entries whose keys a block keeps
+constexpr unsigned kSafe = 0xffffffffu;  // a protected entry's key (no weight has it: it would be a NaN's)
 
 struct SelectSmem {
     unsigned hist[256];
@@ -55,8 +59,10 @@ __device__ __forceinline__ unsigned long long block_prefix(unsigned long long v,
     return before + inc - v;
 }
 
-__global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p) {
+__global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p, int kept_keys) {
     __shared__ SelectSmem sh;
+    extern __shared__ unsigned keys[];  // [kept_keys]
+    pdl_launch_dependents();
     const int b = blockIdx.x, tid = threadIdx.x;
     const int len = p.len[b];
     float *weight = p.weight + (int64_t)b * p.wstride;
@@ -82,8 +88,10 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p) {
     }
     for (int c = tid; c < len; c += NT) {
         const int q = pos[c];
+        const float w = weight[c];
         newest = max(newest, q);
-        bad = bad || q < 0 || weight[c] != weight[c];
+        bad = bad || q < 0 || w != w;
+        if (c < kept_keys) keys[c] = fkey(w);
     }
     newest = __reduce_max_sync(kFull, newest);
     if ((tid & 31) == 0) sh.scan[tid >> 5] = (unsigned)newest;
@@ -91,7 +99,12 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p) {
     newest = (int)__reduce_max_sync(kFull, (int)sh.scan[tid & 31]);
     auto safe = [&](int q) { return q < p.sink || q > newest - p.recent; };
     int mine = 0;
-    for (int c = tid; c < len; c += NT) mine += safe(pos[c]);
+    for (int c = tid; c < len; c += NT)
+        if (safe(pos[c])) {
+            ++mine;
+            if (c < kept_keys) keys[c] = kSafe;
+        }
+    auto key = [&](int c) { return c < kept_keys ? keys[c] : safe(pos[c]) ? kSafe : fkey(weight[c]); };  // (this thread's)
     unsigned long long total;
     block_prefix((unsigned)mine, sh.scan2, &total);
     const int need0 = p.budget - (int)total;
@@ -111,8 +124,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p) {
         if (tid < 256) sh.hist[tid] = 0;
         __syncthreads();
         for (int c = tid; c < len; c += NT) {
-            if (safe(pos[c])) continue;
-            const unsigned k = fkey(weight[c]);
+            const unsigned k = key(c);
+            if (k == kSafe) continue;
             if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255], 1u);
         }
         __syncthreads();
@@ -147,8 +160,8 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p) {
     for (int c0 = 0; c0 < len; c0 += NT) {
         const int c = c0 + tid;
         const bool in = c < len;
-        const bool sf = in && safe(pos[c]);
-        const unsigned k = in ? fkey(weight[c]) : 0u;
+        const unsigned k = in ? key(c) : 0u;
+        const bool sf = in && k == kSafe;
         const bool eq = in && !sf && need0 > 0 && k == prefix;
         const unsigned long long tie = ties + block_prefix(eq, sh.scan2, &total);
         ties += total;
@@ -183,6 +196,7 @@ __global__ void __launch_bounds__(32) evict_move_kernel(EvictParams p, CommitGeo
     __shared__ __align__(128) unsigned char stage[kStage];
     __shared__ __align__(8) unsigned long long bar;
     if (threadIdx.x != 0) return;
+    pdl_wait_primary();
     const int grp = blockIdx.x, b = blockIdx.y;
     const int n = p.n_moves[b];
     if ((int)blockIdx.z >= n) return;
@@ -244,16 +258,28 @@ __global__ void __launch_bounds__(32) evict_move_kernel(EvictParams p, CommitGeo
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t s) {
-    evict_select_kernel<<<(unsigned)p.B, NT, 0, s>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const int64_t capacity = (int64_t)p.max_blocks * p.bs;
+    const int kept = capacity < kKeysMax ? (int)capacity : kKeysMax;
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+    if (e != cudaSuccess) return e;
+    evict_select_kernel<<<(unsigned)p.B, NT, (size_t)kept * 4, s>>>(p, kept);
+    e = cudaGetLastError();
     if (e != cudaSuccess || p.max_moves == 0) return e;
     const CommitGeom geo = commit_geometry(p.L, p.unit_bytes);
     // about 13 stages fit an SM; blocks past a request's moves leave at once
     int64_t z = ((int64_t)sms * 13 + (int64_t)geo.groups * p.B - 1) / ((int64_t)geo.groups * p.B);
     if (z > p.max_moves) z = p.max_moves;
     if (z > 1024) z = 1024;
-    evict_move_kernel<<<dim3((unsigned)geo.groups, (unsigned)p.B, (unsigned)z), 32, 0, s>>>(p, geo);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)geo.groups, (unsigned)p.B, (unsigned)z);
+    cfg.blockDim = dim3(32);
+    cfg.stream = s;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p, geo);
 }
 
 }  // namespace specv

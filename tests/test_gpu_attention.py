@@ -615,6 +615,7 @@ def check_evict(lens, budget, seed=0, sink=0, recent=0, bs=4, dtype=torch.bfloat
     dict(lens=[45, 20], budget=16, layers=9, H=8, D=128, bs=16),
     dict(lens=[40], budget=16, layers=2, H=64, D=256, bs=4),            # a unit of 32 KiB: two pieces
     dict(lens=[5000], budget=4999), dict(lens=[70] * 40, budget=33, recent=33),
+    dict(lens=[60000, 50000, 49152, 49153], budget=49000, layers=1, H=1, D=8, bs=64, ties=True, sink=2, recent=300),
 ])
 def test_evict(kw):
     assert check_evict(**{**kw, "lens": list(kw["lens"])}) >= 0
