@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "attn_params.h"
 #include "kernels.h"
 #include "spec_verify.h"
 

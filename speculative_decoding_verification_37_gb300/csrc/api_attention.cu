@@ -3,6 +3,7 @@
 // spec_evict_kv).
 #include <cmath>
 
+#include "attn_params.h"
 #include "kernels.h"
 #include "spec_verify.h"
 

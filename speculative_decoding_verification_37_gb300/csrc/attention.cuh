@@ -12,8 +12,8 @@
 // that splits nothing 3 to 4 us but joins large items with all SMs.
 #pragma once
 
+#include "attn_params.h"
 #include "common.cuh"
-#include "kernels.h"
 #include "tma.cuh"
 
 namespace specv {

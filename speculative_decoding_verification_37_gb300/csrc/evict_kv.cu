@@ -14,6 +14,7 @@
 // at once, in every layer.  Like the commit, one warp moves up to 16 KiB of a
 // token's 2*L units with the bulk-copy engine, through shared memory.  It is a
 // programmatic dependent of the selection.
+#include "attn_params.h"
 #include "common.cuh"
 #include "kernels.h"
 #include "tma.cuh"
