@@ -536,7 +536,9 @@ int spec_tree_level(const SpecTreeLevelArgs *args, void *workspace, size_t ws_by
  *   status word.
  * Limits: bf16 or f32 (all of q, cache, temp_kv, out), D * element size a
  *   multiple of 16 and D <= 256, H divides Hq, S <= 1024, B <= 32768, q, its
- *   strides, cache, temp_kv and out on 16-byte boundaries.
+ *   strides, cache, temp_kv and out on 16-byte boundaries; softcap <= 1024 in
+ *   bf16 calls (a larger one's rounding would reach the scores), and not so
+ *   small that 2 log2(e) scale / softcap overflows.
  * Arithmetic: f32 sums and softmax statistics; bf16 calls multiply on the
  *   tensor cores with the softmax weights rounded to bf16.  The result does not
  *   depend on timing: sums are taken in a fixed order.
@@ -562,7 +564,7 @@ typedef struct SpecAttentionArgs {
     const int32_t *first_pos;    /* device, int32 [B] or NULL */
     const float *slopes;         /* device, f32 [Hq] or NULL */
     float scale;                 /* finite */
-    float softcap;               /* 0 = off */
+    float softcap;               /* 0 = off; at most 1024 with bf16 */
     int32_t window;              /* 0 = off */
     int32_t shared_len;          /* 0 = off */
     const int32_t *shared_table; /* device, int32 [ceil(shared_len/block_size)] */

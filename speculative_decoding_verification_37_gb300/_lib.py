@@ -411,6 +411,13 @@ def _rows(fn: str, name: str, t: Optional[torch.Tensor], dtype, B: int, width: i
     return t.data_ptr(), t.stride(0) if B > 1 else t.shape[1]
 
 
+def _int32(fn: str, **values) -> None:
+    """ctypes would take the low 32 bits of a larger integer."""
+    for name, v in values.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{fn}: {name} = {v} does not fit in 32 bits")
+
+
 def _cache_shape(fn: str, cache: torch.Tensor, block_size: int):
     shape = cache.shape
     if len(shape) != 6 or shape[1] != 2 or shape[3] != block_size or not cache.is_contiguous():
@@ -469,6 +476,7 @@ def spec_verify_attention(*, q: torch.Tensor, cache: torch.Tensor, block_table: 
     B, mb = block_table.shape
     sb, ss, sh = _query_strides(fn, q, cache, B)
     S, Hq = q.shape[1], q.shape[2]
+    _int32(fn, layer=layer, window=window, shared_len=shared_len)
     kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
     if shared_len > 0 and (shared_table is None or shared_table.numel() * bs < shared_len):
         raise ValueError(f"{fn}: shared_len {shared_len} needs a shared_table of {-(-shared_len // bs)} blocks")
@@ -504,6 +512,7 @@ def spec_attention_weights(*, q: torch.Tensor, lse: torch.Tensor, cache: torch.T
     S, Hq = q.shape[1], q.shape[2]
     kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
     sl, sls = _rows(fn, "slots", slots, i32, B, S, dev)
+    _int32(fn, layer=layer, window=window, shared_len=shared_len, slots_stride=sls)
     w, ws = _rows(fn, "weight", weight, torch.float32, B, mb * bs, dev)
     a = SpecWeightsArgs(
         B, S, Hq, H, D, Ly, layer, _dtype_code(q), q.data_ptr(), sb, ss, sh,
@@ -529,6 +538,7 @@ def spec_evict_kv(*, cache: torch.Tensor, block_table: torch.Tensor, committed_l
     B, mb = block_table.shape
     w, ws = _rows(fn, "weight", weight, torch.float32, B, mb * bs, dev)
     kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
+    _int32(fn, budget=budget, sink=sink, recent=recent)
     a = SpecEvictArgs(
         B, Ly, H, D, bs, cache.element_size(), cache.data_ptr(), nb,
         _checked(fn, "block_table", block_table, i32, (B, mb), dev), mb, budget, sink, recent,

@@ -17,7 +17,10 @@ def workspace(kind: int, B: int, n: int, V: int, device) -> torch.Tensor:
     """A cached zero-filled workspace for (device, kind, B, n, V) (the size of
     some kinds depends on V).  Every call leaves it zeroed, so it is reused
     without clearing; calls that share it must be ordered on one stream.
-    The cache lives as long as the process; clear_workspaces() frees it."""
+    The cache lives as long as the process; clear_workspaces() frees it.
+    A call captured into a CUDA graph before any eager one of its sizes gets a
+    workspace of the graph's own, zeroed by each replay: a cached one would
+    not be zero before the first replay."""
     dev = device if isinstance(device, torch.device) else torch.device(device)
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
@@ -25,7 +28,8 @@ def workspace(kind: int, B: int, n: int, V: int, device) -> torch.Tensor:
     ws = _WORKSPACES.get(key)
     if ws is None:
         ws = L.new_workspace(kind, B, n, V, device=dev)
-        _WORKSPACES[key] = ws
+        if dev.type != "cuda" or not torch.cuda.is_current_stream_capturing():
+            _WORKSPACES[key] = ws
     return ws
 
 

@@ -23,9 +23,12 @@ template <typename A> int scored_call(const A *a, AttnParams &p) {
     if (!std::isfinite(a->scale) || !(a->softcap >= 0.0f) || a->window < 0 || a->shared_len < 0)
         return SPEC_ERR_INVALID_ARG;
     const float cap_arg = a->softcap > 0.0f ? (float)(2.0 * 1.4426950408889634074 / (double)a->softcap) : 0.0f;
-    if (!std::isfinite(a->softcap) || !std::isfinite(cap_arg)) return SPEC_ERR_INVALID_ARG;
+    if (!std::isfinite(a->softcap) || !std::isfinite(cap_arg) || !std::isfinite(a->scale * cap_arg))
+        return SPEC_ERR_INVALID_ARG;
     const int64_t e = a->dtype == SPEC_DTYPE_BF16 ? 2 : 4;
     if (a->D > SPEC_ATTENTION_MAX_D || a->D * e % 16 != 0) return SPEC_ERR_UNSUPPORTED;
+    // the bf16 kernels' tanh is exact to a few 2^-24 of the cap: 2^-12 of a score at 1024
+    if (a->dtype == SPEC_DTYPE_BF16 && a->softcap > 1024.0f) return SPEC_ERR_UNSUPPORTED;
     const int64_t capacity = (int64_t)a->max_blocks * a->block_size;
     if (capacity > 0x7fffffffLL - 2 * SPEC_ATTENTION_MAX_S || a->Hq > 65535) return SPEC_ERR_UNSUPPORTED;
     if (a->shared_len > capacity) return SPEC_ERR_INVALID_ARG;

@@ -10,6 +10,7 @@ import torch
 
 from conftest import ROOT
 from speculative_decoding_verification_37_gb300 import _lib as L
+from speculative_decoding_verification_37_gb300 import api
 from speculative_decoding_verification_37_gb300 import build as B
 
 HEADER = os.path.join(ROOT, "include", "spec_verify.h")
@@ -172,3 +173,42 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
     with pytest.raises(ValueError, match="contiguous last dimension"):
         L._query_strides("f", q.transpose(2, 3), cache, 1)
     assert L._query_strides("f", q, cache, 1) == [0, 256, 64]
+
+
+def test_softcaps_that_the_arithmetic_does_not_hold(lib):
+    """A bf16 cap past 1024 would round the scores; one far below the scale overflows."""
+    for fn, make in (("spec_verify_attention", attention), ("spec_attention_weights", weights)):
+        assert refused(lib, fn, make(softcap=1025.0)) == L.SPEC_ERR_UNSUPPORTED
+        assert refused(lib, fn, make(softcap=1e-30, scale=1e10)) == L.SPEC_ERR_INVALID_ARG
+
+
+def test_binding_refuses_integers_past_32_bits(monkeypatch):
+    monkeypatch.setattr(L, "_cache_shape", lambda fn, cache, bs: cache.shape)  # a CPU cache, nothing is launched
+    cache = torch.zeros(1, 2, 4, 16, 1, 64)
+    q, lse, w = torch.zeros(2, 3, 1, 64), torch.zeros(2, 3, 1), torch.zeros(2, 32)
+    kw = dict(cache=cache, block_table=torch.zeros(2, 2, dtype=torch.int32),
+              committed_len=torch.zeros(2, dtype=torch.int32), block_size=16, workspace=torch.zeros(1))
+    for bad in (dict(layer=1 << 32), dict(window=1 << 32), dict(window=-(1 << 31) - 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            L.spec_verify_attention(q=q, out=q, scale=1.0, **kw, **bad)
+        with pytest.raises(ValueError, match="32 bits"):
+            L.spec_attention_weights(q=q, lse=lse, n_slots=kw["committed_len"], weight=w, scale=1.0, **kw, **bad)
+    with pytest.raises(ValueError, match="32 bits"):
+        L.spec_verify_attention(q=q, out=q, scale=1.0, shared_len=1 << 32, **kw)
+    for bad in (dict(budget=(1 << 32) + 20), dict(budget=8, sink=1 << 32), dict(budget=8, recent=1 << 32)):
+        with pytest.raises(ValueError, match="32 bits"):
+            L.spec_evict_kv(weight=w, key_pos=w.int(), **kw, **bad)
+
+
+def test_a_captured_first_call_does_not_leave_its_workspace_in_the_cache(monkeypatch):
+    """Under capture the zeroing only happens at a replay."""
+    api.clear_workspaces()
+    monkeypatch.setattr(L, "new_workspace", lambda *a, device: torch.zeros(1))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    a = api.workspace(L.SPEC_WS_ATTENTION, 1, 2, 64, torch.device("cuda", 0))
+    b = api.workspace(L.SPEC_WS_ATTENTION, 1, 2, 64, torch.device("cuda", 0))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    c = api.workspace(L.SPEC_WS_ATTENTION, 1, 2, 64, torch.device("cuda", 0))
+    d = api.workspace(L.SPEC_WS_ATTENTION, 1, 2, 64, torch.device("cuda", 0))
+    api.clear_workspaces()
+    assert len({id(x) for x in (a, b, c)}) == 3 and c is d

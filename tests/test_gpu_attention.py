@@ -395,6 +395,28 @@ def test_repeats_graphs_and_streams_agree():
     c.check(cap)
 
 
+def test_captured_before_any_eager_call():
+    """The first call of its sizes under capture: two graphs and the eager
+    calls between them do not share an unzeroed workspace."""
+    c = Case([2000, 33, 900], S=4, H=2, G=4, D=128, seed=23)
+    pos, a = c.args()
+    want = api.verify_attention(*pos, **a)
+    torch.cuda.synchronize()
+    api.clear_workspaces()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, api.verify_attention(*pos, **a)))
+    eager = api.verify_attention(*pos, **a)
+    for g, r in graphs:
+        g.replay()
+        g.replay()
+    torch.cuda.synchronize()
+    for r in (eager, graphs[0][1], graphs[1][1]):
+        assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
+
+
 def test_another_stream_with_a_new_workspace():
     """The workspace's first use on a side stream: zeroed there, before the call."""
     c = Case([700, 40], S=3, H=2, G=2, D=64, seed=21)
