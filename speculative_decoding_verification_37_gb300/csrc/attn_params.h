@@ -90,6 +90,9 @@ struct WeightsParams {
     int64_t wstride;
 };
 cudaError_t launch_weights(const WeightsParams &p, int dtype, int sms, cudaStream_t s);
+// bf16 with p.a.box set (attn_tc_box); 0 candidates a pass: this kernel does not take the call
+int weights_tc_per_pass(const AttnParams &p);
+cudaError_t launch_weights_tc(const WeightsParams &p, int per_pass, int sms, cudaStream_t s);
 
 struct EvictParams {
     int B, L, bs, max_blocks, unit_bytes, budget, sink, recent, max_moves;

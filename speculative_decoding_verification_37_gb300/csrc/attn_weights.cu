@@ -386,6 +386,10 @@ template <typename T> cudaError_t launch_t(const WeightsParams &p, int sms, cuda
 
 cudaError_t launch_weights(const WeightsParams &p, int dtype, int sms, cudaStream_t s) {
     if (dtype != SPEC_DTYPE_BF16) return launch_t<float>(p, sms, s);
+    WeightsParams t = p;
+    t.a.box = attn_tc_box(p.a);
+    const int per_pass = t.a.box ? weights_tc_per_pass(p.a) : 0;
+    if (per_pass > 0) return launch_weights_tc(t, per_pass, sms, s);
     // one candidate's queries must fit: H * (G rounded up to 8) rows
     const int dp = p.a.D <= 64 ? 64 : p.a.D <= 128 ? 128 : 256;
     if ((int64_t)p.a.H * ((p.a.G + 7) / 8 * 8) * (dp * 2 + 36) > 200 * 1024) return launch_t<__nv_bfloat16>(p, sms, s);

@@ -1,0 +1,340 @@
+// The attention weight cached entries accumulate (spec_attention_weights), for
+// bf16 on the fifth-generation tensor cores.  Bound by HBM: K is read once.
+//
+// A tile is 128 entries of one request.  For each cached head K's rows are the
+// 128 rows of an MMA and the head's queries its columns, so that one thread of
+// an epilogue warp holds all scores of one entry: it adds exp(score - lse) up in
+// a register over the heads, and nothing is exchanged but one number an entry
+// between the two groups of epilogue warps, which take the heads in turn.  The
+// queries of a request, all heads, lie in shared memory; TMA boxes bring K, 128
+// KB ahead; four accumulators in TMEM keep the tensor cores, one epilogue group
+// and the other apart.
+#include "attn_tc.cuh"
+
+namespace specv {
+namespace {
+
+constexpr int KT = 128, NT = 256;                 // entries of a tile, epilogue threads
+constexpr int kColumns = 128;                     // queries of a cached head held at once
+constexpr uint32_t kQueries = 80 * 1024;          // bytes: the queries of all heads held at once
+
+template <int NH> struct WtSmem {                 // NH: 64-column halves of a head
+    static constexpr uint32_t kTile = NH * KT * 128;
+    static constexpr int kRing = 8 / NH, kInfo = (int)(kQueries / (NH * 128));
+    alignas(1024) unsigned char k[kRing][kTile];
+    alignas(1024) unsigned char q[kQueries];
+    // a query: -lse (log2 units; -inf: adds nothing), and with -slope (log2
+    // units), position, own entry
+    alignas(16) float nlse[kInfo];
+    alignas(16) float4 info[kInfo];
+    float part[2][KT];
+    AttnPlan plan;
+    alignas(8) unsigned long long full[kRing], empty[kRing], d_full[4], d_free[4], q_full;
+    uint32_t tmem;
+};
+
+__device__ __forceinline__ bool bar_any(int id, int n, bool pred) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((int)pred), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+// A request's committed candidates (by a whole warp): none where it has no keys,
+// -1 for bad data.
+__device__ __forceinline__ int slots_of(const AttnParams &p, const AttnItem &it, int lane) {
+    const int n = it.keys.ok ? p.n_slots[it.b] : 0;
+    bool bad = !it.keys.ok;
+    if (p.slots)
+        for (int j = lane; j < n; j += 32) {
+            const int s = p.slots[(int64_t)it.b * p.slots_stride + j];
+            bad = bad || s < 0 || s >= p.S;
+        }
+    if (__any_sync(kFull, bad)) return -1;
+    return it.keys.lo < it.keys.hi ? n : 0;
+}
+
+template <int NH>
+__global__ void __launch_bounds__(NT + 64, 1)
+    weights_tc_kernel(const __grid_constant__ WeightsParams wp, const __grid_constant__ CUtensorMap map, int per_pass) {
+    using Sm = WtSmem<NH>;
+    using T = __nv_bfloat16;
+    constexpr int NS = Sm::kRing;
+    extern __shared__ unsigned char raw_[];
+    Sm &sh = *reinterpret_cast<Sm *>(reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));
+    const AttnParams &p = wp.a;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sh.d_full[i], 1);
+            mbar_init(&sh.d_free[i], NT / 2);
+        }
+        mbar_init(&sh.q_full, NT);
+        fence_barrier_init();
+    }
+    if (warp < NT / 32) attn_plan<NT>(p, sh.plan, 1, KT);
+    __syncthreads();
+    int64_t u = (int64_t)blockIdx.x * sh.plan.share;
+    const int64_t uend = min(sh.plan.total, u + sh.plan.share);
+    if (u >= uend) return;
+    if (warp == 0) tc_alloc(&sh.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
+    AttnItem it = attn_find<NT>(p, sh.plan, u, 1, 1, KT);
+
+    if (warp == NT / 32) {
+        // ---------------- TMA ----------------
+        const int nbox = KT / p.box;
+        const int zero_row = (int)(2 * p.nb * p.bs);  // past the map: zeros are written
+        int n = 0;
+        while (true) {
+            const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), slots = slots_of(p, it, lane);
+            if (slots < 0 && u == it.u0 && lane == 0) attn_flag(p, it.b);
+            const int *table = p.table + (int64_t)it.b * p.max_blocks;
+            const KeyLine line = slots > 0 ? attn_line(p, it.keys) : KeyLine{0, 0};
+            for (int j0 = 0; j0 < slots; j0 += per_pass)
+                for (int t = t0; t < t1; ++t) {
+                    int r = zero_row;
+                    if (lane < nbox) {
+                        const int k = t * KT + lane * p.box, c = line.lo + k;
+                        if (k < line.entries) {
+                            const int j = (int)fast_div((unsigned)c, p.bs_div), blk = __ldg(table + j);
+                            if (blk < 0 || (int64_t)blk >= p.nb) attn_flag(p, it.b);
+                            else r = blk * p.bs + (c - j * p.bs);
+                        }
+                    }
+#pragma unroll 1
+                    for (int h = 0; h < p.H; ++h, ++n) {
+                        const int s = n % NS;
+                        if (n >= NS && ok) ok = attn_wait(&sh.empty[s], (unsigned)((n / NS - 1) & 1));
+                        if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], Sm::kTile);
+                        __syncwarp();
+                        if (lane < nbox) {
+                            const uint32_t dst = smem_u32(sh.k[s]) + (uint32_t)lane * p.box * (NH * 128);
+                            if (NH == 2) tma5(dst, &map, 0, 0, 0, r >> 3, h, &sh.full[s]);
+                            else tma3(dst, &map, 0, h, r, &sh.full[s]);
+                        }
+                    }
+                }
+            u = it.u0 + it.ntiles;
+            if (u >= uend) break;
+            it = attn_next(p, it, 1, 1, KT);
+        }
+        // no copy may land after the block has gone
+        for (int i = max(0, n - NS); i < n; ++i) ok = mbar_drain(&sh.full[i % NS], (unsigned)((i / NS) & 1)) && ok;
+    } else if (warp == NT / 32 + 1) {
+        // ---------------- MMA ----------------
+        // Operands in atoms of 8 rows x 128 bytes (64 columns).  K: the halves of the
+        // columns follow each other, 8 entries are NH * 1,024 bytes.  Queries: a
+        // head's rows of one half, then of the other.
+        const uint64_t dk = tc_desc(smem_u32(sh.k[0]), 16, NH * 1024), dq = tc_desc(smem_u32(sh.q), 16, 1024);
+        int n = 0, pass = 0;
+        while (true) {
+            const int nt = (int)(min(uend, it.u0 + it.ntiles) - u), slots = slots_of(p, it, lane);
+            if (lane == 0)
+                for (int j0 = 0; j0 < slots; j0 += per_pass, ++pass) {
+                    const int rp = (min(per_pass, slots - j0) * p.G + 15) & ~15;
+                    const uint32_t id = tc_idesc(rp, false), half = (uint32_t)rp * 128 / 16;
+                    if (ok) ok = attn_wait(&sh.q_full, (unsigned)(pass & 1));
+                    tc_fence_after();
+                    for (int t = 0; t < nt; ++t)
+#pragma unroll 1
+                        for (int h = 0; h < p.H; ++h, ++n) {
+                            const int s = n % NS, d = n & 3;
+                            if (n >= 4 && ok) ok = attn_wait(&sh.d_free[d], (unsigned)(((n >> 2) - 1) & 1));
+                            if (ok) ok = attn_wait(&sh.full[s], (unsigned)((n / NS) & 1));
+                            tc_fence_after();
+                            const uint64_t a = dk + (uint32_t)s * (Sm::kTile / 16), b = dq + (uint32_t)h * (NH * half);
+#pragma unroll
+                            for (int k = 0; k < NH * 4; ++k)
+                                tc_mma_ss(tmem + d * kColumns, a + ((k >> 2) * 1024 + (k & 3) * 32) / 16,
+                                          b + (k >> 2) * half + (k & 3) * 32 / 16, id, k > 0);
+                            tc_commit(&sh.empty[s]);
+                            tc_commit(&sh.d_full[d]);
+                        }
+                }
+            __syncwarp();
+            u = it.u0 + it.ntiles;
+            if (u >= uend) break;
+            it = attn_next(p, it, 1, 1, KT);
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        const int grp = warp >> 2, mrow = (warp & 3) * 32 + lane;  // TMEM lane = entry of the tile
+        const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const float cf = p.score.scale * kLog2e, cl = p.score.cap * kLog2e, ca = p.score.scale * p.score.cap_arg;
+        const bool cap = p.score.cap > 0.0f, bias = p.score.bias;
+        int n = 0, tiles = 0;
+        while (true) {
+            const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), slots_n = slots_of(p, it, lane);
+            const int b = it.b;
+            const int *slots = p.slots ? p.slots + (int64_t)b * p.slots_stride : nullptr, *table = p.table + (int64_t)b * p.max_blocks;
+            const int first = p.first ? p.first[b] : (int)0x80000000;
+            const int cand0 = it.keys.len - slots_n;  // the candidates' first entry
+            const KeyLine line = slots_n > 0 ? attn_line(p, it.keys) : KeyLine{0, 0};
+            for (int j0 = 0; j0 < slots_n; j0 += per_pass) {
+                // the queries (both groups are past the last pass's: its last tile's barrier)
+                const int rows = min(per_pass, slots_n - j0) * p.G, rp = (rows + 15) & ~15;
+                bool none = false;  // a query that adds nothing
+                for (int i = tid; i < p.H * rp; i += NT) {
+                    const int h = i / rp, r = i - h * rp, j = j0 + r / p.G, hq = h * p.G + r % p.G;
+                    int own = -1, qp = 0;
+                    float nlse = -INFINITY, slope = 0.0f;
+                    if (r < rows) {
+                        const int s = slots ? slots[j] : j;
+                        const float lse = wp.lse_in[((int64_t)b * p.S + s) * p.Hq + hq];
+                        if (lse != -INFINITY) {
+                            nlse = -lse * kLog2e;
+                            own = cand0 + j;
+                        } else none = true;
+                        qp = p.pos ? p.pos[(int64_t)b * p.S + s] : cand0 + j;
+                        slope = p.slopes ? -p.slopes[hq] * kLog2e : 0.0f;
+                    }
+                    sh.info[i] = make_float4(nlse, slope, __int_as_float(qp), __int_as_float(own));
+                    sh.nlse[i] = nlse;
+                }
+                constexpr int CH = NH * 8, U = 8;  // 16-byte chunks of a query; loads in flight
+#pragma unroll 1
+                for (int i0 = tid; i0 < p.H * rp * CH; i0 += NT * U) {
+                    uint4 x[U];
+#pragma unroll
+                    for (int q = 0; q < U; ++q) {
+                        const int i = i0 + q * NT, row = i / CH, d = (i - row * CH) * 8, h = row / rp, r = row - h * rp;
+                        x[q] = make_uint4(0, 0, 0, 0);
+                        if (h < p.H && r < rows) {
+                            const int jr = r / p.G, s = slots ? slots[j0 + jr] : j0 + jr;
+                            x[q] = ld_nc16(static_cast<const T *>(p.q) + b * p.qsb + s * p.qss + (h * p.G + r - jr * p.G) * p.qsh + d);
+                        }
+                    }
+#pragma unroll
+                    for (int q = 0; q < U; ++q) {
+                        const int i = i0 + q * NT, row = i / CH, c = i - row * CH, h = row / rp, r = row - h * rp;
+                        if (h >= p.H) continue;
+                        *reinterpret_cast<uint4 *>(sh.q + ((uint32_t)(h * NH + (c >> 3)) * rp + r) * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[q];
+                    }
+                }
+                fence_async_shared();
+                mbar_arrive(&sh.q_full);
+                none = bar_any(1, NT, none);
+                for (int t = t0; t < t1; ++t, ++tiles) {
+                    // this thread's entry
+                    const int c0 = line.lo + t * KT, c = c0 + mrow;
+                    bool in = c >= it.keys.lo && c < it.keys.hi;
+                    int kp = c;
+                    if (in) {
+                        const int blk = __ldg(table + fast_div((unsigned)c, p.bs_div));
+                        if (c >= cand0) {
+                            if (p.pos) kp = p.pos[(int64_t)b * p.S + (slots ? slots[c - cand0] : c - cand0)];
+                            if (grp == 0 && j0 == 0 && wp.key_pos_out) wp.key_pos_out[(int64_t)b * p.kps + c] = kp;
+                        } else if (p.key_pos) {
+                            kp = p.key_pos[(int64_t)b * p.kps + c];
+                        }
+                        in = blk >= 0 && (int64_t)blk < p.nb && kp >= first;
+                    }
+                    // every query sees every entry
+                    const bool all = c0 + KT <= cand0 && p.window == 0 && !none;
+                    float acc[2] = {0.0f, 0.0f};
+#pragma unroll 1
+                    for (int h = 0; h < p.H; ++h, ++n) {
+                        if ((n & 1) != grp) continue;
+                        if (ok) ok = attn_wait(&sh.d_full[n & 3], (unsigned)((n >> 2) & 1));
+                        tc_fence_after();
+                        const uint32_t td = tl + (n & 3) * kColumns;
+                        const float *nl = sh.nlse + h * rp;
+                        const float4 *info = sh.info + h * rp;
+#pragma unroll 1
+                        for (int r0 = 0; r0 < rows; r0 += 16) {
+                            float x[16];  // becomes the score in log2 units
+                            tc_ld16(x, td + r0);
+                            tc_wait_ld();
+                            if (cap) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) x[i] = fmaf(-2.0f * cl, __fdividef(1.0f, 1.0f + ex2f(x[i] * ca)), cl);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) x[i] *= cf;
+                            }
+                            if (bias) {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float4 qi = info[r0 + i];
+                                    x[i] = fmaf(qi.y, (float)pos_dist(__float_as_int(qi.z), kp), x[i]);
+                                }
+                            }
+                            if (all && r0 + 16 <= rows) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 l = *reinterpret_cast<const float4 *>(nl + r0 + i);
+                                    acc[0] += ex2f(x[i] + l.x) + ex2f(x[i + 1] + l.y);
+                                    acc[1] += ex2f(x[i + 2] + l.z) + ex2f(x[i + 3] + l.w);
+                                }
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float4 qi = info[r0 + i];
+                                    const int dist = pos_dist(__float_as_int(qi.z), kp);
+                                    const bool v = c <= __float_as_int(qi.w) && (p.window == 0 || dist < p.window);
+                                    const float w = ex2f(x[i] + qi.x);
+                                    acc[i & 1] += v ? w : 0.0f;
+                                }
+                            }
+                        }
+                        tc_fence_before();
+                        mbar_arrive(&sh.d_free[n & 3]);
+                    }
+                    if (grp == 1) sh.part[tiles & 1][mrow] = acc[0] + acc[1];
+                    bar_sync(1, NT);
+                    if (grp == 0 && in) wp.weight[b * wp.wstride + c] += acc[0] + acc[1] + sh.part[tiles & 1][mrow];
+                }
+            }
+            u = it.u0 + it.ntiles;
+            if (u >= uend) break;
+            it = attn_next(p, it, 1, 1, KT);
+        }
+    }
+    if (!ok && lane == 0) atomicOr(p.status, SPEC_FLAG_TIMEOUT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0) tc_dealloc(tmem);
+}
+
+template <int NH> cudaError_t launch(const WeightsParams &p, int per_pass, int sms, cudaStream_t s) {
+    constexpr int smem = (int)sizeof(WtSmem<NH>) + 1024;
+    static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
+    static_assert(WtSmem<NH>::kRing * NH == 8, "the ring");
+    CUtensorMap map;
+    if (!tc_cache_map(p.a, &map)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    weights_tc_kernel<NH><<<sms, NT + 64, smem, s>>>(p, map, per_pass);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Candidates whose queries a pass holds (K is read once per pass): at most
+// kColumns rows of a cached head and kQueries bytes, rows in sixteens.
+int weights_tc_per_pass(const AttnParams &p) {
+    int rows = (int)(kQueries / ((uint32_t)p.H * p.D * 2)) & ~15;
+    if (p.H > 1024) rows = 0;
+    if (rows > kColumns) rows = kColumns;
+    return rows / p.G < p.S ? rows / p.G : p.S;
+}
+
+cudaError_t launch_weights_tc(const WeightsParams &p, int per_pass, int sms, cudaStream_t s) {
+    return p.a.D == 64 ? launch<1>(p, per_pass, sms, s) : launch<2>(p, per_pass, sms, s);
+}
+
+}  // namespace specv
