@@ -23,10 +23,11 @@ template <int NH> struct WtSmem {                 // NH: 64-column halves of a h
     static constexpr int kRing = 8 / NH, kInfo = (int)(kQueries / (NH * 128));
     alignas(1024) unsigned char k[kRing][kTile];
     alignas(1024) unsigned char q[kQueries];
-    // a query: -lse (log2 units; -inf: adds nothing), and with -slope (log2
-    // units), position, own entry
+    // the queries: -lse (log2 units; -inf: adds nothing), -slope (log2 units),
+    // position, own entry (-1: adds nothing)
     alignas(16) float nlse[kInfo];
-    alignas(16) float4 info[kInfo];
+    alignas(16) float slope[kInfo];
+    alignas(16) int qp[kInfo], own[kInfo];
     float part[2][KT];
     AttnPlan plan;
     alignas(8) unsigned long long full[kRing], empty[kRing], d_full[4], d_free[4], q_full;
@@ -186,24 +187,6 @@ __global__ void __launch_bounds__(NT + 64, 1)
             for (int j0 = 0; j0 < slots_n; j0 += per_pass) {
                 // the queries (both groups are past the last pass's: its last tile's barrier)
                 const int rows = min(per_pass, slots_n - j0) * p.G, rp = (rows + 15) & ~15;
-                bool none = false;  // a query that adds nothing
-                for (int i = tid; i < p.H * rp; i += NT) {
-                    const int h = i / rp, r = i - h * rp, j = j0 + r / p.G, hq = h * p.G + r % p.G;
-                    int own = -1, qp = 0;
-                    float nlse = -INFINITY, slope = 0.0f;
-                    if (r < rows) {
-                        const int s = slots ? slots[j] : j;
-                        const float lse = wp.lse_in[((int64_t)b * p.S + s) * p.Hq + hq];
-                        if (lse != -INFINITY) {
-                            nlse = -lse * kLog2e;
-                            own = cand0 + j;
-                        } else none = true;
-                        qp = p.pos ? p.pos[(int64_t)b * p.S + s] : cand0 + j;
-                        slope = p.slopes ? -p.slopes[hq] * kLog2e : 0.0f;
-                    }
-                    sh.info[i] = make_float4(nlse, slope, __int_as_float(qp), __int_as_float(own));
-                    sh.nlse[i] = nlse;
-                }
                 constexpr int CH = NH * 8, U = 8;  // 16-byte chunks of a query; loads in flight
 #pragma unroll 1
                 for (int i0 = tid; i0 < p.H * rp * CH; i0 += NT * U) {
@@ -223,6 +206,26 @@ __global__ void __launch_bounds__(NT + 64, 1)
                         if (h >= p.H) continue;
                         *reinterpret_cast<uint4 *>(sh.q + ((uint32_t)(h * NH + (c >> 3)) * rp + r) * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[q];
                     }
+                }
+                bool none = false;  // a query that adds nothing
+                for (int i = tid; i < p.H * rp; i += NT) {
+                    const int h = i / rp, r = i - h * rp, j = j0 + r / p.G, hq = h * p.G + r % p.G;
+                    int own = -1, qp = 0;
+                    float nlse = -INFINITY, slope = 0.0f;
+                    if (r < rows) {
+                        const int s = slots ? slots[j] : j;
+                        const float lse = wp.lse_in[((int64_t)b * p.S + s) * p.Hq + hq];
+                        if (lse != -INFINITY) {
+                            nlse = -lse * kLog2e;
+                            own = cand0 + j;
+                        } else none = true;
+                        qp = p.pos ? p.pos[(int64_t)b * p.S + s] : cand0 + j;
+                        slope = p.slopes ? -p.slopes[hq] * kLog2e : 0.0f;
+                    }
+                    sh.nlse[i] = nlse;
+                    sh.slope[i] = slope;
+                    sh.qp[i] = qp;
+                    sh.own[i] = own;
                 }
                 fence_async_shared();
                 mbar_arrive(&sh.q_full);
@@ -251,43 +254,45 @@ __global__ void __launch_bounds__(NT + 64, 1)
                         if (ok) ok = attn_wait(&sh.d_full[n & 3], (unsigned)((n >> 2) & 1));
                         tc_fence_after();
                         const uint32_t td = tl + (n & 3) * kColumns;
-                        const float *nl = sh.nlse + h * rp;
-                        const float4 *info = sh.info + h * rp;
+                        const int q0 = h * rp;
 #pragma unroll 1
                         for (int r0 = 0; r0 < rows; r0 += 16) {
                             float x[16];  // becomes the score in log2 units
                             tc_ld16(x, td + r0);
                             tc_wait_ld();
-                            if (cap) {
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) x[i] = fmaf(-2.0f * cl, __fdividef(1.0f, 1.0f + ex2f(x[i] * ca)), cl);
-                            } else {
+                            for (int i = 0; i < 16; i += 4) {
+                                if (r0 + i >= rows) break;
+                                const int q = q0 + r0 + i;
+                                const float4 l = *reinterpret_cast<const float4 *>(sh.nlse + q);
+                                float *y = x + i;
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) x[i] *= cf;
-                            }
-                            if (bias) {
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float4 qi = info[r0 + i];
-                                    x[i] = fmaf(qi.y, (float)pos_dist(__float_as_int(qi.z), kp), x[i]);
+                                for (int e = 0; e < 4; ++e)
+                                    y[e] = cap ? fmaf(-2.0f * cl, __fdividef(1.0f, 1.0f + ex2f(y[e] * ca)), cl) : y[e] * cf;
+                                int dist[4];
+                                if (bias || !all) {
+                                    const int4 qp = *reinterpret_cast<const int4 *>(sh.qp + q);
+                                    dist[0] = pos_dist(qp.x, kp), dist[1] = pos_dist(qp.y, kp);
+                                    dist[2] = pos_dist(qp.z, kp), dist[3] = pos_dist(qp.w, kp);
                                 }
-                            }
-                            if (all && r0 + 16 <= rows) {
-#pragma unroll
-                                for (int i = 0; i < 16; i += 4) {
-                                    const float4 l = *reinterpret_cast<const float4 *>(nl + r0 + i);
-                                    acc[0] += ex2f(x[i] + l.x) + ex2f(x[i + 1] + l.y);
-                                    acc[1] += ex2f(x[i + 2] + l.z) + ex2f(x[i + 3] + l.w);
+                                if (bias) {
+                                    const float4 sl = *reinterpret_cast<const float4 *>(sh.slope + q);
+                                    y[0] = fmaf(sl.x, (float)dist[0], y[0]);
+                                    y[1] = fmaf(sl.y, (float)dist[1], y[1]);
+                                    y[2] = fmaf(sl.z, (float)dist[2], y[2]);
+                                    y[3] = fmaf(sl.w, (float)dist[3], y[3]);
                                 }
-                            } else {
+                                y[0] = ex2f(y[0] + l.x), y[1] = ex2f(y[1] + l.y);
+                                y[2] = ex2f(y[2] + l.z), y[3] = ex2f(y[3] + l.w);
+                                if (!all || r0 + i + 4 > rows) {
+                                    const int4 own = *reinterpret_cast<const int4 *>(sh.own + q);
+                                    const int at[4] = {own.x, own.y, own.z, own.w};
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float4 qi = info[r0 + i];
-                                    const int dist = pos_dist(__float_as_int(qi.z), kp);
-                                    const bool v = c <= __float_as_int(qi.w) && (p.window == 0 || dist < p.window);
-                                    const float w = ex2f(x[i] + qi.x);
-                                    acc[i & 1] += v ? w : 0.0f;
+                                    for (int e = 0; e < 4; ++e)
+                                        if (c > at[e] || (p.window > 0 && !all && dist[e] >= p.window)) y[e] = 0.0f;
                                 }
+                                acc[0] += y[0] + y[1];
+                                acc[1] += y[2] + y[3];
                             }
                         }
                         tc_fence_before();
