@@ -32,6 +32,12 @@ __device__ __forceinline__ float lg2f(float x) {
     return y;
 }
 
+__device__ __forceinline__ float rcpf(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // mbar_wait_bounded in a few instructions: the kernels wait in many places.
 __device__ __forceinline__ bool attn_wait(unsigned long long *bar, unsigned phase) {
 #pragma unroll 1
@@ -46,7 +52,7 @@ __device__ __forceinline__ bool attn_wait(unsigned long long *bar, unsigned phas
 // limits +-softcap.
 __device__ __forceinline__ float cap_score(float x, float cap, float two_log2e_over_cap) {
     const float e = ex2f(x * two_log2e_over_cap);
-    return fmaf(-2.0f * cap, __fdividef(1.0f, 1.0f + e), cap);
+    return fmaf(-2.0f * cap, rcpf(1.0f + e), cap);
 }
 
 // The score of one (query, key) pair in natural units; masks are the caller's.

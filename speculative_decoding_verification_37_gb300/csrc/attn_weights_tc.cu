@@ -230,21 +230,26 @@ __global__ void __launch_bounds__(NT + 64, 1)
                 fence_async_shared();
                 mbar_arrive(&sh.q_full);
                 none = bar_any(1, NT, none);
-                for (int t = t0; t < t1; ++t, ++tiles) {
-                    // this thread's entry
-                    const int c0 = line.lo + t * KT, c = c0 + mrow;
-                    bool in = c >= it.keys.lo && c < it.keys.hi;
-                    int kp = c;
-                    if (in) {
-                        const int blk = __ldg(table + fast_div((unsigned)c, p.bs_div));
-                        if (c >= cand0) {
-                            if (p.pos) kp = p.pos[(int64_t)b * p.S + (slots ? slots[c - cand0] : c - cand0)];
-                            if (grp == 0 && j0 == 0 && wp.key_pos_out) wp.key_pos_out[(int64_t)b * p.kps + c] = kp;
-                        } else if (p.key_pos) {
-                            kp = p.key_pos[(int64_t)b * p.kps + c];
-                        }
-                        in = blk >= 0 && (int64_t)blk < p.nb && kp >= first;
+                // this thread's entry of a tile: its block (-1: not there) and position
+                int blk_next, kp_next;
+                auto look_up = [&](int t) {
+                    const int c = line.lo + t * KT + mrow;
+                    blk_next = -1;
+                    kp_next = c;
+                    if (c < it.keys.lo || c >= it.keys.hi) return;
+                    blk_next = __ldg(table + fast_div((unsigned)c, p.bs_div));
+                    if (c >= cand0) {
+                        if (p.pos) kp_next = p.pos[(int64_t)b * p.S + (slots ? slots[c - cand0] : c - cand0)];
+                        if (grp == 0 && j0 == 0 && wp.key_pos_out) wp.key_pos_out[(int64_t)b * p.kps + c] = kp_next;
+                    } else if (p.key_pos) {
+                        kp_next = p.key_pos[(int64_t)b * p.kps + c];
                     }
+                };
+                look_up(t0);
+                for (int t = t0; t < t1; ++t, ++tiles) {
+                    const int c0 = line.lo + t * KT, c = c0 + mrow, kp = kp_next;
+                    const bool in = blk_next >= 0 && (int64_t)blk_next < p.nb && kp >= first;
+                    if (t + 1 < t1) look_up(t + 1);
                     // every query sees every entry
                     const bool all = c0 + KT <= cand0 && p.window == 0 && !none;
                     float acc[2] = {0.0f, 0.0f};
@@ -261,38 +266,41 @@ __global__ void __launch_bounds__(NT + 64, 1)
                             tc_ld16(x, td + r0);
                             tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 16; i += 4) {
-                                if (r0 + i >= rows) break;
-                                const int q = q0 + r0 + i;
-                                const float4 l = *reinterpret_cast<const float4 *>(sh.nlse + q);
-                                float *y = x + i;
+                            for (int i8 = 0; i8 < 16; i8 += 8) {
+                                if (r0 + i8 >= rows) break;
 #pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    y[e] = cap ? fmaf(-2.0f * cl, __fdividef(1.0f, 1.0f + ex2f(y[e] * ca)), cl) : y[e] * cf;
-                                int dist[4];
-                                if (bias || !all) {
-                                    const int4 qp = *reinterpret_cast<const int4 *>(sh.qp + q);
-                                    dist[0] = pos_dist(qp.x, kp), dist[1] = pos_dist(qp.y, kp);
-                                    dist[2] = pos_dist(qp.z, kp), dist[3] = pos_dist(qp.w, kp);
-                                }
-                                if (bias) {
-                                    const float4 sl = *reinterpret_cast<const float4 *>(sh.slope + q);
-                                    y[0] = fmaf(sl.x, (float)dist[0], y[0]);
-                                    y[1] = fmaf(sl.y, (float)dist[1], y[1]);
-                                    y[2] = fmaf(sl.z, (float)dist[2], y[2]);
-                                    y[3] = fmaf(sl.w, (float)dist[3], y[3]);
-                                }
-                                y[0] = ex2f(y[0] + l.x), y[1] = ex2f(y[1] + l.y);
-                                y[2] = ex2f(y[2] + l.z), y[3] = ex2f(y[3] + l.w);
-                                if (!all || r0 + i + 4 > rows) {
-                                    const int4 own = *reinterpret_cast<const int4 *>(sh.own + q);
-                                    const int at[4] = {own.x, own.y, own.z, own.w};
-#pragma unroll
+                                for (int i = i8; i < i8 + 8; i += 4) {
+                                    const int q = q0 + r0 + i;
+                                    const float4 l = *reinterpret_cast<const float4 *>(sh.nlse + q);
+                                    float *y = x + i;
+    #pragma unroll
                                     for (int e = 0; e < 4; ++e)
-                                        if (c > at[e] || (p.window > 0 && !all && dist[e] >= p.window)) y[e] = 0.0f;
-                                }
-                                acc[0] += y[0] + y[1];
-                                acc[1] += y[2] + y[3];
+                                        y[e] = cap ? fmaf(-2.0f * cl, rcpf(1.0f + ex2f(y[e] * ca)), cl) : y[e] * cf;
+                                    int dist[4];
+                                    if (bias || !all) {
+                                        const int4 qp = *reinterpret_cast<const int4 *>(sh.qp + q);
+                                        dist[0] = pos_dist(qp.x, kp), dist[1] = pos_dist(qp.y, kp);
+                                        dist[2] = pos_dist(qp.z, kp), dist[3] = pos_dist(qp.w, kp);
+                                    }
+                                    if (bias) {
+                                        const float4 sl = *reinterpret_cast<const float4 *>(sh.slope + q);
+                                        y[0] = fmaf(sl.x, (float)dist[0], y[0]);
+                                        y[1] = fmaf(sl.y, (float)dist[1], y[1]);
+                                        y[2] = fmaf(sl.z, (float)dist[2], y[2]);
+                                        y[3] = fmaf(sl.w, (float)dist[3], y[3]);
+                                    }
+                                    y[0] = ex2f(y[0] + l.x), y[1] = ex2f(y[1] + l.y);
+                                    y[2] = ex2f(y[2] + l.z), y[3] = ex2f(y[3] + l.w);
+                                    if (!all || r0 + i + 4 > rows) {
+                                        const int4 own = *reinterpret_cast<const int4 *>(sh.own + q);
+                                        const int at[4] = {own.x, own.y, own.z, own.w};
+    #pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            if (c > at[e] || (p.window > 0 && !all && dist[e] >= p.window)) y[e] = 0.0f;
+                                    }
+                                    acc[0] += y[0] + y[1];
+                                    acc[1] += y[2] + y[3];
+                                  }
                             }
                         }
                         tc_fence_before();
