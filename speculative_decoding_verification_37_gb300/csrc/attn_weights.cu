@@ -147,7 +147,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
     }
 }
 
-// bf16 version, on the warp tensor instructions; bound by HBM.
+// bf16 version, on the warp tensor instructions, for the head and page sizes
+// that attn_weights_tc.cu does not take.
 //
 // A warp owns 16 entries of a tile for all cached heads: the entries' K rows are
 // the rows (M = 16) of its products, the queries the columns (N = 8).  The order
@@ -196,6 +197,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
         for (int j0 = 0; j0 < n && !skip && it.keys.lo < it.keys.hi; j0 += per_pass) {
             const int nj = min(per_pass, n - j0), rows = nj * p.G, rp = (rows + 7) / 8 * 8;
             __syncthreads();
+            bool none = false;  // a query that adds nothing
             for (int i = tid; i < p.H * rp; i += WNT) {
                 const int h = i / rp, r = i - h * rp, j = j0 + r / p.G, hq = h * p.G + r % p.G;
                 int own = -1, qp = 0;
@@ -206,7 +208,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
                     if (lse != -INFINITY) {
                         nlse = -lse * kLog2e;
                         own = cand0 + j;
-                    }
+                    } else none = true;
                     qp = p.pos ? p.pos[(int64_t)b * p.S + s] : cand0 + j;
                     slope = p.slopes ? p.slopes[hq] : 0.0f;
                 }
@@ -235,7 +237,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
                         }
                     }
             }
-            __syncthreads();
+            none = __syncthreads_or(none);
             // this lane's entries: rows g and g + 8 of the warp's 16
             int64_t off[2], off_next[2];
             auto look_up = [&](int t, int64_t (&o)[2]) {
@@ -281,7 +283,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
                 // candidates' own entries and the window mask by query
                 const bool special = c0 + 16 > cand0 || p.window > 0;
                 float acc[2] = {0.0f, 0.0f};
-                const bool plain = !special && p.score.cap == 0.0f && !p.score.bias;
+                const bool plain = !special && !none && p.score.cap == 0.0f && !p.score.bias;
                 const float cf = p.score.scale * kLog2e;
                 auto head = [&](const uint4 (&x)[NB][2], int h) {
                     const unsigned char *qr = sq + (size_t)(h * rp + g) * PITCH + q4 * 16;
@@ -295,7 +297,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
                             mma(y, x[i][0].x, x[i][1].x, x[i][0].y, x[i][1].y, v.x, v.y);
                             mma(z, x[i][0].z, x[i][1].z, x[i][0].w, x[i][1].w, v.z, v.w);
                         }
-                        if (plain) {
+                        if (plain && r0 + 8 <= rows) {
                             const float2 nl = *reinterpret_cast<const float2 *>(s_nlse + q0 + r0);
                             acc[0] += ex2f(fmaf(y[0] + z[0], cf, nl.x)) + ex2f(fmaf(y[1] + z[1], cf, nl.y));
                             acc[1] += ex2f(fmaf(y[2] + z[2], cf, nl.x)) + ex2f(fmaf(y[3] + z[3], cf, nl.y));

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
                                     const int q = q0 + r0 + i;
                                     const float4 l = *reinterpret_cast<const float4 *>(sh.nlse + q);
                                     float *y = x + i;
-    #pragma unroll
+#pragma unroll
                                     for (int e = 0; e < 4; ++e)
                                         y[e] = cap ? fmaf(-2.0f * cl, rcpf(1.0f + ex2f(y[e] * ca)), cl) : y[e] * cf;
                                     int dist[4];
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
                                     if (!all || r0 + i + 4 > rows) {
                                         const int4 own = *reinterpret_cast<const int4 *>(sh.own + q);
                                         const int at[4] = {own.x, own.y, own.z, own.w};
-    #pragma unroll
+#pragma unroll
                                         for (int e = 0; e < 4; ++e)
                                             if (c > at[e] || (p.window > 0 && !all && dist[e] >= p.window)) y[e] = 0.0f;
                                     }

@@ -542,6 +542,40 @@ def test_entry_weights(kw, dtype, start):
             assert np.array_equal(a["key_pos"][b].cpu().numpy()[lo:n], want[lo:n])
 
 
+@pytest.mark.parametrize("kw", [
+    dict(H=3, D=128, G=4, lens=[700, 129, 128, 127]), dict(H=1, G=8, S=9, lens=[1000, 5, 0, 260]),
+    dict(H=20, S=6, lens=[300, 50]), dict(H=8, G=8, D=128, S=12, lens=[400, 260], cap=20.0),
+    dict(H=32, G=1, D=128, S=3, lens=[200, 17]), dict(bs=128, D=128, lens=[300, 128, 1]), dict(bs=8, lens=[131, 8, 9]),
+    dict(G=3, S=7, D=128, lens=[520, 90], cap=9.0, slopes=True), dict(G=5, S=11, lens=[600, 300], slopes=True, window=200),
+    dict(H=8, G=4, D=128, S=8, lens=[1500, 1100, 30, 2000] * 12, cap=30.0, slopes=True),
+    dict(H=5, G=2, S=4, lens=list(range(90, 500, 7)), gaps=True, docs=0.3), dict(H=2, G=64, D=128, S=5, lens=[300, 40]),
+])
+def test_entry_weights_of_many_tiles(kw):
+    """Odd heads, several passes over the queries, one row past a multiple of the
+    columns, long and many requests."""
+    test_entry_weights(kw, "bf16", 0)
+
+
+@pytest.mark.parametrize("bs", [16, 5])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_entry_weights_of_candidates_without_keys(bs, dtype):
+    """A candidate whose lse is -inf adds nothing, whatever K holds."""
+    c, n_slots, slots, pos, lse = weights_case(dict(D=64, bs=bs, lens=[300, 200, 40]), 5, dtype)
+    n_slots[:] = 2
+    slots[:, :2] = [0, 1]
+    lse[:] = -np.inf
+    (q, cache, table, lens), a = c.args()
+    for k in ("temp_kv", "tree_mask"):
+        a.pop(k)
+    cache.fill_(float("nan"))
+    weight = torch.rand((c.B, c.max_blocks * bs), device="cuda")
+    want = weight.clone()
+    a.update(pos=torch.from_numpy(pos).cuda(), slots=torch.from_numpy(slots).cuda())
+    api.attention_weights(q, torch.from_numpy(lse).cuda(), cache, table, lens, torch.from_numpy(n_slots).cuda(), weight, **a)
+    torch.cuda.synchronize()
+    assert torch.equal(weight, want)
+
+
 def test_entry_weights_without_slots_or_positions():
     """The chain's defaults: candidate j is slot j at its own entry."""
     c = Case([40, 9], S=4, H=1, G=2, D=64, inplace=True, seed=12)
