@@ -9,7 +9,8 @@
 //
 // Bound by shared-memory reads and FMA issue (per key 2*D FMA for each query),
 // not by HBM: R = 4 reads 8 times 16 bytes for 64 FMA where R = 1 reads 5 for
-// 16.  Few queries take R = 1, whose blocks are smaller and more.
+// 16.  Few queries take R = 1, whose blocks are smaller and more.  8 requests of
+// 15 queries on up to 777 entries of 2 heads of 72: 27.6 us in a graph.
 #include "attention.cuh"
 
 namespace specv {

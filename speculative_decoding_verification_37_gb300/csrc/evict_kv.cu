@@ -5,15 +5,18 @@
 // protected ones (sinks, newest) and the heaviest others; the threshold is the
 // exact need-th largest order key, found by four 8-bit histogram passes, ties
 // by index.  The keys stay in shared memory where they fit (48 K entries; read
-// from L2 in every pass, 2,304 entries took 14 us).  It writes the list of moves (kept entries at or past the budget,
-// evicted ones below it, both ascending), moves the weights and positions and
-// sets the lengths.
+// from L2 in every pass, 2,304 entries took 14 us).  It writes the list of moves
+// (kept entries at or past the budget, evicted ones below it, both ascending),
+// moves the weights and positions and sets the lengths.  Bound by its barriers:
+// a block per request, four passes of histogram and scan.
 //
 // evict_move_kernel: the moves' sources lie at or past the budget and their
 // destinations below it, so no move can overwrite another's source and all run
 // at once, in every layer.  Like the commit, one warp moves up to 16 KiB of a
 // token's 2*L units with the bulk-copy engine, through shared memory.  It is a
-// programmatic dependent of the selection.
+// programmatic dependent of the selection.  Bound by HBM: 16 requests, 32 layers
+// of 2 x 8 heads of 128, from up to 2,304 entries to 2,048, 372 MB both ways in
+// 63 us (5.9 TB/s); both kernels 80 us.
 #include "attn_params.h"
 #include "common.cuh"
 #include "kernels.h"
