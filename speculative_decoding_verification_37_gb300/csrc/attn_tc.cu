@@ -25,7 +25,9 @@
 // 32,768, 704 us, 6.3 TB/s; the prefix of 8,192 entries for 512 x 8 queries,
 // 525 us, 1,048 TFLOP/s.  Short items are bound by what each costs alone, 5 to 6
 // us: a masked last tile, the join of the copies, the division.  On the warp
-// instructions (attn_mma.cu) the first takes 207 us and the second 1,469.
+// instructions (attn_mma.cu, pages of 4) the first takes 263 us, the second 1,198.
+// Registers are what is short: the softmax threads use all 168, and sharing them
+// out anew between the warps (88/208 to 136/184) made every case slower.
 //
 // A masked key's V may hold anything: where a tile masks a key, the softmax
 // threads look at V's rows, one each, zero what is not finite and make NaN the
