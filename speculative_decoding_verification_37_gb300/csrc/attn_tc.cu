@@ -87,7 +87,7 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
     return r != 0;
 }
 
-template <int NH, int C, int W>
+template <int NH, int C, int W, bool WH>
 __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
     attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap cache_map,
                    const __grid_constant__ CUtensorMap temp_map) {
@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
     // TMEM columns: two score tiles (P lies over the first half of each), then
     // one or two accumulators
     constexpr uint32_t kS = 0, kO = 256;
+    using Lay = TcLayout<NH, WH>;
     bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
     AttnItem it = attn_find<NT>(p, sh.plan, u, items, rtiles, KT);
 
@@ -180,20 +181,17 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], K::kTile);
                 __syncwarp();
                 if (lane < nbox) {
-                    // row groups of 8: 1,024 bytes for each half of the columns
-                    const uint32_t dst = smem_u32(sh.kv[s]) + (uint32_t)lane * p.box * (NH * 128);
+                    const uint32_t dst = smem_u32(sh.kv[s]) + (uint32_t)(lane * p.box >> 3) * Lay::group;
                     const int z = is_v && r >= 0 && r != zero_row ? r + v_row : r;
                     const int plane = 2 * (it.b * p.layers + p.layer) + is_v;
                     if (r < 0) {  // candidates: 8 rows and 64 columns at a time
                         for (int g = 0; g < p.box; g += 8)
 #pragma unroll
                             for (int h = 0; h < NH; ++h)
-                                tma4(dst + (uint32_t)(g >> 3) * (NH * 1024) + h * 1024, &temp_map, h * 64, it.h, -1 - r + g,
+                                tma4(dst + (uint32_t)(g >> 3) * Lay::group + h * Lay::half, &temp_map, h * 64, it.h, -1 - r + g,
                                      plane, &sh.full[s]);
-                    } else if (NH == 2) {
-                        tma5(dst, &cache_map, 0, 0, 0, z >> 3, it.h, &sh.full[s]);
                     } else {
-                        tma3(dst, &cache_map, 0, it.h, z, &sh.full[s]);
+                        tc_copy_box<NH, WH>(dst, &cache_map, z, it.h, &sh.full[s]);
                     }
                 }
                 ++n;
@@ -218,15 +216,15 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
         // ---------------- MMA ----------------
         if (lane == 0) {
             // Operands in atoms of 8 rows x 128 bytes (64 columns).  Q: the next 8
-            // rows 1,024 bytes on, the next 64 columns kHalf.  K and V: the halves
-            // of the columns follow each other, so 8 keys are NH * 1,024 bytes and
-            // the next 64 columns 1,024.  16 columns of K and Q are 32 bytes; V's
-            // columns are its N, contiguous (lbo: the next 64, sbo: the next 8 keys).
+            // rows 1,024 bytes on, the next 64 columns kHalf.  K and V: Lay::group and
+            // Lay::half.  16 columns of K and Q are 32 bytes; V's columns are its N,
+            // contiguous (lbo: the next 64, sbo: the next 8 keys).
             constexpr uint32_t id_s = tc_idesc(KT, false), id_o = tc_idesc(NH * 64, true);
             // (one thread issues everything: an operand's descriptor is one addition.
             // Put together anew, they held the tensor cores to half their rate.)
-            const uint64_t dq = tc_desc(smem_u32(sh.q[0][0]), 16, 1024), dk = tc_desc(smem_u32(sh.kv[0]), 16, NH * 1024),
-                           dv = tc_desc(smem_u32(sh.kv[0]), 1024, NH * 1024);
+            const uint64_t dq = tc_desc(smem_u32(sh.q[0][0]), 16, 1024), dk = tc_desc(smem_u32(sh.kv[0]), 16, Lay::group),
+                           dv = tc_desc(smem_u32(sh.kv[0]), Lay::half, Lay::group);
+            constexpr uint32_t k_half = Lay::half / 16, v_step = Lay::group * 2 / 16;  // V: 16 keys
             int n = 0, j = 0, item = 0;
             auto wait_full = [&](int i) {
                 if (ok) ok = attn_wait(&sh.full[i % NS], (unsigned)((i / NS) & 1));
@@ -236,14 +234,14 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                 const uint64_t a = dq + (uint32_t)((item % K::kQB) * K::kQT + qt) * (K::kTile / 16), b = dk + (uint32_t)slot * (K::kTile / 16);
 #pragma unroll
                 for (int k = 0; k < NH * 4; ++k)
-                    tc_mma_ss(tmem + kS + d * 128, a + ((k >> 2) * kHalf + (k & 3) * 32) / 16, b + ((k >> 2) * 1024 + (k & 3) * 32) / 16,
+                    tc_mma_ss(tmem + kS + d * 128, a + ((k >> 2) * kHalf + (k & 3) * 32) / 16, b + (k >> 2) * k_half + (k & 3) * 32 / 16,
                               id_s, k > 0);
             };
             auto values = [&](int o, int pt, int slot, bool first) {
                 const uint64_t b = dv + (uint32_t)slot * (K::kTile / 16);
 #pragma unroll
                 for (int k = 0; k < KT / 16; ++k)
-                    tc_mma_ts(tmem + kO + o * 128, tmem + kS + pt * 128 + k * 8, b + k * (NH * 2048 / 16), id_o, !(first && k == 0));
+                    tc_mma_ts(tmem + kO + o * 128, tmem + kS + pt * 128 + k * 8, b + k * v_step, id_o, !(first && k == 0));
             };
             auto wait_p = [&](int i, unsigned phase) {
                 if (ok) ok = attn_wait(&sh.p_full[i], phase);
@@ -538,17 +536,17 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                     const int db = W == 1 ? grp : 0;
                     if (ok) ok = attn_wait(&sh.full[nv % NS], (unsigned)((nv / NS) & 1));
                     if (W != 2 || grp == 0) {
-                        unsigned char *vr = sh.kv[nv % NS] + (mrow >> 3) * (NH * 1024) + (mrow & 7) * 128;
+                        unsigned char *vr = sh.kv[nv % NS] + (mrow >> 3) * Lay::group + (mrow & 7) * 128;
                         uint32_t found = 0;
 #pragma unroll 4
                         for (int i = 0; i < NH * 8; ++i) {
                             // (rows lie 128 bytes apart: neighbours start at another chunk)
-                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * 1024 + ((i + lane) & 7) * 16);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(vr + (i >> 3) * Lay::half + ((i + lane) & 7) * 16);
                             found |= nonfinite2(y.x) | nonfinite2(y.y) | nonfinite2(y.z) | nonfinite2(y.w);
                         }
                         if (found) {
                             for (int i = 0; i < NH * 8; ++i)
-                                *reinterpret_cast<uint4 *>(vr + (i >> 3) * 1024 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(vr + (i >> 3) * Lay::half + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
                         }
                         const unsigned b = __ballot_sync(kFull, found != 0u);
                         if (lane == 0) sh.dirty[db][wq] = b;
@@ -726,13 +724,13 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
 }
 
 // ---- host ------------------------------------------------------------------
-template <int NH, int C, int W>
+template <int NH, int C, int W, bool WH>
 cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {
     using K = TcCfg<NH, C, W>;
     constexpr int smem = (int)sizeof(TcSmem<NH, C, W>) + 1024;
     static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
     static_assert(K::kRows <= kAttnSlotRows * K::kQT, "partial results");
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NH, C, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NH, C, W, WH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int grid = sms < kAttnSmsMax ? sms : kAttnSmsMax;
     cudaLaunchConfig_t cfg = {};
@@ -745,25 +743,24 @@ cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = p.mode == 0 && p.P > 0 ? 1 : 0;  // after the shared pass's join
-    e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<NH, C, W>, p, cm, tm);
+    e = cudaLaunchKernelEx(&cfg, attn_tc_kernel<NH, C, W, WH>, p, cm, tm);
     return e == cudaSuccess && W != 1 ? launch_attn_join(p, K::kRows, grid, s) : e;
 }
 
-template <int NH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {
+template <int NH, bool WH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &cm, const CUtensorMap &tm, int sms, cudaStream_t s) {
     const int64_t rows = p.mode == 1 ? (int64_t)p.B * p.S * p.G : (int64_t)p.S * p.G;
-    if (rows <= 32) return launch<NH, 4, 1>(p, cm, tm, sms, s);
-    if (rows <= 64) return launch<NH, 2, 1>(p, cm, tm, sms, s);
-    if (rows <= 128 || p.mode == 0) return launch<NH, 1, 0>(p, cm, tm, sms, s);
-    return launch<NH, 1, 2>(p, cm, tm, sms, s);
+    if (rows <= 32) return launch<NH, 4, 1, WH>(p, cm, tm, sms, s);
+    if (rows <= 64) return launch<NH, 2, 1, WH>(p, cm, tm, sms, s);
+    if (rows <= 128 || p.mode == 0) return launch<NH, 1, 0, WH>(p, cm, tm, sms, s);
+    return launch<NH, 1, 2, WH>(p, cm, tm, sms, s);
 }
 
 }  // namespace
 
 // Rows of a page a box takes: the pages must be whole boxes and a tile's 128
-// keys too, 8 rows at least (a swizzle atom).  Head sizes that fill the
-// swizzle's 64 columns (others would read past their rows).
+// keys too, 8 rows at least (a swizzle atom).
 int attn_tc_box(const AttnParams &p) {
-    if ((p.D != 64 && p.D != 128) || 2 * p.nb * p.bs > 0x7fffff00LL || (int64_t)p.B * p.layers > 0x3fffffffLL) return 0;
+    if (p.D > 128 || 2 * p.nb * p.bs > 0x7fffff00LL || (int64_t)p.B * p.layers > 0x3fffffffLL) return 0;
     int box = 128;
     while (box >= 8 && p.bs % box != 0) box >>= 1;
     return box >= 8 && tc_encode_fn() ? box : 0;
@@ -781,7 +778,8 @@ cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t s) {
         ok = tc_encode(&tm, p.temp_base, 4, dims, strides, box);
     }
     if (!ok) return cudaErrorInvalidValue;
-    return p.D == 64 ? launch_nh<1>(p, cm, tm, sms, s) : launch_nh<2>(p, cm, tm, sms, s);
+    if (p.D <= 64) return launch_nh<1, true>(p, cm, tm, sms, s);
+    return p.D == 128 ? launch_nh<2, true>(p, cm, tm, sms, s) : launch_nh<2, false>(p, cm, tm, sms, s);
 }
 
 }  // namespace specv

@@ -164,6 +164,27 @@ inline bool tc_encode(CUtensorMap *m, const void *base, int rank, const cuuint64
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A tile of 128 keys in shared memory: atoms of 8 rows x 128 bytes (64 columns).
+// Heads of 128 come whole, a box of a page's rows a copy, the halves of their
+// columns next to each other; others a half a copy, zeros past their columns, and
+// then all rows of the second half behind those of the first.
+// (WH: whole; constants, because sums put together at run time cost heads of 128
+// 1 to 2%.)
+template <int NH, bool WH> struct TcLayout {
+    static constexpr uint32_t group = NH == 2 && WH ? 2048 : 1024;  // bytes from 8 rows to the next 8
+    static constexpr uint32_t half = NH == 2 && WH ? 1024 : 128 * 128;  // from a half to the other
+};
+// One box: p.box rows of head h from row r on.
+template <int NH, bool WH>
+__device__ __forceinline__ void tc_copy_box(uint32_t dst, const CUtensorMap *m, int r, int h, unsigned long long *bar) {
+    if (NH == 2 && WH) {
+        tma5(dst, m, 0, 0, 0, r >> 3, h, bar);
+    } else {
+        tma3(dst, m, 0, h, r, bar);
+        if (NH == 2) tma3(dst + TcLayout<NH, WH>::half, m, 64, h, r, bar);
+    }
+}
+
 // The layer's K and V planes, a box of p.box rows of one cached head a copy.
 inline bool tc_cache_map(const AttnParams &p, CUtensorMap *cm) {
     const cuuint64_t row = (cuuint64_t)p.H * p.D * 2, rows = (cuuint64_t)(2 * p.nb * p.bs);
@@ -172,7 +193,7 @@ inline bool tc_cache_map(const AttnParams &p, CUtensorMap *cm) {
         const cuuint32_t box[5] = {64, 8, 2, (cuuint32_t)p.box / 8, 1};
         return tc_encode(cm, p.kc, 5, dims, strides, box);
     } else {
-        const cuuint64_t dims[3] = {64, (cuuint64_t)p.H, rows}, strides[2] = {128, row};
+        const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)p.H, rows}, strides[2] = {(cuuint64_t)p.D * 2, row};
         const cuuint32_t box[3] = {64, 1, (cuuint32_t)p.box};
         return tc_encode(cm, p.kc, 3, dims, strides, box);
     }

@@ -67,7 +67,7 @@ __device__ __forceinline__ int slots_of(const AttnParams &p, const AttnItem &it,
     return it.keys.lo < it.keys.hi ? n : 0;
 }
 
-template <int NH>
+template <int NH, bool WH>
 __global__ void __launch_bounds__(NT + 64, 1)
     weights_tc_kernel(const __grid_constant__ WeightsParams wp, const __grid_constant__ CUtensorMap map, int per_pass) {
     using Sm = WtSmem<NH>;
@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    using Lay = TcLayout<NH, WH>;
     bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
     AttnItem it = attn_find<NT>(p, sh.plan, u, 1, 1, KT);
 
@@ -130,9 +131,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
                         if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], Sm::kTile);
                         __syncwarp();
                         if (lane < nbox) {
-                            const uint32_t dst = smem_u32(sh.k[s]) + (uint32_t)lane * p.box * (NH * 128);
-                            if (NH == 2) tma5(dst, &map, 0, 0, 0, r >> 3, h, &sh.full[s]);
-                            else tma3(dst, &map, 0, h, r, &sh.full[s]);
+                            tc_copy_box<NH, WH>(smem_u32(sh.k[s]) + (uint32_t)(lane * p.box >> 3) * Lay::group, &map, r, h, &sh.full[s]);
                         }
                     }
                 }
@@ -144,10 +143,8 @@ __global__ void __launch_bounds__(NT + 64, 1)
         for (int i = max(0, n - NS); i < n; ++i) ok = mbar_drain(&sh.full[i % NS], (unsigned)((i / NS) & 1)) && ok;
     } else if (warp == NT / 32 + 1) {
         // ---------------- MMA ----------------
-        // Operands in atoms of 8 rows x 128 bytes (64 columns).  K: the halves of the
-        // columns follow each other, 8 entries are NH * 1,024 bytes.  Queries: a
-        // head's rows of one half, then of the other.
-        const uint64_t dk = tc_desc(smem_u32(sh.k[0]), 16, NH * 1024), dq = tc_desc(smem_u32(sh.q), 16, 1024);
+        // Queries: a head's rows of one half of the columns, then of the other.
+        const uint64_t dk = tc_desc(smem_u32(sh.k[0]), 16, Lay::group), dq = tc_desc(smem_u32(sh.q), 16, 1024);
         int n = 0, pass = 0;
         while (true) {
             const int nt = (int)(min(uend, it.u0 + it.ntiles) - u), slots = slots_of(p, it, lane);
@@ -167,7 +164,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
                             const uint64_t a = dk + (uint32_t)s * (Sm::kTile / 16), b = dq + (uint32_t)h * (NH * half);
 #pragma unroll
                             for (int k = 0; k < NH * 4; ++k)
-                                tc_mma_ss(tmem + d * kColumns, a + ((k >> 2) * 1024 + (k & 3) * 32) / 16,
+                                tc_mma_ss(tmem + d * kColumns, a + (k >> 2) * (Lay::half / 16) + (k & 3) * 32 / 16,
                                           b + (k >> 2) * half + (k & 3) * 32 / 16, id, k > 0);
                             tc_commit(&sh.empty[s]);
                             tc_commit(&sh.d_full[d]);
@@ -203,7 +200,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
                     for (int q = 0; q < U; ++q) {
                         const int i = i0 + q * NT, row = i / CH, d = (i - row * CH) * 8, h = row / rp, r = row - h * rp;
                         x[q] = make_uint4(0, 0, 0, 0);
-                        if (h < p.H && r < rows) {
+                        if (h < p.H && r < rows && d < p.D) {
                             const int jr = r / p.G, s = slots ? slots[j0 + jr] : j0 + jr;
                             x[q] = ld_nc16(static_cast<const T *>(p.q) + b * p.qsb + s * p.qss + (h * p.G + r - jr * p.G) * p.qsh + d);
                         }
@@ -331,15 +328,15 @@ __global__ void __launch_bounds__(NT + 64, 1)
     if (warp == 0) tc_dealloc(tmem);
 }
 
-template <int NH> cudaError_t launch(const WeightsParams &p, int per_pass, int sms, cudaStream_t s) {
+template <int NH, bool WH> cudaError_t launch(const WeightsParams &p, int per_pass, int sms, cudaStream_t s) {
     constexpr int smem = (int)sizeof(WtSmem<NH>) + 1024;
     static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
     static_assert(WtSmem<NH>::kRing * NH == 8, "the ring");
     CUtensorMap map;
     if (!tc_cache_map(p.a, &map)) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<NH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(weights_tc_kernel<NH, WH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    weights_tc_kernel<NH><<<sms, NT + 64, smem, s>>>(p, map, per_pass);
+    weights_tc_kernel<NH, WH><<<sms, NT + 64, smem, s>>>(p, map, per_pass);
     return cudaGetLastError();
 }
 
@@ -348,14 +345,14 @@ template <int NH> cudaError_t launch(const WeightsParams &p, int per_pass, int s
 // Candidates whose queries a pass holds (K is read once per pass): at most
 // kColumns rows of a cached head and kQueries bytes, rows in sixteens.
 int weights_tc_per_pass(const AttnParams &p) {
-    int rows = (int)(kQueries / ((uint32_t)p.H * p.D * 2)) & ~15;
-    if (p.H > 1024) rows = 0;
+    int rows = (int)(kQueries / ((uint32_t)p.H * (p.D <= 64 ? 128 : 256))) & ~15;
     if (rows > kColumns) rows = kColumns;
     return rows / p.G < p.S ? rows / p.G : p.S;
 }
 
 cudaError_t launch_weights_tc(const WeightsParams &p, int per_pass, int sms, cudaStream_t s) {
-    return p.a.D == 64 ? launch<1>(p, per_pass, sms, s) : launch<2>(p, per_pass, sms, s);
+    if (p.a.D <= 64) return launch<1, true>(p, per_pass, sms, s);
+    return p.a.D == 128 ? launch<2, true>(p, per_pass, sms, s) : launch<2, false>(p, per_pass, sms, s);
 }
 
 }  // namespace specv

@@ -294,6 +294,34 @@ def test_scales(dtype, G, bs):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("bs", [16, 4])
+@pytest.mark.parametrize("D,G,S", [(8, 2, 5), (24, 8, 6), (40, 16, 5), (56, 3, 3), (72, 2, 5), (80, 8, 6), (96, 16, 5),
+                                   (104, 4, 3), (112, 16, 9), (120, 1, 1)])
+def test_head_sizes(D, G, S, bs):
+    """Heads that fill their tiles' columns in part: nothing of the next head's
+    columns shows, whatever they hold."""
+    kw = dict(S=S, H=2, G=G, D=D, bs=bs, tree=True, cap=20.0, slopes=True, docs=0.2, seed=D)
+    c = Case([300, 40, 129, 512], **kw)
+    clean = c.run()
+    c.check(clean)
+    dirty = Case([300, 40, 129, 512], **kw)
+    dirty.cache[..., 1, :] = float("nan")
+    dirty.temp[..., 1, :] = float("inf")
+    r = dirty.run()
+    assert torch.equal(r.out[:, :, :G], clean.out[:, :, :G]) and torch.equal(r.lse[:, :, :G], clean.lse[:, :, :G])
+
+
+@pytest.mark.parametrize("kw", [
+    dict(D=96, shared=700, G=8, S=9, lens=[700 + 7 * i for i in range(17)], tree=True, cap=30.0),
+    dict(D=72, shared=90, G=2, S=5, lens=[90, 200, 333]), dict(D=40, shared=400, G=16, S=9, lens=[500, 400, 401]),
+    dict(D=96, S=12, G=8, lens=[2000, 1500, 900], docs=0.4), dict(D=112, S=1, G=4, lens=[3000, 5, 700], inplace=True, gaps=True, window=900),
+    dict(D=80, S=40, G=4, lens=[900, 100], tree=True)])
+def test_head_sizes_of_long_and_shared_keys(kw):
+    kw = dict(kw)
+    c = Case(kw.pop("lens"), H=2, seed=3, **kw)
+    c.check(c.run())
+
+
 def test_growing_maxima():
     """Scores that rise along the keys, so that every tile brings a new maximum."""
     for G, D in ((2, 64), (8, 128), (16, 64)):
@@ -549,6 +577,7 @@ def test_entry_weights(kw, dtype, start):
     dict(G=3, S=7, D=128, lens=[520, 90], cap=9.0, slopes=True), dict(G=5, S=11, lens=[600, 300], slopes=True, window=200),
     dict(H=8, G=4, D=128, S=8, lens=[1500, 1100, 30, 2000] * 12, cap=30.0, slopes=True),
     dict(H=5, G=2, S=4, lens=list(range(90, 500, 7)), gaps=True, docs=0.3), dict(H=2, G=64, D=128, S=5, lens=[300, 40]),
+    dict(H=2, G=4, D=96, lens=[700, 129, 64]), dict(H=3, G=4, D=72, S=9, lens=[400, 30], cap=9.0), dict(H=2, G=8, D=40, S=9, lens=[300, 129]),
 ])
 def test_entry_weights_of_many_tiles(kw):
     """Odd heads, several passes over the queries, one row past a multiple of the
