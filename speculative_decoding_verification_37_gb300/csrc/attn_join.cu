@@ -10,7 +10,7 @@ namespace {
 
 constexpr int kWarps = 8;
 
-template <typename T> __global__ void __launch_bounds__(32 * kWarps) attn_join_kernel(AttnParams p, int rt_rows) {
+template <typename T> __global__ void __launch_bounds__(32 * kWarps, 4) attn_join_kernel(AttnParams p, int rt_rows) {
     // what comes next may start once every block here has
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -23,7 +23,7 @@ template <typename T> __global__ void __launch_bounds__(32 * kWarps) attn_join_k
         if (k >= nrows) return;
         const int b = p.mode == 1 ? (int)(k / per) : it.b, q = (int)(k - (p.mode == 1 ? (int64_t)b * per : 0));
         const int s = q / p.G;
-        attn_join_row<T, 8>(p, it.ok, rt_rows, blockIdx.x, it.blocks, r,
+        attn_join_row<T, 4>(p, it.ok, rt_rows, blockIdx.x, it.blocks, r,
                             ((int64_t)b * p.S + s) * p.Hq + it.h * p.G + (q - s * p.G));
     }
 }
