@@ -43,6 +43,19 @@ constexpr int KT = 128;
 constexpr uint32_t kHalf = KT * 128;  // bytes: 128 keys x 64 columns
 constexpr int kInfo = 8;              // tiles whose notes are kept
 
+// Two floats an instruction (PK), or one: the pairs' registers are neighbours,
+// which the kernel of two query tiles pays for with more spills (793 -> 801 us
+// for 512 x 8 queries on a shared prefix; the capped tree without: 283, with: 272).
+template <bool PK> __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    return PK ? __fmul2_rn(a, b) : make_float2(a.x * b.x, a.y * b.y);
+}
+template <bool PK> __device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    return PK ? __fadd2_rn(a, b) : make_float2(a.x + b.x, a.y + b.y);
+}
+template <bool PK> __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    return PK ? __ffma2_rn(a, b, c) : make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
+
 // How the two softmax groups share the work: W = 0 one group, 1 tiles in turn, 2
 // a query tile each.
 template <int NH, int C, int W> struct TcCfg {
@@ -472,22 +485,43 @@ __global__ void __launch_bounds__(TcCfg<NH, C, W>::kThreads, 1)
                         float y[32];
                         tc_ldx<32>(y, ts + i);
                         tc_wait_ld();
+                        // (bound by issue: two scores an instruction)
+                        constexpr bool PK = W != 2;
                         if (p.score.cap > 0.0f) {
+                            const float ca = scale * p.score.cap_arg, c2 = -2.0f * p.score.cap;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] = cap_score(y[e] * scale, p.score.cap, p.score.cap_arg);
+                            for (int e = 0; e < 32; e += 2) {  // cap_score
+                                float2 v = mul2<PK>(make_float2(y[e], y[e + 1]), make_float2(ca, ca));
+                                v = add2<PK>(make_float2(ex2f(v.x), ex2f(v.y)), make_float2(1.0f, 1.0f));
+                                v = fma2<PK>(make_float2(rcpf(v.x), rcpf(v.y)), make_float2(c2, c2),
+                                               make_float2(p.score.cap, p.score.cap));
+                                y[e] = v.x, y[e + 1] = v.y;
+                            }
                         } else {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) y[e] *= scale;
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 v = mul2<PK>(make_float2(y[e], y[e + 1]), make_float2(scale, scale));
+                                y[e] = v.x, y[e + 1] = v.y;
+                            }
                         }
                         const int *kp = sh.kp[kb] + cb + i;
                         if (p.score.bias) {
+                            const float2 ns = make_float2(-slope, -slope);
                             if (listed) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] = fmaf(-slope, (float)pos_dist(qp, kp[e]), y[e]);
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 d = make_float2((float)pos_dist(qp, kp[e]), (float)pos_dist(qp, kp[e + 1]));
+                                    const float2 v = fma2<PK>(ns, d, make_float2(y[e], y[e + 1]));
+                                    y[e] = v.x, y[e + 1] = v.y;
+                                }
                             } else {
                                 const float d0 = (float)(qp - (c0 + cb + i));
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) y[e] = fmaf(-slope, d0 - (float)e, y[e]);
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 d = add2<PK>(make_float2(d0, d0), make_float2((float)-e, (float)(-e - 1)));
+                                    const float2 v = fma2<PK>(ns, d, make_float2(y[e], y[e + 1]));
+                                    y[e] = v.x, y[e + 1] = v.y;
+                                }
                             }
                         }
                         if (special) {

@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(NT + 64, 1)
         // ---------------- epilogue ----------------
         const int grp = warp >> 2, mrow = (warp & 3) * 32 + lane;  // TMEM lane = entry of the tile
         const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const float cf = p.score.scale * kLog2e, cl = p.score.cap * kLog2e, ca = p.score.scale * p.score.cap_arg;
         const bool cap = p.score.cap > 0.0f, bias = p.score.bias;
+        const float cl = p.score.cap * kLog2e, cm = p.score.scale * (cap ? p.score.cap_arg : kLog2e);
         int n = 0, tiles = 0;
         while (true) {
             const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), slots_n = slots_of(p, it, lane);
@@ -279,8 +279,15 @@ __global__ void __launch_bounds__(NT + 64, 1)
                                     const float4 l = *reinterpret_cast<const float4 *>(sh.nlse + q);
                                     float *y = x + i;
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        y[e] = cap ? fmaf(-2.0f * cl, rcpf(1.0f + ex2f(y[e] * ca)), cl) : y[e] * cf;
+                                    for (int e = 0; e < 4; e += 2) {
+                                        float2 v = __fmul2_rn(make_float2(y[e], y[e + 1]), make_float2(cm, cm));
+                                        if (cap) {  // cap_score
+                                            v = __fadd2_rn(make_float2(ex2f(v.x), ex2f(v.y)), make_float2(1.0f, 1.0f));
+                                            v = __ffma2_rn(make_float2(rcpf(v.x), rcpf(v.y)), make_float2(-2.0f * cl, -2.0f * cl),
+                                                           make_float2(cl, cl));
+                                        }
+                                        y[e] = v.x, y[e + 1] = v.y;
+                                    }
                                     int dist[4];
                                     if (bias || !all) {
                                         const int4 qp = *reinterpret_cast<const int4 *>(sh.qp + q);
