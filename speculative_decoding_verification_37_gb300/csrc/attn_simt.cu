@@ -12,11 +12,18 @@
 // 16.  Few queries take R = 1, whose blocks are smaller and more.  8 requests of
 // 15 queries on up to 777 entries of 2 heads of 72: 27.6 us in a graph.
 #include "attention.cuh"
+#include "tma.cuh"
 
 namespace specv {
 namespace {
 
 constexpr int KT = 32, NT = 128;
+
+// 16 bytes, or zeros where `bytes` is 0
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 template <typename T, int DP, int RT> struct SimtSmem {
     float q[RT][DP];
@@ -25,18 +32,19 @@ template <typename T, int DP, int RT> struct SimtSmem {
     float s[RT][KT + 1];
     float o[RT][DP];
     float m[RT], l[RT];
-    int kp[KT];
-    int64_t koff[KT];      // element offset of the key's row; -1: none
+    int kp[2][KT];         // two tiles' keys: position,
+    int64_t koff[2][KT];   // element offset of the row; -1: none
     AttnRows<RT> rows;
     AttnPlan plan;
     int last;
 };
 
-template <typename T, int DP, int R> __global__ void __launch_bounds__(NT) attn_simt_kernel(AttnParams p) {
+template <typename T, int DP, int R>
+__global__ void __launch_bounds__(NT, DP == 256 || R == 4 ? 2 : 4) attn_simt_kernel(AttnParams p) {
     constexpr int RT = 16 * R;
     extern __shared__ __align__(16) unsigned char raw[];
     SimtSmem<T, DP, RT> &sh = *reinterpret_cast<SimtSmem<T, DP, RT> *>(raw);
-    constexpr int VEC = Elem<T>::VEC;
+    static_assert(sizeof(T) == 4, "rows are copied as they are");
     const int tid = threadIdx.x, row0 = tid >> 3, sub = tid & 7;  // rows row0, row0 + 16, ...
     const int per = p.S * p.G;
     const int64_t nrows = p.mode == 1 ? (int64_t)p.B * per : per;
@@ -64,42 +72,50 @@ template <typename T, int DP, int R> __global__ void __launch_bounds__(NT) attn_
         }
         const int t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
         const int *table = p.mode == 1 ? p.stable : p.table + (int64_t)it.b * p.max_blocks;
-        for (int t = (int)(u - it.u0); t < t1; ++t) {
-            const int c0 = it.keys.lo + t * KT, n = min(KT, it.keys.hi - c0);  // n <= 0: no keys
-            __syncthreads();
+        const int t0 = (int)(u - it.u0);
+        // this thread's key of a tile (the first KT threads)
+        int64_t off_next = -1;
+        int kp_next = 0;
+        auto look_up = [&](int t) {
+            const int c = it.keys.lo + t * KT + tid;
+            off_next = -1;
+            if (tid >= KT || c >= it.keys.hi) return;
+            if (p.tk && p.mode == 0 && c >= it.keys.len) {
+                off_next = (int64_t)it.b * p.tsb + ((int64_t)(c - it.keys.len) * p.H + it.h) * p.D;
+            } else {
+                off_next = entry_offset(p, table, c, it.h);
+                if (off_next < 0) attn_flag(p, it.b);
+            }
+            kp_next = key_position(p, it, c);
+        };
+        auto keep = [&](int t) {
             if (tid < KT) {
-                const int c = c0 + tid;
-                int64_t off = -1;
-                if (tid < n) {
-                    if (p.tk && p.mode == 0 && c >= it.keys.len) {
-                        off = (int64_t)it.b * p.tsb + ((int64_t)(c - it.keys.len) * p.H + it.h) * p.D;
-                    } else {
-                        off = entry_offset(p, table, c, it.h);
-                        if (off < 0) attn_flag(p, it.b);
-                    }
-                    sh.kp[tid] = key_position(p, it, c);
-                }
-                sh.koff[tid] = off;
+                sh.koff[t & 1][tid] = off_next;
+                sh.kp[t & 1][tid] = kp_next;
             }
-            __syncthreads();
-            for (int i = tid; i < KT * (DP / VEC); i += NT) {
-                const int k = i / (DP / VEC), d = (i - k * (DP / VEC)) * VEC;
-                const int64_t off = sh.koff[k];
-                float x[VEC], y[VEC];
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) x[e] = y[e] = 0.0f;
-                if (off >= 0 && d < p.D) {
-                    const bool cand = p.tk && p.mode == 0 && c0 + k >= it.keys.len;
-                    unpack<T>(ld_nc16(static_cast<const T *>(cand ? p.tk : p.kc) + off + d), x);
-                    unpack<T>(ld_nc16(static_cast<const T *>(cand ? p.tv : p.vc) + off + d), y);
-                }
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    sh.k[k][d + e] = x[e];
-                    sh.v[k][d + e] = y[e];
-                }
+        };
+        auto copy = [&](int t, bool v) {  // a tile's K or V rows, zeros where there is none
+            for (int i = tid; i < KT * (DP / 4); i += NT) {
+                const int k = i / (DP / 4), d = (i - k * (DP / 4)) * 4;
+                const int64_t off = sh.koff[t & 1][k];
+                const bool in = off >= 0 && d < p.D, cand = p.tk && p.mode == 0 && it.keys.lo + t * KT + k >= it.keys.len;
+                const T *from = static_cast<const T *>(v ? (cand ? p.tv : p.vc) : (cand ? p.tk : p.kc));
+                cp_async16(smem_u32(v ? &sh.v[k][d] : &sh.k[k][d]), in ? from + off + d : from, in ? 16 : 0);
             }
-            __syncthreads();
+        };
+        look_up(t0);
+        keep(t0);
+        __syncthreads();
+        copy(t0, false);
+        cp_async_wait_all();
+        __syncthreads();
+        // V arrives while the scores are taken, the next K during the rest
+        for (int t = t0; t < t1; ++t) {
+            const int c0 = it.keys.lo + t * KT;
+            const int *s_kp = sh.kp[t & 1];
+            const int64_t *s_koff = sh.koff[t & 1];
+            if (t + 1 < t1) look_up(t + 1);
+            copy(t, true);
             float dot[R][4];
 #pragma unroll
             for (int r = 0; r < R; ++r) dot[r][0] = dot[r][1] = dot[r][2] = dot[r][3] = 0.0f;
@@ -116,6 +132,10 @@ template <typename T, int DP, int R> __global__ void __launch_bounds__(NT) attn_
                         dot[r][j] = fmaf(a[r].x, b.x, fmaf(a[r].y, b.y, fmaf(a[r].z, b.z, fmaf(a[r].w, b.w, dot[r][j]))));
                 }
             }
+            if (t + 1 < t1) keep(t + 1);
+            cp_async_wait_all();
+            __syncthreads();
+            if (t + 1 < t1) copy(t + 1, false);
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const int row = row0 + 16 * r;
@@ -124,9 +144,9 @@ template <typename T, int DP, int R> __global__ void __launch_bounds__(NT) attn_
                 for (int j = 0; j < 4; ++j) {
                     const int k = sub + 8 * j;
                     float x = -INFINITY;
-                    if (sh.koff[k] >= 0) {
-                        const int dist = pos_dist(sh.rows.qp[row], sh.kp[k]);
-                        if (attn_visible<RT>(p, it, sh.rows, row, c0 + k, sh.kp[k], dist))
+                    if (s_koff[k] >= 0) {
+                        const int dist = pos_dist(sh.rows.qp[row], s_kp[k]);
+                        if (attn_visible<RT>(p, it, sh.rows, row, c0 + k, s_kp[k], dist))
                             x = attn_score<sizeof(T) == 4>(dot[r][j], p.score, sh.rows.slope[row], dist);
                     }
                     dot[r][j] = x;
@@ -170,6 +190,8 @@ template <typename T, int DP, int R> __global__ void __launch_bounds__(NT) attn_
                         }
                 }
             }
+            cp_async_wait_all();
+            __syncthreads();
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
