@@ -20,7 +20,7 @@
 //     are joined in shared memory in a fixed order.
 // Measured (pages of 4): 64 requests of 5 queries on 2,048 entries of 8 heads of
 // 128, 263 us, 2.1 TB/s; single queries on up to 32,768, 1,198 us, 3.7 TB/s
-// (attn_tc.cu, where the pages allow it: 108 and 704).
+// (attn_tc.cu, where the pages allow it: 106 and 698).
 // Scores and sums are f32; the softmax weights are rounded to bf16 for the
 // product with V (at most 2^-8 of each weight, what the values carry
 // themselves), their sum is taken before the rounding.

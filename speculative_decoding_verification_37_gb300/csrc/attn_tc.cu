@@ -21,9 +21,9 @@
 // scale, well within f32 and bf16).
 //
 // Measured (copy rate 6.8 TB/s, cuBLAS 1,948 TFLOP/s): 64 requests of 5 queries on
-// 2,048 entries of 8 heads of 128, 108 us, 5.0 TB/s; single queries on up to
-// 32,768, 704 us, 6.3 TB/s; the prefix of 8,192 entries for 512 x 8 queries,
-// 525 us, 1,048 TFLOP/s.  Short items are bound by what each costs alone, 5 to 6
+// 2,048 entries of 8 heads of 128, 106 us, 5.1 TB/s; single queries on up to
+// 32,768, 698 us, 6.3 TB/s; the prefix of 8,192 entries for 512 x 8 queries,
+// 525 us, 1,048 TFLOP/s.  Short items are bound by what each costs alone, 6 to 9
 // us: a masked last tile, the join of the copies, the division.  On the warp
 // instructions (attn_mma.cu, pages of 4) the first takes 263 us, the second 1,198.
 // Registers are what is short: the softmax threads use all 168, and sharing them

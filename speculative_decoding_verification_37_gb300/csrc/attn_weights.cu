@@ -150,7 +150,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
 // bf16 version, on the warp tensor instructions, for the head and page sizes
 // that attn_weights_tc.cu does not take.  Bound by latency: the registers that
 // hold K leave 16 warps an SM (512 ragged requests of up to 4,096 entries, 8
-// heads of 128: 728 us, 3.0 TB/s; there 413).
+// heads of 128: 728 us, 3.0 TB/s; there 394).
 //
 // A warp owns 16 entries of a tile for all cached heads: the entries' K rows are
 // the rows (M = 16) of its products, the queries the columns (N = 8).  The order

@@ -12,7 +12,7 @@
 //
 // Measured (8 heads of 128, 4 queries each): 64 requests of 2,048 entries 62 us,
 // 4.4 TB/s, of which 5 to 10 pass before the first product; 512 ragged ones of up
-// to 4,096, 361 us, 6.1 TB/s; with capped and biased scores 413.  A query costs
+// to 4,096, 361 us, 6.1 TB/s; with capped and biased scores 394.  A query costs
 // the epilogue an addition and an exponential an entry, a tanh two steps of the
 // special-function unit more; leaving out the columns past the last query was
 // worth 90 us, looking a tile's entries up a tile ahead 11.  K straight to
