@@ -3,15 +3,16 @@
 // weight[c] += sum over the committed candidates j with c <= e_j and the query
 // heads h of exp(x(j, h, c) - lse(j, h)).  The softmax's sum is known, so no
 // pass over the values and no second pass is needed: K is read once.  A tile
-// is 64 entries of one request with all its cached heads, so one thread owns
-// an entry's whole sum: nothing is added atomically and the result does not
+// is 32 or 128 entries of one request with all its cached heads, so an entry's sum
+// stays in one block: nothing is added atomically and the result does not
 // depend on timing.
 #include "attention.cuh"
+#include "tma.cuh"
 
 namespace specv {
 namespace {
 
-constexpr int KT = 64, NT = 128, RQ = 16;  // entries per tile, queries staged at a time
+constexpr int KT = 32, NT = 128, RQ = 16;  // entries per tile, queries staged at a time
 
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -21,9 +22,9 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
 }
 
 template <typename T, int DP> struct WSmem {
-    float k[KT][DP + 4];
+    float k[2][KT][DP + 4];  // this head's and the next one's
     float q[RQ][DP];
-    float part[KT];
+    float part[NT / KT][KT];
     int64_t koff[KT];
     int kp[KT];
     int qp[RQ], own[RQ], first;   // position, own entry (-1: no such query)
@@ -31,14 +32,23 @@ template <typename T, int DP> struct WSmem {
     AttnPlan plan;
 };
 
-// CUDA-core version: any element type.  Two threads share an entry, each
-// taking half the queries.
+// CUDA-core version: any element type.  A lane has an entry, a warp a quarter of
+// the queries, whose elements are broadcast; the next head's rows are copied
+// while this one's scores are taken.  Bound by issue and by the queries' staging
+// for each head and 16 of them (f32, 64 requests of 2,048 entries, 8 heads of 128:
+// up to 5 x 4 queries a head 613 us, up to 4 of them 323, 1.7 TB/s; all of a
+// head's rows before its scores, two lanes an entry: 788 and 530).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {  // zeros where `bytes` is 0
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt_kernel(WeightsParams wp) {
     extern __shared__ __align__(16) unsigned char raw[];
     WSmem<T, DP> &sh = *reinterpret_cast<WSmem<T, DP> *>(raw);
     const AttnParams &p = wp.a;
     constexpr int VEC = Elem<T>::VEC;
-    const int tid = threadIdx.x, key = tid & (KT - 1), half = tid / KT;
+    const int tid = threadIdx.x, key = tid & (KT - 1), part = tid / KT;
     attn_plan<NT>(p, sh.plan, 1, KT);
     int64_t u = (int64_t)blockIdx.x * sh.plan.share;
     const int64_t uend = min(sh.plan.total, u + sh.plan.share);
@@ -72,18 +82,30 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
                 sh.kp[tid] = kp;
             }
             float acc = 0.0f;
-            for (int h = 0; h < p.H; ++h) {
-                __syncthreads();
+            auto copy = [&](int h) {
                 for (int i = tid; i < KT * (DP / VEC); i += NT) {
                     const int k = i / (DP / VEC), d = (i - k * (DP / VEC)) * VEC;
-                    float x[VEC];
+                    const bool in = sh.koff[k] >= 0 && d < p.D;
+                    const T *from = static_cast<const T *>(p.kc) + (in ? sh.koff[k] + (int64_t)h * p.D + d : 0);
+                    float *to = &sh.k[h & 1][k][d];
+                    if constexpr (sizeof(T) == 4) {
+                        cp_async16(smem_u32(to), from, in ? 16 : 0);
+                    } else {
+                        float x[VEC];
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) x[e] = 0.0f;
-                    if (sh.koff[k] >= 0 && d < p.D)
-                        unpack<T>(ld_nc16(static_cast<const T *>(p.kc) + sh.koff[k] + (int64_t)h * p.D + d), x);
+                        for (int e = 0; e < VEC; ++e) x[e] = 0.0f;
+                        if (in) unpack<T>(ld_nc16(from), x);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) sh.k[k][d + e] = x[e];
+                        for (int e = 0; e < VEC; ++e) to[e] = x[e];
+                    }
                 }
+            };
+            __syncthreads();
+            copy(0);
+            for (int h = 0; h < p.H; ++h) {
+                cp_async_wait_all();
+                __syncthreads();  // this head's rows are there, the last one's done with
+                if (h + 1 < p.H) copy(h + 1);
                 for (int r0 = 0; r0 < rows; r0 += RQ) {
                     __syncthreads();
                     if (tid < RQ) {
@@ -98,47 +120,50 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
                             sh.slope[tid] = p.slopes ? p.slopes[hq] : 0.0f;
                         }
                     }
-                    for (int i = tid; i < RQ * DP; i += NT) {
-                        const int k = i / DP, d = i - k * DP, r = r0 + k;
-                        float x = 0.0f;
+#pragma unroll
+                    for (int i = tid; i < RQ * (DP / VEC); i += NT) {
+                        const int k = i / (DP / VEC), d = (i - k * (DP / VEC)) * VEC, r = r0 + k;
+                        float x[VEC];
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) x[e] = 0.0f;
                         if (r < rows && d < p.D) {
                             const int j = r / p.G, s = slots ? slots[j] : j;
-                            x = to_f32(static_cast<const T *>(p.q)[b * p.qsb + s * p.qss + (h * p.G + r - j * p.G) * p.qsh + d]);
+                            unpack<T>(ld_nc16(static_cast<const T *>(p.q) + b * p.qsb + s * p.qss + (h * p.G + r - j * p.G) * p.qsh + d), x);
                         }
-                        sh.q[k][d] = x;
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) sh.q[k][d + e] = x[e];
                     }
                     __syncthreads();
-#pragma unroll
-                    for (int g = 0; g < RQ / 8; ++g) {
-                        const int q0 = half * (RQ / 2) + g * 4;
-                        float dot[4] = {0.f, 0.f, 0.f, 0.f};
+                    const int q0 = part * (RQ / (NT / KT));
+                    float dot[4] = {0.f, 0.f, 0.f, 0.f};
+                    static_assert(RQ == 4 * (NT / KT), "four queries a thread");
 #pragma unroll 4
-                        for (int d = 0; d < DP; d += 4) {
-                            const float4 a = *reinterpret_cast<const float4 *>(&sh.k[key][d]);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float4 q = *reinterpret_cast<const float4 *>(&sh.q[q0 + j][d]);
-                                dot[j] = fmaf(a.x, q.x, fmaf(a.y, q.y, fmaf(a.z, q.z, fmaf(a.w, q.w, dot[j]))));
-                            }
-                        }
+                    for (int d = 0; d < DP; d += 4) {
+                        const float4 a = *reinterpret_cast<const float4 *>(&sh.k[h & 1][key][d]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            const int q = q0 + j, c = c0 + key;
-                            if (sh.koff[key] < 0 || c > sh.own[q]) continue;
-                            const int dist = pos_dist(sh.qp[q], sh.kp[key]);
-                            if (sh.kp[key] < first || (p.window > 0 && dist >= p.window)) continue;
-                            acc += exp2f(fmaf(attn_score<sizeof(T) == 4>(dot[j], p.score, sh.slope[q], dist), kLog2e, -sh.lse2[q]));
+                            const float4 q = *reinterpret_cast<const float4 *>(&sh.q[q0 + j][d]);
+                            dot[j] = fmaf(a.x, q.x, fmaf(a.y, q.y, fmaf(a.z, q.z, fmaf(a.w, q.w, dot[j]))));
                         }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int q = q0 + j, c = c0 + key;
+                        if (sh.koff[key] < 0 || c > sh.own[q]) continue;
+                        const int dist = pos_dist(sh.qp[q], sh.kp[key]);
+                        if (sh.kp[key] < first || (p.window > 0 && dist >= p.window)) continue;
+                        acc += exp2f(fmaf(attn_score<sizeof(T) == 4>(dot[j], p.score, sh.slope[q], dist), kLog2e, -sh.lse2[q]));
                     }
                 }
             }
-            if (half == 1) sh.part[key] = acc;
+            sh.part[part][key] = acc;
             __syncthreads();
-            if (half == 0 && key < nk && sh.koff[key] >= 0) {
-                const int c = c0 + key;
-                wp.weight[b * wp.wstride + c] += acc + sh.part[key];
+            if (part == 0 && key < nk && sh.koff[key] >= 0) {
+#pragma unroll
+                for (int q = 1; q < NT / KT; ++q) acc += sh.part[q][key];
+                wp.weight[b * wp.wstride + c0 + key] += acc;
             }
-            if (half == 1 && key < nk && wp.key_pos_out && c0 + key >= cand0)
+            if (part == 1 && key < nk && wp.key_pos_out && c0 + key >= cand0)
                 wp.key_pos_out[(int64_t)b * p.kps + c0 + key] = sh.kp[key];
         }
         u = it.u0 + it.ntiles;
