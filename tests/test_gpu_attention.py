@@ -501,6 +501,16 @@ def test_many_tiles_per_block(D, G, S, H):
     assert torch.equal(r.out, again.out) and torch.equal(r.lse, again.lse)
 
 
+@pytest.mark.parametrize("D,G,S,H", [(64, 2, 3, 4), (128, 4, 5, 3), (128, 8, 9, 2), (256, 3, 2, 2), (72, 1, 1, 5), (200, 8, 6, 1)])
+def test_many_tiles_per_block_f32(D, G, S, H):
+    """The same in float32: 16 and 32 rows a block, several row tiles, long items."""
+    c = Case([2500, 700, 2000, 33], S=S, H=H, G=G, D=D, seed=D + G, dtype="f32", docs=0.1, slopes=True)
+    r = c.run()
+    c.check(r)
+    again = c.run()
+    assert torch.equal(r.out, again.out) and torch.equal(r.lse, again.lse)
+
+
 # ---------------------------------------------------------------------------
 # entry weights
 # ---------------------------------------------------------------------------
@@ -577,12 +587,22 @@ def test_entry_weights(kw, dtype, start):
     dict(G=3, S=7, D=128, lens=[520, 90], cap=9.0, slopes=True), dict(G=5, S=11, lens=[600, 300], slopes=True, window=200),
     dict(H=8, G=4, D=128, S=8, lens=[1500, 1100, 30, 2000] * 12, cap=30.0, slopes=True),
     dict(H=5, G=2, S=4, lens=list(range(90, 500, 7)), gaps=True, docs=0.3), dict(H=2, G=64, D=128, S=5, lens=[300, 40]),
+    dict(H=128, G=1, D=128, S=3, lens=[70, 7]), dict(H=65, G=3, D=256, S=2, lens=[40]),
     dict(H=2, G=4, D=96, lens=[700, 129, 64]), dict(H=3, G=4, D=72, S=9, lens=[400, 30], cap=9.0), dict(H=2, G=8, D=40, S=9, lens=[300, 129]),
 ])
 def test_entry_weights_of_many_tiles(kw):
     """Odd heads, several passes over the queries, one row past a multiple of the
     columns, long and many requests."""
     test_entry_weights(kw, "bf16", 0)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(H=3, D=128, G=4, lens=[700, 129, 33, 31]), dict(H=1, G=8, S=9, lens=[1000, 5, 0, 260]), dict(H=4, D=256, G=5, S=7, lens=[400, 90]),
+    dict(H=8, G=4, S=8, lens=[500, 900, 30] * 9, cap=30.0, slopes=True), dict(H=5, G=2, D=100, S=4, bs=7, lens=[300, 77, 410], gaps=True, docs=0.3)])
+def test_entry_weights_of_many_tiles_f32(kw):
+    """Odd heads (the last one's buffer), several blocks, rows past a multiple of
+    the queries staged at a time."""
+    test_entry_weights(kw, "f32", 0)
 
 
 @pytest.mark.parametrize("bs", [16, 5])
