@@ -318,6 +318,19 @@ __device__ __forceinline__ int key_position(const AttnParams &p, const AttnItem 
     return p.key_pos ? p.key_pos[(int64_t)it.b * p.kps + c] : c;
 }
 
+// Mode 2, a request's first tile, its slots good: the positions of the committed
+// candidates whose entries lie among the shared ones, which no tile holds (threads
+// `tid` of `nt`).
+__device__ __forceinline__ void shared_positions(const WeightsParams &wp, const AttnItem &it, int tid, int nt) {
+    const AttnParams &p = wp.a;
+    if (!wp.key_pos_out) return;
+    const int cand0 = it.keys.len - p.n_slots[it.b];
+    for (int c = cand0 + tid; c < it.keys.lo; c += nt) {
+        const int j = c - cand0, s = p.slots ? p.slots[(int64_t)it.b * p.slots_stride + j] : j;
+        wp.key_pos_out[(int64_t)it.b * p.kps + c] = p.pos ? p.pos[(int64_t)it.b * p.S + s] : c;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // results
 // ---------------------------------------------------------------------------

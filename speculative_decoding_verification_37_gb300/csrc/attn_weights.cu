@@ -61,6 +61,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
         for (int j = tid; slots && j < n; j += NT) bad = bad || slots[j] < 0 || slots[j] >= p.S;
         const bool skip = __syncthreads_or(bad);
         if (skip && u == it.u0 && tid == 0) attn_flag(p, b);
+        if (!skip && u == it.u0) shared_positions(wp, it, tid, NT);
         const int t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), rows = n * p.G;
         const int first = p.first ? p.first[b] : (int)0x80000000;
         for (int t = (int)(u - it.u0); t < t1 && !skip; ++t) {
@@ -217,6 +218,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
         for (int j = tid; slots && j < n; j += WNT) bad = bad || slots[j] < 0 || slots[j] >= p.S;
         const bool skip = __syncthreads_or(bad);
         if (skip && u == it.u0 && tid == 0) attn_flag(p, b);
+        if (!skip && u == it.u0) shared_positions(wp, it, tid, WNT);
         const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
         const int first = p.first ? p.first[b] : (int)0x80000000;
         const int cand0 = it.keys.len - n;  // the candidates' first entry

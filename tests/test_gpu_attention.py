@@ -873,3 +873,46 @@ def test_rounds_of_tree_decoding_with_eviction():
             want = np.array([x[2] for x in shadow[b]]).transpose(1, 2, 0, 3, 4)
             assert np.array_equal(got, want), (rnd, b)
     assert evicted > 0 and int(text.min()) > budget
+
+
+# every kernel of the entry weights: tcgen05, the warp instructions, the CUDA cores in both types
+WEIGHT_KERNELS = [("bf16", dict(D=64)), ("bf16", dict(D=128, G=4)), ("bf16", dict(D=64, bs=5)), ("bf16", dict(D=160)),
+                  ("bf16", dict(H=65, G=3, D=256)), ("f32", dict(D=72, bs=5))]
+
+
+@pytest.mark.parametrize("dtype,kw", WEIGHT_KERNELS)
+def test_entry_weights_positions_below_a_shared_prefix(dtype, kw):
+    """Every committed candidate's entry gets its position, also where it lies
+    among the shared entries, whose weights stay as they are; a skipped
+    request's positions stay too."""
+    P, S, n = 40, 3, 3
+    lens = [P, P + 1, P + n, P + 20, P - 2, n, 200, P, P + 1]
+    c = Case(lens, S=S, inplace=True, dtype=dtype, seed=31, **{**dict(H=2, G=2), **kw})
+    (q, cache, table, dl), _ = c.args()
+    width = c.max_blocks * c.bs
+    rng = np.random.default_rng(7)
+    n_slots = np.array([n] * 7 + [2, n], np.int32)
+    slots = np.tile(np.arange(S, dtype=np.int32), (c.B, 1))
+    slots[8, 1] = S                                       # bad: the request is skipped
+    pos = (1000 + rng.permutation(c.B * S).reshape(c.B, S)).astype(np.int32)
+    kp0 = rng.integers(0, 900, (c.B, width)).astype(np.int32)
+    w0 = rng.uniform(0, 2, (c.B, width)).astype(np.float32)
+    lse = rng.uniform(3, 6, (c.B, S, c.H * c.G)).astype(np.float32)
+    d = lambda x: torch.from_numpy(x).cuda()  # noqa: E731
+    key_pos, weight, flags = d(kp0.copy()), d(w0.copy()), torch.zeros(c.B, dtype=torch.int32, device="cuda")
+    api.attention_weights(q, d(lse), cache, table, dl, d(n_slots), weight, block_size=c.bs, slots=d(slots), pos=d(pos),
+                          key_pos=key_pos, shared_len=P, flags=flags, **c.score)
+    torch.cuda.synchronize()
+    assert flags.tolist() == [0] * 8 + [1]
+    kp, w = kp0.copy(), w0.astype(np.float64)
+    for b, length in enumerate(lens[:8]):
+        m = int(n_slots[b])
+        kp[b, length - m:length] = pos[b, :m]
+        k = O.entries(c.planes()[0], c.table[b].tolist(), c.bs, length)
+        gain = O.entry_weights(c.q[b, :m].double().numpy(), lse[b, :m].astype(np.float64), k, pos[b, :m], kp[b, :length], m,
+                               start=P, **c.score)
+        tol = (2 * c.score_error(b, k) + (m * c.H * c.G + 32) * 2.0 ** -24) * gain + 2.0 ** -23 * (w0[b, :length] + gain)
+        w[b, :length] += gain
+        assert (np.abs(weight[b, :length].double().cpu().numpy() - w[b, :length]) <= tol + 1e-30).all(), b
+        assert np.array_equal(weight[b, :min(P, length)].cpu().numpy(), w0[b, :min(P, length)])
+    assert np.array_equal(key_pos.cpu().numpy(), kp)
