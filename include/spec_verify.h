@@ -521,8 +521,12 @@ int spec_tree_level(const SpecTreeLevelArgs *args, void *workspace, size_t ws_by
  *   dist >= window, or its position is below first_pos[b] (the start of the
  *   current document).  out = softmax(x) . v over the keys not masked;
  *   lse = log(sum(exp(x))).  A query with no key left gets out = 0, lse = -inf.
- *   What lies in a masked place, NaN included, does not matter.  A NaN or
- *   infinite K or V that is not masked gives non-finite results in its rows.
+ *   What lies in a masked place, NaN included, does not matter.  A score
+ *   that is NaN and not masked makes its query's out and lse NaN, however its
+ *   keys are split; an infinite one enters as the formula has it (a cap makes it
+ *   +-softcap, -inf without one is a weight of 0, +inf gives NaN).  A V that is
+ *   not finite makes the columns that give it a weight non-finite, or all of the
+ *   row's; with a weight that rounds to 0 it may or may not show.
  * Shared prefix: with shared_len > 0 the first shared_len entries of every
  *   request lie in the blocks of shared_table (block_table's entries for them
  *   are not read where a block holds shared entries only) and are read once

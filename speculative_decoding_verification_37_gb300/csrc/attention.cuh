@@ -439,12 +439,12 @@ __device__ __forceinline__ void attn_join_row(const AttnParams &p, bool ok, int 
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
         for (int c = 0; c < n; c += U) {
-            if ((c & 31) == 0) {  // the weights of the next 32 blocks (0: it saw no key of the row)
+            if ((c & 31) == 0) {  // the weights of the next 32 blocks (0: no key of the row, NaN scores alone, or far below)
                 const bool mine = c + lane < n;
                 const float a = c == 0 ? mc : mine ? __ldcg(part(c + lane) + o_m + r) : -INFINITY;
                 const float b = c == 0 ? lc : mine ? __ldcg(part(c + lane) + o_l + r) : 0.0f;
                 w = mine ? rel_weight(a, m) : 0.0f;
-                lw = w == 0.0f ? 0.0f : b * w;
+                lw = b * w;  // (a NaN sum stays one: its block saw a NaN score)
             }
             if (c > 0) load(c);
 #pragma unroll

@@ -916,3 +916,66 @@ def test_entry_weights_positions_below_a_shared_prefix(dtype, kw):
         assert (np.abs(weight[b, :length].double().cpu().numpy() - w[b, :length]) <= tol + 1e-30).all(), b
         assert np.array_equal(weight[b, :min(P, length)].cpu().numpy(), w0[b, :min(P, length)])
     assert np.array_equal(key_pos.cpu().numpy(), kp)
+
+
+# items split over blocks, on every kernel: tcgen05 with 32, 64 and 128 rows, the warp instructions, the CUDA cores
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+@pytest.mark.parametrize("what", ["query", "tile", "newest", "light"])
+def test_nan_of_split_items_shows(what, dtype, G, bs):
+    """A NaN that a row sees reaches its result however its keys are split: in
+    the query, in all the keys that one block sees, in the newest keys alone
+    behind whole tiles, in a key whose block's weights underflow."""
+    c = Case([2560, 40], S=5, H=2, G=G, D=64, bs=bs, dtype=dtype, seed=17, slopes=what == "light")
+    if c.slopes is not None:
+        c.slopes[:] = 1.0
+    clean = c.run()
+    c.check(clean)
+    nan, rows = float("nan"), torch.ones((2, 5, 2 * G), dtype=torch.bool)
+    rows[1] = rows[:, :, G:] = False                      # request 0, cached head 0 (the tile, the newest, the light one)
+    if what == "query":
+        c.q[0, 2] = nan
+        rows[:] = False
+        rows[0, 2] = True
+    elif what == "newest":
+        c.temp[0, 0, 0, :, 0] = nan
+    else:
+        for e in range(1280, 1408) if what == "tile" else (5,):
+            c.cache[0, 0, c.table[0, e // bs], e % bs, 0] = nan
+    r = c.run()
+    out, lse, rows = r.out.float(), r.lse, rows.cuda()
+    assert torch.isnan(out[rows]).all() and torch.isnan(lse[rows]).all()
+    assert torch.equal(r.out[~rows], clean.out[~rows]) and torch.equal(lse[~rows], clean.lse[~rows])
+
+
+@pytest.mark.parametrize("dtype,bs", [("bf16", 16), ("bf16", 5), ("f32", 16)])
+@pytest.mark.parametrize("G,S", [(2, 2), (8, 6)])
+def test_nan_of_a_split_shared_prefix_shows(G, S, dtype, bs):
+    """The same in the pass over a shared prefix, up to 64 and more rows."""
+    c = Case([1300, 1333, 1500, 1281], S=S, H=2, G=G, D=64, bs=bs, dtype=dtype, seed=18, shared=1280)
+    clean = c.run()
+    c.check(clean)
+    for e in range(256, 512):
+        c.cache[0, 0, c.stable[e // bs], e % bs, 0] = float("nan")
+    r = c.run()
+    assert torch.isnan(r.out[:, :, :G].float()).all() and torch.isnan(r.lse[:, :, :G]).all()
+    assert torch.equal(r.out[:, :, G:], clean.out[:, :, G:]) and torch.equal(r.lse[:, :, G:], clean.lse[:, :, G:])
+
+
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+def test_infinite_scores(dtype, G, bs):
+    """An infinite score is the cap where there is one (the same as a huge score's);
+    without one it weighs nothing at -inf and makes its row NaN at +inf."""
+    for cap in (5.0, 0.0):
+        c = Case([300, 33], S=5, H=1, G=G, D=64, bs=bs, dtype=dtype, seed=22, cap=cap)
+        row = c.cache[0, 0, c.table[0, 200 // bs], 200 % bs, 0]
+        row.zero_()
+        got = []
+        for x in (1e30, float("inf")):
+            row[7] = x
+            got.append(c.run())
+        huge, inf = got
+        nan = torch.zeros(inf.lse.shape, dtype=torch.bool, device="cuda")
+        if cap == 0.0:
+            nan[0] = c.q[0, :, :, 7].cuda() > 0
+        assert torch.isnan(inf.lse[nan]).all() and torch.isnan(inf.out[nan].float()).all()
+        assert torch.equal(inf.out[~nan], huge.out[~nan]) and torch.equal(inf.lse[~nan], huge.lse[~nan])
