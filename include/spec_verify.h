@@ -105,6 +105,8 @@ extern "C" {
 #define SPEC_WS_ATTENTION_SHARED 7 /* SPEC_WS_ATTENTION plus one f32 row per (request, candidate,
                                 head) for the part over a shared prefix */
 #define SPEC_WS_EVICT 8 /* n = budget, V = max_blocks * block_size: the moves of each request */
+#define SPEC_WS_ZEROED 32768 /* of the kinds 6, 7 and 8 only so many bytes, from the start on, have to
+                                be zero before the first call */
 
 /*
  * Chain verification, sampled (temperature > 0) or greedy (temperature == 0).
@@ -547,7 +549,10 @@ int spec_tree_level(const SpecTreeLevelArgs *args, void *workspace, size_t ws_by
  *   tensor cores with the softmax weights rounded to bf16.  The result does not
  *   depend on timing: sums are taken in a fixed order.
  * Workspace: SPEC_WS_ATTENTION bytes, or SPEC_WS_ATTENTION_SHARED with
- *   shared_len > 0; zero before the first call, left zeroed where it must be.
+ *   shared_len > 0; zero (SPEC_WS_ZEROED bytes) before the first call, left
+ *   zeroed where it must be.  It holds the call's partial results: calls that
+ *   can be in flight together (two streams, a graph's replay beside an eager
+ *   call) need one each.
  */
 #define SPEC_ATTENTION_MAX_D 256
 #define SPEC_ATTENTION_MAX_S 1024
@@ -651,6 +656,7 @@ int spec_attention_weights(const SpecWeightsArgs *args, void *workspace, size_t 
  *   negative position, or (its positions repeat) more than `budget` protected
  *   entries is left as it is and flagged SPEC_FLAG_BAD_INPUT.
  * Workspace: SPEC_WS_EVICT bytes (no zeroing needed but for the status word).
+ *   It holds the moves: one for each call that can be in flight.
  */
 typedef struct SpecEvictArgs {
     int32_t B, L, H, D, block_size, elem_bytes;

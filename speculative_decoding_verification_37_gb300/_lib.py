@@ -23,6 +23,7 @@ SPEC_FLAG_BAD_INPUT, SPEC_FLAG_FALLBACK, SPEC_FLAG_BAD_ROW, SPEC_FLAG_TIMEOUT = 
 SPEC_WS_CHAIN, SPEC_WS_TREE, SPEC_WS_COMMIT, SPEC_WS_CHAIN_TOPK, SPEC_WS_CHAIN_FULL = 0, 1, 2, 3, 4
 SPEC_WS_TREE_LEVEL = 5
 SPEC_WS_ATTENTION, SPEC_WS_ATTENTION_SHARED, SPEC_WS_EVICT = 6, 7, 8
+SPEC_WS_ZEROED = 32768  # bytes of those three kinds that must be zero before the first call
 SPEC_FLAG_EOS, SPEC_FLAG_LIMIT = 16, 32
 SPEC_TREE_MAX_HEADS = 64
 TOPK_FAST_MAX = 128   # top_k served by the candidate-pool path when the workspace holds it
@@ -200,9 +201,14 @@ def spec_workspace_bytes(kind: int, B: int, n: int, V: int) -> int:
 
 
 def new_workspace(kind: int, B: int, n: int, V: int, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace (torch allocates it; the library never does)."""
+    """A workspace, zero where it has to be before the first call (torch allocates
+    it; the library never does)."""
     nbytes = max(spec_workspace_bytes(kind, B, n, V), 256)
-    return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    if kind not in (SPEC_WS_ATTENTION, SPEC_WS_ATTENTION_SHARED, SPEC_WS_EVICT):
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    ws[:SPEC_WS_ZEROED].zero_()  # (a captured call does this in every replay)
+    return ws
 
 
 def spec_ngram_draft(*, history: torch.Tensor, hist_len: torch.Tensor, gamma: int, n_min: int,

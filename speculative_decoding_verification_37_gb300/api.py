@@ -13,18 +13,29 @@ from . import _lib as L
 _WORKSPACES: Dict[Tuple, torch.Tensor] = {}
 
 
-def workspace(kind: int, B: int, n: int, V: int, device) -> torch.Tensor:
+# kinds that hold a call's intermediate results: one for each stream
+_PER_STREAM = (L.SPEC_WS_ATTENTION, L.SPEC_WS_ATTENTION_SHARED, L.SPEC_WS_EVICT)
+
+
+def workspace(kind: int, B: int, n: int, V: int, device, stream: int = 0) -> torch.Tensor:
     """A cached zero-filled workspace for (device, kind, B, n, V) (the size of
     some kinds depends on V).  Every call leaves it zeroed, so it is reused
     without clearing; calls that share it must be ordered on one stream.
     The cache lives as long as the process; clear_workspaces() frees it.
     A call captured into a CUDA graph before any eager one of its sizes gets a
     workspace of the graph's own, zeroed by each replay: a cached one would
-    not be zero before the first replay."""
+    not be zero before the first replay.
+    The attention's and the eviction's kinds are cached for each stream (its raw
+    handle, 0: the default stream), so that calls in flight on two streams do not
+    meet, and every captured call gets its own: its graph may be replayed on any
+    stream, beside eager calls and other graphs."""
     dev = device if isinstance(device, torch.device) else torch.device(device)
     if dev.type == "cuda" and dev.index is None:
         dev = torch.device("cuda", torch.cuda.current_device())
-    key = (dev.type, dev.index, kind, B, n, V)
+    per_stream = kind in _PER_STREAM
+    if per_stream and dev.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        return L.new_workspace(kind, B, n, V, device=dev)
+    key = (dev.type, dev.index, kind, B, n, V, stream if per_stream else 0)
     ws = _WORKSPACES.get(key)
     if ws is None:
         ws = L.new_workspace(kind, B, n, V, device=dev)
@@ -180,6 +191,15 @@ def _allocating_on(stream):
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
+def _stream_of(stream, t: torch.Tensor):
+    """The stream a call runs on (the current one of t's device for None) and its raw handle."""
+    if stream is None:
+        if not t.is_cuda:  # (the call refuses it)
+            return None, 0
+        stream = torch.cuda.current_stream(t.device)
+    return stream, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
 @dataclass
 class AttentionOut:
     out: torch.Tensor            # [B, S, Hq, D], q's type
@@ -209,13 +229,16 @@ def verify_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     tanh; slopes f32 [Hq] subtract slope * distance; window > 0 and first_pos
     (int32 [B]) mask by position.  With shared_len > 0 every request's first
     shared_len entries lie in shared_table's blocks and are read once for the
-    whole batch.  A query that sees no key gets 0 and an lse of -inf."""
+    whole batch.  A query that sees no key gets 0 and an lse of -inf.
+    Calls on different streams, and captured ones, may be in flight together;
+    with a ws of the caller's own only those that do not share it."""
     B, S, Hq, D = q.shape
     with _allocating_on(stream):
         out = AttentionOut(out=torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device),
                            lse=torch.empty((B, S, Hq), dtype=torch.float32, device=q.device))
+        stream, raw = _stream_of(stream, q)
         if ws is None:
-            ws = workspace(L.SPEC_WS_ATTENTION_SHARED if shared_len > 0 else L.SPEC_WS_ATTENTION, B, S * Hq, D, q.device)
+            ws = workspace(L.SPEC_WS_ATTENTION_SHARED if shared_len > 0 else L.SPEC_WS_ATTENTION, B, S * Hq, D, q.device, raw)
     L.spec_verify_attention(q=q, cache=cache, block_table=block_table, committed_len=committed_len,
                             block_size=block_size, out=out.out, lse=out.lse, workspace=ws, layer=layer,
                             scale=D ** -0.5 if scale is None else scale, temp_kv=temp_kv, tree_mask=tree_mask,
@@ -256,10 +279,12 @@ def evict_kv(cache: torch.Tensor, block_table: torch.Tensor, committed_len: torc
     and in every layer: the entries at positions below `sink`, the `recent`
     newest positions and the heaviest others stay; those at or past the
     budget move into the places of the evicted ones.  cache, committed_len,
-    weight and key_pos are updated on the device."""
+    weight and key_pos are updated on the device.  Streams, captures and ws as
+    for verify_attention."""
     if ws is None:
         with _allocating_on(stream):
-            ws = workspace(L.SPEC_WS_EVICT, block_table.shape[0], budget, block_table.shape[1] * block_size, cache.device)
+            stream, raw = _stream_of(stream, cache)
+            ws = workspace(L.SPEC_WS_EVICT, block_table.shape[0], budget, block_table.shape[1] * block_size, cache.device, raw)
     L.spec_evict_kv(cache=cache, block_table=block_table, committed_len=committed_len, weight=weight,
                     key_pos=key_pos, block_size=block_size, budget=budget, workspace=ws, sink=sink, recent=recent,
                     blocks_in_use=blocks_in_use, flags=flags, stream=stream)

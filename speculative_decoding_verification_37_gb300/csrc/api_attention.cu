@@ -83,6 +83,8 @@ size_t attn_ws_layout(int32_t B, int32_t n, int32_t D, bool shared, void *base, 
     off += ws_align(kAttnBlocksMax * sizeof(SplitItem));
     const size_t o_cnt = off;
     off += ws_align(kAttnBlocksMax * sizeof(unsigned));
+    static_assert(kWsHeader + kAttnBlocksMax * (sizeof(SplitItem) + sizeof(unsigned)) + 2 * 256 <= SPEC_WS_ZEROED,
+                  "the counters lie in the zeroed part");
     const size_t o_part = off;
     off += ws_align((size_t)kAttnSmsMax * 2 * kAttnSlotRows * (shared ? 2 : 1) * ((size_t)D + 2) * sizeof(float));
     const size_t o_pre = off;

@@ -1,5 +1,6 @@
 """The attention, entry-weight and eviction entry points on the CPU: struct
 layouts, workspace sizes and the refusals, all before anything is enqueued."""
+import contextlib
 import ctypes
 import os
 import subprocess
@@ -212,3 +213,55 @@ def test_a_captured_first_call_does_not_leave_its_workspace_in_the_cache(monkeyp
     d = api.workspace(L.SPEC_WS_ATTENTION, 1, 2, 64, torch.device("cuda", 0))
     api.clear_workspaces()
     assert len({id(x) for x in (a, b, c)}) == 3 and c is d
+
+
+def test_a_workspace_for_each_stream(lib):
+    """The kinds that hold a call's intermediate results are not shared between
+    streams, whose calls may be in flight together; the others' only state is theirs."""
+    api.clear_workspaces()
+    for kind in (L.SPEC_WS_ATTENTION, L.SPEC_WS_ATTENTION_SHARED, L.SPEC_WS_EVICT):
+        a, b, c = (api.workspace(kind, 2, 8, 64, "cpu", stream=s) for s in (0, 7, 7))
+        assert b is c and a.data_ptr() != b.data_ptr() and a is api.workspace(kind, 2, 8, 64, "cpu")
+        assert a.numel() >= L.spec_workspace_bytes(kind, 2, 8, 64) and not a[:L.SPEC_WS_ZEROED].any()
+    assert api.workspace(L.SPEC_WS_COMMIT, 2, 0, 0, "cpu", stream=7) is api.workspace(L.SPEC_WS_COMMIT, 2, 0, 0, "cpu")
+    api.clear_workspaces()
+
+
+def test_calls_use_their_streams_workspace(lib, monkeypatch):
+    """verify_attention and evict_kv on two streams: workspaces apart, the same
+    one again on the same stream, the caller's own where it gives one."""
+    used = []
+    monkeypatch.setattr(L, "spec_verify_attention", lambda **kw: used.append((kw["workspace"], kw["stream"])))
+    monkeypatch.setattr(L, "spec_evict_kv", lambda **kw: used.append((kw["workspace"], kw["stream"])))
+    monkeypatch.setattr(api, "_allocating_on", lambda stream: contextlib.nullcontext())
+    api.clear_workspaces()
+    cache, table, lens = torch.zeros(1, 2, 4, 16, 1, 64), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q, w, pos = torch.zeros(2, 3, 1, 64), torch.zeros(2, 32), torch.zeros(2, 32, dtype=torch.int32)
+    calls = (lambda **kw: api.verify_attention(q, cache, table, lens, block_size=16, **kw),
+             lambda **kw: api.verify_attention(q, cache, table, lens, block_size=16, shared_len=5, shared_table=table[0], **kw),
+             lambda **kw: api.evict_kv(cache, table, lens, w, pos, block_size=16, budget=8, **kw))
+    for call in calls:
+        used.clear()
+        mine = torch.zeros(1)
+        for kw in (dict(stream=3), dict(stream=4), dict(stream=3), dict(stream=4, ws=mine)):
+            call(**kw)
+        (a, s), (b, t), (c, _), (d, _) = used
+        assert a is c and a.data_ptr() != b.data_ptr() and d is mine and (s, t) == (3, 4)
+    api.clear_workspaces()
+
+
+def test_every_captured_call_gets_a_workspace_of_its_own(monkeypatch):
+    """Also after an eager call of its sizes, on the stream that captures: two
+    graphs, or a graph and eager calls, can be in flight together."""
+    api.clear_workspaces()
+    monkeypatch.setattr(L, "new_workspace", lambda *a, device: torch.zeros(1))
+    capturing = False
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    dev = torch.device("cuda", 0)
+    for kind in (L.SPEC_WS_ATTENTION, L.SPEC_WS_ATTENTION_SHARED, L.SPEC_WS_EVICT):
+        eager = api.workspace(kind, 1, 2, 64, dev)
+        capturing = True
+        graphs = [api.workspace(kind, 1, 2, 64, dev) for _ in range(2)]
+        capturing = False
+        assert len({id(x) for x in (eager, *graphs)}) == 3 and api.workspace(kind, 1, 2, 64, dev) is eager
+    api.clear_workspaces()

@@ -979,3 +979,85 @@ def test_infinite_scores(dtype, G, bs):
             nan[0] = c.q[0, :, :, 7].cuda() > 0
         assert torch.isnan(inf.lse[nan]).all() and torch.isnan(inf.out[nan].float()).all()
         assert torch.equal(inf.out[~nan], huge.out[~nan]) and torch.equal(inf.lse[~nan], huge.lse[~nan])
+
+
+# kernels that leave partial results: joined by the last block (32, 64 rows), by a second kernel, the others
+AT_ONCE = [dict(G=4), dict(G=8), dict(G=16), dict(G=16, shared=640), dict(G=4, bs=5), dict(G=4, dtype="f32"),
+           dict(G=4, shared=640, bs=5)]
+
+
+def at_once(n, *calls):
+    """Every call n times, each on a stream of its own, all streams at once: its results."""
+    streams = [torch.cuda.Stream() for _ in calls]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in calls]
+    for _ in range(n):
+        for s, call, to in zip(streams, calls, got):
+            with torch.cuda.stream(s):
+                to.append(call())
+    torch.cuda.synchronize()
+    return got
+
+
+@pytest.mark.parametrize("kw", AT_ONCE)
+def test_attention_on_two_streams_at_once(kw):
+    """Calls of the same sizes with other inputs, in flight together, by the
+    current stream and by stream=."""
+    cases = [Case([4000, 900, 1100], S=5, H=2, D=64, seed=s, **kw) for s in (40, 41)]
+    args = [c.args() for c in cases]
+    want = [api.verify_attention(*pos, **a) for pos, a in args]
+    for c, r in zip(cases, want):
+        c.check(r, rows=[0])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    calls = [lambda pos=pos, a=a: api.verify_attention(*pos, **a) for pos, a in args]
+    calls += [lambda pos=pos, a=a, s=s: api.verify_attention(*pos, stream=s, **a) for (pos, a), s in zip(args, streams)]
+    for results, ref in zip(at_once(25, *calls), want * 2):
+        for r in results:
+            assert torch.equal(r.out, ref.out) and torch.equal(r.lse, ref.lse)
+
+
+@pytest.mark.parametrize("kw", AT_ONCE[1:4])
+def test_graphs_beside_eager_calls(kw):
+    """Two graphs captured on one stream after an eager call there, replayed on two
+    others while that stream goes on."""
+    cases = [Case([4000, 900, 1100], S=5, H=2, D=64, seed=s, **kw) for s in (42, 43, 44)]
+    args = [c.args() for c in cases]
+    want = [api.verify_attention(*pos, **a) for pos, a in args]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for pos, a in args[:2]:
+        with torch.cuda.stream(s):
+            api.verify_attention(*pos, **a)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            graphs.append((g, api.verify_attention(*pos, **a)))
+    torch.cuda.synchronize()
+    eager = at_once(25, graphs[0][0].replay, graphs[1][0].replay,
+                    lambda: api.verify_attention(*args[2][0], stream=s, **args[2][1]))[2]
+    for r, ref in [(graphs[0][1], want[0]), (graphs[1][1], want[1])] + [(r, want[2]) for r in eager]:
+        assert torch.equal(r.out, ref.out) and torch.equal(r.lse, ref.lse)
+
+
+def test_evictions_on_two_streams_at_once():
+    """The lists of moves of two batches of the same sizes."""
+    lens, bs = [900, 1200, 1000, 700], 16
+    batches = [evict_case(lens, 600, layers=4, D=64, bs=bs, seed=s, order="mixed") for s in (50, 51)]
+    given, calls = [], []
+    for table, bits, w, pos, nb in batches:
+        t = [torch.from_numpy(x).cuda() for x in (table, w, pos)]
+        n, cache = torch.tensor(lens, dtype=torch.int32, device="cuda"), bits.cuda().view(torch.bfloat16)
+
+        def once(t=t, n=n, cache=cache):
+            held = [cache.clone(), n.clone(), t[1].clone(), t[2].clone()]
+            api.evict_kv(held[0], t[0], *held[1:], block_size=bs, budget=600, sink=4, recent=50)
+            return held
+        given.append(once())
+        torch.cuda.synchronize()
+        calls.append(once)
+    for results, want in zip(at_once(25, *calls), given):
+        for held in results:
+            for x, y in zip(held, want):
+                assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
