@@ -17,7 +17,7 @@ _WORKSPACES: Dict[Tuple, torch.Tensor] = {}
 _PER_STREAM = (L.SPEC_WS_ATTENTION, L.SPEC_WS_ATTENTION_SHARED, L.SPEC_WS_EVICT)
 
 
-def workspace(kind: int, B: int, n: int, V: int, device, stream: int = 0) -> torch.Tensor:
+def workspace(kind: int, B: int, n: int, V: int, device, stream: Optional[int] = None) -> torch.Tensor:
     """A cached zero-filled workspace for (device, kind, B, n, V) (the size of
     some kinds depends on V).  Every call leaves it zeroed, so it is reused
     without clearing; calls that share it must be ordered on one stream.
@@ -25,9 +25,11 @@ def workspace(kind: int, B: int, n: int, V: int, device, stream: int = 0) -> tor
     A call captured into a CUDA graph before any eager one of its sizes gets a
     workspace of the graph's own, zeroed by each replay: a cached one would
     not be zero before the first replay.
-    The attention's and the eviction's kinds are cached for each stream (its raw
-    handle, 0: the default stream), so that calls in flight on two streams do not
-    meet, and every captured call gets its own: its graph may be replayed on any
+    The attention's and the eviction's kinds (zero in the SPEC_WS_ZEROED bytes
+    that have to be) are cached for each stream (the raw handle of a stream that
+    is current; None: the current one), so that calls in flight on two streams do
+    not meet; a stream has one of each kind, as large as its largest call so far
+    wanted.  Every captured call gets its own: its graph may be replayed on any
     stream, beside eager calls and other graphs."""
     dev = device if isinstance(device, torch.device) else torch.device(device)
     if dev.type == "cuda" and dev.index is None:
@@ -35,13 +37,38 @@ def workspace(kind: int, B: int, n: int, V: int, device, stream: int = 0) -> tor
     per_stream = kind in _PER_STREAM
     if per_stream and dev.type == "cuda" and torch.cuda.is_current_stream_capturing():
         return L.new_workspace(kind, B, n, V, device=dev)
-    key = (dev.type, dev.index, kind, B, n, V, stream if per_stream else 0)
+    if not per_stream:
+        stream = 0
+    elif stream is None:  # (before CUDA's first use the default stream is current)
+        on_gpu = dev.type == "cuda" and torch.cuda.is_initialized()
+        stream = torch.cuda.current_stream(dev).cuda_stream if on_gpu else 0
+    key = (dev.type, dev.index, kind, B, n, V, stream)
     ws = _WORKSPACES.get(key)
+    if ws is None and per_stream:
+        return _grown(key, dev)
     if ws is None:
         ws = L.new_workspace(kind, B, n, V, device=dev)
         if dev.type != "cuda" or not torch.cuda.is_current_stream_capturing():
             _WORKSPACES[key] = ws
     return ws
+
+
+def _grown(key: Tuple, dev: torch.device) -> torch.Tensor:
+    """The stream's workspace of this kind, kept under its sizes too; a larger one
+    takes its place, status word included, where these sizes want it (the other
+    parts are scratch, or zero between calls)."""
+    kind, B, n, V, stream = key[2:]
+    one = (dev.type, dev.index, kind, stream)
+    old = _WORKSPACES.get(one)
+    if old is None or old.numel() < L.spec_workspace_bytes(kind, B, n, V):
+        ws = L.new_workspace(kind, B, n, V, device=dev)
+        if old is not None:
+            ws[:4].copy_(old[:4])
+            for k in [k for k, x in _WORKSPACES.items() if x is old]:
+                _WORKSPACES[k] = ws
+        _WORKSPACES[one] = ws
+    _WORKSPACES[key] = _WORKSPACES[one]
+    return _WORKSPACES[one]
 
 
 def clear_workspaces() -> None:

@@ -265,3 +265,22 @@ def test_every_captured_call_gets_a_workspace_of_its_own(monkeypatch):
         capturing = False
         assert len({id(x) for x in (eager, *graphs)}) == 3 and api.workspace(kind, 1, 2, 64, dev) is eager
     api.clear_workspaces()
+
+
+def test_a_stream_has_one_workspace_of_a_kind(lib):
+    """Batches that grow and shrink, other heads, other budgets: one workspace of
+    the largest size so far, with the status word of the one it replaced."""
+    for kind, V in ((L.SPEC_WS_ATTENTION, 64), (L.SPEC_WS_ATTENTION_SHARED, 64), (L.SPEC_WS_EVICT, 2048)):
+        api.clear_workspaces()
+        first = api.workspace(kind, 1, 8, V, "cpu", stream=5)
+        first.view(torch.int32)[0] = 1
+        other = api.workspace(kind, 1, 8, V, "cpu", stream=6)
+        for B in list(range(1, 65)) + list(range(64, 0, -1)):
+            for n, v in ((8, V), (40, V), (300, 2 * V)):
+                w = api.workspace(kind, B, n, v, "cpu", stream=5)
+                assert w.numel() >= L.spec_workspace_bytes(kind, B, n, v) and w.view(torch.int32)[0] == 1
+        held = {w.data_ptr(): w.numel() for k, w in api._WORKSPACES.items() if k[-1] == 5}
+        assert list(held.values()) == [L.spec_workspace_bytes(kind, 64, 300, 2 * V)]
+        assert api.workspace(kind, 1, 8, V, "cpu", stream=5) is w and api.workspace(kind, 1, 8, V, "cpu", stream=6) is other
+        assert not w[4:L.SPEC_WS_ZEROED].any() and other.view(torch.int32)[0] == 0
+    api.clear_workspaces()

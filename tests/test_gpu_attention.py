@@ -1061,3 +1061,18 @@ def test_evictions_on_two_streams_at_once():
         for held in results:
             for x, y in zip(held, want):
                 assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_calls_of_other_sizes_on_one_workspace():
+    """A stream's calls of growing and shrinking sizes, heads and kinds share
+    its workspace, and their results do not change."""
+    api.clear_workspaces()
+    cases = [Case([700, 40], S=3, H=2, G=2, D=64, seed=60), Case([2000, 900, 5], S=9, H=2, G=16, D=128, seed=61),
+             Case([1500, 800], S=6, H=2, G=8, D=96, seed=62, shared=700), Case([333], S=2, H=1, G=3, D=200, seed=63),
+             Case([900, 700, 701, 800], S=8, H=2, G=8, D=128, seed=64, shared=690), Case([2100, 60], S=5, H=2, G=4, D=256, dtype="f32", seed=65)]
+    args = [c.args() for c in cases]
+    for order in (range(6), range(5, -1, -1)):
+        results = [(cases[i], api.verify_attention(*args[i][0], **args[i][1])) for i in order]
+        for c, r in results:
+            c.check(r)
+    assert len({w.data_ptr() for k, w in api._WORKSPACES.items() if k[2] in api._PER_STREAM}) == 2
