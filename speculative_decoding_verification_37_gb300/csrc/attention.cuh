@@ -130,7 +130,8 @@ __device__ __forceinline__ KeyLine attn_line(const AttnParams &p, const KeyRange
     const int mask = ~(p.box - 1);  // (a power of two)
     k.lo = r.lo & mask;
     const int end = p.tk && p.mode == 0 ? r.len : r.hi;
-    k.entries = (end - k.lo + p.box - 1) & mask;
+    // (no entry in range: none is looked up, though `lo` may lie inside a page)
+    k.entries = r.lo < end ? (end - k.lo + p.box - 1) & mask : 0;
     return k;
 }
 

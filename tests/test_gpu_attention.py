@@ -1076,3 +1076,28 @@ def test_calls_of_other_sizes_on_one_workspace():
         for c, r in results:
             c.check(r)
     assert len({w.data_ptr() for k, w in api._WORKSPACES.items() if k[2] in api._PER_STREAM}) == 2
+
+
+@pytest.mark.parametrize("dtype,bs", [("bf16", 16), ("bf16", 64), ("bf16", 5), ("f32", 16)])
+@pytest.mark.parametrize("G", [2, 8, 16])
+def test_a_request_without_entries_of_its_own_reads_none(G, dtype, bs):
+    """Requests that end where the shared prefix does, inside a page, and one
+    whose document begins past its entries: the table's id of that page is not
+    read, and nothing is flagged."""
+    c = Case([50, 50, 70], S=6, H=2, G=G, D=64, bs=bs, dtype=dtype, seed=19, shared=50)
+    c.check(c.run())
+    pos, a = c.args()
+    pos[2][:2, 50 // bs] = -1
+    pos[2][1, 50 // bs] = c.nb
+    flags = torch.zeros(3, dtype=torch.int32, device="cuda")
+    r = api.verify_attention(*pos, flags=flags, **a)
+    assert flags.tolist() == [0, 0, 0]
+    c.check(r)
+    c = Case([50, 70], S=6, H=2, G=G, D=64, bs=bs, dtype=dtype, seed=20)
+    c.first = np.array([50, 0], np.int32)
+    pos, a = c.args()
+    pos[2][0] = -1
+    flags = torch.zeros(2, dtype=torch.int32, device="cuda")
+    r = api.verify_attention(*pos, flags=flags, **a)
+    assert flags.tolist() == [0, 0]
+    c.check(r)
