@@ -46,8 +46,10 @@ template <typename T, int DP, int RT> struct SimtSmem {
 
 // Blocks an SM holds: 32 rows of 128 columns want 168 registers a thread (64 x 5
 // queries on 2,048 entries: 1,063 us in four blocks of 128, 719 in three, 867 in
-// two), of 64 columns 128 (417 in four, 485 in three).
-constexpr int blocks_of(int DP, int R) { return DP == 256 ? 2 : R == 1 || DP == 64 ? 4 : 3; }
+// two), of 64 columns 128 (417 in four, 485 in three); 32 rows of 256 columns fill
+// an SM's shared memory alone (a grid of two took turns on it: 16 requests of 5 x 4
+// queries a head on 2,048 entries 595 us, of one 533; of 13 x 4 queries 1,141, 1,104).
+constexpr int blocks_of(int DP, int R) { return DP == 256 ? (R == 1 ? 2 : 1) : R == 1 || DP == 64 ? 4 : 3; }
 
 template <typename T, int DP, int R>
 __global__ void __launch_bounds__(NT, blocks_of(DP, R)) attn_simt_kernel(AttnParams p) {
@@ -234,7 +236,8 @@ __global__ void __launch_bounds__(NT, blocks_of(DP, R)) attn_simt_kernel(AttnPar
 }
 
 template <typename T, int DP, int R> cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
-    const int smem = (int)sizeof(SimtSmem<T, DP, 16 * R>);
+    constexpr int smem = (int)sizeof(SimtSmem<T, DP, 16 * R>);
+    static_assert(blocks_of(DP, R) * (smem + 1024) <= 228 * 1024, "so many blocks' shared memory an SM has");
     cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<T, DP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // (at most 8 / R blocks an SM: the workspace's partial results)
