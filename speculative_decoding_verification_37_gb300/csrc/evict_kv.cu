@@ -37,6 +37,12 @@ struct SelectSmem {
     unsigned digit, above;
 };
 
+// Pages of n entries; pages may be as large as the table (n + bs - 1 would not fit).
+__host__ __device__ constexpr int pages_of(int n, int bs) { return n / bs + (n % bs != 0); }
+static_assert(pages_of(2000, 0x7fffffff - 1100) == 1 && pages_of(0x7fffffff - 1100, 0x7fffffff - 1100) == 1 &&
+                  pages_of(0, 4) == 0 && pages_of(8, 4) == 2 && pages_of(9, 4) == 3,
+              "pages");
+
 // exclusive prefix of v over the block, total in *all; two barriers
 __device__ __forceinline__ unsigned long long block_prefix(unsigned long long v, unsigned long long *buf, unsigned long long *all) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -77,7 +83,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p, int kep
     if (bad || len <= p.budget) {
         if (tid == 0) {
             p.n_moves[b] = 0;
-            if (p.blocks_in_use && !bad) p.blocks_in_use[b] = (len + p.bs - 1) / p.bs;
+            if (p.blocks_in_use && !bad) p.blocks_in_use[b] = pages_of(len, p.bs);
             if (bad) {
                 if (p.flags) atomicOr(p.flags + b, SPEC_FLAG_BAD_INPUT);
                 atomicOr(p.status, SPEC_FLAG_BAD_INPUT);
@@ -86,7 +92,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p, int kep
         return;
     }
     int newest = -1;
-    for (int i = tid; i < (len + p.bs - 1) / p.bs; i += NT) {
+    for (int i = tid; i < pages_of(len, p.bs); i += NT) {
         const int blk = table[i];
         bad = bad || blk < 0 || (int64_t)blk >= p.nb;
     }
@@ -115,7 +121,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p, int kep
     if (__syncthreads_or(bad || need0 < 0)) {
         if (tid == 0) {
             p.n_moves[b] = 0;
-            if (p.blocks_in_use) p.blocks_in_use[b] = (len + p.bs - 1) / p.bs;
+            if (p.blocks_in_use) p.blocks_in_use[b] = pages_of(len, p.bs);
             if (p.flags) atomicOr(p.flags + b, SPEC_FLAG_BAD_INPUT);
             atomicOr(p.status, SPEC_FLAG_BAD_INPUT);
         }
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(NT) evict_select_kernel(EvictParams p, int kep
     if (tid == 0) {
         p.n_moves[b] = n;
         p.len[b] = p.budget;
-        if (p.blocks_in_use) p.blocks_in_use[b] = (p.budget + p.bs - 1) / p.bs;
+        if (p.blocks_in_use) p.blocks_in_use[b] = pages_of(p.budget, p.bs);
     }
 }
 
