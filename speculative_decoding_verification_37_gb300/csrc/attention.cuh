@@ -321,9 +321,8 @@ __device__ __forceinline__ int key_position(const AttnParams &p, const AttnItem 
 
 // Mode 2, a request's first tile, its slots good: the positions of the committed
 // candidates whose entries lie among the shared ones, which no tile holds (threads
-// `tid` of `nt`).  Out of line: inline it took registers from the loops (f32, 64
-// requests of 2,048 entries: 625 us, so 550).
-static __device__ __noinline__ void shared_positions(const WeightsParams &wp, const AttnItem &it, int tid, int nt) {
+// `tid` of `nt`).
+__device__ __forceinline__ void shared_positions(const WeightsParams &wp, const AttnItem &it, int tid, int nt) {
     const AttnParams &p = wp.a;
     if (!wp.key_pos_out) return;
     const int cand0 = it.keys.len - p.n_slots[it.b];

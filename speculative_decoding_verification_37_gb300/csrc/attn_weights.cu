@@ -21,6 +21,12 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Out of line: inline it took registers from the loops (f32, 64 requests of 2,048
+// entries: 625 us, so 550).
+__device__ __noinline__ void shared_positions_call(const WeightsParams &wp, const AttnItem &it, int tid, int nt) {
+    shared_positions(wp, it, tid, nt);
+}
+
 template <typename T, int DP> struct WSmem {
     float k[2][KT][DP + 4];  // this head's and the next one's
     float q[RQ][DP];
@@ -61,7 +67,7 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
         for (int j = tid; slots && j < n; j += NT) bad = bad || slots[j] < 0 || slots[j] >= p.S;
         const bool skip = __syncthreads_or(bad);
         if (skip && u == it.u0 && tid == 0) attn_flag(p, b);
-        if (!skip && u == it.u0) shared_positions(wp, it, tid, NT);
+        if (!skip && u == it.u0) shared_positions_call(wp, it, tid, NT);
         const int t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), rows = n * p.G;
         const int first = p.first ? p.first[b] : (int)0x80000000;
         for (int t = (int)(u - it.u0); t < t1 && !skip; ++t) {
@@ -218,7 +224,7 @@ template <int DP> __global__ void __launch_bounds__(WNT, DP == 256 ? 1 : 2) weig
         for (int j = tid; slots && j < n; j += WNT) bad = bad || slots[j] < 0 || slots[j] >= p.S;
         const bool skip = __syncthreads_or(bad);
         if (skip && u == it.u0 && tid == 0) attn_flag(p, b);
-        if (!skip && u == it.u0) shared_positions(wp, it, tid, WNT);
+        if (!skip && u == it.u0) shared_positions_call(wp, it, tid, WNT);
         const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
         const int first = p.first ? p.first[b] : (int)0x80000000;
         const int cand0 = it.keys.len - n;  // the candidates' first entry

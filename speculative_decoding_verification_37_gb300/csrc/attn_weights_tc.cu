@@ -111,6 +111,7 @@ __global__ void __launch_bounds__(NT + 64, 1)
         while (true) {
             const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), slots = slots_of(p, it, lane);
             if (slots < 0 && u == it.u0 && lane == 0) attn_flag(p, it.b);
+            if (slots >= 0 && u == it.u0) shared_positions(wp, it, lane, 32);
             const int *table = p.table + (int64_t)it.b * p.max_blocks;
             const KeyLine line = slots > 0 ? attn_line(p, it.keys) : KeyLine{0, 0};
             for (int j0 = 0; j0 < slots; j0 += per_pass)
@@ -186,7 +187,6 @@ __global__ void __launch_bounds__(NT + 64, 1)
             const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0), slots_n = slots_of(p, it, lane);
             const int b = it.b;
             const int *slots = p.slots ? p.slots + (int64_t)b * p.slots_stride : nullptr, *table = p.table + (int64_t)b * p.max_blocks;
-            if (slots_n >= 0 && u == it.u0) shared_positions(wp, it, tid, NT);
             const int first = p.first ? p.first[b] : (int)0x80000000;
             const int cand0 = it.keys.len - slots_n;  // the candidates' first entry
             const KeyLine line = slots_n > 0 ? attn_line(p, it.keys) : KeyLine{0, 0};
