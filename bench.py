@@ -71,7 +71,8 @@ def _code_only(src: str) -> str:
     return " ".join("".join(out).split())
 
 
-# the operators that this benchmark does not time
+# the operators that this benchmark does not time (api.cu takes nothing of theirs but
+# workspace sizes)
 NOT_TIMED = ("api_attention.cu", "attention.cuh", "attn_", "evict_kv.cu")
 
 

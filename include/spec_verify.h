@@ -51,7 +51,8 @@
  *     runs out sets SPEC_FLAG_TIMEOUT in the status word.
  *   * Logits must not contain NaN or +inf (-inf is allowed and means "never").
  *   * The workspace must be at least spec_workspace_bytes(...) bytes, 256-byte
- *     aligned and zero-filled before its first use; every call leaves it
+ *     aligned and zero-filled before its first use (SPEC_WS_ZEROED bytes of the
+ *     kinds that say so); every call leaves it
  *     zeroed again (except the sticky status word).  Calls sharing one
  *     workspace must be ordered on one stream.
  */
@@ -516,7 +517,7 @@ int spec_tree_level(const SpecTreeLevelArgs *args, void *workspace, size_t ws_by
  *   without a mask iff j <= i.
  * Positions: candidate i is at pos[b][i] (NULL: committed_len[b] + i), entry c
  *   at key_pos[b][c] (row stride key_pos_stride; NULL: c; needed once entries
- *   have been evicted).  They matter to the bias and the masks only.
+ *   have been evicted), all >= 0.  They matter to the bias and the masks only.
  * Score of query i, head h and a key, with dist = their positions' difference:
  *   x = scale * (q . k);  softcap > 0: x = softcap * tanh(x / softcap);
  *   slopes: x -= slopes[h] * dist;  the key is masked when window > 0 and
@@ -546,8 +547,10 @@ int spec_tree_level(const SpecTreeLevelArgs *args, void *workspace, size_t ws_by
  *   bf16 calls (a larger one's rounding would reach the scores), and not so
  *   small that 2 log2(e) scale / softcap overflows.
  * Arithmetic: f32 sums and softmax statistics; bf16 calls multiply on the
- *   tensor cores with the softmax weights rounded to bf16.  The result does not
- *   depend on timing: sums are taken in a fixed order.
+ *   tensor cores with the softmax weights rounded to bf16 (their sum is not), and
+ *   take the cap's tanh from the hardware's exponential and reciprocal, to a few
+ *   2^-24 of the cap.  The result does not depend on timing: sums are taken in a
+ *   fixed order.
  * Workspace: SPEC_WS_ATTENTION bytes, or SPEC_WS_ATTENTION_SHARED with
  *   shared_len > 0; zero (SPEC_WS_ZEROED bytes) before the first call, left
  *   zeroed where it must be.  It holds the call's partial results: calls that
@@ -649,7 +652,7 @@ int spec_attention_weights(const SpecWeightsArgs *args, void *workspace, size_t 
  * request whose length is in range.  Entries at or past the new length keep
  * their bytes.
  * A batch that shares a prefix passes sink >= shared_len, so that no shared
- * entry moves.
+ * entry moves; its tables name the shared blocks here.
  * Errors: SPEC_ERR_INVALID_ARG for budget < 1, sink < 0, recent < 0 or sink +
  *   recent > budget.  A request with a length outside [0, max_blocks *
  *   block_size], a block id it holds outside [0, num_blocks), a NaN weight or

@@ -258,7 +258,8 @@ def verify_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Te
     shared_len entries lie in shared_table's blocks and are read once for the
     whole batch.  A query that sees no key gets 0 and an lse of -inf.
     Calls on different streams, and captured ones, may be in flight together;
-    with a ws of the caller's own only those that do not share it."""
+    with a ws of the caller's own only those that do not share it (a captured
+    call's status word can be read only there)."""
     B, S, Hq, D = q.shape
     with _allocating_on(stream):
         out = AttentionOut(out=torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device),

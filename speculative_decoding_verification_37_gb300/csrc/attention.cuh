@@ -21,6 +21,9 @@ namespace specv {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+// The hardware's 2^x (2 ulp) and log2 (2^-22), in float32 calls for the joins and lse
+// only: a partial sum's weight moves by 2^-22 of itself, lse by 2^-22, which its own
+// rounding reaches from 4 on.  (The weights of a float32 call are exp2f's.)
 __device__ __forceinline__ float ex2f(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -42,7 +42,7 @@ template <typename T, int DP> struct WSmem {
 // the queries, whose elements are broadcast; the next head's rows are copied
 // while this one's scores are taken.  Bound by issue and by the queries' staging
 // for each head and 16 of them (f32, 64 requests of 2,048 entries, 8 heads of 128:
-// up to 5 x 4 queries a head 613 us, up to 4 of them 323, 1.7 TB/s; all of a
+// up to 5 x 4 queries a head 550 us, up to 4 of them 298, 1.8 TB/s; all of a
 // head's rows before its scores, two lanes an entry: 788 and 530).
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {  // zeros where `bytes` is 0
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -182,7 +182,8 @@ template <typename T, int DP> __global__ void __launch_bounds__(NT) weights_simt
 // bf16 version, on the warp tensor instructions, for the head and page sizes
 // that attn_weights_tc.cu does not take.  Bound by latency: the registers that
 // hold K leave 16 warps an SM (512 ragged requests of up to 4,096 entries, 8
-// heads of 128: 728 us, 3.0 TB/s; there 394).
+// heads of 128, capped and biased: 729 us with pages of 4, 3.0 TB/s, 706 of 16,
+// which take 394 there).
 //
 // A warp owns 16 entries of a tile for all cached heads: the entries' K rows are
 // the rows (M = 16) of its products, the queries the columns (N = 8).  The order
