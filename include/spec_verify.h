@@ -52,9 +52,8 @@
  *   * Logits must not contain NaN or +inf (-inf is allowed and means "never").
  *   * The workspace must be at least spec_workspace_bytes(...) bytes, 256-byte
  *     aligned and zero-filled before its first use (SPEC_WS_ZEROED bytes of the
- *     kinds that say so); every call leaves it
- *     zeroed again (except the sticky status word).  Calls sharing one
- *     workspace must be ordered on one stream.
+ *     kinds that say so); every call leaves it zeroed again (except the sticky
+ *     status word).  Calls sharing one workspace must be ordered on one stream.
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H
@@ -601,7 +600,10 @@ int spec_verify_attention(const SpecAttentionArgs *args, void *workspace, size_t
  * of that call's softmax; rejected candidates leave none.)  Adding up over
  * layers and rounds is the caller's choice of calls.  A candidate whose lse is
  * -inf adds nothing.
- * key_pos (in/out when given): entry e_j gets pos[b][slots[b][j]].
+ * Sums are f32; where the queries of a request's candidates do not fit a block at
+ *   once, each part's sum is added to weight by itself (K is then read for each).
+ * key_pos (in/out when given): entry e_j gets pos[b][slots[b][j]], below shared_len
+ *   too.
  * weight's entries at or past committed_len must be zero before the commit
  *   (spec_evict_kv leaves them so).
  * Data errors: n_slots[b] outside [0, S] or above committed_len[b], a
