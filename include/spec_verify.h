@@ -105,6 +105,7 @@ extern "C" {
 #define SPEC_WS_ATTENTION_SHARED 7 /* SPEC_WS_ATTENTION plus one f32 row per (request, candidate,
                                 head) for the part over a shared prefix */
 #define SPEC_WS_EVICT 8 /* n = budget, V = max_blocks * block_size: the moves of each request */
+#define SPEC_WS_KV8 9   /* the 8-bit cache's writer, reader and commit: one arrival counter per request */
 #define SPEC_WS_ZEROED 32768 /* of the kinds 6, 7 and 8 only so many bytes, from the start on, have to
                                 be zero before the first call */
 
@@ -680,6 +681,148 @@ typedef struct SpecEvictArgs {
 } SpecEvictArgs;
 
 int spec_evict_kv(const SpecEvictArgs *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The paged cache in 8 bits.  A row, one entry's K or V in one cached head, is D
+ * e4m3 codes (OCP FP8, 4 exponent and 3 mantissa bits, no infinities) and an
+ * exponent byte s, and stands for code * 2^(s - 127); s = 255 stands for NaN.
+ *   codes [L][2][num_blocks][block_size][H][D], one byte each (K at 0, V at 1),
+ *   scale [L][2][num_blocks][H][block_size], the bytes s.
+ * Block tables, lengths and entries are spec_commit_kv's.
+ * A round's candidates are written to the cache first and read from there, in
+ * their own round as in later ones: a token's K and V are then the same to the
+ * verify forward as to plain decoding, which the losslessness of the acceptance
+ * rule rests on.  One round of a chain, in a layer: spec_write_kv_q8,
+ * spec_verify_attention_q8; after the last one spec_verify_chain with
+ * committed_len (the in-place commit).  Of a tree: spec_verify_tree, then
+ * spec_commit_kv_q8.  The entry weights and the eviction take bf16 and f32 caches
+ * only.
+ *
+ * Writing.  The K and V of new tokens i < n_new[b] of request b (NULL: all S) in
+ * one layer, at k + b*k_stride_b + i*k_stride_s + h*k_stride_h and alike for v, D
+ * elements each, go to entries committed_len[b] + i.  s is the smallest with
+ * max |x| <= 448 * 2^(s - 127), at least 1; the codes are x * 2^(127 - s) rounded
+ * to nearest, ties to even (at most 2^-4 of a value, or 2^-10 * 2^(s - 127)).  A row
+ * that holds a value that is not finite gets s = 255 and codes 0.  Nothing else
+ * is written; committed_len stays, for the other layers and the verify.
+ * Data errors: a negative committed_len[b], an n_new[b] outside [0, S] or entries
+ *   past the table: the request is skipped; a block id outside [0, num_blocks):
+ *   its entries are left out.  Both set SPEC_FLAG_BAD_INPUT in flags[b] and the
+ *   status word.
+ * Limits (of all calls on an 8-bit cache): D a multiple of 16 and <= 256, B <=
+ *   32768, codes on a 16-byte boundary; here k, v and their strides too.
+ * Workspace (this call, the reader and the commit): SPEC_WS_KV8 bytes, zero before
+ *   the first call and left zero but for the status word; calls that can be in
+ *   flight together need one each.
+ */
+typedef struct SpecWriteKvQ8Args {
+    int32_t B, S, H, D, L, layer, dtype; /* dtype of k and v: bf16 or f32 */
+    const void *k, *v;           /* device */
+    int64_t k_stride_b, k_stride_s, k_stride_h; /* elements */
+    int64_t v_stride_b, v_stride_s, v_stride_h;
+    void *codes;                 /* device in/out */
+    uint8_t *scale;              /* device in/out */
+    int64_t num_blocks;
+    int32_t block_size, max_blocks;
+    const int32_t *block_table;  /* device, int32 [B][max_blocks] */
+    const int32_t *committed_len; /* device, int32 [B] */
+    const int32_t *n_new;        /* device, int32 [B] or NULL: S */
+    uint32_t *flags;             /* device in/out [B] or NULL (bits are OR-ed in) */
+} SpecWriteKvQ8Args;
+
+int spec_write_kv_q8(const SpecWriteKvQ8Args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * spec_verify_attention over an 8-bit cache.  The candidates are the cache's
+ * entries committed_len[b] .. + S - 1 (there is no temp_kv); everything else,
+ * queries, positions, scores, masks, the shared prefix, outputs, data errors and
+ * the workspace (SPEC_WS_ATTENTION or SPEC_WS_ATTENTION_SHARED), is as there.
+ * q and out are bf16 or f32.
+ * A K row that stands for NaN makes the rows that see it NaN (out and lse), a V
+ *   row that does their out; a row with a NaN code may read as all NaN.  A query
+ *   that holds a value that is not finite gets NaN where it sees a key.
+ * Arithmetic: f32, softmax statistics included.
+ */
+typedef struct SpecAttentionQ8Args {
+    int32_t B, S, Hq, H, D, L, layer, dtype; /* dtype of q and out */
+    const void *q;               /* device */
+    int64_t q_stride_b, q_stride_s, q_stride_h; /* elements */
+    const void *cache;           /* device, the codes */
+    const uint8_t *cache_scale;  /* device */
+    int64_t num_blocks;
+    int32_t block_size, max_blocks;
+    const int32_t *block_table;  /* device, int32 [B][max_blocks] */
+    const int32_t *committed_len; /* device, int32 [B] */
+    const uint32_t *tree_mask;   /* device, [B][S][ceil(S/32)] or NULL: causal */
+    const int32_t *pos;          /* device, int32 [B][S] or NULL */
+    const int32_t *key_pos;      /* device, int32 [B][key_pos_stride] or NULL */
+    int64_t key_pos_stride;
+    const int32_t *first_pos;    /* device, int32 [B] or NULL */
+    const float *slopes;         /* device, f32 [Hq] or NULL */
+    float scale;                 /* finite */
+    float softcap;               /* 0 = off; at most 1024 with bf16 */
+    int32_t window;              /* 0 = off */
+    int32_t shared_len;          /* 0 = off */
+    const int32_t *shared_table; /* device, int32 [ceil(shared_len/block_size)] */
+    void *out;                   /* device out */
+    float *lse;                  /* device out or NULL */
+    uint32_t *flags;             /* device in/out or NULL */
+} SpecAttentionQ8Args;
+
+int spec_verify_attention_q8(const SpecAttentionQ8Args *args, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * Commit of a tree's accepted path in an 8-bit cache that holds the S candidates
+ * at entries committed_len[b] .. + S - 1: for i < n_slots[b] the codes and
+ * exponents of candidate slots[b][i] move to entry committed_len[b] + i, in every
+ * layer; then committed_len[b] += n_slots[b], and blocks_in_use[b] (optional) =
+ * ceil(length / block_size).  slots ascend (spec_verify_tree's commit_slots do);
+ * with slots NULL the first n_slots[b] candidates are kept where they are.  The
+ * entries past the new length are not defined.
+ * A request with slots that do not ascend within [0, S), n_slots[b] outside [0,
+ *   S], entries past the table or a block id it moves from or to outside [0,
+ *   num_blocks) is left as it is and flagged SPEC_FLAG_BAD_INPUT.  S <= 1024.
+ */
+typedef struct SpecCommitKvQ8Args {
+    int32_t B, S, H, D, L;
+    void *codes;                 /* device in/out */
+    uint8_t *scale;              /* device in/out */
+    int64_t num_blocks;
+    int32_t block_size, max_blocks;
+    const int32_t *block_table;  /* device, int32 [B][max_blocks] */
+    const int32_t *slots;        /* device, int32 [B][slots_stride] or NULL */
+    int32_t slots_stride;        /* >= S when slots != NULL */
+    const int32_t *n_slots;      /* device, int32 [B] */
+    int32_t *committed_len;      /* device in/out [B] */
+    int32_t *blocks_in_use;      /* device out [B] or NULL */
+    uint32_t *flags;             /* device in/out [B] or NULL (bits are OR-ed in) */
+} SpecCommitKvQ8Args;
+
+int spec_commit_kv_q8(const SpecCommitKvQ8Args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Reading back: k and v [B][S][H][D] of one layer get what entries start[b] + i
+ * (NULL: i), i < count[b] (NULL: S), stand for, rounded to their type (exact but
+ * for bf16's and f32's own range), and zeros from count[b] on.
+ * Data errors: a negative start[b], a count[b] outside [0, S] or entries past the
+ *   table give the request zeros, a block id outside [0, num_blocks) its entries;
+ *   both set SPEC_FLAG_BAD_INPUT in flags[b] and the status word.
+ */
+typedef struct SpecReadKvQ8Args {
+    int32_t B, S, H, D, L, layer, dtype; /* dtype of k and v: bf16 or f32 */
+    const void *codes;           /* device */
+    const uint8_t *scale;        /* device */
+    int64_t num_blocks;
+    int32_t block_size, max_blocks;
+    const int32_t *block_table;  /* device, int32 [B][max_blocks] */
+    const int32_t *start;        /* device, int32 [B] or NULL: 0 */
+    const int32_t *count;        /* device, int32 [B] or NULL: S */
+    void *k, *v;                 /* device out, on 16-byte boundaries */
+    uint32_t *flags;             /* device in/out [B] or NULL (bits are OR-ed in) */
+} SpecReadKvQ8Args;
+
+int spec_read_kv_q8(const SpecReadKvQ8Args *args, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Diagnostic: the largest relative error of the GPU's hardware exponential
  * (ex2.approx.ftz.f32) against fp64 over every fp32 input in [-126, 1], on the

@@ -11,3 +11,4 @@ from .ngram_oracle import NgramDraft, ngram_draft  # noqa: F401
 from .tree_build_oracle import Level, Tree, build_tree, expand_level  # noqa: F401
 from .attention_oracle import (Attention, Eviction, attend, candidate_mask, entries, entry_weights,  # noqa: F401
                                evict, hidden, scores)
+from .kv8_oracle import E4M3, kv8_commit, kv8_quantise, kv8_values  # noqa: F401

@@ -23,6 +23,7 @@ SPEC_FLAG_BAD_INPUT, SPEC_FLAG_FALLBACK, SPEC_FLAG_BAD_ROW, SPEC_FLAG_TIMEOUT = 
 SPEC_WS_CHAIN, SPEC_WS_TREE, SPEC_WS_COMMIT, SPEC_WS_CHAIN_TOPK, SPEC_WS_CHAIN_FULL = 0, 1, 2, 3, 4
 SPEC_WS_TREE_LEVEL = 5
 SPEC_WS_ATTENTION, SPEC_WS_ATTENTION_SHARED, SPEC_WS_EVICT = 6, 7, 8
+SPEC_WS_KV8 = 9
 SPEC_WS_ZEROED = 32768  # bytes of those three kinds that must be zero before the first call
 SPEC_FLAG_EOS, SPEC_FLAG_LIMIT = 16, 32
 SPEC_TREE_MAX_HEADS = 64
@@ -31,7 +32,8 @@ TOPK_FAST_MAX = 128   # top_k served by the candidate-pool path when the workspa
 EXPORTED = ("spec_verify_chain", "spec_verify_tree", "spec_commit_kv", "spec_workspace_bytes",
             "spec_get_status", "spec_error_string", "spec_last_cuda_error",
             "spec_verify_chain_static", "spec_selftest_ex2", "spec_ngram_draft", "spec_tree_level",
-            "spec_set_idle_limit", "spec_verify_attention", "spec_attention_weights", "spec_evict_kv")
+            "spec_set_idle_limit", "spec_verify_attention", "spec_attention_weights", "spec_evict_kv",
+            "spec_write_kv_q8", "spec_verify_attention_q8", "spec_commit_kv_q8", "spec_read_kv_q8")
 
 
 class SpecChainArgs(ctypes.Structure):
@@ -122,6 +124,45 @@ class SpecEvictArgs(ctypes.Structure):
                 ("flags", c_void_p)]
 
 
+class SpecWriteKvQ8Args(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("S", c_int32), ("H", c_int32), ("D", c_int32), ("L", c_int32),
+                ("layer", c_int32), ("dtype", c_int32), ("k", c_void_p), ("v", c_void_p),
+                ("k_stride_b", c_int64), ("k_stride_s", c_int64), ("k_stride_h", c_int64),
+                ("v_stride_b", c_int64), ("v_stride_s", c_int64), ("v_stride_h", c_int64),
+                ("codes", c_void_p), ("scale", c_void_p), ("num_blocks", c_int64),
+                ("block_size", c_int32), ("max_blocks", c_int32), ("block_table", c_void_p),
+                ("committed_len", c_void_p), ("n_new", c_void_p), ("flags", c_void_p)]
+
+
+class SpecAttentionQ8Args(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("S", c_int32), ("Hq", c_int32), ("H", c_int32), ("D", c_int32),
+                ("L", c_int32), ("layer", c_int32), ("dtype", c_int32), ("q", c_void_p),
+                ("q_stride_b", c_int64), ("q_stride_s", c_int64), ("q_stride_h", c_int64),
+                ("cache", c_void_p), ("cache_scale", c_void_p), ("num_blocks", c_int64),
+                ("block_size", c_int32), ("max_blocks", c_int32), ("block_table", c_void_p),
+                ("committed_len", c_void_p), ("tree_mask", c_void_p), ("pos", c_void_p),
+                ("key_pos", c_void_p), ("key_pos_stride", c_int64), ("first_pos", c_void_p),
+                ("slopes", c_void_p), ("scale", c_float), ("softcap", c_float), ("window", c_int32),
+                ("shared_len", c_int32), ("shared_table", c_void_p), ("out", c_void_p),
+                ("lse", c_void_p), ("flags", c_void_p)]
+
+
+class SpecCommitKvQ8Args(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("S", c_int32), ("H", c_int32), ("D", c_int32), ("L", c_int32),
+                ("codes", c_void_p), ("scale", c_void_p), ("num_blocks", c_int64),
+                ("block_size", c_int32), ("max_blocks", c_int32), ("block_table", c_void_p),
+                ("slots", c_void_p), ("slots_stride", c_int32), ("n_slots", c_void_p),
+                ("committed_len", c_void_p), ("blocks_in_use", c_void_p), ("flags", c_void_p)]
+
+
+class SpecReadKvQ8Args(ctypes.Structure):
+    _fields_ = [("B", c_int32), ("S", c_int32), ("H", c_int32), ("D", c_int32), ("L", c_int32),
+                ("layer", c_int32), ("dtype", c_int32), ("codes", c_void_p), ("scale", c_void_p),
+                ("num_blocks", c_int64), ("block_size", c_int32), ("max_blocks", c_int32),
+                ("block_table", c_void_p), ("start", c_void_p), ("count", c_void_p), ("k", c_void_p),
+                ("v", c_void_p), ("flags", c_void_p)]
+
+
 class SpecError(RuntimeError):
     def __init__(self, fn: str, code: int):
         msg = f"{fn} returned {code} ({lib().spec_error_string(code).decode()})"
@@ -166,7 +207,9 @@ def lib():
         L.spec_tree_level.argtypes = [POINTER(SpecTreeLevelArgs), c_void_p, c_size_t, c_void_p]
         L.spec_tree_level.restype = c_int
         for f, args in (("spec_verify_attention", SpecAttentionArgs), ("spec_attention_weights", SpecWeightsArgs),
-                        ("spec_evict_kv", SpecEvictArgs)):
+                        ("spec_evict_kv", SpecEvictArgs), ("spec_write_kv_q8", SpecWriteKvQ8Args),
+                        ("spec_verify_attention_q8", SpecAttentionQ8Args), ("spec_commit_kv_q8", SpecCommitKvQ8Args),
+                        ("spec_read_kv_q8", SpecReadKvQ8Args)):
             getattr(L, f).argtypes = [POINTER(args), c_void_p, c_size_t, c_void_p]
             getattr(L, f).restype = c_int
         _LIB = L
@@ -442,8 +485,32 @@ def _query_strides(fn: str, q: torch.Tensor, cache: torch.Tensor, B: int):
         raise ValueError(f"{fn}: q is on {q.device}, cache on {cache.device}")
     if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or (D > 1 and q.stride(3) != 1):
         raise ValueError(f"{fn}: q must be [{B}, S, Hq, {D}] with contiguous last dimension, not {tuple(q.shape)}")
+    return _free_strides(q)
+
+
+def _free_strides(t: torch.Tensor):
     # strides of dimensions of one element do not matter; the library wants them aligned
-    return [st if n > 1 else 0 for st, n in zip(q.stride(), q.shape)][:3]
+    return [st if n > 1 else 0 for st, n in zip(t.stride(), t.shape)][:3]
+
+
+def _cache8_shape(fn: str, codes: torch.Tensor, scale: torch.Tensor, block_size: int):
+    """Shape of an 8-bit cache's codes; its parts checked."""
+    if codes.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"{fn}: codes must be {torch.float8_e4m3fn}, not {codes.dtype}")
+    L, _, nb, bs, H, _ = shape = _cache_shape(fn, codes, block_size)
+    _checked(fn, "scale", scale, torch.uint8, (L, 2, nb, H, bs), codes.device)
+    return shape
+
+
+def _rows4(fn: str, name: str, t: torch.Tensor, dtype, shape, device):
+    """Strides over requests, tokens and heads of a tensor [B, S, H, D]."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not {device}")
+    if t.shape != shape or (shape[3] > 1 and t.stride(3) != 1):
+        raise ValueError(f"{fn}: {name} must be {list(shape)} with contiguous last dimension, not {tuple(t.shape)}")
+    return _free_strides(t)
 
 
 def _launch(fn: str, args, workspace: torch.Tensor, device, stream) -> None:
@@ -550,4 +617,106 @@ def spec_evict_kv(*, cache: torch.Tensor, block_table: torch.Tensor, committed_l
         _checked(fn, "block_table", block_table, i32, (B, mb), dev), mb, budget, sink, recent,
         _checked(fn, "committed_len", committed_len, i32, (B,), dev), w, ws, kp, kps,
         _checked(fn, "blocks_in_use", blocks_in_use, i32, (B,), dev), _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)
+
+
+def spec_write_kv_q8(*, k: torch.Tensor, v: torch.Tensor, codes: torch.Tensor, scale: torch.Tensor,
+                     block_table: torch.Tensor, committed_len: torch.Tensor, block_size: int,
+                     workspace: torch.Tensor, layer: int = 0, n_new: Optional[torch.Tensor] = None,
+                     flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Marshals one spec_write_kv_q8 call: k, v [B, S, H, D] (last dimension
+    contiguous), codes [L, 2, num_blocks, block_size, H, D], scale uint8
+    [L, 2, num_blocks, H, block_size]."""
+    fn = "spec_write_kv_q8"
+    Ly, _, nb, bs, H, D = _cache8_shape(fn, codes, scale, block_size)
+    dev, i32 = codes.device, torch.int32
+    B, mb = block_table.shape
+    if k.dim() != 4:
+        raise ValueError(f"{fn}: k must be [{B}, S, {H}, {D}], not {tuple(k.shape)}")
+    shape = (B, k.shape[1], H, D)
+    ks = _rows4(fn, "k", k, k.dtype, shape, dev)
+    vs = _rows4(fn, "v", v, k.dtype, shape, dev)
+    _int32(fn, layer=layer)
+    a = SpecWriteKvQ8Args(
+        B, shape[1], H, D, Ly, layer, _dtype_code(k), k.data_ptr(), v.data_ptr(), *ks, *vs, codes.data_ptr(),
+        scale.data_ptr(), nb, bs, mb, _checked(fn, "block_table", block_table, i32, (B, mb), dev),
+        _checked(fn, "committed_len", committed_len, i32, (B,), dev), _checked(fn, "n_new", n_new, i32, (B,), dev),
+        _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)
+
+
+def spec_verify_attention_q8(*, q: torch.Tensor, codes: torch.Tensor, cache_scale: torch.Tensor,
+                             block_table: torch.Tensor, committed_len: torch.Tensor, block_size: int,
+                             out: torch.Tensor, workspace: torch.Tensor, scale: float, layer: int = 0,
+                             tree_mask: Optional[torch.Tensor] = None, pos: Optional[torch.Tensor] = None,
+                             key_pos: Optional[torch.Tensor] = None, first_pos: Optional[torch.Tensor] = None,
+                             slopes: Optional[torch.Tensor] = None, softcap: float = 0.0, window: int = 0,
+                             shared_table: Optional[torch.Tensor] = None, shared_len: int = 0,
+                             lse: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+                             stream=None) -> None:
+    """Marshals one spec_verify_attention_q8 call: q, out [B, S, Hq, D] of bf16 or
+    f32, codes and cache_scale as in spec_write_kv_q8, the rest as in
+    spec_verify_attention."""
+    fn = "spec_verify_attention_q8"
+    Ly, _, nb, bs, H, D = _cache8_shape(fn, codes, cache_scale, block_size)
+    dev, i32 = codes.device, torch.int32
+    B, mb = block_table.shape
+    if q.dim() != 4:
+        raise ValueError(f"{fn}: q must be [{B}, S, Hq, {D}], not {tuple(q.shape)}")
+    S, Hq = q.shape[1], q.shape[2]
+    sb, ss, sh = _rows4(fn, "q", q, q.dtype, (B, S, Hq, D), dev)
+    _int32(fn, layer=layer, window=window, shared_len=shared_len)
+    kp, kps = _rows(fn, "key_pos", key_pos, i32, B, mb * bs, dev)
+    if shared_len > 0 and (shared_table is None or shared_table.numel() * bs < shared_len):
+        raise ValueError(f"{fn}: shared_len {shared_len} needs a shared_table of {-(-shared_len // bs)} blocks")
+    a = SpecAttentionQ8Args(
+        B, S, Hq, H, D, Ly, layer, _dtype_code(q), q.data_ptr(), sb, ss, sh, codes.data_ptr(), cache_scale.data_ptr(),
+        nb, bs, mb, _checked(fn, "block_table", block_table, i32, (B, mb), dev),
+        _checked(fn, "committed_len", committed_len, i32, (B,), dev),
+        _checked(fn, "tree_mask", tree_mask, i32, (B, S, (S + 31) // 32), dev),
+        _checked(fn, "pos", pos, i32, (B, S), dev), kp, kps, _checked(fn, "first_pos", first_pos, i32, (B,), dev),
+        _checked(fn, "slopes", slopes, torch.float32, (Hq,), dev), scale, softcap, window, shared_len,
+        _checked(fn, "shared_table", shared_table, i32, (-1,), dev),
+        _checked(fn, "out", out, q.dtype, (B, S, Hq, D), dev), _checked(fn, "lse", lse, torch.float32, (B, S, Hq), dev),
+        _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)
+
+
+def spec_commit_kv_q8(*, codes: torch.Tensor, scale: torch.Tensor, block_table: torch.Tensor, S: int,
+                      n_slots: torch.Tensor, committed_len: torch.Tensor, block_size: int, workspace: torch.Tensor,
+                      slots: Optional[torch.Tensor] = None, blocks_in_use: Optional[torch.Tensor] = None,
+                      flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Marshals one spec_commit_kv_q8 call: slots int32 [B, >= S] or None."""
+    fn = "spec_commit_kv_q8"
+    Ly, _, nb, bs, H, D = _cache8_shape(fn, codes, scale, block_size)
+    dev, i32 = codes.device, torch.int32
+    B, mb = block_table.shape
+    sl, sls = _rows(fn, "slots", slots, i32, B, S, dev)
+    _int32(fn, S=S, slots_stride=sls)
+    a = SpecCommitKvQ8Args(
+        B, S, H, D, Ly, codes.data_ptr(), scale.data_ptr(), nb, bs, mb,
+        _checked(fn, "block_table", block_table, i32, (B, mb), dev), sl, sls,
+        _checked(fn, "n_slots", n_slots, i32, (B,), dev), _checked(fn, "committed_len", committed_len, i32, (B,), dev),
+        _checked(fn, "blocks_in_use", blocks_in_use, i32, (B,), dev), _checked(fn, "flags", flags, i32, (B,), dev))
+    _launch(fn, a, workspace, dev, stream)
+
+
+def spec_read_kv_q8(*, codes: torch.Tensor, scale: torch.Tensor, block_table: torch.Tensor, k: torch.Tensor,
+                    v: torch.Tensor, block_size: int, workspace: torch.Tensor, layer: int = 0,
+                    start: Optional[torch.Tensor] = None, count: Optional[torch.Tensor] = None,
+                    flags: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Marshals one spec_read_kv_q8 call: k, v [B, S, H, D] of bf16 or f32."""
+    fn = "spec_read_kv_q8"
+    Ly, _, nb, bs, H, D = _cache8_shape(fn, codes, scale, block_size)
+    dev, i32 = codes.device, torch.int32
+    B, mb = block_table.shape
+    _int32(fn, layer=layer)
+    if k.dim() != 4:
+        raise ValueError(f"{fn}: k must be [{B}, S, {H}, {D}], not {tuple(k.shape)}")
+    S = k.shape[1]
+    a = SpecReadKvQ8Args(
+        B, S, H, D, Ly, layer, _dtype_code(k), codes.data_ptr(), scale.data_ptr(), nb, bs, mb,
+        _checked(fn, "block_table", block_table, i32, (B, mb), dev), _checked(fn, "start", start, i32, (B,), dev),
+        _checked(fn, "count", count, i32, (B,), dev), _checked(fn, "k", k, k.dtype, (B, S, H, D), dev),
+        _checked(fn, "v", v, k.dtype, (B, S, H, D), dev), _checked(fn, "flags", flags, i32, (B,), dev))
     _launch(fn, a, workspace, dev, stream)

@@ -13,8 +13,8 @@ from . import _lib as L
 _WORKSPACES: Dict[Tuple, torch.Tensor] = {}
 
 
-# kinds that hold a call's intermediate results: one for each stream
-_PER_STREAM = (L.SPEC_WS_ATTENTION, L.SPEC_WS_ATTENTION_SHARED, L.SPEC_WS_EVICT)
+# kinds that hold a call's intermediate results or counters: one for each stream
+_PER_STREAM = (L.SPEC_WS_ATTENTION, L.SPEC_WS_ATTENTION_SHARED, L.SPEC_WS_EVICT, L.SPEC_WS_KV8)
 
 
 def workspace(kind: int, B: int, n: int, V: int, device, stream: Optional[int] = None) -> torch.Tensor:
@@ -26,7 +26,7 @@ def workspace(kind: int, B: int, n: int, V: int, device, stream: Optional[int] =
     workspace of the graph's own, zeroed by each replay: a cached one would
     not be zero before the first replay.
     The attention's and the eviction's kinds (zero in the SPEC_WS_ZEROED bytes
-    that have to be) are cached for each stream (the raw handle of a stream that
+    that have to be) and the 8-bit cache's are cached for each stream (the raw handle of a stream that
     is current; None: the current one), so that calls in flight on two streams do
     not meet; a stream has one of each kind, as large as its largest call so far
     wanted.  Every captured call gets its own: its graph may be replayed on any
@@ -316,6 +316,117 @@ def evict_kv(cache: torch.Tensor, block_table: torch.Tensor, committed_len: torc
     L.spec_evict_kv(cache=cache, block_table=block_table, committed_len=committed_len, weight=weight,
                     key_pos=key_pos, block_size=block_size, budget=budget, workspace=ws, sink=sink, recent=recent,
                     blocks_in_use=blocks_in_use, flags=flags, stream=stream)
+
+
+@dataclass
+class QuantKV:
+    """A paged cache in 8 bits: a row (entry, cached head) stands for
+    codes * 2**(scale - 127), a scale of 255 for NaN."""
+    codes: torch.Tensor          # float8_e4m3fn [L, 2, num_blocks, block_size, H, D]
+    scale: torch.Tensor          # uint8 [L, 2, num_blocks, H, block_size]
+
+
+def quant_kv(layers: int, num_blocks: int, block_size: int, H: int, D: int, device="cuda") -> QuantKV:
+    """An 8-bit cache of zeros."""
+    codes = torch.zeros((layers, 2, num_blocks, block_size, H, D), dtype=torch.uint8, device=device)
+    return QuantKV(codes=codes.view(torch.float8_e4m3fn),
+                   scale=torch.zeros((layers, 2, num_blocks, H, block_size), dtype=torch.uint8, device=device))
+
+
+def _kv8_workspace(ws, B: int, cache: QuantKV, stream):
+    """The stream a call on an 8-bit cache runs on, and its workspace."""
+    stream, raw = _stream_of(stream, cache.codes)
+    return stream, workspace(L.SPEC_WS_KV8, B, 0, 0, cache.codes.device, raw) if ws is None else ws
+
+
+def write_kv_q8(k: torch.Tensor, v: torch.Tensor, cache: QuantKV, block_table: torch.Tensor,
+                committed_len: torch.Tensor, *, block_size: int, layer: int = 0,
+                n_new: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Writes the K and V of new tokens (a prompt's, or a round's candidates) into
+    one layer of an 8-bit cache, in place: token i < n_new[b] (None: all S) of
+    request b becomes entry committed_len[b] + i.  k, v [B, S, H, D] of bf16 or
+    f32, strides free but for the last dimension's.  committed_len stays as it
+    is: verify_chain with committed_len, or commit_kv_q8, advances it once every
+    layer has been written.  Streams, captures and ws as for verify_attention."""
+    with _allocating_on(stream):
+        stream, ws = _kv8_workspace(ws, block_table.shape[0], cache, stream)
+    L.spec_write_kv_q8(k=k, v=v, codes=cache.codes, scale=cache.scale, block_table=block_table,
+                       committed_len=committed_len, block_size=block_size, workspace=ws, layer=layer, n_new=n_new,
+                       flags=flags, stream=stream)
+
+
+def verify_attention_q8(q: torch.Tensor, cache: QuantKV, block_table: torch.Tensor, committed_len: torch.Tensor, *,
+                        block_size: int, layer: int = 0, tree_mask: Optional[torch.Tensor] = None,
+                        pos: Optional[torch.Tensor] = None, key_pos: Optional[torch.Tensor] = None,
+                        first_pos: Optional[torch.Tensor] = None, slopes: Optional[torch.Tensor] = None,
+                        scale: Optional[float] = None, softcap: float = 0.0, window: int = 0,
+                        shared_table: Optional[torch.Tensor] = None, shared_len: int = 0,
+                        flags: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                        stream=None) -> AttentionOut:
+    """verify_attention over an 8-bit cache.  q [B, S, Hq, D] of bf16 or f32; the
+    candidates' K and V are the entries committed_len[b] .. + S - 1, where
+    write_kv_q8 put them, so that they are read in their own round as they will
+    be in later ones.  The other arguments and the results as for
+    verify_attention."""
+    B, S, Hq, D = q.shape
+    with _allocating_on(stream):
+        out = AttentionOut(out=torch.empty((B, S, Hq, D), dtype=q.dtype, device=q.device),
+                           lse=torch.empty((B, S, Hq), dtype=torch.float32, device=q.device))
+        stream, raw = _stream_of(stream, q)
+        if ws is None:
+            ws = workspace(L.SPEC_WS_ATTENTION_SHARED if shared_len > 0 else L.SPEC_WS_ATTENTION, B, S * Hq, D, q.device, raw)
+    L.spec_verify_attention_q8(q=q, codes=cache.codes, cache_scale=cache.scale, block_table=block_table,
+                               committed_len=committed_len, block_size=block_size, out=out.out, lse=out.lse,
+                               workspace=ws, layer=layer, scale=D ** -0.5 if scale is None else scale,
+                               tree_mask=tree_mask, pos=pos, key_pos=key_pos, first_pos=first_pos, slopes=slopes,
+                               softcap=softcap, window=window, shared_table=shared_table, shared_len=shared_len,
+                               flags=flags, stream=stream)
+    return out
+
+
+def commit_kv_q8(cache: QuantKV, block_table: torch.Tensor, slots: Optional[torch.Tensor], n_slots: torch.Tensor,
+                 committed_len: torch.Tensor, *, block_size: int, S: Optional[int] = None,
+                 blocks_in_use: Optional[torch.Tensor] = None, flags: Optional[torch.Tensor] = None,
+                 ws: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Keeps the accepted candidates of a round in an 8-bit cache, in every layer:
+    candidate slots[b][i] (verify_tree's commit_slots, int32 [B, S]) moves from
+    entry committed_len[b] + slots[b][i] to committed_len[b] + i, for i <
+    n_slots[b]; committed_len advances by n_slots.  slots None, with S given: the
+    first n_slots[b] stay where they are.  Streams, captures and ws as for
+    verify_attention."""
+    if S is None:
+        if slots is None:
+            raise ValueError("commit_kv_q8: S is needed without slots")
+        S = slots.shape[1]
+    with _allocating_on(stream):
+        stream, ws = _kv8_workspace(ws, block_table.shape[0], cache, stream)
+    L.spec_commit_kv_q8(codes=cache.codes, scale=cache.scale, block_table=block_table, S=S, n_slots=n_slots,
+                        committed_len=committed_len, block_size=block_size, workspace=ws, slots=slots,
+                        blocks_in_use=blocks_in_use, flags=flags, stream=stream)
+
+
+@dataclass
+class KV:
+    k: torch.Tensor              # [B, n_max, H, D]
+    v: torch.Tensor
+
+
+def read_kv_q8(cache: QuantKV, block_table: torch.Tensor, start: Optional[torch.Tensor] = None,
+               count: Optional[torch.Tensor] = None, *, n_max: int, block_size: int, layer: int = 0,
+               dtype: torch.dtype = torch.bfloat16, flags: Optional[torch.Tensor] = None,
+               ws: Optional[torch.Tensor] = None, stream=None) -> KV:
+    """What the entries start[b] (None: 0) .. + count[b] - 1 (None: n_max entries)
+    of one layer of an 8-bit cache stand for, in bf16 or f32, and zeros from
+    count[b] to n_max.  Streams, captures and ws as for verify_attention."""
+    B, H, D = block_table.shape[0], cache.codes.shape[4], cache.codes.shape[5]
+    with _allocating_on(stream):
+        out = KV(*(torch.empty((B, n_max, H, D), dtype=dtype, device=cache.codes.device) for _ in range(2)))
+        stream, ws = _kv8_workspace(ws, B, cache, stream)
+    L.spec_read_kv_q8(codes=cache.codes, scale=cache.scale, block_table=block_table, k=out.k, v=out.v,
+                      block_size=block_size, workspace=ws, layer=layer, start=start, count=count, flags=flags,
+                      stream=stream)
+    return out
 
 
 @dataclass

@@ -233,6 +233,7 @@ extern "C" size_t spec_workspace_bytes(int kind, int32_t B, int32_t n, int32_t V
     case SPEC_WS_TREE:
         return ws_layout_bytes(B, 0, (size_t)B * (size_t)n * sizeof(unsigned long long), nullptr, nullptr);
     case SPEC_WS_COMMIT:
+    case SPEC_WS_KV8:
         return kWsHeader + ws_align((size_t)B * sizeof(unsigned));
     case SPEC_WS_TREE_LEVEL:
         return tree_level_layout(B, n, V, nullptr, nullptr);

@@ -1,5 +1,5 @@
 // C ABI of the operators around the paged cache: argument checks, workspace
-// layouts, launches (spec_verify_attention, spec_attention_weights,
+// layouts, launches (spec_verify_attention and _q8, spec_attention_weights,
 // spec_evict_kv).
 #include <cmath>
 
@@ -13,7 +13,7 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// The checks and parameters the two calls that score queries share.
+// The checks and parameters the calls that score queries share.
 template <typename A> int scored_call(const A *a, AttnParams &p) {
     if (a->B < 0 || a->B > 32768 || a->S < 1 || a->S > SPEC_ATTENTION_MAX_S || a->H < 1 || a->Hq < 1 ||
         a->Hq % a->H != 0 || a->D < 1 || a->L < 1 || a->layer < 0 || a->layer >= a->L)
@@ -164,6 +164,41 @@ extern "C" int spec_verify_attention(const SpecAttentionArgs *a, void *workspace
         if (err != cudaSuccess) return report_cuda_error(err);
     }
     return report_cuda_error(launch(p));
+}
+
+extern "C" int spec_verify_attention_q8(const SpecAttentionQ8Args *a, void *workspace, size_t ws_bytes, void *stream) {
+    if (!a) return SPEC_ERR_INVALID_ARG;
+    if (a->D > 0 && a->D % 16 != 0) return SPEC_ERR_UNSUPPORTED;  // (codes are copied 16 at a time)
+    AttnParams p;
+    const int chk = scored_call(a, p);
+    if (chk != SPEC_OK || a->B == 0) return chk;
+    if (!a->cache_scale || !a->out || !aligned(a->out, 16)) return SPEC_ERR_INVALID_ARG;
+    if (a->shared_len > 0 && (!a->shared_table || a->key_pos)) return SPEC_ERR_INVALID_ARG;
+    const int kind = a->shared_len > 0 ? SPEC_WS_ATTENTION_SHARED : SPEC_WS_ATTENTION;
+    if ((int64_t)a->S * a->Hq > 0x7fffffffLL) return SPEC_ERR_UNSUPPORTED;
+    if (!workspace || !aligned(workspace, 256) ||
+        ws_bytes < spec_workspace_bytes(kind, a->B, a->S * a->Hq, a->D))
+        return SPEC_ERR_INVALID_ARG;
+    attn_ws_layout(a->B, a->S * a->Hq, a->D, a->shared_len > 0, workspace, &p);
+    const int64_t rows = a->num_blocks * a->block_size * a->H;
+    p.kc = static_cast<const char *>(a->cache) + rows * a->D * 2 * a->layer;
+    p.vc = static_cast<const char *>(p.kc) + rows * a->D;
+    p.ks = a->cache_scale + rows * 2 * a->layer;
+    p.vs = p.ks + rows;
+    p.mask = a->tree_mask;
+    p.stable = a->shared_table;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.min_share = 1;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int sms = device_sms();
+    if (a->shared_len > 0) {
+        AttnParams q = p;
+        q.mode = 1;
+        const cudaError_t err = launch_attn8_simt(q, a->dtype, sms, s);
+        if (err != cudaSuccess) return report_cuda_error(err);
+    }
+    return report_cuda_error(launch_attn8_simt(p, a->dtype, sms, s));
 }
 
 extern "C" int spec_attention_weights(const SpecWeightsArgs *a, void *workspace, size_t ws_bytes, void *stream) {

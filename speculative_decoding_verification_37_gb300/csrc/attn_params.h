@@ -46,6 +46,7 @@ struct AttnParams {
     const void *q;
     int64_t qsb, qss, qsh;
     const void *kc, *vc;          // the layer's planes [nb][bs][H][D]
+    const unsigned char *ks, *vs; // an 8-bit cache's: exponents [nb][H][bs] (kv8.cuh)
     const void *tk, *tv;          // the layer's candidates of request 0, or null (in place)
     int64_t tsb;                  // elements between two requests' candidates
     const void *temp_base;        // [B][layers][2][S][H][D]
@@ -82,6 +83,9 @@ cudaError_t launch_attn_mma(const AttnParams &p, int sms, cudaStream_t s);  // b
 int attn_tc_box(const AttnParams &p);
 cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t s);
 
+// over an 8-bit cache: queries and out bf16 or f32
+cudaError_t launch_attn8_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s);
+
 struct WeightsParams {
     AttnParams a;                 // q, cache, tables, score (P: entries left out)
     const float *lse_in;
@@ -110,6 +114,31 @@ struct EvictParams {
     int2 *moves;                  // [B][max_moves] (from, to) entries
 };
 cudaError_t launch_evict(const EvictParams &p, int sms, cudaStream_t s);
+
+// The 8-bit cache's writer, reader and commit (kv8.cu).
+struct Kv8Params {
+    int B, S, L, H, D, bs, max_blocks;
+    int64_t nb;
+    FastDiv bs_div;
+    const void *k, *v;            // write: [b][s][h][D]
+    int64_t sb[2], ss[2], sh[2];  // K's and V's strides
+    void *out_k, *out_v;          // read: [B][S][H][D]
+    unsigned char *codes, *scale; // the layer's K planes (commit: layer 0's)
+    int64_t plane, splane;        // bytes from a plane to the next
+    const int *table;
+    const int *start, *count;     // first entry (null: 0), entries (null: S)
+    const int *slots;             // commit: null, the first `count`
+    int slots_stride;
+    int *len, *blocks_in_use;     // commit
+    unsigned *flags, *status, *counters;
+    int etiles;                   // the launch's: entry tiles of a request; commit: its blocks
+};
+// blocks of the launches
+int64_t kv8_row_blocks(int32_t B, int32_t S, int32_t H);
+int64_t kv8_commit_blocks(int32_t B, int32_t L);
+cudaError_t launch_kv8_rows(Kv8Params p, int dtype, bool write, cudaStream_t s);
+cudaError_t launch_kv8_commit(Kv8Params p, cudaStream_t s);
+
 // workspace layouts (null base: the size alone)
 size_t attn_ws_layout(int32_t B, int32_t n, int32_t D, bool shared, void *base, AttnParams *p);
 size_t evict_ws_layout(int32_t B, int32_t budget, int32_t capacity, void *base, EvictParams *p);
