@@ -741,7 +741,11 @@ int spec_write_kv_q8(const SpecWriteKvQ8Args *args, void *workspace, size_t work
  * A K row that stands for NaN makes the rows that see it NaN (out and lse), a V
  *   row that does their out; a row with a NaN code may read as all NaN.  A query
  *   that holds a value that is not finite gets NaN where it sees a key.
- * Arithmetic: f32, softmax statistics included.
+ * Arithmetic: f32 sums and softmax statistics.  bf16 calls with D <= 128 on pages
+ *   of a multiple of 8 entries multiply on the tensor cores: a query, scaled by a
+ *   power of two, as the sum of two e4m3 numbers (off by at most 2^-17 of the
+ *   query's largest element), K's codes as they are, the softmax weights times
+ *   V's powers of two rounded to bf16, V's codes exactly.  The others in f32.
  */
 typedef struct SpecAttentionQ8Args {
     int32_t B, S, Hq, H, D, L, layer, dtype; /* dtype of q and out */

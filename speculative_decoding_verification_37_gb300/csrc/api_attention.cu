@@ -192,13 +192,17 @@ extern "C" int spec_verify_attention_q8(const SpecAttentionQ8Args *a, void *work
     p.min_share = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int sms = device_sms();
+    auto launch = [&](AttnParams &x) {
+        x.box = a->dtype == SPEC_DTYPE_BF16 ? attn8_tc_box(x) : 0;
+        return x.box ? launch_attn8_tc(x, sms, s) : launch_attn8_simt(x, a->dtype, sms, s);
+    };
     if (a->shared_len > 0) {
         AttnParams q = p;
         q.mode = 1;
-        const cudaError_t err = launch_attn8_simt(q, a->dtype, sms, s);
+        const cudaError_t err = launch(q);
         if (err != cudaSuccess) return report_cuda_error(err);
     }
-    return report_cuda_error(launch_attn8_simt(p, a->dtype, sms, s));
+    return report_cuda_error(launch(p));
 }
 
 extern "C" int spec_attention_weights(const SpecWeightsArgs *a, void *workspace, size_t ws_bytes, void *stream) {

@@ -1,4 +1,5 @@
-// Attention over the 8-bit paged cache on the CUDA cores.
+// Attention over the 8-bit paged cache on the CUDA cores: float32 queries, heads
+// above 128, pages that are not multiples of 8 entries (the others: attn8_tc.cu).
 //
 // The float32 kernel's scheme (attn_simt.cu): a block holds 16 or 32 queries, a
 // quarter of them a warp, and 32 keys at a time; for the scores a lane has a key,

@@ -84,6 +84,8 @@ int attn_tc_box(const AttnParams &p);
 cudaError_t launch_attn_tc(const AttnParams &p, int sms, cudaStream_t s);
 
 // over an 8-bit cache: queries and out bf16 or f32
+int attn8_tc_box(const AttnParams &p);  // bf16; 0: launch_attn8_tc does not take the call
+cudaError_t launch_attn8_tc(const AttnParams &p, int sms, cudaStream_t s);
 cudaError_t launch_attn8_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s);
 
 struct WeightsParams {
