@@ -7,7 +7,12 @@ term more: the tensor kernels take a query as the sum of two e4m3 numbers after
 scaling its largest element into (224, 448].  The second number's steps are 2^-9
 at least, half of that over 224 is 2^-17.8 of the largest element; what its first
 three bits leave of a bf16 value is otherwise exact.  So a score's error grows by
-at most |scale| 2^-17 max|q| sum|k|."""
+at most |scale| 2^-17 max|q| sum|k|.  The weights, times V's powers of two, are
+rounded to f16 (2^-11 of each, below the bf16 rounding's 2^-8) and held as three
+e4m3 numbers: exactly, or, as the third one's steps end at 2^-19 where the row's
+largest power and a weight of 1 are at 2^5, to half a step, 2^-25 of the largest
+power, for a key, with codes up to 448 and 448 powers at most twice the largest |v|
+that the row sees, over a sum of weights that is at least 1."""
 import math
 
 import numpy as np
@@ -282,6 +287,20 @@ class Case8(Case):
             q = np.abs(self.q[b].double().numpy()).max()
             e += abs(self.score["scale"]) * 2.0 ** -17 * q * float(np.abs(k).sum(-1).max())
         return e
+
+    def check(self, r, rows=None):
+        """As Case.check, with the weights' smallest steps."""
+        self.steps = 0.0
+        if self.dtype == torch.bfloat16:
+            v = self.planes()[1]
+            self.steps = 2.0 ** -25 * 2 * float(np.nanmax(np.abs(v)))
+        super().check(r, rows)
+
+    def oracle(self, b):
+        ref, k, off = super().oracle(b)
+        # (Case.check's tolerance is at least 2^-8 of the mass: the steps go there)
+        ref.mass = ref.mass + 2.0 ** 8 * (len(k) + self.shared) * getattr(self, "steps", 0.0)
+        return ref, k, off
 
 
 SHAPES = [
