@@ -15,17 +15,16 @@
 //   * O^T = V^T P^T.  A weight of 2^-20 next to one of 1 is worth keeping where there are
 //     many, and e4m3 ends at 2^-9.  So a weight, times its key's power of two relative
 //     to the largest that the row has seen, is rounded to f16 and taken apart into three
-//     e4m3 numbers, each of what the one before left, times 32: exact to f16's 11 bits,
-//     or to 2^-25 of a weight of 1 at the largest power.  They are columns of one
-//     product and are added at the item's end.  (With V's codes as f16 in shared memory
-//     instead, two thirds of a thread's instructions were those of the conversion:
-//     single queries on up to 32,768 entries 466 us.)
+//     e5m2 numbers: the upper byte of an f16 is one, and what it leaves is an f16
+//     again.  So the parts cost an AND, a subtraction and half a byte shuffle each, need
+//     no scales, and hold 9 bits, or 2^-24 of a weight of 1 at the largest power.  They are
+//     columns of one product and are added at the item's end.
 //   * A row's largest score lies across the threads.  It is looked for, and the
 //     largest power, in an item's first tile and where a score passes the reference
-//     by 2^3 or a power the smallest of the rows', which one vote of the tile's threads
-//     finds; otherwise nobody needs another's scores.  Tiles go from the last to the
-//     first: with a bias by distance the largest scores come first.  Sums of weights
-//     stay in the threads until the item's end.
+//     by 2^8 or a power the smallest of the rows', which one vote of the tile's threads
+//     finds; otherwise nobody needs another's scores.  Tiles go from the last, which is
+//     full, to the first: with a bias by distance the largest scores come first.  Sums
+//     of weights stay in the threads until the item's end.
 //   * Where a tile hides keys, the threads look whether V holds NaN's code: such a row
 //     becomes zeros and gives its NaN, by way of the power of two, to the rows that
 //     give it weight; the rows that it is hidden from see nothing.
@@ -43,16 +42,17 @@ constexpr int KT = 128, GT = 128, NT = 256;  // keys of a tile; softmax threads 
 constexpr uint32_t kTile = KT * 128;  // bytes of 128 keys x up to 128 codes
 constexpr int kInfo = 8;              // tiles whose notes are kept
 constexpr float kNone = -1e30f;       // the reference of a row that has seen no key
-constexpr float kLag = 3.0f;          // log2 of what a weight may reach
+constexpr float kLag = 8.0f;          // log2 of what a weight may reach
 constexpr int kPowMin = 16;           // exponent byte that smaller powers are taken relative to
-constexpr int kUp = 5;                // log2 of a weight of 1 at the largest power: 2^(kUp + kLag) is a code
+constexpr int kUp = 7;                // log2 of a weight of 1 at the largest power: 2^(kUp + kLag) is an e5m2 number
+constexpr int kParts = 3;             // e5m2 numbers that hold a weight
 
 __device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
 
 // e4m3 x e4m3 -> f32, M = 128, both operands K-major
 __host__ __device__ constexpr uint32_t tc_idesc8(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24); }
-// the same, both operands' rows contiguous
-__host__ __device__ constexpr uint32_t tc_idesc_mn(int n) { return tc_idesc8(n) | (1u << 15) | (1u << 16); }
+// e4m3 x e5m2, both operands' rows contiguous
+__host__ __device__ constexpr uint32_t tc_idesc_mn(int n) { return tc_idesc8(n) | (1u << 10) | (1u << 15) | (1u << 16); }
 __device__ __forceinline__ void tc_mma8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -67,6 +67,12 @@ template <int N> __device__ __forceinline__ void tc_load(float *x, uint32_t t) {
 template <int N> __device__ __forceinline__ void tc_store(uint32_t t, const uint32_t *x) {
 #pragma unroll
     for (int i = 0; i < N; i += 16) tc_st16(t + i, x + i);
+}
+
+__device__ __forceinline__ void tc_st8(uint32_t t, const float *x) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
 }
 
 // a barrier of n threads under an id of its own that joins a predicate
@@ -90,20 +96,26 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Two f16 as e4m3 codes; `h` becomes what they leave, times 32.
-__device__ __forceinline__ uint32_t take_e4m3(uint32_t &h) {
+// Two f16, which lose their upper bytes: what e5m2 numbers of them leave.
+__device__ __forceinline__ uint32_t rest_e5m2(uint32_t h) {
+    const uint32_t top = h & 0xff00ff00u;
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&top));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t round_e5m2(uint32_t h) {
     uint16_t c;
-    uint32_t back;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(c));
-    const __half2 up = __half2half2(__ushort_as_half(0x5000)), down = __half2half2(__ushort_as_half(0xd000));  // +-32
-    const __half2 left = __hfma2(*reinterpret_cast<const __half2 *>(&back), down, __hmul2(*reinterpret_cast<const __half2 *>(&h), up));
-    h = *reinterpret_cast<const uint32_t *>(&left);
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
     return c;
 }
 // 2^e of -126 <= e <= 127; below: 0
 __device__ __forceinline__ float pow2i(int e) { return e < -126 ? 0.0f : __uint_as_float((unsigned)(e + 127) << 23); }
 
+// the warp's largest, a NaN left out
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
 // op over the warp's lanes of each of N rows' values: lane i has the result of row i
 // (N = 16: of row i / 2) in v[0].
 template <int N, typename F> __device__ __forceinline__ void reduce_rows(float (&v)[N], F &&op) {
@@ -139,12 +151,14 @@ template <int NH, int RT> struct Team8 {
     alignas(1024) unsigned char p[2][kP];            // two tiles' P^T: a key's weights, three parts of four
     alignas(16) float ref[RT], corr[RT], corr_o[RT], gain[RT];  // references (log2 units), what sums and O are
                                                      // multiplied by, what weights are at a power of 1
-    alignas(16) float top[4][RT], pow[4][RT];        // the warps' largest scores and powers; at the end sums of weights
+    alignas(16) float top[4][RT];                    // the warps' largest scores; at the end sums of weights
+    alignas(16) int pow[4][RT];                      // and powers
     alignas(16) float cf[RT];                        // scale times what the queries were divided by; without cap and bias times log2(e)
     alignas(16) float qp[RT];                        // positions after the item's first
     alignas(16) int low[RT];                         // first visible position
     alignas(16) float fa[RT], fc[RT];                // output: factors of O and of the shared part
-    AttnRows<RT> rows;
+    AttnRows<RT> rows[2];
+    unsigned words[RT][5];                           // a tile's candidates in the rows' tree masks
     int pow_min, low_max, qp0;                       // the smallest largest power; the largest `low`; the first position
     unsigned sc[kInfo][2][KT / 4];                   // exponent bytes of a tile's K and V
     unsigned bad[kInfo];                             // boxes of a tile with a bad block
@@ -157,7 +171,15 @@ template <int NH, int RT> struct Tc8Smem {
     uint32_t tmem;
 };
 
-template <int NH, int RT>
+// the item after `it` (one copy of this code)
+static __device__ __noinline__ void next_item(const AttnParams &p, AttnItem &it, int items, int rtiles) {
+    it = attn_next(p, it, items, rtiles, KT);
+}
+// The first key of an item's line of tiles: the last tile is full, the first has what
+// is left (whole boxes).
+__device__ __forceinline__ int line_start(const KeyLine &line, int ntiles) { return line.lo - (ntiles * KT - line.entries); }
+
+template <int NH, int RT, bool plain>
 __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
     attn8_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap cache_map) {
     using H = Team8<NH, RT>;
@@ -204,8 +226,8 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
     int64_t u = part * share;
     const int64_t uend = min(all.plan.total, u + share);
     // TMEM columns: the teams' two score tiles, then their accumulators
-    const uint32_t col_s = tmem + grp * 2 * RT, col_o = tmem + (2 * G + 3 * grp) * RT;
-    static_assert(5 * G * RT <= 512, "columns");
+    const uint32_t col_s = tmem + grp * 2 * RT, col_o = tmem + (2 * G + kParts * grp) * RT;
+    static_assert((2 + kParts) * G * RT <= 512, "columns");
     bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
     if (u < uend) {
         AttnItem it = attn_find<NT>(p, all.plan, u, items, rtiles, KT);
@@ -226,19 +248,20 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                 int blk = 0, row = 0;
                 unsigned ks = 0u, vs = 0u;
                 bool bad = false;
+                const int start = line_start(line, it.ntiles);
                 auto has = [&](int t) {
-                    const int k = t * KT + lane * 4;
-                    return t >= t0 && k < line.entries && line.lo + k < it.keys.hi;
+                    const int c = start + t * KT + lane * 4;
+                    return t >= t0 && it.keys.ok && c >= line.lo && c < it.keys.hi;
                 };
                 auto block_of = [&](int t) {
-                    return has(t) ? __ldg(table + fast_div((unsigned)(line.lo + t * KT + lane * 4), p.bs_div)) : 0;
+                    return has(t) ? __ldg(table + fast_div((unsigned)(start + t * KT + lane * 4), p.bs_div)) : 0;
                 };
                 auto entry_of = [&](int t) {
                     ks = vs = 0u;
                     row = zero_row;
                     bad = false;
                     if (has(t)) {
-                        const int c = line.lo + t * KT + lane * 4, at = c - (int)fast_div((unsigned)c, p.bs_div) * p.bs;
+                        const int c = start + t * KT + lane * 4, at = c - (int)fast_div((unsigned)c, p.bs_div) * p.bs;
                         bad = blk < 0 || (int64_t)blk >= p.nb;
                         if (!bad) {
                             row = blk * p.bs + at;
@@ -287,7 +310,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                 }
                 u = it.u0 + it.ntiles;
                 if (u >= uend) break;
-                it = attn_next(p, it, items, rtiles, KT);
+                next_item(p, it, items, rtiles);
             }
             // no copy may land after the block has gone
             for (int i = max(0, n - H::KS); i < n; ++i) ok = mbar_drain(&sh.k_full[i % H::KS], (unsigned)((i / H::KS) & 1)) && ok;
@@ -299,7 +322,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                 // columns of K and Q are 32 bytes.  Values: the rows are keys, the products'
                 // K, whose elements (V's columns: M; P's weights: N) are contiguous, up to 128
                 // of V (zeros past the head) and 64 or 128 of P in an atom's row.
-                constexpr uint32_t id_s = tc_idesc8(RT), id_o = tc_idesc_mn(3 * RT);
+                constexpr uint32_t id_s = tc_idesc8(RT), id_o = tc_idesc_mn(kParts * RT);
                 const uint64_t dq = tc_desc(smem_u32(sh.q[0]), 16, 1024), dk = tc_desc(smem_u32(sh.k[0]), 16, 1024),
                                dv = tc_desc(smem_u32(sh.v[0]), 0, 1024),
                                dp = RT == 16 ? tc_desc64(smem_u32(sh.p[0]), 512) : tc_desc(smem_u32(sh.p[0]), 0, 1024);
@@ -341,7 +364,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     ++item;
                     u = it.u0 + it.ntiles;
                     if (u >= uend) break;
-                    it = attn_next(p, it, items, rtiles, KT);
+                    next_item(p, it, items, rtiles);
                 }
             }
             __syncwarp();
@@ -352,20 +375,23 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
             const uint32_t lanes = (uint32_t)(wq * 32) << 16;
             const uint32_t to = col_o + lanes;
             const bool by_pos = p.window > 0 || p.first != nullptr;
-            const bool plain = p.score.cap == 0.0f && !p.score.bias;
             const uint32_t neg = p.score.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale: the queries are negated
             const float scale = fabsf(p.score.scale) * (plain ? kLog2e : 1.0f);
             constexpr unsigned kRowLanes = RT == 16 ? 0xffffu : kFull;
             int item = 0, n = 0;
-            while (true) {
-                // ---- the item's rows and queries: 8 elements a thread at a time
-                AttnRows<RT> &w = sh.rows;
+            auto start_rows = [&] {  // of an item: nothing seen yet
+                if (key < RT) {
+                    sh.ref[key] = kNone;
+                    sh.gain[key] = pow2i(127 + kUp - kPowMin);
+                }
+            };
+            // An item's rows and queries: 8 elements a thread at a time.  The next item's are
+            // prepared before this one's output.
+            auto prepare = [&](AttnRows<RT> &w) {
                 attn_rows<RT, GT>(p, it, w, key);
                 if (key < RT) {
                     const int lo = max(w.first[key], p.window > 0 ? w.qp[key] - p.window + 1 : (int)0x80000000);
                     sh.low[key] = lo;
-                    sh.ref[key] = kNone;
-                    sh.gain[key] = pow2i(127 + kUp - kPowMin);
                     const bool is = w.out[key] >= 0;
                     const int most = __reduce_max_sync(kRowLanes, is ? lo : (int)0x80000000);
                     const int qp0 = __reduce_min_sync(kRowLanes, is ? w.qp[key] : 0x7fffffff);
@@ -377,47 +403,51 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                 }
                 bar_sync(bar, GT);
                 constexpr int LR = NH * 8, Q = RT * LR / GT;          // lanes of a row; a thread's pieces
-                {
-                    const int d = (key % LR) * 8;
-                    uint4 v[Q];
+                const int d = (key % LR) * 8;
+                uint4 v[Q];
 #pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        const int r = key / LR + i * (GT / LR);
-                        v[i] = make_uint4(0, 0, 0, 0);
-                        if (w.q[r] >= 0 && d < p.D) v[i] = ld_nc16(static_cast<const T *>(p.q) + w.q[r] + d);
+                for (int i = 0; i < Q; ++i) {
+                    const int r = key / LR + i * (GT / LR);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (w.q[r] >= 0 && d < p.D) v[i] = ld_nc16(static_cast<const T *>(p.q) + w.q[r] + d);
+                }
+#pragma unroll
+                for (int i = 0; i < Q; ++i) {
+                    const int r = key / LR + i * (GT / LR);
+                    v[i].x ^= neg, v[i].y ^= neg, v[i].z ^= neg, v[i].w ^= neg;
+                    float x[8], top = 0.0f;
+                    unpack<T>(v[i], x);
+                    if (nonfinite2(v[i].x) | nonfinite2(v[i].y) | nonfinite2(v[i].z) | nonfinite2(v[i].w)) top = INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+#pragma unroll
+                    for (int o = LR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                    const unsigned s = kv8_scale(top);
+                    const float f = s == 255u ? 0.0f : kv8_inverse(s);
+                    if (key % LR == 0) sh.cf[r] = scale * kv8_power(s);
+                    uint32_t a[2], b[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a[e] = kv8_code2(x[4 * e] * f, x[4 * e + 1] * f) | kv8_code2(x[4 * e + 2] * f, x[4 * e + 3] * f) << 16;
+                        const float4 y = kv8_value4(a[e]);
+                        b[e] = kv8_code2(x[4 * e] * f - y.x, x[4 * e + 1] * f - y.y) |
+                               kv8_code2(x[4 * e + 2] * f - y.z, x[4 * e + 3] * f - y.w) << 16;
                     }
-#pragma unroll
-                    for (int i = 0; i < Q; ++i) {
-                        const int r = key / LR + i * (GT / LR);
-                        v[i].x ^= neg, v[i].y ^= neg, v[i].z ^= neg, v[i].w ^= neg;
-                        float x[8], top = 0.0f;
-                        unpack<T>(v[i], x);
-                        if (nonfinite2(v[i].x) | nonfinite2(v[i].y) | nonfinite2(v[i].z) | nonfinite2(v[i].w)) top = INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
-#pragma unroll
-                        for (int o = LR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-                        const unsigned s = kv8_scale(top);
-                        const float f = s == 255u ? 0.0f : kv8_inverse(s);
-                        if (key % LR == 0) sh.cf[r] = scale * kv8_power(s);
-                        uint32_t a[2], b[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            a[e] = kv8_code2(x[4 * e] * f, x[4 * e + 1] * f) | kv8_code2(x[4 * e + 2] * f, x[4 * e + 3] * f) << 16;
-                            const float4 y = kv8_value4(a[e]);
-                            b[e] = kv8_code2(x[4 * e] * f - y.x, x[4 * e + 1] * f - y.y) |
-                                   kv8_code2(x[4 * e + 2] * f - y.z, x[4 * e + 3] * f - y.w) << 16;
-                        }
-                        const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
-                        *reinterpret_cast<uint2 *>(sh.q[0] + at) = make_uint2(a[0], a[1]);
-                        *reinterpret_cast<uint2 *>(sh.q[1] + at) = make_uint2(b[0], b[1]);
-                    }
+                    const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
+                    *reinterpret_cast<uint2 *>(sh.q[0] + at) = make_uint2(a[0], a[1]);
+                    *reinterpret_cast<uint2 *>(sh.q[1] + at) = make_uint2(b[0], b[1]);
                 }
                 fence_async_shared();
                 bar_sync(bar, GT);
                 mbar_arrive(&sh.q_full);
+            };
+            start_rows();
+            prepare(sh.rows[0]);
+            while (true) {
+                const AttnRows<RT> &w = sh.rows[item & 1];
                 const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
                 const KeyLine line = it.keys.ok ? attn_line(p, it.keys) : KeyLine{0, 0};
+                const int start = line_start(line, it.ntiles);
                 const int low_max = sh.low_max, qp0 = sh.qp0;
                 int pow_min = 0;                 // the smallest of the rows' largest powers
                 float l[RT];                     // sums of this thread's weights
@@ -425,14 +455,14 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                 for (int r = 0; r < RT; ++r) l[r] = 0.0f;
                 // position of this thread's key of tile t, when key_pos is given: read a tile ahead
                 auto key_pos_of = [&](int t) {
-                    const int k = t * KT + key, c = line.lo + k;
-                    return k < line.entries && c < it.keys.len ? __ldg(p.key_pos + (int64_t)it.b * p.kps + c) : 0;
+                    const int c = start + t * KT + key;
+                    return it.keys.ok && c >= line.lo && c < it.keys.len ? __ldg(p.key_pos + (int64_t)it.b * p.kps + c) : 0;
                 };
                 int kp_next = p.key_pos ? key_pos_of(t1 - 1) : 0;
                 const int n0 = n;
 #pragma unroll 1
                 for (int t = t1 - 1; t >= t0; --t, ++n) {
-                    const int k0 = t * KT, c0 = line.lo + k0;
+                    const int c0 = start + t * KT;
                     int kp = c0 + key;
                     if (p.key_pos) {
                         kp = kp_next;
@@ -447,14 +477,39 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     const unsigned bad = sh.bad[n % kInfo];
                     // whether the tile may mask a key: the line's ends, candidates, a bad
                     // block, the window's and the document's first tile
-                    const bool special = !it.keys.ok || c0 < it.keys.lo || c0 + KT > it.keys.len || k0 + KT > line.entries ||
+                    const bool special = !it.keys.ok || c0 < it.keys.lo || c0 + KT > it.keys.len ||
                                          bad != 0u || (by_pos && (p.key_pos || c0 < low_max));
                     const int cand = c0 + key - it.keys.len;           // the key as a candidate, or < 0
                     bool in = true;
                     if (special) {
-                        in = it.keys.ok && k0 + key < line.entries && c0 + key >= it.keys.lo && c0 + key < it.keys.hi &&
+                        in = it.keys.ok && c0 + key >= it.keys.lo && c0 + key < it.keys.hi &&
                              !((bad >> (key / p.box)) & 1u);
                         if (in && cand >= 0) kp = key_position(p, it, c0 + key);
+                    }
+                    unsigned seen = kFull;                             // bit r: by row r
+                    if (special) {
+                        // (the tree masks' words of a tile with candidates: loaded once, by the rows)
+                        const bool tree = p.mode == 0 && p.mask && c0 + KT > it.keys.len;
+                        const int word0 = max(c0 - it.keys.len, 0) >> 5;
+                        if (tree) {
+                            for (int i = key; i < RT * 5; i += GT) {
+                                const int r = i / 5, x = word0 + i - r * 5;
+                                sh.words[r][i - r * 5] = x < p.W ? p.mask[((int64_t)it.b * p.S + w.cand[r]) * p.W + x] : 0u;
+                            }
+                            bar_sync(bar, GT);
+                        }
+                        if (!in) {
+                            seen = 0u;
+                        } else if (by_pos || (p.mode == 0 && cand >= 0)) {
+                            const int x = (cand >> 5) - word0;
+                            seen = 0u;
+#pragma unroll 8
+                            for (int r = 0; r < RT; ++r) {
+                                bool s = !by_pos || kp >= sh.low[r];
+                                if (p.mode == 0 && cand >= 0) s = s && (tree ? (sh.words[r][x] >> (cand & 31)) & 1u : cand <= w.cand[r]);
+                                seen |= (unsigned)s << r;
+                            }
+                        }
                     }
                     const uint32_t ts = col_s + (n & 1) * RT + lanes;
                     const float kd = (float)pos_dist(qp0, kp);
@@ -510,14 +565,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                         }
                         if (special) {
 #pragma unroll
-                            for (int r = 0; r < RT; ++r) {
-                                bool seen = in && (!by_pos || kp >= sh.low[r]);
-                                if (seen && p.mode == 0 && cand >= 0) {
-                                    const int s = w.cand[r];
-                                    seen = p.mask ? (p.mask[((int64_t)it.b * p.S + s) * p.W + (cand >> 5)] >> (cand & 31)) & 1u : cand <= s;
-                                }
-                                if (!seen) y[r] = -INFINITY;
-                            }
+                            for (int r = 0; r < RT; ++r) y[r] = (seen >> r) & 1u ? y[r] : -INFINITY;
                         }
                         if (!raw) {
                             const float over = max_of<RT>(y);
@@ -527,28 +575,31 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                         }
                         // The tile's largest scores and powers; a new reference where a row's score
                         // has grown past 2^kLag of the old one.
-                        {
-                            const int to_row = RT == 32 ? lane : lane >> 1;
-                            float v[RT];
+                        float mine = -INFINITY;  // of row `lane`
+                        int most = 0;
+                        const int every = __reduce_max_sync(kFull, pw);
 #pragma unroll
-                            for (int r = 0; r < RT; ++r) v[r] = y[r];
-                            reduce_rows<RT>(v, [](float a, float b) { return fmaxf(a, b); });
-                            if (RT == 32 || (lane & 1) == 0) sh.top[wq][to_row] = v[0];
-                            if (special) {
-#pragma unroll
-                                for (int r = 0; r < RT; ++r) {
-                                    const int most = __reduce_max_sync(kFull, y[r] == -INFINITY ? 0 : pw);
-                                    if (lane == 0) sh.pow[wq][r] = (float)most;
-                                }
-                            } else {  // every row sees every key
-                                const int most = __reduce_max_sync(kFull, pw);
-                                if (lane < RT) sh.pow[wq][lane] = (float)most;
+                        for (int r = 0; r < RT; ++r) {
+                            const float m = warp_max(y[r]);
+                            if (lane == r) mine = m;
+                        }
+                        if (special) {
+#pragma unroll 8
+                            for (int r = 0; r < RT; ++r) {
+                                const int m = __reduce_max_sync(kFull, (seen >> r) & 1u ? pw : 0);
+                                if (lane == r) most = m;
                             }
+                        } else {  // every row sees every key
+                            most = every;
+                        }
+                        if (lane < RT) {
+                            sh.top[wq][lane] = mine;
+                            sh.pow[wq][lane] = most;
                         }
                         bar_sync(bar, GT);
                         if (key < RT) {
                             const float top = fmaxf(fmaxf(sh.top[0][key], sh.top[1][key]), fmaxf(sh.top[2][key], sh.top[3][key]));
-                            const int most = (int)fmaxf(fmaxf(sh.pow[0][key], sh.pow[1][key]), fmaxf(sh.pow[2][key], sh.pow[3][key]));
+                            const int most = max(max(sh.pow[0][key], sh.pow[1][key]), max(sh.pow[2][key], sh.pow[3][key]));
                             const float old = sh.ref[key];
                             const bool grew = top > old + kLag || (old == kNone && top > kNone);
                             const float f = grew ? ex2f(old - top) : 1.0f;
@@ -572,7 +623,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                             if (ok) ok = attn_wait(&sh.pv_done[(n - 1) & 1], (unsigned)(((n - 1) >> 1) & 1));
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < 3 * RT; c += 16) {
+                            for (int c = 0; c < kParts * RT; c += 16) {
                                 const float *f = sh.corr_o + (c & (RT - 1));
                                 float o[16];
                                 uint32_t z[16];
@@ -613,7 +664,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     const bool pick = special || vf != vf;
 #pragma unroll
                     for (int r = 0; r < RT; r += 16) {
-                        uint32_t z[3][4];
+                        uint32_t h[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int q = r + 2 * i;
@@ -625,26 +676,34 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                             // (a V that stands for NaN does not show where it has no weight; a hidden
                             // one's power may be any)
                             if (pick) b = pair(a.x == 0.0f ? 0.0f : b.x, a.y == 0.0f ? 0.0f : b.y);
-                            uint32_t h = pack_f16(b.x, b.y);
-#pragma unroll
-                            for (int c = 0; c < 3; ++c) {
-                                const uint32_t two = take_e4m3(h);
-                                if (i & 1) z[c][i / 2] |= two << 16;
-                                else z[c][i / 2] = two;
-                            }
+                            h[i] = pack_f16(b.x, b.y);
                         }
+                        auto put = [&](int c) {
+                            uint32_t z[4];
 #pragma unroll
-                        for (int c = 0; c < 3; ++c)
-                            *reinterpret_cast<uint4 *>(pp + (((c * (RT / 16) + r / 16) ^ sw) << 4)) = make_uint4(z[c][0], z[c][1], z[c][2], z[c][3]);
+                            for (int i = 0; i < 4; ++i) z[i] = c < 2 ? __byte_perm(h[2 * i], h[2 * i + 1], 0x7531) : h[2 * i] | h[2 * i + 1] << 16;
+                            *reinterpret_cast<uint4 *>(pp + (((c * (RT / 16) + r / 16) ^ sw) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+                        };
+                        put(0);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[i] = rest_e5m2(h[i]);
+                        put(1);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[i] = round_e5m2(rest_e5m2(h[i]));
+                        put(2);
                     }
                     fence_async_shared();
                     tc_fence_before();
                     mbar_arrive(&sh.p_full[n & 1]);
                 }
-                // ---- the item's end: sums of weights over the threads
+                // ---- the item's end: the next one's queries, then this one's output
                 const AttnItem done = it;
                 const int64_t end = it.u0 + it.ntiles;
-                if (end < uend) it = attn_next(p, it, items, rtiles, KT);
+                u = end;
+                if (end < uend) {
+                    next_item(p, it, items, rtiles);
+                    prepare(sh.rows[item & 1 ^ 1]);
+                }
                 reduce_rows<RT>(l, [](float a, float b) { return a + b; });
                 if (RT == 32 || (lane & 1) == 0) sh.top[wq][RT == 32 ? lane : lane >> 1] = l[0];
                 // the shared part's results are there, and its partial results done with
@@ -656,81 +715,150 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     c0 = (int)(done.u0 / share);
                     c1 = (int)((end - 1) / share);
                 }
-                const bool split = c0 != c1;
-                // a part's results: slot 0 the item that began before it, slot 1 the one that goes on
-                float *mine = p.part + ((int64_t)part * 2 + (part == c0 ? 1 : 0)) * ((int64_t)RT * (p.D + 2));
                 bar_sync(bar, GT);
+                float s = 0.0f, m = -INFINITY, back = 1.0f;  // of row `key`: sum, reference, what O is divided by
                 if (key < RT) {
-                    float s = (sh.top[0][key] + sh.top[1][key]) + (sh.top[2][key] + sh.top[3][key]);
-                    const bool some = s > 0.0f || s != s;  // a NaN sum stays NaN
-                    const float m = some ? sh.ref[key] : -INFINITY, back = 1.0f / sh.gain[key];  // (powers of two)
-                    const int64_t row = w.out[key];
-                    float fa = back, fc = 0.0f;
-                    if (split) {
-                        __stcg(mine + (int64_t)RT * p.D + key, m);
-                        __stcg(mine + (int64_t)RT * p.D + RT + key, s);
-                    } else if (row >= 0) {
-                        float lse2 = some ? m + lg2f(s) : -INFINITY;
-                        if (p.mode == 0 && p.P > 0 && done.keys.ok) {
-                            const float lp = p.pre_lse[row], mm = fmaxf(m, lp), a = rel_weight(m, mm), c = lp != lp ? lp : rel_weight(lp, mm);
-                            s = s * a + c;
-                            lse2 = s > 0.0f || s != s ? mm + lg2f(s) : -INFINITY;
-                            fa *= a;
-                            fc = c;
-                        }
-                        const float inv = lse2 == -INFINITY ? 0.0f : 1.0f / s;
-                        fa *= inv;
-                        fc *= inv;
-                        if (p.mode == 1) p.pre_lse[row] = lse2;
-                        else if (p.lse) p.lse[row] = lse2 * kLn2;
-                    }
-                    sh.fa[key] = fa;
-                    sh.fc[key] = fc;
+                    s = (sh.top[0][key] + sh.top[1][key]) + (sh.top[2][key] + sh.top[3][key]);
+                    if (s > 0.0f || s != s) m = sh.ref[key];  // a NaN sum stays NaN
+                    sh.fa[key] = back = 1.0f / sh.gain[key];  // (powers of two)
                 }
-                bar_sync(bar, GT);
                 if (ok) ok = attn_wait(&sh.pv_done[(n - 1) & 1], (unsigned)(((n - 1) >> 1) & 1));
                 tc_fence_after();
-                const bool join = p.mode == 0 && p.P > 0 && done.keys.ok && !split;
-                // (code that runs once an item stays short: it comes from far away)
+                bool write = true;
+                if (c0 != c1) {
+                    // Part c's results: slot 0 of a part holds the item that began before it, slot
+                    // 1 the one that goes on after it.  The part that arrives last joins them, into
+                    // its own O, and leaves the counter zero.
+                    const int64_t slot = (int64_t)RT * (p.D + 2);
+                    auto part_of = [&](int c) { return p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot; };
+                    float *mine = part_of(part);
+                    bar_sync(bar, GT);
+                    if (key < RT) {
+                        __stcg(mine + (int64_t)RT * p.D + key, m);
+                        __stcg(mine + (int64_t)RT * p.D + RT + key, s);
+                    }
 #pragma unroll 1
-                for (int h = 0; h < RT; h += 8) {
-                    float o[3][8];
+                    for (int h = 0; h < RT; h += 8) {
+                        float o[kParts][8];
 #pragma unroll
-                    for (int c = 0; c < 3; ++c) tc_ld8(o[c], to + c * RT + h);
-                    tc_wait_ld();
-                    if (key >= p.D) continue;
+                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * RT + h);
+                        tc_wait_ld();
+                        if (key < p.D)
 #pragma unroll
-                    for (int r = 0; r < 8; ++r) {
-                        const int64_t row = w.out[h + r];
-                        if (row < 0) continue;
-                        const float f = sh.fa[h + r];
-                        float x = f == 0.0f ? 0.0f : fmaf(fmaf(o[2][r], 0.03125f, o[1][r]), 0.03125f, o[0][r]) * f;
-                        const int64_t at = row * p.D + key;
-                        if (split) {
-                            __stcg(mine + (int64_t)(h + r) * p.D + key, x);
-                            continue;
+                            for (int r = 0; r < 8; ++r) __stcg(mine + (int64_t)(h + r) * p.D + key, (o[0][r] + o[1][r] + o[2][r]) * sh.fa[h + r]);
+                    }
+                    __threadfence();
+                    bar_sync(bar, GT);
+                    if (key == 0) {
+                        sh.last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
+                        if (sh.last) p.counters[c0] = 0u;
+                    }
+                    bar_sync(bar, GT);
+                    write = sh.last;
+                    if (write) {
+                        __threadfence();
+                        // m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
+                        constexpr int TR = GT / RT;  // threads of a row
+                        const int r = key / TR;
+                        float mm = -INFINITY, ll = 0.0f;
+                        for (int c = c0 + key % TR; c <= c1; c += TR) mm = fmaxf(mm, __ldcg(part_of(c) + (int64_t)RT * p.D + r));
+#pragma unroll
+                        for (int o = TR / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, o));
+                        for (int c = c0 + key % TR; c <= c1; c += TR) {
+                            const float *q = part_of(c) + (int64_t)RT * p.D + r;
+                            ll += __ldcg(q + RT) * rel_weight(__ldcg(q), mm);
                         }
-                        if (join) x = fmaf(p.pre_o[at], sh.fc[h + r], x);
-                        if (p.mode == 1) p.pre_o[at] = x;
-                        else static_cast<T *>(p.out)[at] = __float2bfloat16(x);
+#pragma unroll
+                        for (int o = TR / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(kFull, ll, o);
+                        if (key % TR == 0) {
+                            sh.top[0][r] = mm;
+                            sh.top[1][r] = ll;
+                        }
+                        bar_sync(bar, GT);
+#pragma unroll 1
+                        for (int h = 0; h < RT; h += 8) {
+                            float o[8], z[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = z[e] = 0.0f;
+#pragma unroll 2
+                            for (int c = c0; c <= c1; ++c) {
+                                const float *q = part_of(c);
+                                float x[8], a[8];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    a[e] = __ldcg(q + (int64_t)RT * p.D + h + e);
+                                    x[e] = key < p.D ? __ldcg(q + (int64_t)(h + e) * p.D + key) : 0.0f;
+                                }
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const float f = rel_weight(a[e], sh.top[0][h + e]);
+                                    if (f != 0.0f) o[e] = fmaf(x[e], f, o[e]);
+                                }
+                            }
+                            tc_st8(to + h, o);
+                            tc_st8(to + RT + h, z);
+                            tc_st8(to + 2 * RT + h, z);
+                        }
+                        tc_wait_st();
+                        if (key < RT) {
+                            m = sh.top[0][key];
+                            s = sh.top[1][key];
+                            back = 1.0f;
+                        }
+                    }
+                }
+                if (write) {
+                    if (key < RT) {
+                        const int64_t row = w.out[key];
+                        float fa = 0.0f, fc = 0.0f;
+                        if (row >= 0) {
+                            float lse2 = s > 0.0f || s != s ? m + lg2f(s) : -INFINITY;
+                            fa = back;
+                            if (p.mode == 0 && p.P > 0 && done.keys.ok) {
+                                const float lp = p.pre_lse[row], mm = fmaxf(m, lp), a = rel_weight(m, mm), c = lp != lp ? lp : rel_weight(lp, mm);
+                                s = s * a + c;
+                                lse2 = s > 0.0f || s != s ? mm + lg2f(s) : -INFINITY;
+                                fa *= a;
+                                fc = c;
+                            }
+                            const float inv = lse2 == -INFINITY ? 0.0f : 1.0f / s;
+                            fa *= inv;
+                            fc *= inv;
+                            if (p.mode == 1) p.pre_lse[row] = lse2;
+                            else if (p.lse) p.lse[row] = lse2 * kLn2;
+                        }
+                        sh.fa[key] = fa;
+                        sh.fc[key] = fc;
+                    }
+                    bar_sync(bar, GT);
+                    const bool join = p.mode == 0 && p.P > 0 && done.keys.ok;
+                    // (code that runs once an item stays short: it comes from far away)
+#pragma unroll 1
+                    for (int h = 0; h < RT; h += 8) {
+                        float o[kParts][8], sp[8];
+#pragma unroll
+                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * RT + h);
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) sp[r] = join && w.out[h + r] >= 0 && key < p.D ? p.pre_o[w.out[h + r] * p.D + key] : 0.0f;
+                        tc_wait_ld();
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const int64_t row = w.out[h + r], at = row * p.D + key;
+                            const float f = sh.fa[h + r];
+                            float x = f == 0.0f ? 0.0f : (o[0][r] + o[1][r] + o[2][r]) * f;
+                            if (join) x = fmaf(sp[r], sh.fc[h + r], x);
+                            if (row >= 0 && key < p.D) {
+                                if (p.mode == 1) p.pre_o[at] = x;
+                                else static_cast<T *>(p.out)[at] = __float2bfloat16(x);
+                            }
+                        }
                     }
                 }
                 tc_fence_before();
-                if (split) {  // the part that arrives last joins them; the counter is left zero
-                    __threadfence();
-                    bar_sync(bar, GT);
-                    if (key == 0) sh.last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
-                    bar_sync(bar, GT);
-                    if (sh.last) {
-                        __threadfence();
-                        for (int r = wq; r < RT; r += 4)
-                            if (w.out[r] >= 0) attn_join_row<T, 8>(p, done.keys.ok, RT, c0, c1 - c0 + 1, r, w.out[r]);
-                        if (key == 0) p.counters[c0] = 0u;
-                    }
-                }
-                bar_sync(bar, GT);  // (the rows and factors are done with)
-                u = end;
                 if (u >= uend) break;
+                bar_sync(bar, GT);  // (the references and factors are done with)
+                start_rows();
+                bar_sync(bar, GT);
                 ++item;
             }
         }
@@ -743,11 +871,11 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
 }
 
 // ---- host ------------------------------------------------------------------
-template <int NH, int RT> cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
+template <int NH, int RT, bool PLAIN> cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
     constexpr int smem = (int)sizeof(Tc8Smem<NH, RT>) + 1024;
     static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
     static_assert(kTeams<RT> * RT <= kAttnSlotRows && kTeams<RT> * kAttnSmsMax <= kAttnBlocksMax, "partial results of the teams");
-    cudaError_t e = cudaFuncSetAttribute(attn8_tc_kernel<NH, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(attn8_tc_kernel<NH, RT, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kAttnSmsMax ? sms : kAttnSmsMax));
@@ -759,12 +887,14 @@ template <int NH, int RT> cudaError_t launch(const AttnParams &p, const CUtensor
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = p.mode == 0 && p.P > 0 ? 1 : 0;  // after the shared pass
-    return cudaLaunchKernelEx(&cfg, attn8_tc_kernel<NH, RT>, p, cm);
+    return cudaLaunchKernelEx(&cfg, attn8_tc_kernel<NH, RT, PLAIN>, p, cm);
 }
 
 template <int NH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
     const int64_t rows = p.mode == 1 ? (int64_t)p.B * p.S * p.G : (int64_t)p.S * p.G;
-    return rows <= 16 ? launch<NH, 16>(p, cm, sms, s) : launch<NH, 32>(p, cm, sms, s);
+    const bool plain = p.score.cap == 0.0f && !p.score.bias;
+    if (plain) return rows <= 16 ? launch<NH, 16, true>(p, cm, sms, s) : launch<NH, 32, true>(p, cm, sms, s);
+    return rows <= 16 ? launch<NH, 16, false>(p, cm, sms, s) : launch<NH, 32, false>(p, cm, sms, s);
 }
 
 }  // namespace

@@ -10,7 +10,7 @@ three bits leave of a bf16 value is otherwise exact.  So a score's error grows b
 at most |scale| 2^-17 max|q| sum|k|.  The weights, times V's powers of two, are
 rounded to f16 (2^-11 of each, below the bf16 rounding's 2^-8) and held as three
 e4m3 numbers: exactly, or, as the third one's steps end at 2^-19 where the row's
-largest power and a weight of 1 are at 2^5, to half a step, 2^-25 of the largest
+largest power and a weight of 1 are at 2^5, to half a step, 2^-24 of the largest
 power, for a key, with codes up to 448 and 448 powers at most twice the largest |v|
 that the row sees, over a sum of weights that is at least 1."""
 import math
