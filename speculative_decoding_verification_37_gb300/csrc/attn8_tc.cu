@@ -1,9 +1,9 @@
 // Attention over the 8-bit paged cache for bf16 queries on the fifth-generation
 // tensor cores (attention.cuh: score, split, join; kv8.cuh: the cache's numbers).
 //
-// One persistent block per SM, in two or three teams that know nothing of each other:
-// a team has a warp that copies, a warp that issues MMAs, four softmax warps and its
-// own share of the line of tiles, so that what one waits for (a product's end, an
+// One persistent block per SM, in three teams that know nothing of each other: a team
+// has a warp that copies, four softmax warps and its own share of the line of tiles
+// (one warp issues the MMAs of all), so that what one waits for (a product's end, an
 // item's first keys, its output) the others' work covers.  A tile is 128 keys, down
 // the MMA's rows; an item's 16 or 32 queries are its columns: a thread has a key,
 // with the key's power of two, position and masks, and the MMA does no work for
@@ -40,7 +40,7 @@ namespace {
 
 constexpr int KT = 128, GT = 128, NT = 256;  // keys of a tile; softmax threads of a team; threads that plan
 constexpr uint32_t kTile = KT * 128;  // bytes of 128 keys x up to 128 codes
-constexpr int kInfo = 8;              // tiles whose notes are kept
+constexpr int kInfo = 4;              // tiles whose notes are kept
 constexpr float kNone = -1e30f;       // the reference of a row that has seen no key
 constexpr float kLag = 8.0f;          // log2 of what a weight may reach
 constexpr int kPowMin = 16;           // exponent byte that smaller powers are taken relative to
@@ -69,12 +69,6 @@ template <int N> __device__ __forceinline__ void tc_store(uint32_t t, const uint
     for (int i = 0; i < N; i += 16) tc_st16(t + i, x + i);
 }
 
-__device__ __forceinline__ void tc_st8(uint32_t t, const float *x) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "f"(x[0]), "f"(x[1]), "f"(x[2]),
-                 "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
-}
-
 // a barrier of n threads under an id of its own that joins a predicate
 __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
     int r;
@@ -87,9 +81,22 @@ __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
     return r != 0;
 }
 
-// Shared-memory operand, 64-byte swizzle (8 rows of 64 bytes an atom)
+// Shared-memory operands: 64- and 32-byte swizzles (8 rows of so many bytes an atom)
 __device__ __forceinline__ uint64_t tc_desc64(uint32_t addr, uint32_t sbo) {
     return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (4ull << 61);
+}
+__device__ __forceinline__ uint64_t tc_desc32(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (6ull << 61);
+}
+// whether a barrier's phase is over; waits for nothing
+__device__ __forceinline__ bool mbar_test(unsigned long long *bar, unsigned phase) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(phase)
+        : "memory");
+    return ok != 0u;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
@@ -138,17 +145,18 @@ template <int N, typename F> __device__ __forceinline__ void reduce_rows(float (
     }
 }
 
-// Teams of a block: three need 112 registers a thread, which 32 rows do not fit.
-template <int RT> constexpr int kTeams = RT == 16 ? 3 : 2;
+constexpr int kTeams = 3;
 
 // What a team has.
 template <int NH, int RT> struct Team8 {
-    static constexpr uint32_t kQ = RT * 128, kP = KT * 4 * RT;  // bytes of a part of the queries; of P^T
-    static constexpr int KS = 2, VS = RT == 16 ? 1 : 2;         // buffers for K and V
+    static constexpr uint32_t kQ = RT * 128;         // bytes of a part of the queries
+    // P^T: 16 queries: a key's 64 bytes, three parts of four; 32: a part's 4 KB after another
+    static constexpr uint32_t kP = RT == 16 ? KT * 64 : KT * kParts * 32, kStep = RT == 16 ? 32 * 64 : 32 * 32;
+    static constexpr int KS = 2;                     // buffers for K
     alignas(1024) unsigned char k[KS][kTile];
-    alignas(1024) unsigned char v[VS][kTile];
+    alignas(1024) unsigned char v[kTile];
     alignas(1024) unsigned char q[2][kQ];            // the queries' first and second parts
-    alignas(1024) unsigned char p[2][kP];            // two tiles' P^T: a key's weights, three parts of four
+    alignas(1024) unsigned char p[kP];
     alignas(16) float ref[RT], corr[RT], corr_o[RT], gain[RT];  // references (log2 units), what sums and O are
                                                      // multiplied by, what weights are at a power of 1
     alignas(16) float top[4][RT];                    // the warps' largest scores; at the end sums of weights
@@ -162,11 +170,13 @@ template <int NH, int RT> struct Team8 {
     int pow_min, low_max, qp0;                       // the smallest largest power; the largest `low`; the first position
     unsigned sc[kInfo][2][KT / 4];                   // exponent bytes of a tile's K and V
     unsigned bad[kInfo];                             // boxes of a tile with a bad block
-    alignas(8) unsigned long long k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], p_full[2], pv_done[2], q_full;
+    int first[kInfo];                                // whether an item begins
+    alignas(8) unsigned long long k_full[KS], k_empty[KS], v_full, s_full[2], p_full, pv_done, q_full;
+    int scored, weighed, begun, tiles;               // the MMA warp's: tiles so far, items begun, tiles in all
     int last;
 };
 template <int NH, int RT> struct Tc8Smem {
-    Team8<NH, RT> team[kTeams<RT>];
+    Team8<NH, RT> team[kTeams];
     AttnPlan plan;
     uint32_t tmem;
 };
@@ -180,16 +190,16 @@ static __device__ __noinline__ void next_item(const AttnParams &p, AttnItem &it,
 __device__ __forceinline__ int line_start(const KeyLine &line, int ntiles) { return line.lo - (ntiles * KT - line.entries); }
 
 template <int NH, int RT, bool plain>
-__global__ void __launch_bounds__(192 * kTeams<RT>, 1)
+__global__ void __launch_bounds__(128 * kTeams + 128, 1)
     attn8_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap cache_map) {
     using H = Team8<NH, RT>;
-    constexpr int G = kTeams<RT>, NW = 4 * G;  // teams; softmax warps
+    constexpr int G = kTeams, NW = 4 * G;  // teams; softmax warps
     using T = __nv_bfloat16;
     extern __shared__ unsigned char raw_[];
     Tc8Smem<NH, RT> &all = *reinterpret_cast<Tc8Smem<NH, RT> *>(
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int grp = warp < NW ? warp >> 2 : (warp - NW) % G;  // then a warp a team for copies, one for MMAs
+    const int grp = warp < NW ? warp >> 2 : warp < NW + G ? warp - NW : 0;  // then a warp a team for copies, one for MMAs
     H &sh = all.team[grp];
     const int per = p.S * p.G;
     const int64_t nrows = p.mode == 1 ? (int64_t)p.B * per : per;
@@ -200,15 +210,11 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
             mbar_init(&h.k_full[s], 1);
             mbar_init(&h.k_empty[s], 1);
         }
-        for (int s = 0; s < H::VS; ++s) {
-            mbar_init(&h.v_full[s], 1);
-            mbar_init(&h.v_empty[s], 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            mbar_init(&h.s_full[s], 1);
-            mbar_init(&h.p_full[s], GT);
-            mbar_init(&h.pv_done[s], 1);
-        }
+        mbar_init(&h.v_full, 1);
+        mbar_init(&h.s_full[0], 1);
+        mbar_init(&h.s_full[1], 1);
+        mbar_init(&h.p_full, GT);
+        mbar_init(&h.pv_done, 1);
         mbar_init(&h.q_full, GT);
         fence_barrier_init();
     }
@@ -226,12 +232,70 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
     int64_t u = part * share;
     const int64_t uend = min(all.plan.total, u + share);
     // TMEM columns: the teams' two score tiles, then their accumulators
-    const uint32_t col_s = tmem + grp * 2 * RT, col_o = tmem + (2 * G + kParts * grp) * RT;
+    constexpr uint32_t kO = 2 * G * RT;
+    const uint32_t col_s = tmem + grp * 2 * RT, col_o = tmem + kO + kParts * grp * RT;
     static_assert((2 + kParts) * G * RT <= 512, "columns");
     bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
-    if (u < uend) {
+    if (warp == NW + G) {
+        // ---------------- MMAs ----------------
+        // A team's next product where its weights and V are there, its next scores where its
+        // K is, and, of an item's first, the queries.
+        if (lane == 0) {
+            // Operands.  Scores: atoms of 8 rows x 128 bytes, the next 8 rows 1,024 bytes on;
+            // 32 columns of K and Q are 32 bytes.  Values: the rows are keys, the products' K,
+            // whose elements (V's columns: M; P's weights: N) are contiguous: 128 of V (zeros
+            // past the head), 48 of P, or 32 and the next 32 a part further on.
+            constexpr uint32_t id_s = tc_idesc8(RT), id_o = tc_idesc_mn(kParts * RT);
+            int left = 0, idle = 0;
+            for (int g = 0; g < G; ++g) {
+                H &t = all.team[g];
+                const int64_t at = ((int64_t)g * gridDim.x + blockIdx.x) * share;
+                t.scored = t.weighed = t.begun = 0;
+                left += t.tiles = (int)max((int64_t)0, min(all.plan.total, at + share) - at);
+            }
+            while (left > 0 && idle < (int)kSpinLimit) {
+                ++idle;
+#pragma unroll 1
+                for (int g = 0; g < G; ++g) {
+                    H &t = all.team[g];
+                    const int n = t.scored, j = t.weighed;
+                    if (j < n && mbar_test(&t.v_full, (unsigned)(j & 1)) && mbar_test(&t.p_full, (unsigned)(j & 1))) {
+                        tc_fence_after();
+                        const uint64_t a = tc_desc(smem_u32(t.v), 0, 1024),
+                                       b = RT == 16 ? tc_desc64(smem_u32(t.p), 512) : tc_desc32(smem_u32(t.p), KT * 32, 256);
+                        const bool add = !t.first[j % kInfo];
+#pragma unroll
+                        for (int k = 0; k < KT / 32; ++k)
+                            tc_mma8(tmem + kO + kParts * g * RT, a + k * (4096 / 16), b + k * (H::kStep / 16), id_o, add || k > 0);
+                        tc_commit(&t.pv_done);
+                        t.weighed = j + 1;
+                        --left;
+                        idle = 0;
+                    }
+                    if (n < t.tiles && n < t.weighed + 2 && mbar_test(&t.k_full[n % H::KS], (unsigned)((n / H::KS) & 1))) {
+                        const bool first = t.first[n % kInfo];
+                        if (!first || mbar_test(&t.q_full, (unsigned)(t.begun & 1))) {
+                            tc_fence_after();
+                            const uint64_t a = tc_desc(smem_u32(t.k[n % H::KS]), 16, 1024), b = tc_desc(smem_u32(t.q[0]), 16, 1024);
+#pragma unroll
+                            for (int k = 0; k < NH * 4; ++k)  // first parts, second parts
+                                tc_mma8(tmem + (2 * g + (n & 1)) * RT, a + (k % (NH * 2)) * (32 / 16),
+                                        b + (k / (NH * 2)) * (H::kQ / 16) + (k % (NH * 2)) * (32 / 16), id_s, k > 0);
+                            tc_commit(&t.k_empty[n % H::KS]);
+                            tc_commit(&t.s_full[n & 1]);
+                            t.scored = n + 1;
+                            t.begun += first;
+                            idle = 0;
+                        }
+                    }
+                }
+            }
+            ok = left == 0;
+        }
+        __syncwarp();
+    } else if (u < uend) {
         AttnItem it = attn_find<NT>(p, all.plan, u, items, rtiles, KT);
-        if (warp >= NW && warp < NW + G) {
+        if (warp >= NW) {
             // ---------------- copies ----------------
             const int nbox = KT / p.box;
             const int zero_row = (int)(2 * p.nb * p.bs);  // past the map: zeros are written
@@ -293,7 +357,10 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                         if (n >= H::KS && ok) ok = attn_wait(&sh.k_empty[s], (unsigned)((n / H::KS - 1) & 1));
                         sh.sc[i][0][lane] = ks;
                         sh.sc[i][1][lane] = vs;
-                        if (lane == 0) sh.bad[i] = b;
+                        if (lane == 0) {
+                            sh.bad[i] = b;
+                            sh.first[i] = t == t1 - 1;
+                        }
                         __syncwarp();  // (the notes, before the arrival)
                         copy(sh.k[s], &sh.k_full[s], box);
                         box_v = box == zero_row ? box : box + v_row;
@@ -302,10 +369,10 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                         ++n;
                     }
                     if (t < t1 - 1) {
-                        const int j = n - (t >= t0 ? 2 : 1), s = j % H::VS;
-                        if (j >= H::VS && ok) ok = attn_wait(&sh.v_empty[s], (unsigned)((j / H::VS - 1) & 1));
+                        const int j = n - (t >= t0 ? 2 : 1);
+                        if (j > 0 && ok) ok = attn_wait(&sh.pv_done, (unsigned)((j - 1) & 1));
                         __syncwarp();
-                        copy(sh.v[s], &sh.v_full[s], box_before);
+                        copy(sh.v, &sh.v_full, box_before);
                     }
                 }
                 u = it.u0 + it.ntiles;
@@ -314,60 +381,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
             }
             // no copy may land after the block has gone
             for (int i = max(0, n - H::KS); i < n; ++i) ok = mbar_drain(&sh.k_full[i % H::KS], (unsigned)((i / H::KS) & 1)) && ok;
-            for (int i = max(0, n - H::VS); i < n; ++i) ok = mbar_drain(&sh.v_full[i % H::VS], (unsigned)((i / H::VS) & 1)) && ok;
-        } else if (warp >= NW + G) {
-            // ---------------- MMA ----------------
-            if (lane == 0) {
-                // Scores: atoms of 8 rows x 128 bytes, the next 8 rows 1,024 bytes on; 32
-                // columns of K and Q are 32 bytes.  Values: the rows are keys, the products'
-                // K, whose elements (V's columns: M; P's weights: N) are contiguous, up to 128
-                // of V (zeros past the head) and 64 or 128 of P in an atom's row.
-                constexpr uint32_t id_s = tc_idesc8(RT), id_o = tc_idesc_mn(kParts * RT);
-                const uint64_t dq = tc_desc(smem_u32(sh.q[0]), 16, 1024), dk = tc_desc(smem_u32(sh.k[0]), 16, 1024),
-                               dv = tc_desc(smem_u32(sh.v[0]), 0, 1024),
-                               dp = RT == 16 ? tc_desc64(smem_u32(sh.p[0]), 512) : tc_desc(smem_u32(sh.p[0]), 0, 1024);
-                int n = 0, j = 0, item = 0;
-                while (true) {
-                    const int nt = (int)(min(uend, it.u0 + it.ntiles) - u);
-                    if (ok) ok = attn_wait(&sh.q_full, (unsigned)(item & 1));
-                    tc_fence_after();
-                    // S0 S1, P0 V0, S2, P1 V1, S3 ...
-#pragma unroll 1
-                    for (int i = 0; i < nt + 2; ++i) {
-                        if (i >= 2) {
-                            const int s = j % H::VS;
-                            if (ok) ok = attn_wait(&sh.v_full[s], (unsigned)((j / H::VS) & 1));
-                            if (ok) ok = attn_wait(&sh.p_full[j & 1], (unsigned)((j >> 1) & 1));
-                            tc_fence_after();
-                            const uint64_t a = dv + (uint32_t)s * (kTile / 16), b = dp + (uint32_t)(j & 1) * (H::kP / 16);
-#pragma unroll
-                            for (int k = 0; k < KT / 32; ++k)
-                                tc_mma8(col_o, a + k * (4096 / 16), b + k * (H::kP / 4 / 16), id_o, !(i == 2 && k == 0));
-                            tc_commit(&sh.v_empty[s]);
-                            tc_commit(&sh.pv_done[j & 1]);
-                            ++j;
-                        }
-                        if (i < nt) {
-                            const int s = n % H::KS;
-                            if (ok) ok = attn_wait(&sh.k_full[s], (unsigned)((n / H::KS) & 1));
-                            tc_fence_after();
-                            const uint64_t a = dk + (uint32_t)s * (kTile / 16);
-#pragma unroll
-                            for (int k = 0; k < NH * 4; ++k)  // first parts, second parts
-                                tc_mma8(col_s + (n & 1) * RT, a + (k % (NH * 2)) * (32 / 16),
-                                        dq + (k / (NH * 2)) * (H::kQ / 16) + (k % (NH * 2)) * (32 / 16), id_s, k > 0);
-                            tc_commit(&sh.k_empty[s]);
-                            tc_commit(&sh.s_full[n & 1]);
-                            ++n;
-                        }
-                    }
-                    ++item;
-                    u = it.u0 + it.ntiles;
-                    if (u >= uend) break;
-                    next_item(p, it, items, rtiles);
-                }
-            }
-            __syncwarp();
+            ok = mbar_drain(&sh.v_full, (unsigned)((n - 1) & 1)) && ok;
         } else {
             // ---------------- softmax ----------------
             const int wq = warp & 3, key = tid & (GT - 1);            // key of a tile; row of the MMA: TMEM lane
@@ -620,7 +634,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                             l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
                         }
                         if (n > n0) {  // O, still once the product before has ended
-                            if (ok) ok = attn_wait(&sh.pv_done[(n - 1) & 1], (unsigned)(((n - 1) >> 1) & 1));
+                            if (ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < kParts * RT; c += 16) {
@@ -640,9 +654,8 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     float vf = kv8_power(vs);
                     if (special) {
                         // V's NaN must not meet the weights of rows that do not see it
-                        const int s = n % H::VS;
-                        if (ok) ok = attn_wait(&sh.v_full[s], (unsigned)((n / H::VS) & 1));
-                        unsigned char *vr = sh.v[s] + key * 128;
+                        if (ok) ok = attn_wait(&sh.v_full, (unsigned)(n & 1));
+                        unsigned char *vr = sh.v + key * 128;
                         uint32_t nan = 0;
 #pragma unroll 1
                         for (int i = 0; i < 8; ++i) {  // (neighbours start at another chunk)
@@ -656,11 +669,11 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                             for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(vr + (i << 4)) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    // P's buffer is free once the product two tiles ago has ended
-                    if (n > n0 + 1 && ok) ok = attn_wait(&sh.pv_done[n & 1], (unsigned)(((n - 2) >> 1) & 1));
+                    // P's buffer is free once the product before has ended
+                    if (n > n0 && ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
                     // weights: summed, times V's power of two to three e4m3 numbers
-                    unsigned char *pp = sh.p[n & 1] + key * (4 * RT);
-                    const int sw = RT == 16 ? (key >> 1) & 3 : key & 7;  // the swizzle of 64 or 128 bytes
+                    unsigned char *pp = sh.p + key * (RT == 16 ? 64 : 32);
+                    const int sw = RT == 16 ? (key >> 1) & 3 : (key >> 2) & 1;  // the swizzle of 64 or 32 bytes
                     const bool pick = special || vf != vf;
 #pragma unroll
                     for (int r = 0; r < RT; r += 16) {
@@ -682,7 +695,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                             uint32_t z[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) z[i] = c < 2 ? __byte_perm(h[2 * i], h[2 * i + 1], 0x7531) : h[2 * i] | h[2 * i + 1] << 16;
-                            *reinterpret_cast<uint4 *>(pp + (((c * (RT / 16) + r / 16) ^ sw) << 4)) = make_uint4(z[0], z[1], z[2], z[3]);
+                            *reinterpret_cast<uint4 *>(pp + (RT == 16 ? (c ^ sw) << 4 : c * (KT * 32) + ((r / 16 ^ sw) << 4))) = make_uint4(z[0], z[1], z[2], z[3]);
                         };
                         put(0);
 #pragma unroll
@@ -694,7 +707,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     }
                     fence_async_shared();
                     tc_fence_before();
-                    mbar_arrive(&sh.p_full[n & 1]);
+                    mbar_arrive(&sh.p_full);
                 }
                 // ---- the item's end: the next one's queries, then this one's output
                 const AttnItem done = it;
@@ -722,7 +735,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                     if (s > 0.0f || s != s) m = sh.ref[key];  // a NaN sum stays NaN
                     sh.fa[key] = back = 1.0f / sh.gain[key];  // (powers of two)
                 }
-                if (ok) ok = attn_wait(&sh.pv_done[(n - 1) & 1], (unsigned)(((n - 1) >> 1) & 1));
+                if (ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
                 tc_fence_after();
                 bool write = true;
                 if (c0 != c1) {
@@ -737,7 +750,7 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
                         __stcg(mine + (int64_t)RT * p.D + key, m);
                         __stcg(mine + (int64_t)RT * p.D + RT + key, s);
                     }
-#pragma unroll 1
+#pragma unroll
                     for (int h = 0; h < RT; h += 8) {
                         float o[kParts][8];
 #pragma unroll
@@ -747,58 +760,73 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
 #pragma unroll
                             for (int r = 0; r < 8; ++r) __stcg(mine + (int64_t)(h + r) * p.D + key, (o[0][r] + o[1][r] + o[2][r]) * sh.fa[h + r]);
                     }
-                    __threadfence();
                     bar_sync(bar, GT);
-                    if (key == 0) {
+                    if (key == 0) {  // (its fence covers what the barrier has shown it)
+                        __threadfence();
                         sh.last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
+                        __threadfence();
                         if (sh.last) p.counters[c0] = 0u;
                     }
                     bar_sync(bar, GT);
                     write = sh.last;
                     if (write) {
-                        __threadfence();
                         // m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
-                        constexpr int TR = GT / RT;  // threads of a row
-                        const int r = key / TR;
-                        float mm = -INFINITY, ll = 0.0f;
-                        for (int c = c0 + key % TR; c <= c1; c += TR) mm = fmaxf(mm, __ldcg(part_of(c) + (int64_t)RT * p.D + r));
+                        constexpr int TR = GT / RT;  // threads of a row; parts at a time
+                        const int r = key / TR, k = key % TR, np = c1 - c0 + 1;
+                        auto of_row = [&](int c) { return part_of(c0 + c) + (int64_t)RT * p.D + r; };
+                        float mc = k < np ? __ldcg(of_row(k)) : -INFINITY, lc = k < np ? __ldcg(of_row(k) + RT) : 0.0f, mm = mc;
+                        for (int c = k + TR; c < np; c += TR) mm = fmaxf(mm, __ldcg(of_row(c)));
 #pragma unroll
                         for (int o = TR / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, o));
-                        for (int c = c0 + key % TR; c <= c1; c += TR) {
-                            const float *q = part_of(c) + (int64_t)RT * p.D + r;
-                            ll += __ldcg(q + RT) * rel_weight(__ldcg(q), mm);
+                        float ll = 0.0f;
+#pragma unroll 1
+                        for (int c = 0; c < np; c += TR) {
+                            if (c > 0) {
+                                mc = c + k < np ? __ldcg(of_row(c + k)) : -INFINITY;
+                                lc = c + k < np ? __ldcg(of_row(c + k) + RT) : 0.0f;
+                                bar_sync(bar, GT);
+                            }
+                            const float f = rel_weight(mc, mm);
+                            ll += lc * f;
+                            (&sh.top[0][0])[k * RT + r] = f;  // (TR * RT of them)
+                            bar_sync(bar, GT);
+                            const int some = min(TR, np - c);
+#pragma unroll 1
+                            for (int h = 0; h < RT; h += 16) {
+                                float o[16];
+                                if (c > 0) {
+                                    tc_ld16(o, to + h);
+                                    tc_wait_ld();
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+                                }
+#pragma unroll 2
+                                for (int i = 0; i < some; ++i) {
+                                    const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &sh.top[0][0] + i * RT + h;
+                                    float x[16];
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) x[e] = key < p.D ? __ldcg(q + (int64_t)e * p.D) : 0.0f;
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        if (g[e] != 0.0f) o[e] = fmaf(x[e], g[e], o[e]);
+                                }
+                                tc_st16(to + h, reinterpret_cast<const uint32_t *>(o));
+                            }
                         }
 #pragma unroll
                         for (int o = TR / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(kFull, ll, o);
-                        if (key % TR == 0) {
+#pragma unroll 1
+                        for (int h = RT; h < kParts * RT; h += 16) {
+                            uint32_t z[16] = {};
+                            tc_st16(to + h, z);
+                        }
+                        bar_sync(bar, GT);  // (the weights are done with)
+                        if (k == 0) {
                             sh.top[0][r] = mm;
                             sh.top[1][r] = ll;
                         }
                         bar_sync(bar, GT);
-#pragma unroll 1
-                        for (int h = 0; h < RT; h += 8) {
-                            float o[8], z[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = z[e] = 0.0f;
-#pragma unroll 2
-                            for (int c = c0; c <= c1; ++c) {
-                                const float *q = part_of(c);
-                                float x[8], a[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    a[e] = __ldcg(q + (int64_t)RT * p.D + h + e);
-                                    x[e] = key < p.D ? __ldcg(q + (int64_t)(h + e) * p.D + key) : 0.0f;
-                                }
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float f = rel_weight(a[e], sh.top[0][h + e]);
-                                    if (f != 0.0f) o[e] = fmaf(x[e], f, o[e]);
-                                }
-                            }
-                            tc_st8(to + h, o);
-                            tc_st8(to + RT + h, z);
-                            tc_st8(to + 2 * RT + h, z);
-                        }
                         tc_wait_st();
                         if (key < RT) {
                             m = sh.top[0][key];
@@ -874,12 +902,12 @@ __global__ void __launch_bounds__(192 * kTeams<RT>, 1)
 template <int NH, int RT, bool PLAIN> cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
     constexpr int smem = (int)sizeof(Tc8Smem<NH, RT>) + 1024;
     static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
-    static_assert(kTeams<RT> * RT <= kAttnSlotRows && kTeams<RT> * kAttnSmsMax <= kAttnBlocksMax, "partial results of the teams");
+    static_assert(kTeams * RT <= kAttnSlotRows && kTeams * kAttnSmsMax <= kAttnBlocksMax, "partial results of the teams");
     cudaError_t e = cudaFuncSetAttribute(attn8_tc_kernel<NH, RT, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kAttnSmsMax ? sms : kAttnSmsMax));
-    cfg.blockDim = dim3(192 * kTeams<RT>);
+    cfg.blockDim = dim3(128 * kTeams + 128);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at;
