@@ -69,7 +69,7 @@ extern "C" int spec_write_kv_q8(const SpecWriteKvQ8Args *a, void *workspace, siz
     p.sh[1] = a->v_stride_h;
     p.start = a->committed_len;
     p.count = a->n_new;
-    return report_cuda_error(launch_kv8_rows(p, a->dtype, true, static_cast<cudaStream_t>(stream)));
+    return report_cuda_error(launch_kv8_rows(p, a->dtype, true, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int spec_read_kv_q8(const SpecReadKvQ8Args *a, void *workspace, size_t ws_bytes, void *stream) {
@@ -84,7 +84,7 @@ extern "C" int spec_read_kv_q8(const SpecReadKvQ8Args *a, void *workspace, size_
     p.out_v = a->v;
     p.start = a->start;
     p.count = a->count;
-    return report_cuda_error(launch_kv8_rows(p, a->dtype, false, static_cast<cudaStream_t>(stream)));
+    return report_cuda_error(launch_kv8_rows(p, a->dtype, false, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int spec_commit_kv_q8(const SpecCommitKvQ8Args *a, void *workspace, size_t ws_bytes, void *stream) {

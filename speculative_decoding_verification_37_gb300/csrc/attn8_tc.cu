@@ -64,11 +64,6 @@ template <int N> __device__ __forceinline__ void tc_load(float *x, uint32_t t) {
     if (N == 16) tc_ld16(x, t);
     else tc_ldx<N>(x, t);
 }
-template <int N> __device__ __forceinline__ void tc_store(uint32_t t, const uint32_t *x) {
-#pragma unroll
-    for (int i = 0; i < N; i += 16) tc_st16(t + i, x + i);
-}
-
 // a barrier of n threads under an id of its own that joins a predicate
 __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
     int r;

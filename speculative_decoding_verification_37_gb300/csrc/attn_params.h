@@ -138,7 +138,7 @@ struct Kv8Params {
 // blocks of the launches
 int64_t kv8_row_blocks(int32_t B, int32_t S, int32_t H);
 int64_t kv8_commit_blocks(int32_t B, int32_t L);
-cudaError_t launch_kv8_rows(Kv8Params p, int dtype, bool write, cudaStream_t s);
+cudaError_t launch_kv8_rows(const Kv8Params &p, int dtype, bool write, int sms, cudaStream_t s);
 cudaError_t launch_kv8_commit(Kv8Params p, cudaStream_t s);
 
 // workspace layouts (null base: the size alone)

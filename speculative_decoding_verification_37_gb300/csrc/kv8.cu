@@ -1,11 +1,17 @@
 // The 8-bit cache's writer, reader and the commit of a tree's path
 // (spec_write_kv_q8, spec_read_kv_q8, spec_commit_kv_q8); its numbers: kv8.cuh.
 //
-// Writing and reading: a block has 16 entries and up to 32 heads of K or V, a group
-// of lanes a row, 8 values a lane; a row's largest magnitude is a few shuffles.
-// The rows' exponents lie a head's next to each other, so that attention reads a
-// page's in one piece: they pass through shared memory and leave 16 bytes a head.
-// Bound by HBM.
+// Writing and reading: a block has 16 or 64 entries and up to 32 heads of K or V, a
+// group of lanes a row, 16 values a lane where they are written and 8 where they are
+// read; a row's largest magnitude is a few shuffles.  The rows' exponents lie a head's
+// next to each other, so that attention reads a page's in one piece: they pass
+// through shared memory and leave a head's entries together.  64 entries where that
+// gives every SM two blocks (fewer look-ups and starts: prompts read back 117 us
+// instead of 145), else 16.
+// Measured: 65,600 entries of 8 heads of 128, bf16 parts of a fused projection's
+// output, written in 81 us (4.9 TB/s; with 8 values a lane 98, bound by issue), as
+// many read back, 8,192 a request with zeros, in 117 us (5.8 TB/s).  Both are bound by
+// HBM and by what a row costs besides.
 //
 // Commit: a kept candidate's codes and exponents move from entry len + slots[i] to
 // len + i.  slots ascend, so slots[i] >= i, and a place is read before, or in the
@@ -20,7 +26,7 @@
 namespace specv {
 namespace {
 
-constexpr int kEntries = 16, kHeads = 32, kThreads = 256;
+constexpr int kHeads = 32, kThreads = 256;
 
 struct Place {
     int64_t entry;  // blk * bs + offset, or -1
@@ -39,22 +45,57 @@ __device__ __forceinline__ Place place_of(const Kv8Params &p, int b, int c) {
     return Place{(int64_t)blk * p.bs + off, (int64_t)blk * p.H * p.bs + off};
 }
 
-// 8 values of a row
-template <typename T> struct Raw8;
-template <> struct Raw8<__nv_bfloat16> {
-    uint4 v;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = ld_nc16(p); }
-    __device__ __forceinline__ void values(float *x) const { unpack<__nv_bfloat16>(v, x); }
-};
-template <> struct Raw8<float> {
-    uint4 v, w;
-    __device__ __forceinline__ void load(const float *p) {
-        v = ld_nc16(p);
-        w = ld_nc16(p + 4);
+// the larger, or NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_nan2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// 16 values of a row; their largest magnitude (NaN if one is); their codes
+template <typename T> struct Raw16;
+template <> struct Raw16<__nv_bfloat16> {
+    uint4 v[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        v[0] = ld_nc16(p);
+        v[1] = ld_nc16(p + 8);
     }
-    __device__ __forceinline__ void values(float *x) const {
-        unpack<float>(v, x);
-        unpack<float>(w, x + 4);
+    __device__ __forceinline__ float top() const {
+        uint32_t a = 0u;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            constexpr uint32_t m = 0x7fff7fffu;
+            a = max_nan2(a, max_nan2(max_nan2(v[i].x & m, v[i].y & m), max_nan2(v[i].z & m, v[i].w & m)));
+        }
+        return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    }
+    __device__ __forceinline__ void values(int i, float *x) const { unpack<__nv_bfloat16>(v[i], x); }
+};
+template <> struct Raw16<float> {
+    uint4 v[4];
+    __device__ __forceinline__ void load(const float *p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ld_nc16(p + 4 * i);
+    }
+    __device__ __forceinline__ float top() const {
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x[4];
+            unpack<float>(v[i], x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a = max_nan(a, fabsf(x[e]));
+        }
+        return a;
+    }
+    __device__ __forceinline__ void values(int i, float *x) const {  // 8 of them
+        unpack<float>(v[2 * i], x);
+        unpack<float>(v[2 * i + 1], x + 4);
     }
 };
 __device__ __forceinline__ void store8(float *to, const float *x) {
@@ -74,8 +115,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16 *to, const float *x) {
 struct Tile {
     int b, e0, h0, heads, kv;
 };
-// Blocks: K/V fastest, then head chunks, entries, requests.
-__device__ __forceinline__ Tile tile_of(const Kv8Params &p) {
+// Blocks: K/V fastest, then head chunks, E entries, requests.
+template <int E> __device__ __forceinline__ Tile tile_of(const Kv8Params &p) {
     Tile t;
     int64_t i = blockIdx.x;
     t.kv = (int)(i & 1);
@@ -84,16 +125,16 @@ __device__ __forceinline__ Tile tile_of(const Kv8Params &p) {
     t.h0 = (int)(i % chunks) * kHeads;
     i /= chunks;
     t.heads = min(kHeads, p.H - t.h0);
-    t.e0 = (int)(i % p.etiles) * kEntries;
+    t.e0 = (int)(i % p.etiles) * E;
     t.b = (int)(i / p.etiles);
     return t;
 }
 
 // G: lanes of a row
-template <typename T, int G> __global__ void __launch_bounds__(kThreads) write_kv8_kernel(Kv8Params p) {
-    __shared__ Place place[kEntries];
-    __shared__ unsigned char scale[kHeads][kEntries];
-    const Tile t = tile_of(p);
+template <typename T, int G, int E> __global__ void __launch_bounds__(kThreads) write_kv8_kernel(Kv8Params p) {
+    __shared__ Place place[E];
+    __shared__ unsigned char scale[kHeads][E];
+    const Tile t = tile_of<E>(p);
     const int tid = threadIdx.x;
     const int len = p.start[t.b], n = p.count ? p.count[t.b] : p.S;
     const bool good = len >= 0 && n >= 0 && n <= p.S && (int64_t)len + n <= (int64_t)p.max_blocks * p.bs;
@@ -104,72 +145,64 @@ template <typename T, int G> __global__ void __launch_bounds__(kThreads) write_k
         }
         return;
     }
-    const int entries = min(kEntries, n - t.e0);
+    const int entries = min(E, n - t.e0);
     if (entries <= 0) return;
-    if (tid < entries) place[tid] = place_of(p, t.b, len + t.e0 + tid);
-    __syncthreads();
-    constexpr int NG = kThreads / G, U = 4;
-    const int d = (tid % G) * 8, rows = entries * t.heads;
+    constexpr int NG = kThreads / G;
+    const int d = (tid % G) * 16, rows = entries * t.heads;
     const bool in = d < p.D;
+    // row r of the block: entry, head
+    auto at = [&](int r, int &e, int &h) {
+        e = r / t.heads;
+        h = r - e * t.heads;
+        return r < rows;
+    };
     const T *src = static_cast<const T *>(t.kv ? p.v : p.k) + t.b * p.sb[t.kv];
     unsigned char *codes = p.codes + (t.kv ? p.plane : 0);
-    for (int base = 0; base < rows; base += NG * U) {  // (every lane takes part in the shuffles)
-        const int r0 = base + tid / G;
-        Raw8<T> raw[U];
+    Raw16<T> raw;
+    auto load = [&](int r) {
+        int e, h;
+        if (at(r, e, h) && in) raw.load(src + (t.e0 + e) * p.ss[t.kv] + (t.h0 + h) * p.sh[t.kv] + d);
+    };
+    load(tid / G);  // (the first rows are on their way while the blocks are looked up)
+    if (tid < entries) place[tid] = place_of(p, t.b, len + t.e0 + tid);
+    __syncthreads();
+    for (int base = 0; base < rows; base += NG) {  // (every lane takes part in the shuffles)
+        const int r = base + tid / G;
+        if (base > 0) load(r);
+        int e, h;
+        const bool is = at(r, e, h);
+        float top = is && in ? raw.top() : 0.0f;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * NG, e = r / t.heads, h = t.h0 + r - e * t.heads;
-            if (r < rows && in) raw[u].load(src + (t.e0 + e) * p.ss[t.kv] + h * p.sh[t.kv] + d);
-        }
-        float top[U];
+        for (int q = G / 2; q > 0; q >>= 1) top = max_nan(top, __shfl_xor_sync(kFull, top, q));
+        if (!is) continue;
+        const unsigned s = kv8_scale(top);
+        if (d == 0) scale[h][e] = (unsigned char)s;
+        if (!in || place[e].entry < 0) continue;
+        uint32_t c[4] = {0u, 0u, 0u, 0u};
+        if (s != 255u) {
+            const float f = kv8_inverse(s);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            top[u] = 0.0f;
-            if (r0 + u * NG < rows && in) {
+            for (int i = 0; i < 2; ++i) {
                 float x[8];
-                raw[u].values(x);
-                bool odd = false;  // (fmaxf leaves a NaN out)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    top[u] = fmaxf(top[u], fabsf(x[i]));
-                    odd = odd || x[i] != x[i];
-                }
-                if (odd) top[u] = INFINITY;
+                raw.values(i, x);
+                c[2 * i] = kv8_code2(x[0] * f, x[1] * f) | kv8_code2(x[2] * f, x[3] * f) << 16;
+                c[2 * i + 1] = kv8_code2(x[4] * f, x[5] * f) | kv8_code2(x[6] * f, x[7] * f) << 16;
             }
-#pragma unroll
-            for (int q = G / 2; q > 0; q >>= 1) top[u] = fmaxf(top[u], __shfl_xor_sync(kFull, top[u], q));
         }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * NG;
-            if (r >= rows) break;
-            const int e = r / t.heads, h = r - e * t.heads;
-            const unsigned s = kv8_scale(top[u]);
-            if (d == 0) scale[h][e] = (unsigned char)s;
-            if (!in || place[e].entry < 0) continue;
-            uint2 c = make_uint2(0u, 0u);
-            if (s != 255u) {
-                float x[8];
-                raw[u].values(x);
-                const float f = kv8_inverse(s);
-                c.x = kv8_code2(x[0] * f, x[1] * f) | kv8_code2(x[2] * f, x[3] * f) << 16;
-                c.y = kv8_code2(x[4] * f, x[5] * f) | kv8_code2(x[6] * f, x[7] * f) << 16;
-            }
-            *reinterpret_cast<uint2 *>(codes + (place[e].entry * p.H + t.h0 + h) * p.D + d) = c;
-        }
+        *reinterpret_cast<uint4 *>(codes + (place[e].entry * p.H + t.h0 + h) * p.D + d) = make_uint4(c[0], c[1], c[2], c[3]);
     }
     __syncthreads();
     unsigned char *sc = p.scale + (t.kv ? p.splane : 0);
-    for (int i = tid; i < t.heads * kEntries; i += kThreads) {
-        const int h = i / kEntries, e = i - h * kEntries;
+    for (int i = tid; i < t.heads * E; i += kThreads) {
+        const int h = i / E, e = i - h * E;
         if (e < entries && place[e].entry >= 0) sc[place[e].scale + (int64_t)(t.h0 + h) * p.bs] = scale[h][e];
     }
 }
 
-template <typename T, int G> __global__ void __launch_bounds__(kThreads) read_kv8_kernel(Kv8Params p) {
-    __shared__ Place place[kEntries];
-    __shared__ float power[kHeads][kEntries];
-    const Tile t = tile_of(p);
+template <typename T, int G, int E> __global__ void __launch_bounds__(kThreads) read_kv8_kernel(Kv8Params p) {
+    __shared__ Place place[E];
+    __shared__ float power[kHeads][E];
+    const Tile t = tile_of<E>(p);
     const int tid = threadIdx.x;
     const int start = p.start ? p.start[t.b] : 0, n = p.count ? p.count[t.b] : p.S;
     const bool good = start >= 0 && n >= 0 && n <= p.S && (int64_t)start + n <= (int64_t)p.max_blocks * p.bs;
@@ -177,40 +210,48 @@ template <typename T, int G> __global__ void __launch_bounds__(kThreads) read_kv
         if (p.flags) atomicOr(p.flags + t.b, SPEC_FLAG_BAD_INPUT);
         atomicOr(p.status, SPEC_FLAG_BAD_INPUT);
     }
-    const int entries = min(kEntries, p.S - t.e0), held = good ? min(entries, n - t.e0) : 0;
+    const int entries = min(E, p.S - t.e0), held = good ? min(entries, n - t.e0) : 0;
     if (tid < entries) place[tid] = tid < held ? place_of(p, t.b, start + t.e0 + tid) : Place{-1, 0};
     __syncthreads();
     const unsigned char *sc = p.scale + (t.kv ? p.splane : 0), *codes = p.codes + (t.kv ? p.plane : 0);
-    for (int i = tid; i < t.heads * kEntries; i += kThreads) {
-        const int h = i / kEntries, e = i - h * kEntries;
+    for (int i = tid; i < t.heads * E; i += kThreads) {
+        const int h = i / E, e = i - h * E;
         if (e < entries && place[e].entry >= 0)
             power[h][e] = kv8_power(__ldg(sc + place[e].scale + (int64_t)(t.h0 + h) * p.bs));
     }
     __syncthreads();
-    constexpr int NG = kThreads / G, U = 4;
+    constexpr int NG = kThreads / G, U = 8;
     const int d = (tid % G) * 8, rows = entries * t.heads;
     if (d >= p.D) return;
+    auto at = [&](int r, int &e, int &h) {
+        e = r / t.heads;
+        h = r - e * t.heads;
+        return r < rows;
+    };
     T *out = static_cast<T *>(t.kv ? p.out_v : p.out_k) + ((int64_t)t.b * p.S + t.e0) * p.H * p.D;
     for (int r0 = tid / G; r0 < rows; r0 += NG * U) {
         uint2 c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * NG, e = r / t.heads, h = t.h0 + r - e * t.heads;
+            int e, h;
             c[u] = make_uint2(0u, 0u);
-            if (r < rows && place[e].entry >= 0)
-                c[u] = __ldg(reinterpret_cast<const uint2 *>(codes + (place[e].entry * p.H + h) * p.D + d));
+            if (at(r0 + u * NG, e, h) && place[e].entry >= 0)
+                c[u] = __ldg(reinterpret_cast<const uint2 *>(codes + (place[e].entry * p.H + t.h0 + h) * p.D + d));
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * NG;
-            if (r >= rows) continue;
-            const int e = r / t.heads, h = r - e * t.heads;
+            int e, h;
+            if (!at(r0 + u * NG, e, h)) continue;
             const float f = place[e].entry >= 0 ? power[h][e] : 0.0f;
             const float4 a = kv8_value4(c[u].x), b = kv8_value4(c[u].y);
             const float x[8] = {a.x * f, a.y * f, a.z * f, a.w * f, b.x * f, b.y * f, b.z * f, b.w * f};
             store8(out + ((int64_t)e * p.H + t.h0 + h) * p.D + d, x);
         }
     }
+}
+
+int64_t row_blocks(int32_t B, int32_t S, int32_t H, int E) {
+    return (int64_t)B * ((S + E - 1) / E) * ((H + kHeads - 1) / kHeads) * 2;
 }
 
 constexpr int kCommitThreads = 128, kCommitUnits = kCommitThreads / 32;
@@ -281,12 +322,13 @@ __global__ void __launch_bounds__(kCommitThreads) commit_kv8_kernel(Kv8Params p)
     }
 }
 
-template <typename T> cudaError_t launch_rows(const Kv8Params &p, bool write, cudaStream_t s) {
-    const int64_t grid = kv8_row_blocks(p.B, p.S, p.H);  // (checked: below 2^31)
+template <typename T, int E> cudaError_t launch_rows(Kv8Params p, bool write, cudaStream_t s) {
+    p.etiles = (p.S + E - 1) / E;
+    const unsigned grid = (unsigned)row_blocks(p.B, p.S, p.H, E);  // (checked: below 2^31)
     auto go = [&](auto g) {
-        constexpr int G = decltype(g)::value;
-        if (write) write_kv8_kernel<T, G><<<(unsigned)grid, kThreads, 0, s>>>(p);
-        else read_kv8_kernel<T, G><<<(unsigned)grid, kThreads, 0, s>>>(p);
+        constexpr int G = decltype(g)::value;  // 8 values a lane
+        if (write) write_kv8_kernel<T, G / 2, E><<<grid, kThreads, 0, s>>>(p);
+        else read_kv8_kernel<T, G, E><<<grid, kThreads, 0, s>>>(p);
         return cudaGetLastError();
     };
     if (p.D <= 64) return go(std::integral_constant<int, 8>{});
@@ -296,17 +338,17 @@ template <typename T> cudaError_t launch_rows(const Kv8Params &p, bool write, cu
 
 }  // namespace
 
-int64_t kv8_row_blocks(int32_t B, int32_t S, int32_t H) {
-    return (int64_t)B * ((S + kEntries - 1) / kEntries) * ((H + kHeads - 1) / kHeads) * 2;
-}
+int64_t kv8_row_blocks(int32_t B, int32_t S, int32_t H) { return row_blocks(B, S, H, 16); }
 
 int64_t kv8_commit_blocks(int32_t B, int32_t L) {
     return (int64_t)B * (((int64_t)2 * L + kCommitUnits - 1) / kCommitUnits);
 }
 
-cudaError_t launch_kv8_rows(Kv8Params p, int dtype, bool write, cudaStream_t s) {
-    p.etiles = (p.S + kEntries - 1) / kEntries;
-    return dtype == SPEC_DTYPE_BF16 ? launch_rows<__nv_bfloat16>(p, write, s) : launch_rows<float>(p, write, s);
+cudaError_t launch_kv8_rows(const Kv8Params &p, int dtype, bool write, int sms, cudaStream_t s) {
+    const bool many = row_blocks(p.B, p.S, p.H, 64) >= 2 * sms;
+    if (dtype == SPEC_DTYPE_BF16)
+        return many ? launch_rows<__nv_bfloat16, 64>(p, write, s) : launch_rows<__nv_bfloat16, 16>(p, write, s);
+    return many ? launch_rows<float, 64>(p, write, s) : launch_rows<float, 16>(p, write, s);
 }
 
 cudaError_t launch_kv8_commit(Kv8Params p, cudaStream_t s) {

@@ -8,11 +8,12 @@ scaling its largest element into (224, 448].  The second number's steps are 2^-9
 at least, half of that over 224 is 2^-17.8 of the largest element; what its first
 three bits leave of a bf16 value is otherwise exact.  So a score's error grows by
 at most |scale| 2^-17 max|q| sum|k|.  The weights, times V's powers of two, are
-rounded to f16 (2^-11 of each, below the bf16 rounding's 2^-8) and held as three
-e4m3 numbers: exactly, or, as the third one's steps end at 2^-19 where the row's
-largest power and a weight of 1 are at 2^5, to half a step, 2^-24 of the largest
-power, for a key, with codes up to 448 and 448 powers at most twice the largest |v|
-that the row sees, over a sum of weights that is at least 1."""
+rounded to f16 (2^-11 of each) and held as three e5m2 numbers: each of the first two
+takes at least 3 of the 11 bits, the third is rounded to 3 (2^-9 of the weight at most),
+together below the 2^-8 of a bf16 rounding that Case.check allows.  e5m2's steps end
+at 2^-16; a weight of 1 at the row's largest power is at 2^7, so half a step is 2^-24 of
+the largest power, for a key, with codes up to 448 and 448 powers at most twice the
+largest |v| that the row sees, over a sum of weights that is at least 1."""
 import math
 
 import numpy as np
@@ -117,6 +118,33 @@ def test_write(kw, dtype):
         # (a zero's sign is the input's in both)
         assert np.array_equal(got[1], scale) and np.array_equal(got[0], codes)
     assert not flags.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("kw", [dict(B=80, S=70, H=1, D=128, bs=16), dict(B=160, S=3, H=3, D=64, bs=8),
+                                dict(B=9, S=1100, H=2, D=16, bs=48), dict(B=3, S=3300, H=1, D=144, bs=1)])
+def test_many_entries_written_and_read_back(kw, dtype):
+    """Enough blocks for the wide ones; the same numbers as in one request after the other."""
+    B, S, H, D, bs = (kw[k] for k in ("B", "S", "H", "D", "bs"))
+    rng, g = np.random.default_rng(S), torch.Generator().manual_seed(S)
+    k, v = (special_rows((torch.randn((B, S, H, D), generator=g) * 3).to(DT[dtype])) for _ in range(2))
+    lens = rng.integers(0, 20, B).tolist()
+    count = [S, 0, 1] + rng.integers(0, S + 1, B - 3).tolist()
+    table, nb, _ = tables(rng, [n + S for n in lens], bs)
+    codes, scale = random_cache(rng, 1, nb, bs, H, D)
+    cache = on_gpu(codes, scale)
+    api.write_kv_q8(k.cuda(), v.cuda(), cache, i32(table), i32(lens), block_size=bs, n_new=i32(count))
+    r = api.read_kv_q8(cache, i32(table), i32(lens), i32(count), n_max=S, block_size=bs, dtype=torch.float32)
+    for i, (x, back) in enumerate(((k, r.k), (v, r.v))):
+        for b in range(B):
+            c, s = O.kv8_quantise(x[b, :count[b]].double().numpy())
+            at = lens[b] + np.arange(count[b])
+            blk, off = table[b, at // bs], at % bs
+            codes[0, i, blk, off], scale[0, i, blk, :, off] = c, s
+            want = torch.from_numpy(np.concatenate([O.kv8_values(c, s), np.zeros((S - count[b], H, D))])).float()
+            assert torch.equal(back[b].cpu().nan_to_num(nan=7.0, posinf=8.0, neginf=9.0), want.nan_to_num(nan=7.0, posinf=8.0, neginf=9.0))
+    got = off_gpu(cache)
+    assert np.array_equal(got[1], scale) and np.array_equal(got[0], codes)
 
 
 def test_write_bad_requests():
@@ -293,7 +321,7 @@ class Case8(Case):
         self.steps = 0.0
         if self.dtype == torch.bfloat16:
             v = self.planes()[1]
-            self.steps = 2.0 ** -25 * 2 * float(np.nanmax(np.abs(v)))
+            self.steps = 2.0 ** -24 * 2 * float(np.nanmax(np.abs(v)))
         super().check(r, rows)
 
     def oracle(self, b):
