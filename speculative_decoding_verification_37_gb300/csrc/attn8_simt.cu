@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(NT, blocks_of(DP, R)) attn8_simt_kernel(AttnPa
 template <typename T, int DP, int R> cudaError_t launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr int smem = (int)sizeof(Simt8Smem<T, DP, 16 * R>);
     static_assert(blocks_of(DP, R) * (smem + 1024) <= 228 * 1024, "so many blocks' shared memory an SM has");
-    cudaError_t e = cudaFuncSetAttribute(attn8_simt_kernel<T, DP, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = ensure_smem_attr(attn8_simt_kernel<T, DP, R>, smem, done);
     if (e != cudaSuccess) return e;
     // (at most 8 / R blocks an SM: the workspace's partial results)
     const int grid = (sms < kAttnSmsMax ? sms : kAttnSmsMax) * blocks_of(DP, R);

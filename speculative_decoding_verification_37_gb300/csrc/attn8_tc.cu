@@ -1,13 +1,15 @@
 // Attention over the 8-bit paged cache for bf16 queries on the fifth-generation
 // tensor cores (attention.cuh: score, split, join; kv8.cuh: the cache's numbers).
 //
-// One persistent block per SM, in three teams that know nothing of each other: a team
-// has a warp that copies, four softmax warps and its own share of the line of tiles
-// (one warp issues the MMAs of all), so that what one waits for (a product's end, an
-// item's first keys, its output) the others' work covers.  A tile is 128 keys, down
-// the MMA's rows; an item's 16 or 32 queries are its columns: a thread has a key,
-// with the key's power of two, position and masks, and the MMA does no work for
-// queries that are not there.  K and V go to the tensor cores as the codes they are:
+// One persistent block per SM, in teams that know nothing of each other: a team has a
+// warp that copies, 128 softmax threads for each 16 of an item's rows and its own
+// share of the line of tiles (one warp issues the MMAs of all), so that what one waits
+// for (a product's end, an item's first keys, its output) the others' work covers:
+// three teams for up to 16 rows a cached head (group of queries x candidates), two of
+// 32 rows, which share a tile's copies between two halves, for more.  A tile is 128
+// keys, down the MMA's rows; the queries are its columns: a thread has a key, with
+// the key's power of two, position and masks, and the MMA does no work for queries
+// that are not there.  K and V go to the tensor cores as the codes they are:
 //   * S^T = K Q^T.  A query, scaled by a power of two, is the sum of two e4m3 numbers
 //     (8 significant bits, as bf16 has; the smallest elements may lose 2^-17 of the
 //     largest); both products go into one accumulator.  A key's power of two
@@ -21,13 +23,31 @@
 //     columns of one product and are added at the item's end.
 //   * A row's largest score lies across the threads.  It is looked for, and the
 //     largest power, in an item's first tile and where a score passes the reference
-//     by 2^8 or a power the smallest of the rows', which one vote of the tile's threads
-//     finds; otherwise nobody needs another's scores.  Tiles go from the last, which is
-//     full, to the first: with a bias by distance the largest scores come first.  Sums
-//     of weights stay in the threads until the item's end.
+//     by 2^7 or a power the smallest of the rows' by more than 2, which one vote of the
+//     half's threads finds; otherwise nobody needs another's scores.  Tiles go from the
+//     last, which is full, to the first: with a bias by distance the largest scores
+//     come first.  Sums of weights stay in the threads until the item's end.
 //   * Where a tile hides keys, the threads look whether V holds NaN's code: such a row
-//     becomes zeros and gives its NaN, by way of the power of two, to the rows that
-//     give it weight; the rows that it is hidden from see nothing.
+//     becomes zeros and gives its NaN to the rows that see it; the rows that it is
+//     hidden from see nothing.
+//
+// What bounds it.  Single queries on up to 32,768 entries, 64 requests, 8 heads of 128:
+// 376 us, 5.9 TB/s of the 6.65 that a copy reaches.  64 requests of 5 queries x group 4
+// on 2,048 entries: 91 us (3.0 TB/s; the tiles themselves run at 6.2): a team's start
+// (13 us) and each change of items (14 us: the next queries, partial results, the
+// first tile's references) run code that is in no cache any more and comes from far
+// away, one miss of some 1,000 clk after another.  That is why the rest is short: 16 rows a
+// thread (32, with the loops twice as long: 8 x 5 queries on 40 entries 15.1 us
+// instead of 12.9, a shared prefix of 4,096 entries 137 instead of 130; only a capped
+// tree, 52 rows, was faster so: 314 instead of 325), and why K and V ask L2 to let go
+// of them first (single queries 406 -> 388 us, the chain 92 -> 89).  128 x 13 queries x group 4
+// on 2,048 entries, capped and biased, 325 us: bound by the softmax's instructions
+// (30 a weight; 46 % of the issue slots) and the second reading of keys for the rows
+// past 32; one tile of 64 rows, its threads at 96 registers, was no faster (326).
+//
+// The MMAs: an MMA of 128 x N x 32 takes 32 + N/4 clk, and 54 at least if its thread is
+// not an elected one (the operands are then moved to uniform registers each time);
+// a page's box of 16 rows of 128 bytes some 119 clk of the copy engine.
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
@@ -35,16 +55,20 @@
 #include "kv8.cuh"
 #include "tma.cuh"
 
+#include <type_traits>
+
 namespace specv {
 namespace {
 
-constexpr int KT = 128, GT = 128, NT = 256;  // keys of a tile; softmax threads of a team; threads that plan
+constexpr int KT = 128, RT = 16, GT = 128;  // keys of a tile; rows that a thread has; threads that hold a tile's keys
+constexpr int NT = 256;               // threads that plan
 constexpr uint32_t kTile = KT * 128;  // bytes of 128 keys x up to 128 codes
 constexpr int kInfo = 4;              // tiles whose notes are kept
 constexpr float kNone = -1e30f;       // the reference of a row that has seen no key
-constexpr float kLag = 8.0f;          // log2 of what a weight may reach
+constexpr float kLag = 7.0f;          // log2 of what a weight may reach
+constexpr int kMore = 1;              // powers that many above a row's largest still fit
 constexpr int kPowMin = 16;           // exponent byte that smaller powers are taken relative to
-constexpr int kUp = 7;                // log2 of a weight of 1 at the largest power: 2^(kUp + kLag) is an e5m2 number
+constexpr int kUp = 7;                // log2 of a weight of 1 at the largest power: 2^(kUp + kLag + kMore) is an e5m2 number
 constexpr int kParts = 3;             // e5m2 numbers that hold a weight
 
 __device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
@@ -59,10 +83,6 @@ __device__ __forceinline__ void tc_mma8(uint32_t d, uint64_t a, uint64_t b, uint
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
-}
-template <int N> __device__ __forceinline__ void tc_load(float *x, uint32_t t) {
-    if (N == 16) tc_ld16(x, t);
-    else tc_ldx<N>(x, t);
 }
 // a barrier of n threads under an id of its own that joins a predicate
 __device__ __forceinline__ bool bar_or(int id, int n, bool pred) {
@@ -82,6 +102,26 @@ __device__ __forceinline__ uint64_t tc_desc64(uint32_t addr, uint32_t sbo) {
 }
 __device__ __forceinline__ uint64_t tc_desc32(uint32_t addr, uint32_t lbo, uint32_t sbo) {
     return (uint64_t)((addr >> 4) & 0x3fff) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) | (1ull << 46) | (6ull << 61);
+}
+// L2's policy for a copy: read once, or kept as anything else is
+__device__ __forceinline__ uint64_t l2_policy(bool once) {
+    uint64_t a, b;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(a));
+    asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(b));
+    return once ? a : b;
+}
+__device__ __forceinline__ void tma3_hint(uint32_t dst, const CUtensorMap *m, int x, int y, int z, unsigned long long *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(
+            dst),
+        "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+// one of a warp's threads; the compiler knows that it is one
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0u;
 }
 // whether a barrier's phase is over; waits for nothing
 __device__ __forceinline__ bool mbar_test(unsigned long long *bar, unsigned phase) {
@@ -140,41 +180,53 @@ template <int N, typename F> __device__ __forceinline__ void reduce_rows(float (
     }
 }
 
-constexpr int kTeams = 3;
-
-// What a team has.
-template <int NH, int RT> struct Team8 {
-    static constexpr uint32_t kQ = RT * 128;         // bytes of a part of the queries
-    // P^T: 16 queries: a key's 64 bytes, three parts of four; 32: a part's 4 KB after another
-    static constexpr uint32_t kP = RT == 16 ? KT * 64 : KT * kParts * 32, kStep = RT == 16 ? 32 * 64 : 32 * 32;
+// What 16 of an item's rows have, for the 128 threads that hold a tile's keys.
+struct Rows8 {
+    alignas(16) float nref[RT], zero[RT];            // the references (log2 units), negated; zeros
+    alignas(16) float corr[RT], corr_o[RT], gain[RT];  // what sums and O are multiplied by (at the
+                                                     // end: O and the shared part); what weights are at a power of 1
+    alignas(16) float top[4][RT];                    // the warps' largest scores; at the end sums of weights
+    alignas(16) int pow[4][RT];                      // and powers
+    alignas(16) float cf[RT];                        // what a product is multiplied by for log2 units or the cap's exponent
+    alignas(16) float qp[RT], slope[RT];             // positions after the first; bias by distance, log2 units
+    alignas(16) int low[RT];                         // first visible position
+    AttnRows<RT> rows[2];
+    unsigned words[RT][5];                           // a tile's candidates in the rows' tree masks
+    int pow_min, qp0;                                // the smallest largest power; the first position
+    int low_max[2];                                  // the largest `low`, by turns of items
+    int last;
+};
+// What a team has: HV times RT rows, 128 threads for each RT.
+template <int NH, int HV> struct Team8 {
+    static constexpr int kTeams = HV == 1 ? 3 : 2, kRows = HV * RT, kThreads = HV * GT;
+    static constexpr int kSoftWarps = kTeams * HV * 4;
+    static constexpr uint32_t kQ = kRows * 128;      // bytes of a part of the queries
+    // P^T: 16 rows: a key's 64 bytes, three parts of four; 32: 32 bytes of a part, a part
+    // after another
+    static constexpr uint32_t kPart = KT * 32, kP = HV == 1 ? KT * 64 : kParts * kPart, kStep = HV == 1 ? 32 * 64 : 32 * 32;
     static constexpr int KS = 2;                     // buffers for K
     alignas(1024) unsigned char k[KS][kTile];
     alignas(1024) unsigned char v[kTile];
     alignas(1024) unsigned char q[2][kQ];            // the queries' first and second parts
     alignas(1024) unsigned char p[kP];
-    alignas(16) float ref[RT], corr[RT], corr_o[RT], gain[RT];  // references (log2 units), what sums and O are
-                                                     // multiplied by, what weights are at a power of 1
-    alignas(16) float top[4][RT];                    // the warps' largest scores; at the end sums of weights
-    alignas(16) int pow[4][RT];                      // and powers
-    alignas(16) float cf[RT];                        // scale times what the queries were divided by; without cap and bias times log2(e)
-    alignas(16) float qp[RT];                        // positions after the item's first
-    alignas(16) int low[RT];                         // first visible position
-    alignas(16) float fa[RT], fc[RT];                // output: factors of O and of the shared part
-    AttnRows<RT> rows[2];
-    unsigned words[RT][5];                           // a tile's candidates in the rows' tree masks
-    int pow_min, low_max, qp0;                       // the smallest largest power; the largest `low`; the first position
+    Rows8 half[HV];
     unsigned sc[kInfo][2][KT / 4];                   // exponent bytes of a tile's K and V
     unsigned bad[kInfo];                             // boxes of a tile with a bad block
     int first[kInfo];                                // whether an item begins
     alignas(8) unsigned long long k_full[KS], k_empty[KS], v_full, s_full[2], p_full, pv_done, q_full;
-    int scored, weighed, begun, tiles;               // the MMA warp's: tiles so far, items begun, tiles in all
-    int last;
 };
-template <int NH, int RT> struct Tc8Smem {
-    Team8<NH, RT> team[kTeams];
+template <int NH, int HV> struct Tc8Smem {
+    Team8<NH, HV> team[Team8<NH, HV>::kTeams];
     AttnPlan plan;
     uint32_t tmem;
 };
+
+template <int N> __device__ __forceinline__ float sum_parts(const float (&o)[N][8], int r) {
+    float x = o[0][r];
+#pragma unroll
+    for (int c = 1; c < N; ++c) x += o[c][r];
+    return x;
+}
 
 // the item after `it` (one copy of this code)
 static __device__ __noinline__ void next_item(const AttnParams &p, AttnItem &it, int items, int rtiles) {
@@ -184,21 +236,25 @@ static __device__ __noinline__ void next_item(const AttnParams &p, AttnItem &it,
 // is left (whole boxes).
 __device__ __forceinline__ int line_start(const KeyLine &line, int ntiles) { return line.lo - (ntiles * KT - line.entries); }
 
-template <int NH, int RT, bool plain>
-__global__ void __launch_bounds__(128 * kTeams + 128, 1)
+template <int NH, int HV> constexpr int threads_of() {
+    using H = Team8<NH, HV>;
+    return 32 * (H::kSoftWarps + H::kTeams + 1);
+}
+template <int NH, int HV, bool plain>
+__global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
     attn8_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap cache_map) {
-    using H = Team8<NH, RT>;
-    constexpr int G = kTeams, NW = 4 * G;  // teams; softmax warps
+    using H = Team8<NH, HV>;
+    constexpr int G = H::kTeams, NW = H::kSoftWarps;  // teams; softmax warps
     using T = __nv_bfloat16;
     extern __shared__ unsigned char raw_[];
-    Tc8Smem<NH, RT> &all = *reinterpret_cast<Tc8Smem<NH, RT> *>(
+    Tc8Smem<NH, HV> &all = *reinterpret_cast<Tc8Smem<NH, HV> *>(
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw_) + 1023) & ~uintptr_t(1023)));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int grp = warp < NW ? warp >> 2 : warp < NW + G ? warp - NW : 0;  // then a warp a team for copies, one for MMAs
+    const int grp = warp < NW ? warp / (4 * HV) : warp < NW + G ? warp - NW : 0;  // then a warp a team for copies, one for MMAs
     H &sh = all.team[grp];
     const int per = p.S * p.G;
     const int64_t nrows = p.mode == 1 ? (int64_t)p.B * per : per;
-    const int rtiles = (int)((nrows + RT - 1) / RT), items = p.H * rtiles;
+    const int rtiles = (int)((nrows + H::kRows - 1) / H::kRows), items = p.H * rtiles;
     if (tid < G) {
         H &h = all.team[tid];
         for (int s = 0; s < H::KS; ++s) {
@@ -208,9 +264,9 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
         mbar_init(&h.v_full, 1);
         mbar_init(&h.s_full[0], 1);
         mbar_init(&h.s_full[1], 1);
-        mbar_init(&h.p_full, GT);
+        mbar_init(&h.p_full, H::kThreads);
         mbar_init(&h.pv_done, 1);
-        mbar_init(&h.q_full, GT);
+        mbar_init(&h.q_full, H::kThreads);
         fence_barrier_init();
     }
     if (p.mode == 1) pdl_launch_dependents();  // (they wait before they use what this kernel writes)
@@ -227,59 +283,59 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
     int64_t u = part * share;
     const int64_t uend = min(all.plan.total, u + share);
     // TMEM columns: the teams' two score tiles, then their accumulators
-    constexpr uint32_t kO = 2 * G * RT;
-    const uint32_t col_s = tmem + grp * 2 * RT, col_o = tmem + kO + kParts * grp * RT;
-    static_assert((2 + kParts) * G * RT <= 512, "columns");
+    constexpr uint32_t kO = 2 * G * H::kRows, kOCols = kParts * H::kRows;
+    static_assert(kO + G * kOCols <= 512, "columns");
     bool ok = true;  // after a wait has run out nothing waits any more; the call is flagged
     if (warp == NW + G) {
         // ---------------- MMAs ----------------
         // A team's next product where its weights and V are there, its next scores where its
         // K is, and, of an item's first, the queries.
-        if (lane == 0) {
+        if (elect_one()) {
             // Operands.  Scores: atoms of 8 rows x 128 bytes, the next 8 rows 1,024 bytes on;
             // 32 columns of K and Q are 32 bytes.  Values: the rows are keys, the products' K,
             // whose elements (V's columns: M; P's weights: N) are contiguous: 128 of V (zeros
             // past the head), 48 of P, or 32 and the next 32 a part further on.
-            constexpr uint32_t id_s = tc_idesc8(RT), id_o = tc_idesc_mn(kParts * RT);
+            constexpr uint32_t id_s = tc_idesc8(H::kRows), id_o = tc_idesc_mn(kParts * H::kRows);
             int left = 0, idle = 0;
+            int scored[G], weighed[G], begun[G], tiles[G];  // of the teams: tiles so far, items begun, tiles in all
+#pragma unroll
             for (int g = 0; g < G; ++g) {
-                H &t = all.team[g];
                 const int64_t at = ((int64_t)g * gridDim.x + blockIdx.x) * share;
-                t.scored = t.weighed = t.begun = 0;
-                left += t.tiles = (int)max((int64_t)0, min(all.plan.total, at + share) - at);
+                scored[g] = weighed[g] = begun[g] = 0;
+                left += tiles[g] = (int)max((int64_t)0, min(all.plan.total, at + share) - at);
             }
             while (left > 0 && idle < (int)kSpinLimit) {
                 ++idle;
-#pragma unroll 1
+#pragma unroll
                 for (int g = 0; g < G; ++g) {
                     H &t = all.team[g];
-                    const int n = t.scored, j = t.weighed;
+                    const int n = scored[g], j = weighed[g];
                     if (j < n && mbar_test(&t.v_full, (unsigned)(j & 1)) && mbar_test(&t.p_full, (unsigned)(j & 1))) {
                         tc_fence_after();
                         const uint64_t a = tc_desc(smem_u32(t.v), 0, 1024),
-                                       b = RT == 16 ? tc_desc64(smem_u32(t.p), 512) : tc_desc32(smem_u32(t.p), KT * 32, 256);
-                        const bool add = !t.first[j % kInfo];
+                                       b = HV == 1 ? tc_desc64(smem_u32(t.p), 512) : tc_desc32(smem_u32(t.p), H::kPart, 256);
+                        const uint32_t add = !t.first[j % kInfo];
 #pragma unroll
                         for (int k = 0; k < KT / 32; ++k)
-                            tc_mma8(tmem + kO + kParts * g * RT, a + k * (4096 / 16), b + k * (H::kStep / 16), id_o, add || k > 0);
+                            tc_mma8(tmem + kO + g * kOCols, a + k * (4096 / 16), b + k * (H::kStep / 16), id_o, k > 0 ? 1u : add);
                         tc_commit(&t.pv_done);
-                        t.weighed = j + 1;
+                        weighed[g] = j + 1;
                         --left;
                         idle = 0;
                     }
-                    if (n < t.tiles && n < t.weighed + 2 && mbar_test(&t.k_full[n % H::KS], (unsigned)((n / H::KS) & 1))) {
+                    if (n < tiles[g] && n < weighed[g] + 2 && mbar_test(&t.k_full[n % H::KS], (unsigned)((n / H::KS) & 1))) {
                         const bool first = t.first[n % kInfo];
-                        if (!first || mbar_test(&t.q_full, (unsigned)(t.begun & 1))) {
+                        if (!first || mbar_test(&t.q_full, (unsigned)(begun[g] & 1))) {
                             tc_fence_after();
                             const uint64_t a = tc_desc(smem_u32(t.k[n % H::KS]), 16, 1024), b = tc_desc(smem_u32(t.q[0]), 16, 1024);
 #pragma unroll
                             for (int k = 0; k < NH * 4; ++k)  // first parts, second parts
-                                tc_mma8(tmem + (2 * g + (n & 1)) * RT, a + (k % (NH * 2)) * (32 / 16),
+                                tc_mma8(tmem + (2 * g + (n & 1)) * H::kRows, a + (k % (NH * 2)) * (32 / 16),
                                         b + (k / (NH * 2)) * (H::kQ / 16) + (k % (NH * 2)) * (32 / 16), id_s, k > 0);
                             tc_commit(&t.k_empty[n % H::KS]);
                             tc_commit(&t.s_full[n & 1]);
-                            t.scored = n + 1;
-                            t.begun += first;
+                            scored[g] = n + 1;
+                            begun[g] += first;
                             idle = 0;
                         }
                     }
@@ -292,6 +348,9 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
         AttnItem it = attn_find<NT>(p, all.plan, u, items, rtiles, KT);
         if (warp >= NW) {
             // ---------------- copies ----------------
+            // A shared prefix is read by many; the others' keys, once, would push the code that
+            // runs once an item out of L2.
+            const uint64_t policy = l2_policy(p.mode == 0);
             const int nbox = KT / p.box;
             const int zero_row = (int)(2 * p.nb * p.bs);  // past the map: zeros are written
             const int v_row = (int)(p.nb * p.bs);
@@ -333,7 +392,7 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                 auto copy = [&](unsigned char *to, unsigned long long *bar, int r) {
                     if (lane == 0) mbar_arrive_expect_tx(bar, kTile);
                     __syncwarp();
-                    if (lane < nbox) tma3(smem_u32(to) + (uint32_t)(lane * p.box) * 128u, &cache_map, 0, it.h, r, bar);
+                    if (lane < nbox) tma3_hint(smem_u32(to) + (uint32_t)(lane * p.box) * 128u, &cache_map, 0, it.h, r, bar, policy);
                 };
                 blk = block_of(t1 - 1);
                 entry_of(t1 - 1);
@@ -380,34 +439,47 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
         } else {
             // ---------------- softmax ----------------
             const int wq = warp & 3, key = tid & (GT - 1);            // key of a tile; row of the MMA: TMEM lane
-            const int bar = 2 + grp;
+            const int half = HV == 1 ? 0 : (warp >> 2) & 1;            // of the item's rows
+            const int bar = 2 + (warp >> 2);                          // the half's barrier; the team's
+            auto team_sync = [&] { bar_sync(HV == 1 ? bar : 2 + NW / 4 + grp, H::kThreads); };
+            Rows8 &hs = sh.half[half];
             const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-            const uint32_t to = col_o + lanes;
+            const uint32_t col_s = tmem + grp * 2 * H::kRows + half * RT + lanes, to = tmem + kO + grp * kOCols + half * RT + lanes;
             const bool by_pos = p.window > 0 || p.first != nullptr;
             const uint32_t neg = p.score.scale < 0.0f ? 0x80008000u : 0u;  // a negative scale: the queries are negated
-            const float scale = fabsf(p.score.scale) * (plain ? kLog2e : 1.0f);
-            constexpr unsigned kRowLanes = RT == 16 ? 0xffffu : kFull;
+            const bool cap = !plain && p.score.cap > 0.0f;
+            // Scores are log2 units; capped ones (cap_score) without the cap itself, which
+            // all have in common: lse gets it back.
+            const float scale = fabsf(p.score.scale) * (cap ? p.score.cap_arg : kLog2e);
+            const float2 cap2 = pair(-2.0f * kLog2e * p.score.cap, -2.0f * kLog2e * p.score.cap);
+            const float shift = cap ? kLog2e * p.score.cap : 0.0f;
+            constexpr unsigned kRowLanes = 0xffffu;
             int item = 0, n = 0;
             auto start_rows = [&] {  // of an item: nothing seen yet
                 if (key < RT) {
-                    sh.ref[key] = kNone;
-                    sh.gain[key] = pow2i(127 + kUp - kPowMin);
+                    hs.nref[key] = -kNone;
+                    hs.zero[key] = 0.0f;
+                    hs.gain[key] = pow2i(127 + kUp - kPowMin);
                 }
             };
             // An item's rows and queries: 8 elements a thread at a time.  The next item's are
             // prepared before this one's output.
-            auto prepare = [&](AttnRows<RT> &w) {
-                attn_rows<RT, GT>(p, it, w, key);
+            auto prepare = [&](int turn) {
+                AttnRows<RT> &w = hs.rows[turn];
+                AttnItem of = it;
+                of.rt = it.rt * HV + half;
+                attn_rows<RT, GT>(p, of, w, key);
                 if (key < RT) {
                     const int lo = max(w.first[key], p.window > 0 ? w.qp[key] - p.window + 1 : (int)0x80000000);
-                    sh.low[key] = lo;
+                    hs.low[key] = lo;
                     const bool is = w.out[key] >= 0;
                     const int most = __reduce_max_sync(kRowLanes, is ? lo : (int)0x80000000);
                     const int qp0 = __reduce_min_sync(kRowLanes, is ? w.qp[key] : 0x7fffffff);
-                    sh.qp[key] = is ? (float)pos_dist(w.qp[key], qp0) : 0.0f;
+                    hs.qp[key] = is ? (float)pos_dist(w.qp[key], qp0) : 0.0f;
+                    hs.slope[key] = -kLog2e * w.slope[key];
                     if (lane == 0) {
-                        sh.low_max = most;
-                        sh.qp0 = qp0;
+                        hs.low_max[turn] = most;
+                        hs.qp0 = qp0;
                     }
                 }
                 bar_sync(bar, GT);
@@ -433,7 +505,7 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                     for (int o = LR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
                     const unsigned s = kv8_scale(top);
                     const float f = s == 255u ? 0.0f : kv8_inverse(s);
-                    if (key % LR == 0) sh.cf[r] = scale * kv8_power(s);
+                    if (key % LR == 0) hs.cf[r] = scale * kv8_power(s);
                     uint32_t a[2], b[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -442,22 +514,23 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                         b[e] = kv8_code2(x[4 * e] * f - y.x, x[4 * e + 1] * f - y.y) |
                                kv8_code2(x[4 * e + 2] * f - y.z, x[4 * e + 3] * f - y.w) << 16;
                     }
-                    const uint32_t at = r * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
+                    const uint32_t at = (half * RT + r) * 128 + (((d >> 4) ^ (r & 7)) << 4) + (d & 8);
                     *reinterpret_cast<uint2 *>(sh.q[0] + at) = make_uint2(a[0], a[1]);
                     *reinterpret_cast<uint2 *>(sh.q[1] + at) = make_uint2(b[0], b[1]);
                 }
                 fence_async_shared();
-                bar_sync(bar, GT);
+                team_sync();
                 mbar_arrive(&sh.q_full);
             };
             start_rows();
-            prepare(sh.rows[0]);
+            prepare(0);
             while (true) {
-                const AttnRows<RT> &w = sh.rows[item & 1];
+                const AttnRows<RT> &w = hs.rows[item & 1];
                 const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
                 const KeyLine line = it.keys.ok ? attn_line(p, it.keys) : KeyLine{0, 0};
                 const int start = line_start(line, it.ntiles);
-                const int low_max = sh.low_max, qp0 = sh.qp0;
+                const int qp0 = hs.qp0;
+                const int low_max = max(hs.low_max[item & 1], sh.half[HV - 1 - half].low_max[item & 1]);  // (every row's)
                 int pow_min = 0;                 // the smallest of the rows' largest powers
                 float l[RT];                     // sums of this thread's weights
 #pragma unroll
@@ -503,7 +576,7 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                         if (tree) {
                             for (int i = key; i < RT * 5; i += GT) {
                                 const int r = i / 5, x = word0 + i - r * 5;
-                                sh.words[r][i - r * 5] = x < p.W ? p.mask[((int64_t)it.b * p.S + w.cand[r]) * p.W + x] : 0u;
+                                hs.words[r][i - r * 5] = x < p.W ? p.mask[((int64_t)it.b * p.S + w.cand[r]) * p.W + x] : 0u;
                             }
                             bar_sync(bar, GT);
                         }
@@ -514,62 +587,53 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                             seen = 0u;
 #pragma unroll 8
                             for (int r = 0; r < RT; ++r) {
-                                bool s = !by_pos || kp >= sh.low[r];
-                                if (p.mode == 0 && cand >= 0) s = s && (tree ? (sh.words[r][x] >> (cand & 31)) & 1u : cand <= w.cand[r]);
+                                bool s = !by_pos || kp >= hs.low[r];
+                                if (p.mode == 0 && cand >= 0) s = s && (tree ? (hs.words[r][x] >> (cand & 31)) & 1u : cand <= w.cand[r]);
                                 seen |= (unsigned)s << r;
                             }
                         }
                     }
-                    const uint32_t ts = col_s + (n & 1) * RT + lanes;
+                    const uint32_t ts = col_s + (n & 1) * H::kRows;
                     const float kd = (float)pos_dist(qp0, kp);
+                    const float2 kd2 = pair(kd, kd);
                     // Scores in log2 units less the references; without them (raw) to find new ones.
                     float y[RT];
                     bool raw = n == n0;
 #pragma unroll 1
                     while (true) {
-                        tc_load<RT>(y, ts);
+                        tc_ld16(y, ts);
                         tc_wait_ld();
-                        const float2 kf2 = pair(kf, kf), e2 = pair(kLog2e, kLog2e);
+                        const float2 kf2 = pair(kf, kf);
 #pragma unroll
                         for (int r = 0; r < RT; r += 4) {  // (the key's factor first: with the query's it is the score's size)
                             const float2 a = __fmul2_rn(pair(y[r], y[r + 1]), kf2), b = __fmul2_rn(pair(y[r + 2], y[r + 3]), kf2);
                             y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
                         }
-                        if (!plain) {
-                            if (p.score.cap > 0.0f) {  // cap_score
-                                const float2 s2 = pair(p.score.cap_arg, p.score.cap_arg), c2 = pair(-2.0f * p.score.cap, -2.0f * p.score.cap),
-                                             cap2 = pair(p.score.cap, p.score.cap), one = pair(1.0f, 1.0f);
+                        const float *nref = raw ? hs.zero : hs.nref;
+                        if (cap) {
+                            const float2 one = pair(1.0f, 1.0f);
 #pragma unroll
-                                for (int r = 0; r < RT; r += 2) {
-                                    float2 a = __fmul2_rn(__fmul2_rn(pair(y[r], y[r + 1]), *reinterpret_cast<const float2 *>(&sh.cf[r])), s2);
-                                    a = __fadd2_rn(pair(ex2f(a.x), ex2f(a.y)), one);
-                                    a = __ffma2_rn(pair(rcpf(a.x), rcpf(a.y)), c2, cap2);
-                                    y[r] = a.x, y[r + 1] = a.y;
-                                }
-                            } else {
-#pragma unroll
-                                for (int r = 0; r < RT; r += 2) {
-                                    const float2 a = __fmul2_rn(pair(y[r], y[r + 1]), *reinterpret_cast<const float2 *>(&sh.cf[r]));
-                                    y[r] = a.x, y[r + 1] = a.y;
-                                }
-                            }
-                            if (p.score.bias) {  // (both terms of the distance are positive for entries: no cancellation)
-                                const float2 kd2 = pair(kd, kd);
-#pragma unroll
-                                for (int r = 0; r < RT; r += 2) {
-                                    const float2 d = __fadd2_rn(*reinterpret_cast<const float2 *>(&sh.qp[r]), kd2);
-                                    const float2 s = *reinterpret_cast<const float2 *>(&w.slope[r]);
-                                    const float2 a = __ffma2_rn(pair(-s.x, -s.y), d, pair(y[r], y[r + 1]));
-                                    y[r] = a.x, y[r + 1] = a.y;
-                                }
+                            for (int r = 0; r < RT; r += 4) {
+                                const float4 c = *reinterpret_cast<const float4 *>(&hs.cf[r]);
+                                float2 a = __fmul2_rn(pair(y[r], y[r + 1]), pair(c.x, c.y)), b = __fmul2_rn(pair(y[r + 2], y[r + 3]), pair(c.z, c.w));
+                                a = __fadd2_rn(pair(ex2f(a.x), ex2f(a.y)), one), b = __fadd2_rn(pair(ex2f(b.x), ex2f(b.y)), one);
+                                y[r] = rcpf(a.x), y[r + 1] = rcpf(a.y), y[r + 2] = rcpf(b.x), y[r + 3] = rcpf(b.y);
                             }
                         }
 #pragma unroll
                         for (int r = 0; r < RT; r += 4) {
-                            const float4 m = raw ? make_float4(0.f, 0.f, 0.f, 0.f) : *reinterpret_cast<const float4 *>(&sh.ref[r]);
-                            const float4 c = plain ? *reinterpret_cast<const float4 *>(&sh.cf[r]) : make_float4(kLog2e, kLog2e, kLog2e, kLog2e);
-                            const float2 a = __ffma2_rn(pair(y[r], y[r + 1]), pair(c.x, c.y), pair(-m.x, -m.y));
-                            const float2 b = __ffma2_rn(pair(y[r + 2], y[r + 3]), pair(c.z, c.w), pair(-m.z, -m.w));
+                            const float4 m = *reinterpret_cast<const float4 *>(nref + r);
+                            float2 a = pair(m.x, m.y), b = pair(m.z, m.w), ca = cap2, cb = cap2;
+                            if (!plain && p.score.bias) {  // (both terms of the distance are positive for entries: no cancellation)
+                                const float4 q = *reinterpret_cast<const float4 *>(&hs.qp[r]), s = *reinterpret_cast<const float4 *>(&hs.slope[r]);
+                                a = __ffma2_rn(pair(s.x, s.y), __fadd2_rn(pair(q.x, q.y), kd2), a);
+                                b = __ffma2_rn(pair(s.z, s.w), __fadd2_rn(pair(q.z, q.w), kd2), b);
+                            }
+                            if (!cap) {
+                                const float4 c = *reinterpret_cast<const float4 *>(&hs.cf[r]);
+                                ca = pair(c.x, c.y), cb = pair(c.z, c.w);
+                            }
+                            a = __ffma2_rn(pair(y[r], y[r + 1]), ca, a), b = __ffma2_rn(pair(y[r + 2], y[r + 3]), cb, b);
                             y[r] = a.x, y[r + 1] = a.y, y[r + 2] = b.x, y[r + 3] = b.y;
                         }
                         if (special) {
@@ -577,8 +641,10 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                             for (int r = 0; r < RT; ++r) y[r] = (seen >> r) & 1u ? y[r] : -INFINITY;
                         }
                         if (!raw) {
-                            const float over = max_of<RT>(y);
-                            if (!bar_or(bar, GT, over > kLag || (in && pw > pow_min))) break;
+                            float over = -INFINITY;
+#pragma unroll
+                            for (int r = 0; r < RT; r += 2) over = fmaxf(fmaxf(over, y[r]), y[r + 1]);
+                            if (!bar_or(bar, GT, over > kLag || (in && pw > pow_min + kMore))) break;
                             raw = true;
                             continue;
                         }
@@ -602,51 +668,51 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                             most = every;
                         }
                         if (lane < RT) {
-                            sh.top[wq][lane] = mine;
-                            sh.pow[wq][lane] = most;
+                            hs.top[wq][lane] = mine;
+                            hs.pow[wq][lane] = most;
                         }
                         bar_sync(bar, GT);
                         if (key < RT) {
-                            const float top = fmaxf(fmaxf(sh.top[0][key], sh.top[1][key]), fmaxf(sh.top[2][key], sh.top[3][key]));
-                            const int most = max(max(sh.pow[0][key], sh.pow[1][key]), max(sh.pow[2][key], sh.pow[3][key]));
-                            const float old = sh.ref[key];
+                            const float top = fmaxf(fmaxf(hs.top[0][key], hs.top[1][key]), fmaxf(hs.top[2][key], hs.top[3][key]));
+                            const int most = max(max(hs.pow[0][key], hs.pow[1][key]), max(hs.pow[2][key], hs.pow[3][key]));
+                            const float old = -hs.nref[key];
                             const bool grew = top > old + kLag || (old == kNone && top > kNone);
                             const float f = grew ? ex2f(old - top) : 1.0f;
-                            const int was = 127 + kUp - ((int)(__float_as_uint(sh.gain[key]) >> 23) - 127), now = max(was, most);
-                            sh.corr[key] = f;
-                            sh.corr_o[key] = f * pow2i(was - now);
-                            sh.gain[key] = pow2i(127 + kUp - now);
-                            if (grew) sh.ref[key] = top;
+                            const int was = 127 + kUp - ((int)(__float_as_uint(hs.gain[key]) >> 23) - 127), now = max(was, most);
+                            hs.corr[key] = f;
+                            hs.corr_o[key] = f * pow2i(was - now);
+                            hs.gain[key] = pow2i(127 + kUp - now);
+                            if (grew) hs.nref[key] = -top;
                             const int least = __reduce_min_sync(kRowLanes, grew || old != kNone ? now : 254);
-                            if (lane == 0) sh.pow_min = least;
+                            if (lane == 0) hs.pow_min = least;
                         }
                         bar_sync(bar, GT);
-                        pow_min = sh.pow_min;
+                        pow_min = hs.pow_min;
 #pragma unroll
                         for (int r = 0; r < RT; r += 4) {
-                            const float4 m = *reinterpret_cast<const float4 *>(&sh.ref[r]), f = *reinterpret_cast<const float4 *>(&sh.corr[r]);
-                            y[r] -= m.x, y[r + 1] -= m.y, y[r + 2] -= m.z, y[r + 3] -= m.w;
+                            const float4 m = *reinterpret_cast<const float4 *>(&hs.nref[r]), f = *reinterpret_cast<const float4 *>(&hs.corr[r]);
+                            y[r] += m.x, y[r + 1] += m.y, y[r + 2] += m.z, y[r + 3] += m.w;
                             l[r] *= f.x, l[r + 1] *= f.y, l[r + 2] *= f.z, l[r + 3] *= f.w;
                         }
                         if (n > n0) {  // O, still once the product before has ended
                             if (ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
                             tc_fence_after();
 #pragma unroll 1
-                            for (int c = 0; c < kParts * RT; c += 16) {
-                                const float *f = sh.corr_o + (c & (RT - 1));
-                                float o[16];
-                                uint32_t z[16];
-                                tc_ld16(o, to + c);
+                            for (int c = 0; c < kParts; ++c) {
+                                const uint32_t at = to + c * H::kRows;
+                                float o[RT];
+                                uint32_t z[RT];
+                                tc_ld16(o, at);
                                 tc_wait_ld();
 #pragma unroll
-                                for (int r = 0; r < 16; ++r) z[r] = __float_as_uint(o[r] * f[r]);
-                                tc_st16(to + c, z);
+                                for (int r = 0; r < RT; ++r) z[r] = __float_as_uint(o[r] * hs.corr_o[r]);
+                                tc_st16(at, z);
                             }
                             tc_wait_st();
                         }
                         break;
                     }
-                    float vf = kv8_power(vs);
+                    bool nan_v = vs == 255;
                     if (special) {
                         // V's NaN must not meet the weights of rows that do not see it
                         if (ok) ok = attn_wait(&sh.v_full, (unsigned)(n & 1));
@@ -658,47 +724,52 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                             nan |= ((c.x & 0x7f7f7f7fu) + 0x01010101u) | ((c.y & 0x7f7f7f7fu) + 0x01010101u) |
                                    ((c.z & 0x7f7f7f7fu) + 0x01010101u) | ((c.w & 0x7f7f7f7fu) + 0x01010101u);
                         }
+                        if (HV > 1) team_sync();  // (both have looked)
                         if (nan & 0x80808080u) {
-                            vf = kv8_power(255);
+                            nan_v = true;
 #pragma unroll 1
                             for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(vr + (i << 4)) = make_uint4(0, 0, 0, 0);
                         }
                     }
                     // P's buffer is free once the product before has ended
                     if (n > n0 && ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
-                    // weights: summed, times V's power of two to three e4m3 numbers
-                    unsigned char *pp = sh.p + key * (RT == 16 ? 64 : 32);
-                    const int sw = RT == 16 ? (key >> 1) & 3 : (key >> 2) & 1;  // the swizzle of 64 or 32 bytes
-                    const bool pick = special || vf != vf;
+                    // weights: summed, times V's power of two to three e5m2 numbers
+                    unsigned char *pp = sh.p + key * (HV == 1 ? 64 : 32);
+                    const int sw = HV == 1 ? (key >> 1) & 3 : (key >> 2) & 1;  // the swizzle of 64 or 32 bytes
+                    const float vf = nan_v ? 0.0f : kv8_power(vs);
+                    const float2 vf2 = pair(vf, vf);
+                    {
+                        uint32_t h[RT / 2];
 #pragma unroll
-                    for (int r = 0; r < RT; r += 16) {
-                        uint32_t h[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int q = r + 2 * i;
-                            const float2 g = *reinterpret_cast<const float2 *>(&sh.gain[q]);
+                        for (int i = 0; i < RT / 2; ++i) {
+                            const int q = 2 * i;
+                            const float2 g = *reinterpret_cast<const float2 *>(&hs.gain[q]);
                             const float2 a = pair(ex2f(y[q]), ex2f(y[q + 1]));
                             const float2 sum = __fadd2_rn(pair(l[q], l[q + 1]), a);
                             l[q] = sum.x, l[q + 1] = sum.y;
-                            float2 b = __fmul2_rn(a, __fmul2_rn(g, pair(vf, vf)));
-                            // (a V that stands for NaN does not show where it has no weight; a hidden
-                            // one's power may be any)
-                            if (pick) b = pair(a.x == 0.0f ? 0.0f : b.x, a.y == 0.0f ? 0.0f : b.y);
+                            // (the gain first: a hidden key's power may be any, its weight stays 0)
+                            const float2 b = __fmul2_rn(__fmul2_rn(a, g), vf2);
                             h[i] = pack_f16(b.x, b.y);
                         }
                         auto put = [&](int c) {
                             uint32_t z[4];
 #pragma unroll
                             for (int i = 0; i < 4; ++i) z[i] = c < 2 ? __byte_perm(h[2 * i], h[2 * i + 1], 0x7531) : h[2 * i] | h[2 * i + 1] << 16;
-                            *reinterpret_cast<uint4 *>(pp + (RT == 16 ? (c ^ sw) << 4 : c * (KT * 32) + ((r / 16 ^ sw) << 4))) = make_uint4(z[0], z[1], z[2], z[3]);
+                            *reinterpret_cast<uint4 *>(pp + (HV == 1 ? (c ^ sw) << 4 : c * H::kPart + ((half ^ sw) << 4))) = make_uint4(z[0], z[1], z[2], z[3]);
                         };
                         put(0);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] = rest_e5m2(h[i]);
+                        for (int i = 0; i < RT / 2; ++i) h[i] = rest_e5m2(h[i]);
                         put(1);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] = round_e5m2(rest_e5m2(h[i]));
+                        for (int i = 0; i < RT / 2; ++i) h[i] = round_e5m2(rest_e5m2(h[i]));
                         put(2);
+                    }
+                    if (nan_v) {  // the rows that see it get NaN, the others nothing
+#pragma unroll 1
+                        for (int r = 0; r < RT; ++r)
+                            if ((seen >> r) & 1u)
+                                pp[((half ^ sw) << 4) + r] = 0x7f;
                     }
                     fence_async_shared();
                     tc_fence_before();
@@ -710,10 +781,10 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                 u = end;
                 if (end < uend) {
                     next_item(p, it, items, rtiles);
-                    prepare(sh.rows[item & 1 ^ 1]);
+                    prepare(item & 1 ^ 1);
                 }
                 reduce_rows<RT>(l, [](float a, float b) { return a + b; });
-                if (RT == 32 || (lane & 1) == 0) sh.top[wq][RT == 32 ? lane : lane >> 1] = l[0];
+                if ((lane & 1) == 0) hs.top[wq][lane >> 1] = l[0];
                 // the shared part's results are there, and its partial results done with
                 // (no wait but after a shared pass, whose end this kernel's start overlaps)
                 if (item == 0) pdl_wait_primary();
@@ -726,9 +797,9 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                 bar_sync(bar, GT);
                 float s = 0.0f, m = -INFINITY, back = 1.0f;  // of row `key`: sum, reference, what O is divided by
                 if (key < RT) {
-                    s = (sh.top[0][key] + sh.top[1][key]) + (sh.top[2][key] + sh.top[3][key]);
-                    if (s > 0.0f || s != s) m = sh.ref[key];  // a NaN sum stays NaN
-                    sh.fa[key] = back = 1.0f / sh.gain[key];  // (powers of two)
+                    s = (hs.top[0][key] + hs.top[1][key]) + (hs.top[2][key] + hs.top[3][key]);
+                    if (s > 0.0f || s != s) m = shift - hs.nref[key];  // a NaN sum stays NaN
+                    hs.corr[key] = back = 1.0f / hs.gain[key];  // (powers of two)
                 }
                 if (ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
                 tc_fence_after();
@@ -738,7 +809,7 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                     // 1 the one that goes on after it.  The part that arrives last joins them, into
                     // its own O, and leaves the counter zero.
                     const int64_t slot = (int64_t)RT * (p.D + 2);
-                    auto part_of = [&](int c) { return p.part + ((int64_t)c * 2 + (c == c0 ? 1 : 0)) * slot; };
+                    auto part_of = [&](int c) { return p.part + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * HV + half) * slot; };
                     float *mine = part_of(part);
                     bar_sync(bar, GT);
                     if (key < RT) {
@@ -749,21 +820,21 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                     for (int h = 0; h < RT; h += 8) {
                         float o[kParts][8];
 #pragma unroll
-                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * RT + h);
+                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * H::kRows + h);
                         tc_wait_ld();
                         if (key < p.D)
 #pragma unroll
-                            for (int r = 0; r < 8; ++r) __stcg(mine + (int64_t)(h + r) * p.D + key, (o[0][r] + o[1][r] + o[2][r]) * sh.fa[h + r]);
+                            for (int r = 0; r < 8; ++r) __stcg(mine + (int64_t)(h + r) * p.D + key, sum_parts(o, r) * hs.corr[h + r]);
                     }
                     bar_sync(bar, GT);
                     if (key == 0) {  // (its fence covers what the barrier has shown it)
                         __threadfence();
-                        sh.last = atomicAdd(p.counters + c0, 1u) == (unsigned)(c1 - c0);
+                        hs.last = atomicAdd(p.counters + c0 * HV + half, 1u) == (unsigned)(c1 - c0);
                         __threadfence();
-                        if (sh.last) p.counters[c0] = 0u;
+                        if (hs.last) p.counters[c0 * HV + half] = 0u;
                     }
                     bar_sync(bar, GT);
-                    write = sh.last;
+                    write = hs.last;
                     if (write) {
                         // m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
                         constexpr int TR = GT / RT;  // threads of a row; parts at a time
@@ -783,7 +854,7 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                             }
                             const float f = rel_weight(mc, mm);
                             ll += lc * f;
-                            (&sh.top[0][0])[k * RT + r] = f;  // (TR * RT of them)
+                            (&hs.top[0][0])[k * RT + r] = f;  // (TR * RT of them)
                             bar_sync(bar, GT);
                             const int some = min(TR, np - c);
 #pragma unroll 1
@@ -798,7 +869,7 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                                 }
 #pragma unroll 2
                                 for (int i = 0; i < some; ++i) {
-                                    const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &sh.top[0][0] + i * RT + h;
+                                    const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &hs.top[0][0] + i * RT + h;
                                     float x[16];
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) x[e] = key < p.D ? __ldcg(q + (int64_t)e * p.D) : 0.0f;
@@ -812,20 +883,20 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
 #pragma unroll
                         for (int o = TR / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(kFull, ll, o);
 #pragma unroll 1
-                        for (int h = RT; h < kParts * RT; h += 16) {
-                            uint32_t z[16] = {};
-                            tc_st16(to + h, z);
+                        for (int c = 1; c < kParts; ++c) {
+                            uint32_t z[RT] = {};
+                            tc_st16(to + c * H::kRows, z);
                         }
                         bar_sync(bar, GT);  // (the weights are done with)
                         if (k == 0) {
-                            sh.top[0][r] = mm;
-                            sh.top[1][r] = ll;
+                            hs.top[0][r] = mm;
+                            hs.top[1][r] = ll;
                         }
                         bar_sync(bar, GT);
                         tc_wait_st();
                         if (key < RT) {
-                            m = sh.top[0][key];
-                            s = sh.top[1][key];
+                            m = hs.top[0][key];
+                            s = hs.top[1][key];
                             back = 1.0f;
                         }
                     }
@@ -850,8 +921,8 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                             if (p.mode == 1) p.pre_lse[row] = lse2;
                             else if (p.lse) p.lse[row] = lse2 * kLn2;
                         }
-                        sh.fa[key] = fa;
-                        sh.fc[key] = fc;
+                        hs.corr[key] = fa;
+                        hs.corr_o[key] = fc;
                     }
                     bar_sync(bar, GT);
                     const bool join = p.mode == 0 && p.P > 0 && done.keys.ok;
@@ -860,16 +931,16 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
                     for (int h = 0; h < RT; h += 8) {
                         float o[kParts][8], sp[8];
 #pragma unroll
-                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * RT + h);
+                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * H::kRows + h);
 #pragma unroll
                         for (int r = 0; r < 8; ++r) sp[r] = join && w.out[h + r] >= 0 && key < p.D ? p.pre_o[w.out[h + r] * p.D + key] : 0.0f;
                         tc_wait_ld();
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {
                             const int64_t row = w.out[h + r], at = row * p.D + key;
-                            const float f = sh.fa[h + r];
-                            float x = f == 0.0f ? 0.0f : (o[0][r] + o[1][r] + o[2][r]) * f;
-                            if (join) x = fmaf(sp[r], sh.fc[h + r], x);
+                            const float f = hs.corr[h + r];
+                            float x = f == 0.0f ? 0.0f : sum_parts(o, r) * f;
+                            if (join) x = fmaf(sp[r], hs.corr_o[h + r], x);
                             if (row >= 0 && key < p.D) {
                                 if (p.mode == 1) p.pre_o[at] = x;
                                 else static_cast<T *>(p.out)[at] = __float2bfloat16(x);
@@ -894,15 +965,17 @@ __global__ void __launch_bounds__(128 * kTeams + 128, 1)
 }
 
 // ---- host ------------------------------------------------------------------
-template <int NH, int RT, bool PLAIN> cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
-    constexpr int smem = (int)sizeof(Tc8Smem<NH, RT>) + 1024;
+template <int NH, int HV, bool PLAIN> cudaError_t launch(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
+    constexpr int smem = (int)sizeof(Tc8Smem<NH, HV>) + 1024;
     static_assert(smem <= 227 * 1024 && smem > 114 * 1024, "one block an SM: it takes all of TMEM");
-    static_assert(kTeams * RT <= kAttnSlotRows && kTeams * kAttnSmsMax <= kAttnBlocksMax, "partial results of the teams");
-    cudaError_t e = cudaFuncSetAttribute(attn8_tc_kernel<NH, RT, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    using H = Team8<NH, HV>;
+    static_assert(H::kTeams * H::kRows <= kAttnSlotRows && H::kTeams * HV * kAttnSmsMax <= kAttnBlocksMax, "partial results of the teams");
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = ensure_smem_attr(attn8_tc_kernel<NH, HV, PLAIN>, smem, done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(sms < kAttnSmsMax ? sms : kAttnSmsMax));
-    cfg.blockDim = dim3(128 * kTeams + 128);
+    cfg.blockDim = dim3((threads_of<NH, HV>()));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute at;
@@ -910,14 +983,17 @@ template <int NH, int RT, bool PLAIN> cudaError_t launch(const AttnParams &p, co
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = p.mode == 0 && p.P > 0 ? 1 : 0;  // after the shared pass
-    return cudaLaunchKernelEx(&cfg, attn8_tc_kernel<NH, RT, PLAIN>, p, cm);
+    return cudaLaunchKernelEx(&cfg, attn8_tc_kernel<NH, HV, PLAIN>, p, cm);
 }
 
 template <int NH> cudaError_t launch_nh(const AttnParams &p, const CUtensorMap &cm, int sms, cudaStream_t s) {
     const int64_t rows = p.mode == 1 ? (int64_t)p.B * p.S * p.G : (int64_t)p.S * p.G;
     const bool plain = p.score.cap == 0.0f && !p.score.bias;
-    if (plain) return rows <= 16 ? launch<NH, 16, true>(p, cm, sms, s) : launch<NH, 32, true>(p, cm, sms, s);
-    return rows <= 16 ? launch<NH, 16, false>(p, cm, sms, s) : launch<NH, 32, false>(p, cm, sms, s);
+    auto go = [&](auto hv) {
+        constexpr int HV = decltype(hv)::value;
+        return plain ? launch<NH, HV, true>(p, cm, sms, s) : launch<NH, HV, false>(p, cm, sms, s);
+    };
+    return rows <= RT ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 2>{});
 }
 
 }  // namespace

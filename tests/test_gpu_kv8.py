@@ -280,6 +280,65 @@ def test_commit_bad_requests_stay_as_they_are():
     assert np.array_equal(off_gpu(cache)[0], codes) and np.array_equal(off_gpu(cache)[1], scale)
 
 
+def test_calls_on_two_streams_and_in_graphs():
+    """Two layers written, committed and read at once, eagerly and in a graph each,
+    give what one call after the other gives."""
+    B, S, H, D, bs = 6, 13, 4, 64, 16
+    rng, g = np.random.default_rng(8), torch.Generator(device="cuda").manual_seed(8)
+    lens = rng.integers(0, 60, B).tolist()
+    table, nb, _ = tables(rng, [n + S for n in lens], bs)
+    table, slots = i32(table), i32([[0, 2, 5] + [-1] * 10] * B)
+    x = [torch.randn((2, B, S, H, D), generator=g, device="cuda") for _ in range(2)]
+    caches = [api.quant_kv(2, nb, bs, H, D) for _ in range(2)]
+    starts = [i32(lens) for _ in range(2)]
+
+    def round_(i, stream=None):
+        kw = dict(block_size=bs, stream=stream)
+        for layer in (0, 1):
+            api.write_kv_q8(x[i][0], x[i][1], caches[i], table, starts[i], layer=layer, **kw)
+        api.commit_kv_q8(caches[i], table, slots, i32([3] * B) if stream is None else n3, starts[i], **kw)
+        return api.read_kv_q8(caches[i], table, n_max=60, layer=1, **kw)
+
+    n3 = i32([3] * B)
+    want = []
+    for i in (0, 1):
+        r = round_(i)
+        want.append((off_gpu(caches[i]), r.k.clone(), r.v.clone(), starts[i].tolist()))
+
+    def reset():
+        for i in (0, 1):
+            caches[i].codes.view(torch.uint8).zero_()
+            caches[i].scale.zero_()
+            starts[i].copy_(i32(lens))
+
+    def check(i, r):
+        got = off_gpu(caches[i])
+        assert np.array_equal(got[0], want[i][0][0]) and np.array_equal(got[1], want[i][0][1])
+        assert torch.equal(r.k, want[i][1]) and torch.equal(r.v, want[i][2]) and starts[i].tolist() == want[i][3]
+
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        reset()
+        torch.cuda.synchronize()
+        r = [round_(i, streams[i]) for i in (0, 1)]
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            check(i, r[i])
+    graphs, held = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for i in (0, 1):
+        with torch.cuda.graph(graphs[i], stream=streams[i]):
+            held.append(round_(i, streams[i]))
+    for _ in range(3):
+        reset()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            with torch.cuda.stream(streams[1 - i]):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            check(i, held[i])
+
+
 # ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
@@ -369,7 +428,7 @@ def test_shapes(i, dtype):
     dict(gaps=True, window=50, slopes=True), dict(gaps=True, docs=0.7, cap=2.0),
     dict(tree=True, window=2, docs=0.99), dict(cap=30.0, slopes=True, window=100, docs=0.3, tree=True, gaps=True),
     dict(window=7), dict(tree=True, gaps=True, slopes=True), dict(layers=3, layer=2, spare=40), dict(spread=12.0),
-    dict(spread=40.0, cap=3.0)])
+    dict(spread=40.0, cap=3.0), dict(cap=1024.0), dict(cap=1000.0, slopes=True, gaps=True)])
 def test_scores_and_masks(kw, dtype):
     for G in (3, 9, 20):                                 # 18, 54 and 120 rows
         c = Case8([5, 64, 200, 131, 0 if not kw.get("gaps") else 1, 700], S=6, H=2, G=G, D=64, dtype=dtype, seed=3, **kw)
@@ -440,6 +499,23 @@ def test_a_nan_v_shows_in_the_rows_that_see_it(dtype, G, bs):
         c.scales[0, 1, c.table[1, 200 // bs], 0, 200 % bs] = 255
         r = c.run()
         assert torch.isnan(r.out[1]).all() and torch.equal(r.lse, clean.lse) and torch.equal(r.out[0, 0], clean.out[0, 0])
+
+
+@pytest.mark.parametrize("dtype,G,bs", KERNELS)
+def test_hidden_rows_of_the_largest_powers(dtype, G, bs):
+    """Entries whose exponent is 254, before the document and in other branches,
+    change nothing for the rows that do not see them."""
+    kw = dict(S=6, H=2, G=G, D=64, bs=bs, tree=True, docs=0.5, dtype=dtype, seed=9)
+    clean, c = Case8([70, 300], **kw), Case8([70, 300], **kw)
+    want = clean.run()
+    for b, n in enumerate(c.lens):
+        for e in list(range(int(c.first[b]))) + [n + 5]:
+            c.scales[0, :, c.table[b, e // bs], :, e % bs] = 254
+    r = c.run()
+    # (scores of at most a few units rounded once more; the weights' roundings differ)
+    assert (r.lse[:, :5] - want.lse[:, :5]).abs().max() <= 2.0 ** -18
+    tol = 2.0 ** -7 if dtype == "bf16" else 2.0 ** -20
+    assert (r.out[:, :5].float() - want.out[:, :5].float()).abs().max() <= tol * float(clean.cache[0, 1].abs().max())
 
 
 @pytest.mark.parametrize("dtype,G,bs", KERNELS)
