@@ -32,18 +32,18 @@
 //     hidden from see nothing.
 //
 // What bounds it.  Single queries on up to 32,768 entries, 64 requests, 8 heads of 128:
-// 376 us, 5.9 TB/s of the 6.65 that a copy reaches.  64 requests of 5 queries x group 4
-// on 2,048 entries: 91 us (3.0 TB/s; the tiles themselves run at 6.2): a team's start
-// (13 us) and each change of items (14 us: the next queries, partial results, the
-// first tile's references) run code that is in no cache any more and comes from far
-// away, one miss of some 1,000 clk after another.  That is why the rest is short: 16 rows a
-// thread (32, with the loops twice as long: 8 x 5 queries on 40 entries 15.1 us
-// instead of 12.9, a shared prefix of 4,096 entries 137 instead of 130; only a capped
-// tree, 52 rows, was faster so: 314 instead of 325), and why K and V ask L2 to let go
-// of them first (single queries 406 -> 388 us, the chain 92 -> 89).  128 x 13 queries x group 4
-// on 2,048 entries, capped and biased, 325 us: bound by the softmax's instructions
-// (30 a weight; 46 % of the issue slots) and the second reading of keys for the rows
-// past 32; one tile of 64 rows, its threads at 96 registers, was no faster (326).
+// 376 to 390 us by the GPU, up to 5.9 TB/s of the 6.65 that a copy reaches.  64 requests of
+// 5 queries x group 4 on 2,048 entries: 88 us (3.2 TB/s; the tiles themselves run at 6.2):
+// a team's start (13 us) and each change of items (some 12 us: the next queries, partial
+// results, the first tile's references) run code that is in no cache any more and comes
+// from far away, one miss of some 1,000 clk after another.  That is why the rest is short:
+// 16 rows a thread (32, with the loops twice as long: 8 x 5 queries on 40 entries 15.1 us
+// instead of 13, a shared prefix of 4,096 entries 137 instead of 130), one place for the
+// queries of an item, the first or a later one (chain 91 -> 88 us, tree 324 -> 312), and why
+// K and V ask L2 to let go of them first (single queries 406 -> 388 us, the chain 92 -> 89).
+// 128 x 13 queries x group 4 on 2,048 entries, capped and biased, 312 us: bound by the
+// softmax's instructions (30 a weight; half of the issue slots) and the second reading of
+// keys for the rows past 32; one tile of 64 rows, its threads at 96 registers, was no faster.
 //
 // The MMAs: an MMA of 128 x N x 32 takes 32 + N/4 clk, and 54 at least if its thread is
 // not an elected one (the operands are then moved to uniform registers each time);
@@ -462,8 +462,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                     hs.gain[key] = pow2i(127 + kUp - kPowMin);
                 }
             };
-            // An item's rows and queries: 8 elements a thread at a time.  The next item's are
-            // prepared before this one's output.
+            // An item's rows and queries: 8 elements a thread at a time.
             auto prepare = [&](int turn) {
                 AttnRows<RT> &w = hs.rows[turn];
                 AttnItem of = it;
@@ -522,9 +521,184 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                 team_sync();
                 mbar_arrive(&sh.q_full);
             };
-            start_rows();
-            prepare(0);
-            while (true) {
+            // An item's turn: its queries, the output of the item before, its tiles.
+            AttnItem done = it;
+            float l[RT];                         // sums of this thread's weights
+            for (bool more = true;; ++item) {
+                if (more) prepare(item & 1);
+                if (item > 0) {
+                    const AttnRows<RT> &w = hs.rows[(item & 1) ^ 1];
+                    reduce_rows<RT>(l, [](float a, float b) { return a + b; });
+                    if ((lane & 1) == 0) hs.top[wq][lane >> 1] = l[0];
+                    // the shared part's results are there, and its partial results done with
+                    // (no wait but after a shared pass, whose end this kernel's start overlaps)
+                    if (item == 1) pdl_wait_primary();
+                    // the item's parts: this one alone, or [c0, c1]
+                    int c0 = part, c1 = part;
+                    if (done.u0 < part * share || done.u0 + done.ntiles > part * share + share) {
+                        c0 = (int)(done.u0 / share);
+                        c1 = (int)((done.u0 + done.ntiles - 1) / share);
+                    }
+                    bar_sync(bar, GT);
+                    float s = 0.0f, m = -INFINITY, back = 1.0f;  // of row `key`: sum, reference, what O is divided by
+                    if (key < RT) {
+                        s = (hs.top[0][key] + hs.top[1][key]) + (hs.top[2][key] + hs.top[3][key]);
+                        if (s > 0.0f || s != s) m = shift - hs.nref[key];  // a NaN sum stays NaN
+                        hs.corr[key] = back = 1.0f / hs.gain[key];  // (powers of two)
+                    }
+                    if (ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
+                    tc_fence_after();
+                    bool write = true;
+                    if (c0 != c1) {
+                        // Part c's results: slot 0 of a part holds the item that began before it, slot
+                        // 1 the one that goes on after it.  The part that arrives last joins them, into
+                        // its own O, and leaves the counter zero.
+                        const int64_t slot = (int64_t)RT * (p.D + 2);
+                        auto part_of = [&](int c) { return p.part + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * HV + half) * slot; };
+                        float *mine = part_of(part);
+                        bar_sync(bar, GT);
+                        if (key < RT) {
+                            __stcg(mine + (int64_t)RT * p.D + key, m);
+                            __stcg(mine + (int64_t)RT * p.D + RT + key, s);
+                        }
+#pragma unroll
+                        for (int h = 0; h < RT; h += 8) {
+                            float o[kParts][8];
+#pragma unroll
+                            for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * H::kRows + h);
+                            tc_wait_ld();
+                            if (key < p.D)
+#pragma unroll
+                                for (int r = 0; r < 8; ++r) __stcg(mine + (int64_t)(h + r) * p.D + key, sum_parts(o, r) * hs.corr[h + r]);
+                        }
+                        bar_sync(bar, GT);
+                        if (key == 0) {  // (its fence covers what the barrier has shown it)
+                            __threadfence();
+                            hs.last = atomicAdd(p.counters + c0 * HV + half, 1u) == (unsigned)(c1 - c0);
+                            __threadfence();
+                            if (hs.last) p.counters[c0 * HV + half] = 0u;
+                        }
+                        bar_sync(bar, GT);
+                        write = hs.last;
+                        if (write) {
+                            // m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
+                            constexpr int TR = GT / RT;  // threads of a row; parts at a time
+                            const int r = key / TR, k = key % TR, np = c1 - c0 + 1;
+                            auto of_row = [&](int c) { return part_of(c0 + c) + (int64_t)RT * p.D + r; };
+                            float mc = k < np ? __ldcg(of_row(k)) : -INFINITY, lc = k < np ? __ldcg(of_row(k) + RT) : 0.0f, mm = mc;
+                            for (int c = k + TR; c < np; c += TR) mm = fmaxf(mm, __ldcg(of_row(c)));
+#pragma unroll
+                            for (int o = TR / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, o));
+                            float ll = 0.0f;
+#pragma unroll 1
+                            for (int c = 0; c < np; c += TR) {
+                                if (c > 0) {
+                                    mc = c + k < np ? __ldcg(of_row(c + k)) : -INFINITY;
+                                    lc = c + k < np ? __ldcg(of_row(c + k) + RT) : 0.0f;
+                                    bar_sync(bar, GT);
+                                }
+                                const float f = rel_weight(mc, mm);
+                                ll += lc * f;
+                                (&hs.top[0][0])[k * RT + r] = f;  // (TR * RT of them)
+                                bar_sync(bar, GT);
+                                const int some = min(TR, np - c);
+#pragma unroll 1
+                                for (int h = 0; h < RT; h += 16) {
+                                    float o[16];
+                                    if (c > 0) {
+                                        tc_ld16(o, to + h);
+                                        tc_wait_ld();
+                                    } else {
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) o[e] = 0.0f;
+                                    }
+#pragma unroll 2
+                                    for (int i = 0; i < some; ++i) {
+                                        const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &hs.top[0][0] + i * RT + h;
+                                        float x[16];
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e) x[e] = key < p.D ? __ldcg(q + (int64_t)e * p.D) : 0.0f;
+#pragma unroll
+                                        for (int e = 0; e < 16; ++e)
+                                            if (g[e] != 0.0f) o[e] = fmaf(x[e], g[e], o[e]);
+                                    }
+                                    tc_st16(to + h, reinterpret_cast<const uint32_t *>(o));
+                                }
+                            }
+#pragma unroll
+                            for (int o = TR / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(kFull, ll, o);
+#pragma unroll 1
+                            for (int c = 1; c < kParts; ++c) {
+                                uint32_t z[RT] = {};
+                                tc_st16(to + c * H::kRows, z);
+                            }
+                            bar_sync(bar, GT);  // (the weights are done with)
+                            if (k == 0) {
+                                hs.top[0][r] = mm;
+                                hs.top[1][r] = ll;
+                            }
+                            bar_sync(bar, GT);
+                            tc_wait_st();
+                            if (key < RT) {
+                                m = hs.top[0][key];
+                                s = hs.top[1][key];
+                                back = 1.0f;
+                            }
+                        }
+                    }
+                    if (write) {
+                        if (key < RT) {
+                            const int64_t row = w.out[key];
+                            float fa = 0.0f, fc = 0.0f;
+                            if (row >= 0) {
+                                float lse2 = s > 0.0f || s != s ? m + lg2f(s) : -INFINITY;
+                                fa = back;
+                                if (p.mode == 0 && p.P > 0 && done.keys.ok) {
+                                    const float lp = p.pre_lse[row], mm = fmaxf(m, lp), a = rel_weight(m, mm), c = lp != lp ? lp : rel_weight(lp, mm);
+                                    s = s * a + c;
+                                    lse2 = s > 0.0f || s != s ? mm + lg2f(s) : -INFINITY;
+                                    fa *= a;
+                                    fc = c;
+                                }
+                                const float inv = lse2 == -INFINITY ? 0.0f : 1.0f / s;
+                                fa *= inv;
+                                fc *= inv;
+                                if (p.mode == 1) p.pre_lse[row] = lse2;
+                                else if (p.lse) p.lse[row] = lse2 * kLn2;
+                            }
+                            hs.corr[key] = fa;
+                            hs.corr_o[key] = fc;
+                        }
+                        bar_sync(bar, GT);
+                        const bool join = p.mode == 0 && p.P > 0 && done.keys.ok;
+                        // (code that runs once an item stays short: it comes from far away)
+#pragma unroll 1
+                        for (int h = 0; h < RT; h += 8) {
+                            float o[kParts][8], sp[8];
+#pragma unroll
+                            for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * H::kRows + h);
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) sp[r] = join && w.out[h + r] >= 0 && key < p.D ? p.pre_o[w.out[h + r] * p.D + key] : 0.0f;
+                            tc_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) {
+                                const int64_t row = w.out[h + r], at = row * p.D + key;
+                                const float f = hs.corr[h + r];
+                                float x = f == 0.0f ? 0.0f : sum_parts(o, r) * f;
+                                if (join) x = fmaf(sp[r], hs.corr_o[h + r], x);
+                                if (row >= 0 && key < p.D) {
+                                    if (p.mode == 1) p.pre_o[at] = x;
+                                    else static_cast<T *>(p.out)[at] = __float2bfloat16(x);
+                                }
+                            }
+                        }
+                    }
+                    tc_fence_before();
+                }
+                if (!more) break;
+                bar_sync(bar, GT);  // (the references and factors are done with)
+                start_rows();
+                bar_sync(bar, GT);
                 const AttnRows<RT> &w = hs.rows[item & 1];
                 const int t0 = (int)(u - it.u0), t1 = (int)(min(uend, it.u0 + it.ntiles) - it.u0);
                 const KeyLine line = it.keys.ok ? attn_line(p, it.keys) : KeyLine{0, 0};
@@ -532,7 +706,6 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                 const int qp0 = hs.qp0;
                 const int low_max = max(hs.low_max[item & 1], sh.half[HV - 1 - half].low_max[item & 1]);  // (every row's)
                 int pow_min = 0;                 // the smallest of the rows' largest powers
-                float l[RT];                     // sums of this thread's weights
 #pragma unroll
                 for (int r = 0; r < RT; ++r) l[r] = 0.0f;
                 // position of this thread's key of tile t, when key_pos is given: read a tile ahead
@@ -775,185 +948,10 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                     tc_fence_before();
                     mbar_arrive(&sh.p_full);
                 }
-                // ---- the item's end: the next one's queries, then this one's output
-                const AttnItem done = it;
-                const int64_t end = it.u0 + it.ntiles;
-                u = end;
-                if (end < uend) {
-                    next_item(p, it, items, rtiles);
-                    prepare(item & 1 ^ 1);
-                }
-                reduce_rows<RT>(l, [](float a, float b) { return a + b; });
-                if ((lane & 1) == 0) hs.top[wq][lane >> 1] = l[0];
-                // the shared part's results are there, and its partial results done with
-                // (no wait but after a shared pass, whose end this kernel's start overlaps)
-                if (item == 0) pdl_wait_primary();
-                // the item's parts: this one alone, or [c0, c1]
-                int c0 = part, c1 = part;
-                if (done.u0 < part * share || end > part * share + share) {
-                    c0 = (int)(done.u0 / share);
-                    c1 = (int)((end - 1) / share);
-                }
-                bar_sync(bar, GT);
-                float s = 0.0f, m = -INFINITY, back = 1.0f;  // of row `key`: sum, reference, what O is divided by
-                if (key < RT) {
-                    s = (hs.top[0][key] + hs.top[1][key]) + (hs.top[2][key] + hs.top[3][key]);
-                    if (s > 0.0f || s != s) m = shift - hs.nref[key];  // a NaN sum stays NaN
-                    hs.corr[key] = back = 1.0f / hs.gain[key];  // (powers of two)
-                }
-                if (ok) ok = attn_wait(&sh.pv_done, (unsigned)((n - 1) & 1));
-                tc_fence_after();
-                bool write = true;
-                if (c0 != c1) {
-                    // Part c's results: slot 0 of a part holds the item that began before it, slot
-                    // 1 the one that goes on after it.  The part that arrives last joins them, into
-                    // its own O, and leaves the counter zero.
-                    const int64_t slot = (int64_t)RT * (p.D + 2);
-                    auto part_of = [&](int c) { return p.part + (((int64_t)c * 2 + (c == c0 ? 1 : 0)) * HV + half) * slot; };
-                    float *mine = part_of(part);
-                    bar_sync(bar, GT);
-                    if (key < RT) {
-                        __stcg(mine + (int64_t)RT * p.D + key, m);
-                        __stcg(mine + (int64_t)RT * p.D + RT + key, s);
-                    }
-#pragma unroll
-                    for (int h = 0; h < RT; h += 8) {
-                        float o[kParts][8];
-#pragma unroll
-                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * H::kRows + h);
-                        tc_wait_ld();
-                        if (key < p.D)
-#pragma unroll
-                            for (int r = 0; r < 8; ++r) __stcg(mine + (int64_t)(h + r) * p.D + key, sum_parts(o, r) * hs.corr[h + r]);
-                    }
-                    bar_sync(bar, GT);
-                    if (key == 0) {  // (its fence covers what the barrier has shown it)
-                        __threadfence();
-                        hs.last = atomicAdd(p.counters + c0 * HV + half, 1u) == (unsigned)(c1 - c0);
-                        __threadfence();
-                        if (hs.last) p.counters[c0 * HV + half] = 0u;
-                    }
-                    bar_sync(bar, GT);
-                    write = hs.last;
-                    if (write) {
-                        // m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
-                        constexpr int TR = GT / RT;  // threads of a row; parts at a time
-                        const int r = key / TR, k = key % TR, np = c1 - c0 + 1;
-                        auto of_row = [&](int c) { return part_of(c0 + c) + (int64_t)RT * p.D + r; };
-                        float mc = k < np ? __ldcg(of_row(k)) : -INFINITY, lc = k < np ? __ldcg(of_row(k) + RT) : 0.0f, mm = mc;
-                        for (int c = k + TR; c < np; c += TR) mm = fmaxf(mm, __ldcg(of_row(c)));
-#pragma unroll
-                        for (int o = TR / 2; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(kFull, mm, o));
-                        float ll = 0.0f;
-#pragma unroll 1
-                        for (int c = 0; c < np; c += TR) {
-                            if (c > 0) {
-                                mc = c + k < np ? __ldcg(of_row(c + k)) : -INFINITY;
-                                lc = c + k < np ? __ldcg(of_row(c + k) + RT) : 0.0f;
-                                bar_sync(bar, GT);
-                            }
-                            const float f = rel_weight(mc, mm);
-                            ll += lc * f;
-                            (&hs.top[0][0])[k * RT + r] = f;  // (TR * RT of them)
-                            bar_sync(bar, GT);
-                            const int some = min(TR, np - c);
-#pragma unroll 1
-                            for (int h = 0; h < RT; h += 16) {
-                                float o[16];
-                                if (c > 0) {
-                                    tc_ld16(o, to + h);
-                                    tc_wait_ld();
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) o[e] = 0.0f;
-                                }
-#pragma unroll 2
-                                for (int i = 0; i < some; ++i) {
-                                    const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &hs.top[0][0] + i * RT + h;
-                                    float x[16];
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e) x[e] = key < p.D ? __ldcg(q + (int64_t)e * p.D) : 0.0f;
-#pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        if (g[e] != 0.0f) o[e] = fmaf(x[e], g[e], o[e]);
-                                }
-                                tc_st16(to + h, reinterpret_cast<const uint32_t *>(o));
-                            }
-                        }
-#pragma unroll
-                        for (int o = TR / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(kFull, ll, o);
-#pragma unroll 1
-                        for (int c = 1; c < kParts; ++c) {
-                            uint32_t z[RT] = {};
-                            tc_st16(to + c * H::kRows, z);
-                        }
-                        bar_sync(bar, GT);  // (the weights are done with)
-                        if (k == 0) {
-                            hs.top[0][r] = mm;
-                            hs.top[1][r] = ll;
-                        }
-                        bar_sync(bar, GT);
-                        tc_wait_st();
-                        if (key < RT) {
-                            m = hs.top[0][key];
-                            s = hs.top[1][key];
-                            back = 1.0f;
-                        }
-                    }
-                }
-                if (write) {
-                    if (key < RT) {
-                        const int64_t row = w.out[key];
-                        float fa = 0.0f, fc = 0.0f;
-                        if (row >= 0) {
-                            float lse2 = s > 0.0f || s != s ? m + lg2f(s) : -INFINITY;
-                            fa = back;
-                            if (p.mode == 0 && p.P > 0 && done.keys.ok) {
-                                const float lp = p.pre_lse[row], mm = fmaxf(m, lp), a = rel_weight(m, mm), c = lp != lp ? lp : rel_weight(lp, mm);
-                                s = s * a + c;
-                                lse2 = s > 0.0f || s != s ? mm + lg2f(s) : -INFINITY;
-                                fa *= a;
-                                fc = c;
-                            }
-                            const float inv = lse2 == -INFINITY ? 0.0f : 1.0f / s;
-                            fa *= inv;
-                            fc *= inv;
-                            if (p.mode == 1) p.pre_lse[row] = lse2;
-                            else if (p.lse) p.lse[row] = lse2 * kLn2;
-                        }
-                        hs.corr[key] = fa;
-                        hs.corr_o[key] = fc;
-                    }
-                    bar_sync(bar, GT);
-                    const bool join = p.mode == 0 && p.P > 0 && done.keys.ok;
-                    // (code that runs once an item stays short: it comes from far away)
-#pragma unroll 1
-                    for (int h = 0; h < RT; h += 8) {
-                        float o[kParts][8], sp[8];
-#pragma unroll
-                        for (int c = 0; c < kParts; ++c) tc_ld8(o[c], to + c * H::kRows + h);
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) sp[r] = join && w.out[h + r] >= 0 && key < p.D ? p.pre_o[w.out[h + r] * p.D + key] : 0.0f;
-                        tc_wait_ld();
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            const int64_t row = w.out[h + r], at = row * p.D + key;
-                            const float f = hs.corr[h + r];
-                            float x = f == 0.0f ? 0.0f : sum_parts(o, r) * f;
-                            if (join) x = fmaf(sp[r], hs.corr_o[h + r], x);
-                            if (row >= 0 && key < p.D) {
-                                if (p.mode == 1) p.pre_o[at] = x;
-                                else static_cast<T *>(p.out)[at] = __float2bfloat16(x);
-                            }
-                        }
-                    }
-                }
-                tc_fence_before();
-                if (u >= uend) break;
-                bar_sync(bar, GT);  // (the references and factors are done with)
-                start_rows();
-                bar_sync(bar, GT);
-                ++item;
+                done = it;
+                u = it.u0 + it.ntiles;
+                more = u < uend;
+                if (more) next_item(p, it, items, rtiles);
             }
         }
     }
