@@ -226,6 +226,11 @@ def _stream(stream) -> c_void_p:
     return c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def current_raw_stream(index: int) -> int:
+    """Handle of the device's current stream (a torch.cuda.Stream object costs 3 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype == torch.bfloat16:
         return SPEC_DTYPE_BF16
@@ -518,8 +523,8 @@ def _launch(fn: str, args, workspace: torch.Tensor, device, stream) -> None:
     if workspace.device != device:
         raise ValueError(f"{fn}: the workspace is on {workspace.device}, not {device}")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        stream = current_raw_stream(device.index)
+    raw = stream if type(stream) is int else stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     call = getattr(lib(), fn)
     if torch.cuda.current_device() == device.index:
         code = call(args, workspace.data_ptr(), workspace.numel(), raw)

@@ -210,11 +210,14 @@ def commit_kv(temp_kv: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
                      slots=slots, blocks_in_use=blocks_in_use, flags=flags, stream=stream)
 
 
+_NO_CONTEXT = nullcontext()
+
+
 def _allocating_on(stream):
     """Context in which outputs and a first workspace are allocated (and the
     workspace zeroed) on the stream the call runs on."""
     if stream is None:
-        return nullcontext()
+        return _NO_CONTEXT
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
@@ -223,7 +226,8 @@ def _stream_of(stream, t: torch.Tensor):
     if stream is None:
         if not t.is_cuda:  # (the call refuses it)
             return None, 0
-        stream = torch.cuda.current_stream(t.device)
+        raw = L.current_raw_stream(t.get_device())
+        return raw, raw
     return stream, stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
