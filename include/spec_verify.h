@@ -741,8 +741,8 @@ int spec_write_kv_q8(const SpecWriteKvQ8Args *args, void *workspace, size_t work
  * A K row that stands for NaN makes the rows that see it NaN (out and lse), a V
  *   row that does their out; a row with a NaN code may read as all NaN.  A query
  *   that holds a value that is not finite gets NaN where it sees a key.
- * Arithmetic: f32 sums and softmax statistics.  bf16 calls with D <= 128 on pages
- *   of a multiple of 8 entries multiply on the tensor cores: a query, scaled by a
+ * Arithmetic: f32 sums and softmax statistics.  bf16 calls with D <= 128 (and
+ *   fewer than 2^30 cache entries a layer) multiply on the tensor cores: a query, scaled by a
  *   power of two, as the sum of two e4m3 numbers (off by at most 2^-17 of the
  *   query's largest element), K's codes as they are, the softmax weights times
  *   V's powers of two as the sum of three e5m2 numbers (off by at most 2^-8 of a

@@ -1,5 +1,5 @@
 // Attention over the 8-bit paged cache on the CUDA cores: float32 queries, heads
-// above 128, pages that are not multiples of 8 entries (the others: attn8_tc.cu).
+// above 128 (the others: attn8_tc.cu).
 //
 // The float32 kernel's scheme (attn_simt.cu): a block holds 16 or 32 queries, a
 // quarter of them a warp, and 32 keys at a time; for the scores a lane has a key,
@@ -8,7 +8,9 @@
 // are multiplied, once for all of the warp's queries.  A key's power of two goes
 // into its score and, for V, into its softmax weight: both exact.
 //
-// Bound by issue.
+// Bound by issue (55 % of the slots, a fifth of the stalls on shared memory): 64 requests
+// of 5 queries x group 4 on 2,048 entries, 8 heads of 128, f32: 657 us, 16.4 TFLOP/s; heads
+// of 256, bf16: 1,266 us, 17.0.
 #include "attention.cuh"
 #include "kv8.cuh"
 #include "tma.cuh"

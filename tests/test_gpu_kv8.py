@@ -411,6 +411,8 @@ SHAPES = [
     dict(lens=[131, 5], S=300, H=1, G=1, D=64, bs=8),
     dict(lens=[200, 60], S=7, H=2, G=2, D=64, bs=128), dict(lens=[90], S=4, H=1, G=2, D=128, bs=24),
     dict(lens=[77, 300], S=4, H=2, G=2, D=32), dict(lens=[77, 300], S=4, H=2, G=2, D=48), dict(lens=[77, 300], S=4, H=3, G=2, D=96),
+    dict(lens=[77, 300, 1], S=5, H=3, G=4, D=80, bs=4), dict(lens=[600, 300], S=1, H=2, G=4, D=128, bs=12),
+    dict(lens=[900, 5, 131], S=7, H=2, G=8, D=48, bs=20, tree=True), dict(lens=[1500, 1], S=3, H=2, G=2, D=16, bs=1),
     dict(lens=[77, 300], S=9, H=3, G=4, D=112, bs=8), dict(lens=[2000, 33], S=9, H=3, G=4, D=80),
 ]
 
@@ -452,8 +454,8 @@ def test_shared_prefix(kw, dtype):
     c.check(c.run())
 
 
-# 32, 64 and 128 rows on pages of whole boxes, and the CUDA cores
-KERNELS = [("bf16", 2, 16), ("bf16", 8, 16), ("bf16", 16, 16), ("bf16", 2, 5), ("f32", 8, 16)]
+# one half, two halves, more row tiles; pages of whole boxes, of fours, of any size; the CUDA cores
+KERNELS = [("bf16", 2, 16), ("bf16", 8, 16), ("bf16", 16, 16), ("bf16", 2, 5), ("bf16", 4, 12), ("f32", 8, 16)]
 
 
 @pytest.mark.parametrize("dtype,G,bs", KERNELS)
@@ -640,6 +642,22 @@ def _without(c, b, gone):
     off[:, list(gone)] = True
     c.table = kept
     return O.attend(c.q[b].double().numpy(), k, v, qp, kp, off, slopes=c.slopes, **c.score), k, off
+
+
+@pytest.mark.parametrize("bs", [16, 4])
+def test_exponents_on_any_address(bs):
+    c = Case8([700, 33, 0], S=5, H=2, G=4, D=64, bs=bs, seed=21)
+    want = c.run()
+    c.check(want)
+    scale = torch.from_numpy(c.scales).cuda()
+    for at in (1, 2, 4):
+        held = torch.empty(scale.numel() + 8, dtype=torch.uint8, device="cuda")[at:at + scale.numel()].view(scale.shape)
+        held.copy_(scale)
+        pos, a = c.args()
+        a.pop("temp_kv")
+        r = api.verify_attention_q8(pos[0], api.QuantKV(on_gpu(c.codes, c.scales).codes, held), *pos[2:], **a)
+        c.check(r)
+        assert at < 4 or torch.equal(r.out, want.out)
 
 
 @pytest.mark.parametrize("kw", [dict(G=2), dict(G=8), dict(G=20), dict(G=4, bs=5), dict(G=2, shared=128, lens=[128, 300, 700])])
