@@ -50,8 +50,9 @@
 // keys for the rows past 32; one tile of 64 rows, its threads at 96 registers, was no faster.
 //
 // The MMAs: an MMA of 128 x N x 32 takes 32 + N/4 clk, and 54 at least if its thread is
-// not an elected one (the operands are then moved to uniform registers each time);
-// a page's box of 16 rows of 128 bytes some 119 clk of the copy engine.
+// not an elected one (the operands are then moved to uniform registers each time).
+// Larger pages come in larger boxes: single queries on pages of 64 entries 361 us, of
+// 128 355.
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
