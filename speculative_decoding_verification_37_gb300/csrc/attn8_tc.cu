@@ -678,6 +678,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                                     }
                                     tc_st16(to + h, reinterpret_cast<const uint32_t *>(o));
                                 }
+                                tc_wait_st();  // (the next parts' sums begin with a load of these)
                             }
 #pragma unroll
                             for (int o = TR / 2; o > 0; o >>= 1) ll += __shfl_xor_sync(kFull, ll, o);

@@ -1,0 +1,32 @@
+"""The attention over the 8-bit cache where an item's keys lie in many blocks, and
+where its tiles' notes, copies and partial results go round their buffers often."""
+import pytest
+import torch
+
+from test_gpu_kv8 import Case8
+
+pytestmark = pytest.mark.gpu
+
+
+# tiles of 128 keys, at most one a part: 9, 16, 17 and 33 parts an item
+@pytest.mark.parametrize("n", [1100, 2040, 2100, 4190])
+@pytest.mark.parametrize("G,bs", [(2, 16), (8, 16), (2, 5), (8, 12)])
+def test_items_of_many_parts(n, G, bs):
+    """A small batch's items split over more parts than are joined at a time (8): the
+    oracle's results, and the same bits every time."""
+    c = Case8([n], S=4, H=2, G=G, D=128, bs=bs, seed=n)
+    want = c.run()
+    c.check(want)
+    for _ in range(10):
+        r = c.run()
+        assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
+
+
+@pytest.mark.parametrize("G,bs", [(2, 16), (8, 16), (8, 5)])
+def test_a_shared_prefix_of_many_parts(G, bs):
+    c = Case8([2311, 2304, 2400], S=2, H=1, G=G, D=64, bs=bs, seed=3, shared=2304)
+    want = c.run()
+    c.check(want)
+    for _ in range(10):
+        r = c.run()
+        assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
