@@ -199,6 +199,7 @@ struct Rows8 {
                                                      // end: O and the shared part); what weights are at a power of 1
     alignas(16) float top[4][RT];                    // the warps' largest scores; at the end sums of weights
     alignas(16) int pow[4][RT];                      // and powers
+    alignas(16) float join[GT / RT][RT];             // at a join: weights of some parts (a thread has a part and a row)
     alignas(16) float cf[RT];                        // what a product is multiplied by for log2 units or the cap's exponent
     alignas(16) float qp[RT], slope[RT];             // positions after the first; bias by distance, log2 units
     alignas(16) int low[RT];                         // first visible position
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                                 }
                                 const float f = rel_weight(mc, mm);
                                 ll += lc * f;
-                                (&hs.top[0][0])[k * RT + r] = f;  // (TR * RT of them)
+                                hs.join[k][r] = f;
                                 bar_sync(bar, GT);
                                 const int some = min(TR, np - c);
 #pragma unroll 1
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                                     }
 #pragma unroll 2
                                     for (int i = 0; i < some; ++i) {
-                                        const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &hs.top[0][0] + i * RT + h;
+                                        const float *q = part_of(c0 + c + i) + (int64_t)h * p.D + key, *g = &hs.join[i][h];
                                         float x[16];
 #pragma unroll
                                         for (int e = 0; e < 16; ++e) x[e] = key < p.D ? __ldcg(q + (int64_t)e * p.D) : 0.0f;
