@@ -273,7 +273,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
     if (tid < G) {
         H &h = all.team[tid];
         for (int s = 0; s < H::KS; ++s) {
-            mbar_init(&h.k_full[s], boxes ? 1 : 32);
+            mbar_init(&h.k_full[s], boxes ? 1 : 33);  // (rows: 32 lanes' copies, and the notes)
             mbar_init(&h.k_empty[s], 1);
         }
         mbar_init(&h.v_full, boxes ? 1 : 32);
@@ -468,7 +468,10 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                             sh.any_bad[i] = any;
                             sh.first[i] = t == t1 - 1;
                         }
-                        __syncwarp();  // (the notes, before the arrival)
+                        // the notes, before an arrival that releases them (a lane's copies
+                        // arrive on their own and release no other writes)
+                        __syncwarp();
+                        if (!boxes && lane == 0) mbar_arrive(&sh.k_full[s]);
                         copy(sh.k[s], &sh.k_full[s], row, 0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) row_v[e] = row[e];

@@ -30,3 +30,25 @@ def test_a_shared_prefix_of_many_parts(G, bs):
     for _ in range(10):
         r = c.run()
         assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
+
+
+@pytest.mark.parametrize("bs", [5, 12])
+@pytest.mark.parametrize("G", [2, 8])
+def test_notes_of_tiles_copied_row_by_row(G, bs):
+    """Pages that no box takes, many short items a block: every tile has exponents,
+    bad blocks and a first mark of its own, in turns of a few buffers."""
+    lens = [1 + (37 * i) % 260 for i in range(150)]
+    c = Case8(lens, S=4, H=8, G=G, D=64, bs=bs, seed=31, spread=6.0)
+    want = c.run()
+    c.check(want, rows=range(0, 150, 7))
+    for _ in range(5):
+        r = c.run()
+        assert torch.equal(r.out, want.out) and torch.equal(r.lse, want.lse)
+    # the same requests without their bad blocks' entries
+    for b in range(0, 150, 3):
+        c.table[b, 0] = c.nb
+    r = c.run()
+    alone = [b for b in range(150) if b % 3]
+    assert torch.equal(r.out[alone], want.out[alone]) and torch.equal(r.lse[alone], want.lse[alone])
+    few = [b for b in range(0, 150, 3) if c.lens[b] > bs]
+    assert torch.isfinite(r.out).all() and not torch.equal(r.out[few], want.out[few])
