@@ -75,6 +75,8 @@ constexpr int kMore = 1;              // powers that many above a row's largest 
 constexpr int kPowMin = 16;           // exponent byte that smaller powers are taken relative to
 constexpr int kUp = 7;                // log2 of a weight of 1 at the largest power: 2^(kUp + kLag + kMore) is an e5m2 number
 constexpr int kParts = 3;             // e5m2 numbers that hold a weight
+constexpr int kIdlePolls = 1 << 27;   // of the MMA warp without a product to issue: a poll takes tens of clk and,
+                                      // unlike the other waits' tries, does not suspend, so this is seconds
 
 __device__ __forceinline__ float2 pair(float a, float b) { return make_float2(a, b); }
 
@@ -319,7 +321,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                 scored[g] = weighed[g] = begun[g] = 0;
                 left += tiles[g] = (int)max((int64_t)0, min(all.plan.total, at + share) - at);
             }
-            while (left > 0 && idle < (int)kSpinLimit) {
+            while (left > 0 && idle < kIdlePolls) {
                 ++idle;
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
             }
             ok = left == 0;
         }
-        __syncwarp();
+        ok = __all_sync(kFull, ok);  // (any lane may have been elected; lane 0 reports)
     } else if (u < uend) {
         AttnItem it = attn_find<NT>(p, all.plan, u, items, rtiles, KT);
         if (warp >= NW) {
