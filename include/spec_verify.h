@@ -745,9 +745,9 @@ int spec_write_kv_q8(const SpecWriteKvQ8Args *args, void *workspace, size_t work
  *   fewer than 2^30 cache entries a layer) multiply on the tensor cores: a query, scaled by a
  *   power of two, as the sum of two e4m3 numbers (off by at most 2^-17 of the
  *   query's largest element), K's codes as they are, the softmax weights times
- *   V's powers of two as the sum of three e5m2 numbers (off by at most 2^-8 of a
- *   weight, or 2^-24 of a weight of 1 at the row's largest power), V's codes
- *   exactly.  The others in f32.
+ *   V's powers of two as the sum of three e5m2 numbers (off by at most 2^-8 of
+ *   such a product, or 2^-27 of the row's largest), V's codes exactly.  The others
+ *   in f32.
  */
 typedef struct SpecAttentionQ8Args {
     int32_t B, S, Hq, H, D, L, layer, dtype; /* dtype of q and out */

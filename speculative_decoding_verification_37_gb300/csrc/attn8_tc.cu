@@ -15,16 +15,20 @@
 //     largest); both products go into one accumulator.  A key's power of two
 //     multiplies its scores.
 //   * O^T = V^T P^T.  A weight of 2^-20 next to one of 1 is worth keeping where there are
-//     many, and e4m3 ends at 2^-9.  So a weight, times its key's power of two relative
-//     to the largest that the row has seen, is rounded to f16 and taken apart into three
-//     e5m2 numbers: the upper byte of an f16 is one, and what it leaves is an f16
-//     again.  So the parts cost an AND, a subtraction and half a byte shuffle each, need
-//     no scales, and hold 9 bits, or 2^-24 of a weight of 1 at the largest power.  They are
-//     columns of one product and are added at the item's end.
+//     many, and e4m3 ends at 2^-9.  So a weight times its key's power of two, relative
+//     to the largest such product that the row has seen, is rounded to f16 and taken
+//     apart into three e5m2 numbers: the upper byte of an f16 is one, and what it leaves
+//     is an f16 again; the third is kept times 2^5.  So the parts cost an AND, a
+//     subtraction and half a byte shuffle each, one multiplication in all, and hold 9
+//     bits, or 2^-27 of the largest product: 2^20 keys that all end below it lose 2^-7
+//     of that together.  (The largest power in its place, without the row's weight of it,
+//     would let a V row that the row hardly sees, or a heavy one with little V, take the
+//     others' bits.)  They are columns of one product and are added at the item's end.
 //   * A row's largest score lies across the threads.  It is looked for, and the
-//     largest power, in an item's first tile and where a score passes the reference
-//     by 2^7 or a power the smallest of the rows' by more than 2, which one vote of the
-//     half's threads finds; otherwise nobody needs another's scores.  Tiles go from the
+//     largest product, in an item's first tile and where a score passes the reference
+//     by 2^7 or a product its row's largest by 2^8, which one vote of the half's threads
+//     finds (a thread compares its key's largest score with the smallest of the rows'
+//     limits first); otherwise nobody needs another's scores.  Tiles go from the
 //     last, which is full, to the first: with a bias by distance the largest scores
 //     come first.  Sums of weights stay in the threads until the item's end.
 //   * Where a tile hides keys, the threads look whether V holds NaN's code: such a row
@@ -71,9 +75,10 @@ constexpr uint32_t kTile = KT * 128;  // bytes of 128 keys x up to 128 codes
 constexpr int kInfo = 4;              // tiles whose notes are kept
 constexpr float kNone = -1e30f;       // the reference of a row that has seen no key
 constexpr float kLag = 7.0f;          // log2 of what a weight may reach
-constexpr int kMore = 1;              // powers that many above a row's largest still fit
-constexpr int kPowMin = 16;           // exponent byte that smaller powers are taken relative to
-constexpr int kUp = 7;                // log2 of a weight of 1 at the largest power: 2^(kUp + kLag + kMore) is an e5m2 number
+constexpr int kPowMin = 16;           // exponent byte that smaller products are taken relative to
+constexpr int kUp = 7;                // log2 of a row's largest product of weight and power, when it was last looked for,
+constexpr int kMore = 8;              // and how far it may grow until it is again: 2^(kUp + kMore) is an e5m2 number
+constexpr int kLast = 5;              // log2 of what the last part is multiplied by (it is below 2^10)
 constexpr int kParts = 3;             // e5m2 numbers that hold a weight
 constexpr int kIdlePolls = 1 << 27;   // of the MMA warp without a product to issue: a poll takes tens of clk and,
                                       // unlike the other waits' tries, does not suspend, so this is seconds
@@ -158,9 +163,11 @@ __device__ __forceinline__ uint32_t rest_e5m2(uint32_t h) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&top));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ uint32_t round_e5m2(uint32_t h) {
+__device__ __forceinline__ uint32_t last_e5m2(uint32_t h) {  // times 2^kLast
+    const uint32_t up = (15u + kLast) << 10 | (15u + kLast) << 26;
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&up));
     uint16_t c;
-    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(h));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(c) : "r"(*reinterpret_cast<const uint32_t *>(&r)));
     return c;
 }
 // 2^e of -126 <= e <= 127; below: 0
@@ -199,15 +206,18 @@ struct Rows8 {
     alignas(16) float nref[RT], zero[RT];            // the references (log2 units), negated; zeros
     alignas(16) float corr[RT], corr_o[RT], gain[RT];  // what sums and O are multiplied by (at the
                                                      // end: O and the shared part); what weights are at a power of 1
+    alignas(16) float most[RT], limit[RT];           // log2 of the largest product so far, to the reference (a weight of 1
+                                                     // at a power of 1: 127); of the largest that fits
     alignas(16) float top[4][RT];                    // the warps' largest scores; at the end sums of weights
-    alignas(16) int pow[4][RT];                      // and powers
+    alignas(16) float prod[4][RT];                   // and products, to those scores
     alignas(16) float join[GT / RT][RT];             // at a join: weights of some parts (a thread has a part and a row)
     alignas(16) float cf[RT];                        // what a product is multiplied by for log2 units or the cap's exponent
     alignas(16) float qp[RT], slope[RT];             // positions after the first; bias by distance, log2 units
     alignas(16) int low[RT];                         // first visible position
     AttnRows<RT> rows[2];
     unsigned words[RT][5];                           // a tile's candidates in the rows' tree masks
-    int pow_min, qp0;                                // the smallest largest power; the first position
+    float limit_min;                                 // the smallest of `limit`
+    int qp0;                                         // the first position
     int low_max[2];                                  // the largest `low`, by turns of items
     int last;
 };
@@ -237,11 +247,8 @@ template <int NH, int HV> struct Tc8Smem {
     uint32_t tmem;
 };
 
-template <int N> __device__ __forceinline__ float sum_parts(const float (&o)[N][8], int r) {
-    float x = o[0][r];
-#pragma unroll
-    for (int c = 1; c < N; ++c) x += o[c][r];
-    return x;
+__device__ __forceinline__ float sum_parts(const float (&o)[kParts][8], int r) {
+    return fmaf(o[2][r], 1.0f / (1 << kLast), o[0][r] + o[1][r]);
 }
 
 // the item after `it` (one copy of this code)
@@ -519,6 +526,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                 if (key < RT) {
                     hs.nref[key] = -kNone;
                     hs.zero[key] = 0.0f;
+                    hs.most[key] = kNone;
                     hs.gain[key] = pow2i(127 + kUp - kPowMin);
                 }
             };
@@ -766,7 +774,6 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                 const int start = line_start(line, it.ntiles);
                 const int qp0 = hs.qp0;
                 const int low_max = max(hs.low_max[item & 1], sh.half[HV - 1 - half].low_max[item & 1]);  // (every row's)
-                int pow_min = 0;                 // the smallest of the rows' largest powers
 #pragma unroll
                 for (int r = 0; r < RT; ++r) l[r] = 0.0f;
                 // position of this thread's key of tile t, when key_pos is given: read a tile ahead
@@ -789,7 +796,8 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                     // (the tile's notes were there before its K)
                     const unsigned char *sc = reinterpret_cast<const unsigned char *>(sh.sc[n % kInfo][0]);
                     const float kf = kv8_power(sc[key]);
-                    const int vs = sc[KT + key], pw = vs == 255 ? 0 : vs;
+                    const int vs = sc[KT + key];
+                    const float pw = vs == 255 ? 0.0f : (float)vs;
                     const int bad = sh.any_bad[n % kInfo];
                     // whether the tile may mask a key: the line's ends, candidates, a bad
                     // block, the window's and the document's first tile
@@ -878,50 +886,54 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                             float over = -INFINITY;
 #pragma unroll
                             for (int r = 0; r < RT; r += 2) over = fmaxf(fmaxf(over, y[r]), y[r + 1]);
-                            if (!bar_or(bar, GT, over > kLag || (in && pw > pow_min + kMore))) break;
+                            bool more = over > kLag;
+                            if (over + pw > hs.limit_min) {  // perhaps a product: rows differ
+#pragma unroll
+                                for (int r = 0; r < RT; r += 4) {
+                                    const float4 m = *reinterpret_cast<const float4 *>(&hs.limit[r]);
+                                    more = more || y[r] + pw > m.x || y[r + 1] + pw > m.y || y[r + 2] + pw > m.z || y[r + 3] + pw > m.w;
+                                }
+                            }
+                            if (!bar_or(bar, GT, more)) break;
                             raw = true;
                             continue;
                         }
-                        // The tile's largest scores and powers; a new reference where a row's score
-                        // has grown past 2^kLag of the old one.
-                        float mine = -INFINITY;  // of row `lane`
-                        int most = 0;
-                        const int every = __reduce_max_sync(kFull, pw);
+                        // The tile's largest scores and products, these relative to the warp's largest
+                        // score (so that they are exact, however far from zero scores are); a new
+                        // reference where a row's score has grown past 2^kLag of the old one.
+                        float mine = -INFINITY, prod = -INFINITY;  // of row `lane`
 #pragma unroll
                         for (int r = 0; r < RT; ++r) {
-                            const float m = warp_max(y[r]);
-                            if (lane == r) mine = m;
-                        }
-                        if (special) {
-#pragma unroll 8
-                            for (int r = 0; r < RT; ++r) {
-                                const int m = __reduce_max_sync(kFull, (seen >> r) & 1u ? pw : 0);
-                                if (lane == r) most = m;
-                            }
-                        } else {  // every row sees every key
-                            most = every;
+                            const float m = warp_max(y[r]), g = warp_max(y[r] - m + pw);
+                            if (lane == r) mine = m, prod = g;
                         }
                         if (lane < RT) {
                             hs.top[wq][lane] = mine;
-                            hs.pow[wq][lane] = most;
+                            hs.prod[wq][lane] = prod;
                         }
                         bar_sync(bar, GT);
                         if (key < RT) {
                             const float top = fmaxf(fmaxf(hs.top[0][key], hs.top[1][key]), fmaxf(hs.top[2][key], hs.top[3][key]));
-                            const int most = max(max(hs.pow[0][key], hs.pow[1][key]), max(hs.pow[2][key], hs.pow[3][key]));
                             const float old = -hs.nref[key];
                             const bool grew = top > old + kLag || (old == kNone && top > kNone);
-                            const float f = grew ? ex2f(old - top) : 1.0f;
-                            const int was = 127 + kUp - ((int)(__float_as_uint(hs.gain[key]) >> 23) - 127), now = max(was, most);
-                            hs.corr[key] = f;
-                            hs.corr_o[key] = f * pow2i(was - now);
+                            const float ref = grew ? top : old, by = old - ref;
+                            float most = hs.most[key] + by;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) most = fmaxf(most, hs.prod[i][key] + (hs.top[i][key] - ref));
+                            // (a weight may be above 1: the gain's power of two stays a normal number)
+                            const int was = 127 + kUp - ((int)(__float_as_uint(hs.gain[key]) >> 23) - 127);
+                            const int now = min(max((int)ceilf(most), kPowMin), 254);
+                            hs.most[key] = most;
+                            hs.limit[key] = (float)(now + kMore);
+                            hs.corr[key] = grew ? ex2f(by) : 1.0f;
+                            hs.corr_o[key] = grew ? ex2f(by + (float)(was - now)) : pow2i(was - now);
                             hs.gain[key] = pow2i(127 + kUp - now);
                             if (grew) hs.nref[key] = -top;
-                            const int least = __reduce_min_sync(kRowLanes, grew || old != kNone ? now : 254);
-                            if (lane == 0) hs.pow_min = least;
+                            // (rows that have seen nothing pass kLag at their first key)
+                            const int least = __reduce_min_sync(kRowLanes, ref > kNone ? now + kMore : 254 + kMore);
+                            if (lane == 0) hs.limit_min = (float)least;
                         }
                         bar_sync(bar, GT);
-                        pow_min = hs.pow_min;
 #pragma unroll
                         for (int r = 0; r < RT; r += 4) {
                             const float4 m = *reinterpret_cast<const float4 *>(&hs.nref[r]), f = *reinterpret_cast<const float4 *>(&hs.corr[r]);
@@ -996,7 +1008,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                         for (int i = 0; i < RT / 2; ++i) h[i] = rest_e5m2(h[i]);
                         put(1);
 #pragma unroll
-                        for (int i = 0; i < RT / 2; ++i) h[i] = round_e5m2(rest_e5m2(h[i]));
+                        for (int i = 0; i < RT / 2; ++i) h[i] = last_e5m2(rest_e5m2(h[i]));
                         put(2);
                     }
                     if (nan_v) {  // the rows that see it get NaN, the others nothing
