@@ -409,8 +409,9 @@ template <int RT> __device__ __forceinline__ float *attn_part(const AttnParams &
 // Query r (of the item's RT rows) joined by a warp from the partial results of n
 // blocks, from block c0 on:
 //   m = max m_c, l = sum l_c 2^(m_c - m), o = sum o_c 2^(m_c - m)
-// A lane takes four columns; U blocks' rows are in flight.
-template <typename T, int U>
+// A lane takes four columns; U blocks' rows are in flight.  NANS: sums that are NaN show
+// from a block whose weight is 0 too.
+template <typename T, int U, bool NANS = false>
 __device__ __forceinline__ void attn_join_row(const AttnParams &p, bool ok, int rt_rows, int c0, int n, int r, int64_t row) {
     const int lane = threadIdx.x & 31;
     const int64_t slot = (int64_t)rt_rows * (p.D + 2), o_m = (int64_t)rt_rows * p.D, o_l = o_m + rt_rows;
@@ -455,7 +456,7 @@ __device__ __forceinline__ void attn_join_row(const AttnParams &p, bool ok, int 
             for (int i = 0; i < U; ++i) {
                 const float wc = __shfl_sync(kFull, w, (c + i) & 31);
                 l += __shfl_sync(kFull, lw, (c + i) & 31);
-                if (wc != 0.0f)
+                if (NANS || wc != 0.0f)
                     o = make_float4(fmaf(x[i].x, wc, o.x), fmaf(x[i].y, wc, o.y), fmaf(x[i].z, wc, o.z), fmaf(x[i].w, wc, o.w));
             }
         }
@@ -465,7 +466,7 @@ __device__ __forceinline__ void attn_join_row(const AttnParams &p, bool ok, int 
 
 // After this block's partial result has been stored (NT threads): the block
 // that arrives last joins the item.  The counter is left zero.
-template <typename T, int RT, int NT>
+template <typename T, int RT, int NT, bool NANS>
 __device__ __forceinline__ void attn_join_here(const AttnParams &p, const AttnItem &it, const AttnRows<RT> &w, ItemBlocks ib,
                                                int *last) {
     const int tid = threadIdx.x, n = ib.c1 - ib.c0 + 1;
@@ -476,7 +477,7 @@ __device__ __forceinline__ void attn_join_here(const AttnParams &p, const AttnIt
     if (!*last) return;
     __threadfence();
     for (int r = tid >> 5; r < RT; r += NT / 32)
-        if (w.out[r] >= 0) attn_join_row<T, 8>(p, it.keys.ok, RT, ib.c0, n, r, w.out[r]);
+        if (w.out[r] >= 0) attn_join_row<T, 8, NANS>(p, it.keys.ok, RT, ib.c0, n, r, w.out[r]);
     if (tid == 0) p.counters[ib.c0] = 0u;
     sync_nt<NT>();
 }
@@ -494,7 +495,7 @@ __device__ __forceinline__ void attn_mark(const AttnParams &p, const AttnItem &i
 // The block's result for item `it`, in shared memory: sums so[RT][ld] with
 // reference m2 = sm[r] (log2 units) and weight sl[r].  Ends with the shared
 // memory free for reuse.  A split item is joined by the block that arrives last.
-template <typename T, int RT, int NT>
+template <typename T, int RT, int NT, bool NANS = false>
 __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan &pl, const AttnItem &it,
                                             const AttnRows<RT> &w, const float *so, int ld, const float *sm,
                                             const float *sl, int *last) {
@@ -528,7 +529,7 @@ __device__ __forceinline__ void attn_finish(const AttnParams &p, const AttnPlan 
             __stcg(mine + (int64_t)RT * p.D + r, sm[r]);
             __stcg(mine + (int64_t)RT * p.D + RT + r, sl[r]);
         }
-        attn_join_here<T, RT, NT>(p, it, w, ib, last);
+        attn_join_here<T, RT, NT, NANS>(p, it, w, ib, last);
     } else {
         sync_nt<NT>();
     }

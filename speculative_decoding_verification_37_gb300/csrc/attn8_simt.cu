@@ -181,11 +181,30 @@ __global__ void __launch_bounds__(NT, blocks_of(DP, R)) attn8_simt_kernel(AttnPa
                 m[r] = m2;
                 x[r] = x[r] == 0.0f ? 0.0f : x[r] * vf;  // (a masked key's power may be NaN)
             }
+            // A V row that stands for NaN, or, where a key is masked from a row (and weights of 0 are
+            // skipped below), one with a NaN code, makes the rows that see it NaN whatever their weight.
+            const bool mask = __any_sync(kFull, hidden);  // a masked key's V may hold anything
+            bool nan = vf != vf;
+            if (mask) {
+#pragma unroll 1
+                for (int i = 0; i < DP / 16; ++i) {  // (neighbours start at another chunk)
+                    const uint4 c = *reinterpret_cast<const uint4 *>(&sh.v[lane][((i + lane) % (DP / 16)) * 16]);
+                    nan = nan || kv8_nan4(c.x) || kv8_nan4(c.y) || kv8_nan4(c.z) || kv8_nan4(c.w);
+                }
+            }
+            if (nan && there) {
+                unsigned seen = 0u;
+#pragma unroll 1
+                for (int r = 0; r < RW; ++r)
+                    seen |= (unsigned)attn_visible<RT>(p, it, sh.rows, row0 + r, c0 + lane, kp, pos_dist(sh.rows.qp[row0 + r], kp)) << r;
+#pragma unroll
+                for (int r = 0; r < RW; ++r)
+                    if ((seen >> r) & 1u) x[r] = __uint_as_float(0x7fffffffu);
+            }
 #pragma unroll
             for (int r = 0; r < RW; r += 4)
                 *reinterpret_cast<float4 *>(&sh.s[lane][row0 + r]) = make_float4(x[r], x[r + 1], x[r + 2], x[r + 3]);
             __syncwarp();
-            const bool mask = __any_sync(kFull, hidden);  // a masked key's V may hold anything
 #pragma unroll 4
             for (int k = 0; k < KT; ++k) {
                 float w[RW], b[CB * CW];
@@ -235,7 +254,7 @@ __global__ void __launch_bounds__(NT, blocks_of(DP, R)) attn8_simt_kernel(AttnPa
             }
         }
         __syncthreads();
-        attn_finish<T, RT, NT>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP, sh.m, sh.l, &sh.last);
+        attn_finish<T, RT, NT, true>(p, sh.plan, it, sh.rows, &sh.o[0][0], DP, sh.m, sh.l, &sh.last);
         u = it.u0 + it.ntiles;
         if (u >= uend) break;
         it = attn_next(p, it, p.H * rtiles, rtiles, KT);

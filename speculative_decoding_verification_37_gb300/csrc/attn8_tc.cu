@@ -687,8 +687,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
 #pragma unroll
                                         for (int e = 0; e < 16; ++e) x[e] = key < p.D ? __ldcg(q + (int64_t)e * p.D) : 0.0f;
 #pragma unroll
-                                        for (int e = 0; e < 16; ++e)
-                                            if (g[e] != 0.0f) o[e] = fmaf(x[e], g[e], o[e]);
+                                        for (int e = 0; e < 16; ++e) o[e] = fmaf(x[e], g[e], o[e]);  // (a weight of 0 keeps V's NaN)
                                     }
                                     tc_st16(to + h, reinterpret_cast<const uint32_t *>(o));
                                 }
@@ -753,7 +752,7 @@ __global__ void __launch_bounds__((threads_of<NH, HV>()), 1)
                             for (int r = 0; r < 8; ++r) {
                                 const int64_t row = w.out[h + r], at = row * p.D + key;
                                 const float f = hs.corr[h + r];
-                                float x = f == 0.0f ? 0.0f : sum_parts(o, r) * f;
+                                float x = sum_parts(o, r) * f;  // (a row that sees nothing: zeros; f = 0 keeps V's NaN)
                                 if (join) x = fmaf(sp[r], hs.corr_o[h + r], x);
                                 if (row >= 0 && key < p.D) {
                                     if (p.mode == 1) p.pre_o[at] = x;

@@ -46,4 +46,7 @@ __device__ __forceinline__ float4 kv8_value4(uint32_t codes) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
+// whether one of four codes is NaN
+__device__ __forceinline__ bool kv8_nan4(uint32_t codes) { return (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0u; }
+
 }  // namespace specv

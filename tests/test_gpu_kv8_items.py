@@ -3,6 +3,7 @@ where its tiles' notes, copies and partial results go round their buffers often.
 import pytest
 import torch
 
+from speculative_decoding_verification_37_gb300 import _lib as L
 from test_gpu_kv8 import Case8
 
 pytestmark = pytest.mark.gpu
@@ -47,7 +48,9 @@ def test_notes_of_tiles_copied_row_by_row(G, bs):
     # the same requests without their bad blocks' entries
     for b in range(0, 150, 3):
         c.table[b, 0] = c.nb
-    r = c.run()
+    ws = L.new_workspace(L.SPEC_WS_ATTENTION, 150, 4 * 8 * G, 64)    # (its status word stays set)
+    r = c.run(ws=ws)
+    assert L.spec_get_status(ws) == L.SPEC_FLAG_BAD_INPUT
     alone = [b for b in range(150) if b % 3]
     assert torch.equal(r.out[alone], want.out[alone]) and torch.equal(r.lse[alone], want.lse[alone])
     few = [b for b in range(0, 150, 3) if c.lens[b] > bs]
