@@ -279,16 +279,15 @@ template <typename T, int DP> cudaError_t launch_r(const AttnParams &p, int sms,
     return launch<T, DP, 2>(p, sms, s);
 }
 
-template <typename T> cudaError_t launch_t(const AttnParams &p, int sms, cudaStream_t s) {
-    if (p.D <= 64) return launch_r<T, 64>(p, sms, s);
-    if (p.D <= 128) return launch_r<T, 128>(p, sms, s);
-    return launch_r<T, 256>(p, sms, s);
-}
-
 }  // namespace
 
 cudaError_t launch_attn8_simt(const AttnParams &p, int dtype, int sms, cudaStream_t s) {
-    return dtype == SPEC_DTYPE_BF16 ? launch_t<__nv_bfloat16>(p, sms, s) : launch_t<float>(p, sms, s);
+    // (bf16 heads up to 128 come here from 2^30 entries a layer on, 34 GB of codes at
+    // least: the kernel for wide heads takes them too)
+    if (dtype == SPEC_DTYPE_BF16) return launch_r<__nv_bfloat16, 256>(p, sms, s);
+    if (p.D <= 64) return launch_r<float, 64>(p, sms, s);
+    if (p.D <= 128) return launch_r<float, 128>(p, sms, s);
+    return launch_r<float, 256>(p, sms, s);
 }
 
 }  // namespace specv
