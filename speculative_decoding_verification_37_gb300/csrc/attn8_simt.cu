@@ -9,8 +9,8 @@
 // into its score and, for V, into its softmax weight: both exact.
 //
 // Bound by issue (55 % of the slots, a fifth of the stalls on shared memory): 64 requests
-// of 5 queries x group 4 on 2,048 entries, 8 heads of 128, f32: 657 us, 16.4 TFLOP/s; heads
-// of 256, bf16: 1,266 us, 17.0.
+// of 5 queries x group 4 on 2,048 entries, 8 heads of 128, f32: 662 us, 16.3 TFLOP/s; heads
+// of 256, bf16: 1,290 us, 16.7.
 #include "attention.cuh"
 #include "kv8.cuh"
 #include "tma.cuh"

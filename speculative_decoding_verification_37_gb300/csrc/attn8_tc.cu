@@ -36,12 +36,12 @@
 //     hidden from see nothing.
 //   * Pages that are a multiple of 8 entries come in boxes of the copy engine; of others
 //     each lane copies 16 bytes of a row at a time: 64 x 5 queries on 2,048 entries in pages
-//     of 5 273 us instead of 89 (CUDA cores: 664), single queries 1,326 instead of 376 (2,733).
+//     of 5 280 us instead of 89 (CUDA cores: 664), single queries 1,329 instead of 377 (2,733).
 //     That form is built once, for any scores.
 //
 // What bounds it.  Single queries on up to 32,768 entries, 64 requests, 8 heads of 128:
-// 376 to 390 us by the GPU, up to 5.9 TB/s of the 6.65 that a copy reaches.  64 requests of
-// 5 queries x group 4 on 2,048 entries: 88 us (3.2 TB/s; the tiles themselves run at 6.2):
+// 377 to 392 us by the GPU, up to 5.9 TB/s of the 6.65 that a copy reaches.  64 requests of
+// 5 queries x group 4 on 2,048 entries: 89 us (3.1 TB/s; the tiles themselves run at 6.2):
 // a team's start (13 us) and each change of items (some 12 us: the next queries, partial
 // results, the first tile's references) run code that is in no cache any more and comes
 // from far away, one miss of some 1,000 clk after another.  That is why the rest is short:
@@ -49,14 +49,15 @@
 // instead of 13, a shared prefix of 4,096 entries 137 instead of 130), one place for the
 // queries of an item, the first or a later one (chain 91 -> 88 us, tree 324 -> 312), and why
 // K and V ask L2 to let go of them first (single queries 406 -> 388 us, the chain 92 -> 89).
-// 128 x 13 queries x group 4 on 2,048 entries, capped and biased, 312 us: bound by the
-// softmax's instructions (30 a weight; half of the issue slots) and the second reading of
+// 128 x 13 queries x group 4 on 2,048 entries, capped and biased, 325 us: bound by the
+// softmax's instructions (30 a weight; half of the issue slots; the two halves' forms have 96
+// registers, which spills some 80 bytes, because there are 19 warps) and the second reading of
 // keys for the rows past 32; one tile of 64 rows, its threads at 96 registers, was no faster.
 //
 // The MMAs: an MMA of 128 x N x 32 takes 32 + N/4 clk, and 54 at least if its thread is
 // not an elected one (the operands are then moved to uniform registers each time).
-// Larger pages come in larger boxes: single queries on pages of 64 entries 361 us, of
-// 128 355.
+// Larger pages come in larger boxes: single queries on pages of 64 entries 360 to
+// 379 us, of 128 354 to 378.
 #include <cuda_fp16.h>
 
 #include "attention.cuh"
